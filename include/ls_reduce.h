@@ -416,6 +416,206 @@ ls_status ls_cross_entropy_bw(void *dlogits, const void *logits, const int32_t *
                               const float *lse, const float *dloss, int64_t rows,
                               int64_t vocab, ls_dtype dt, void *stream);
 
+/* Limits of the softmax with a relative position bias. */
+#define LS_MAX_RELPOS_DISTANCE ((int64_t)2048)
+#define LS_MAX_RELPOS_BUCKETS ((int64_t)65536)
+
+/*
+ * Attention softmax with a learned relative position bias by buckets,
+ * forward.  The scaled softmax (ls_softmax_fw_scaled) plus one learned number
+ * per (bucket of the distance from query to key, head).  The Tq queries are
+ * the last Tq of the Tk key positions, so with R = max_distance:
+ *     r    = min(max(j - (i + Tk - Tq), -R), R)
+ *     z_ij = scale * x[b,h,i,j] + table[bucket[r + R], h] + mask[b,j]
+ *     out[b,h,i,:] = softmax over the visible j of z_i
+ * A key is invisible when its mask element is -inf or, with causal, when it
+ * lies in the query's future (j > i + Tk - Tq); invisible keys are written as
+ * 0 and their scores never matter, NaN or not.  A row without a visible key,
+ * or whose every z is -inf, is written as zeros.  A single decoding step is
+ * Tq = 1.
+ *
+ *   out    [B,H,Tq,Tk] dt, device, written.  May equal `inp` (in place).
+ *   inp    [B,H,Tq,Tk] dt, device, read.
+ *   mask   [B,Tk] dt additive mask, device, read; NULL means no mask.  Any
+ *          value: 0, -inf, the type's lowest value, a finite bias.
+ *   table  [num_buckets,H] dt, device, read: the learned bias.
+ *   bucket [2R + 1] int32, device, read: the bucket of each clipped distance
+ *          -R ... R.  Ids outside [0, num_buckets) add no bias.
+ *   causal, scale  as for ls_softmax_fw_scaled (Tq > Tk only without causal).
+ * Errors: LS_ERR_INVALID_ARG for NULL out / inp / table / bucket with a
+ * non-empty problem, negative sizes, num_buckets or max_distance < 1, causal
+ * with Tq > Tk, scale not finite or <= 0; LS_ERR_UNSUPPORTED for an unknown
+ * dtype or sizes beyond the limits above or LS_MAX_ROW_LENGTH (Tq and Tk).
+ */
+ls_status ls_softmax_fw_relpos(void *out, const void *inp, const void *mask, const void *table,
+                               const int32_t *bucket, int64_t B, int64_t H, int64_t Tq,
+                               int64_t Tk, int64_t num_buckets, int64_t max_distance, int causal,
+                               float scale, ls_dtype dt, void *stream);
+
+/*
+ * Bytes of device workspace ls_softmax_bw_relpos needs for H heads and
+ * max_distance, whatever the other sizes and the dtype.  0 for sizes that it
+ * refuses.  Host-only; launches nothing.
+ */
+size_t ls_softmax_bw_relpos_workspace_size(int64_t H, int64_t max_distance);
+
+/*
+ * Attention softmax with a relative position bias, backward: the gradients of
+ * the scores and of the table.  On visible keys, with s = sum over visible k
+ * of out_k * dout_k,
+ *     dz_ij      = out_ij * (dout_ij - s_i)
+ *     dinp_ij    = scale * dz_ij                      (0 on invisible keys)
+ *     dtable[k,h] = sum over every b, i and visible j with
+ *                   bucket[r + R] == k of dz[b,h,i,j]
+ * dz enters the table's sum in FP32, before dinp is rounded.  Invisible keys
+ * are neither read from dout / out_fw nor summed.  The sums are taken in an
+ * order that depends only on the arguments: bitwise reproducible.
+ *
+ *   dinp    [B,H,Tq,Tk] dt, device, written.  May equal `dout`.
+ *   dtable  [num_buckets,H] float32, device, written (overwritten; zeros when
+ *           there is no score).
+ *   dout, out_fw  [B,H,Tq,Tk] dt, device, read on visible keys only.
+ *   mask, bucket, causal, scale  as given to the forward.
+ *   workspace  device scratch of at least
+ *           ls_softmax_bw_relpos_workspace_size(H, max_distance) bytes,
+ *           16-byte aligned, contents ignored.  May be NULL when there is no
+ *           score.  Calls that overlap on the GPU must not share it.
+ * Errors as for ls_softmax_fw_relpos, plus LS_ERR_WORKSPACE.
+ */
+ls_status ls_softmax_bw_relpos(void *dinp, float *dtable, const void *dout, const void *out_fw,
+                               const void *mask, const int32_t *bucket, int64_t B, int64_t H,
+                               int64_t Tq, int64_t Tk, int64_t num_buckets, int64_t max_distance,
+                               int causal, float scale, void *workspace, size_t workspace_bytes,
+                               ls_dtype dt, void *stream);
+
+/* Largest head size of the per-head norm. */
+#define LS_MAX_HEAD_DIM ((int64_t)1024)
+
+/*
+ * RMSNorm of every query head and every key head, and the rotation by the
+ * token's position, in one pass (ls_rmsnorm_fw over rows of D features, with
+ * one gamma for all query heads and one for all key heads).  Per row x of
+ * token t:
+ *     rstd = 1 / sqrt(mean(x^2) + eps),   n_j = x_j * rstd * gamma_j
+ *     (y_a, y_b) = (n_a c - n_b s, n_b c + n_a s),  c = cos[positions[t], p],
+ *                                                   s = sin[positions[t], p]
+ * for the pairs p < rot / 2, which are (p, p + rot / 2), or (2p, 2p + 1) when
+ * interleaved; y_j = n_j for j >= rot.  rot = 0 is the norm alone.
+ * The normed value is not rounded before the rotation.
+ *
+ *   q_out, k_out  [tokens,Hq,D], [tokens,Hk,D] dt, device, written.  May equal
+ *                 q and k (in place, same strides).
+ *   q_rstd, k_rstd  [tokens,Hq], [tokens,Hk] float32, device, written (saved
+ *                 for the backward); NULL: not written.
+ *   q, k          [tokens,Hq,D], [tokens,Hk,D] dt, device, read.
+ *   *_stride      elements from one token to the next (>= heads * D; heads
+ *                 and features are dense), so q and k may be slices of one
+ *                 packed projection.
+ *   gamma_q, gamma_k  [D] dt, device, read.
+ *   cos, sin      [max_pos, rot / 2] float32, device, read.
+ *   positions     [tokens] int32, device, read.  A position outside
+ *                 [0, max_pos) makes the token's rotated features NaN.
+ * Hq or Hk may be 0 (its pointers are then ignored).
+ * Errors: LS_ERR_INVALID_ARG for a NULL pointer that is needed, negative
+ * sizes, D < 1, rot odd or outside [0, D], a stride below heads * D, eps < 0
+ * or not finite; LS_ERR_UNSUPPORTED for an unknown dtype or D beyond
+ * LS_MAX_HEAD_DIM; LS_ERR_MISALIGNED as everywhere.
+ */
+ls_status ls_qk_norm_rope_fw(void *q_out, void *k_out, float *q_rstd, float *k_rstd,
+                             const void *q, const void *k, const void *gamma_q,
+                             const void *gamma_k, const float *cos, const float *sin,
+                             const int32_t *positions, int64_t tokens, int64_t Hq, int64_t Hk,
+                             int64_t D, int64_t rot, int64_t max_pos, int64_t q_out_stride,
+                             int64_t k_out_stride, int64_t q_stride, int64_t k_stride,
+                             int interleaved, float eps, ls_dtype dt, void *stream);
+
+/*
+ * Bytes of device workspace ls_qk_norm_rope_bw needs.  0 for no tokens and
+ * for sizes that it refuses.  Host-only; launches nothing.
+ */
+size_t ls_qk_norm_rope_bw_workspace_size(int64_t tokens, int64_t Hq, int64_t Hk, int64_t D);
+
+/*
+ * Per-head norm with rotation, backward: the gradients of q and k and of both
+ * gammas, in one pass over the inputs.  With dn the upstream gradient turned
+ * back by the position's angles, xhat = x * rstd and g = gamma * dn, per row:
+ *     dx_j     = rstd * (g_j - xhat_j * sum_k(g_k xhat_k) / D)
+ *     dgamma_j = sum over every token and head of the side of dn_j * xhat_j
+ * The gamma sums are taken in an order that depends only on the sizes.
+ *
+ *   dq, dk        [tokens,heads,D] dt, device, written.  May equal dq_out and
+ *                 dk_out (same strides).
+ *   dgamma_q, dgamma_k  [D] float32, device, written (overwritten; zeros when
+ *                 tokens == 0).
+ *   dq_out, dk_out  gradients of the forward's outputs, dt, device, read.
+ *   q, k, gamma_*, cos, sin, positions  as given to the forward.
+ *   q_rstd, k_rstd  as saved by the forward.
+ *   workspace     device scratch of at least
+ *                 ls_qk_norm_rope_bw_workspace_size(tokens, Hq, Hk, D) bytes,
+ *                 16-byte aligned, contents ignored; may be NULL when that is
+ *                 0.  Calls that overlap on the GPU must not share it.
+ * A position outside the table makes the token's gradients NaN, and the
+ * gamma gradients of the rotated features.  Errors as for the forward, plus
+ * LS_ERR_WORKSPACE.
+ */
+ls_status ls_qk_norm_rope_bw(void *dq, void *dk, float *dgamma_q, float *dgamma_k,
+                             const void *dq_out, const void *dk_out, const void *q, const void *k,
+                             const void *gamma_q, const void *gamma_k, const float *q_rstd,
+                             const float *k_rstd, const float *cos, const float *sin,
+                             const int32_t *positions, int64_t tokens, int64_t Hq, int64_t Hk,
+                             int64_t D, int64_t rot, int64_t max_pos, int64_t dq_stride,
+                             int64_t dk_stride, int64_t dq_out_stride, int64_t dk_out_stride,
+                             int64_t q_stride, int64_t k_stride, int interleaved, void *workspace,
+                             size_t workspace_bytes, ls_dtype dt, void *stream);
+
+/*
+ * Bytes of device workspace ls_grad_norm and ls_grad_clip need for a list of
+ * `count` tensors, whatever their sizes.  Host-only; launches nothing.
+ */
+size_t ls_grad_norm_workspace_size(int64_t count);
+
+/*
+ * Global norm of a list of gradient tensors:
+ *     norm = sqrt(sum over all tensors of the sum of g^2)
+ * Squares are summed in FP32 within 8 vectors of a thread (in FP64 where they
+ * would over- or underflow) and in FP64 beyond, in an order that depends only
+ * on the list: bitwise reproducible.  inf or NaN elements give inf or NaN.
+ *
+ *   norm    [1] float32, device, written (0 for an empty list).
+ *   grads, sizes, dtypes  HOST arrays of `count` entries, read before the
+ *           call returns: device pointers to dense tensors, their element
+ *           counts and their ls_dtype codes (types may be mixed).  A pointer
+ *           needs only its element's alignment.  Tensors of 0 elements are
+ *           skipped.
+ *   workspace  device scratch of at least ls_grad_norm_workspace_size(count)
+ *           bytes, 16-byte aligned, contents ignored; may be NULL for an
+ *           empty list.  Calls that overlap on the GPU must not share it.
+ * Errors: LS_ERR_INVALID_ARG for NULL pointers, negative counts or sizes;
+ * LS_ERR_UNSUPPORTED for an unknown dtype; LS_ERR_MISALIGNED;
+ * LS_ERR_WORKSPACE; LS_ERR_CUDA.
+ */
+ls_status ls_grad_norm(float *norm, const void *const *grads, const int64_t *sizes,
+                       const int32_t *dtypes, int64_t count, void *workspace,
+                       size_t workspace_bytes, void *stream);
+
+/*
+ * Clipping by the global norm: the norm as ls_grad_norm computes it, and
+ *     out = g * min(1, max_norm / (norm + eps))
+ * for every tensor.  In place (out[i] == grads[i]) a list that needs no
+ * clipping is left as it is, unwritten.  A NaN norm makes every output NaN;
+ * an infinite one makes finite elements 0 and infinite ones NaN.
+ *
+ *   out     HOST array of `count` device pointers, written, each of its
+ *           gradient's size and dtype; may equal grads entry by entry.  No
+ *           other overlap between entries is allowed.
+ *   max_norm  finite and > 0.   eps  finite and >= 0.
+ * Other arguments and errors as for ls_grad_norm; LS_ERR_INVALID_ARG for a
+ * bad max_norm or eps.
+ */
+ls_status ls_grad_clip(float *norm, void *const *out, const void *const *grads,
+                       const int64_t *sizes, const int32_t *dtypes, int64_t count, float max_norm,
+                       float eps, void *workspace, size_t workspace_bytes, void *stream);
+
 /* Static, human-readable name of a status code (never NULL). */
 const char *ls_status_string(ls_status s);
 

@@ -10,6 +10,8 @@ if the library is missing or a call fails, they raise.
 """
 from __future__ import annotations
 
+import ctypes
+
 from ._lib import (LS_BF16, LS_ERR_CUDA, ls_cross_entropy_bw, ls_cross_entropy_fw,
                    ls_softmax_bw_masked_scaled, ls_softmax_fw_scaled, LS_ERR_INVALID_ARG, LS_ERR_MISALIGNED,  # noqa: F401
                    LS_ERR_UNSUPPORTED, LS_ERR_WORKSPACE, LS_F16, LS_F32, LS_OK, LsError,
@@ -18,6 +20,9 @@ from ._lib import (LS_BF16, LS_ERR_CUDA, ls_cross_entropy_bw, ls_cross_entropy_f
                    ls_layernorm_fw, ls_rmsnorm_bw_dgamma,
                    ls_rmsnorm_bw_dinp, ls_rmsnorm_fw, ls_softmax_bw, ls_softmax_bw_masked,
                    ls_softmax_fw, load, status_string)
+from ._lib import (ls_grad_clip, ls_grad_norm, ls_grad_norm_workspace_size, ls_qk_norm_rope_bw,
+                   ls_qk_norm_rope_bw_workspace_size, ls_qk_norm_rope_fw, ls_softmax_bw_relpos,
+                   ls_softmax_bw_relpos_workspace_size, ls_softmax_fw_relpos)
 
 __all__ = [
     "softmax_fw", "softmax_bw", "softmax_bw_masked", "layernorm_fw", "layernorm_bw_dinp",
@@ -28,6 +33,12 @@ __all__ = [
     "ls_softmax_fw", "ls_softmax_bw", "ls_softmax_bw_masked", "ls_layernorm_fw", "ls_layernorm_bw_dinp",
     "ls_layernorm_bw_dgamma_dbeta", "ls_layernorm_bw_dgamma_dbeta_workspace_size",
     "ls_layernorm_bw", "ls_layernorm_bw_workspace_size", "ls_rmsnorm_fw", "ls_rmsnorm_bw_dinp", "ls_rmsnorm_bw_dgamma",
+    "relpos_buckets", "softmax_fw_relpos", "softmax_bw_relpos", "softmax_relpos_workspace",
+    "rope_tables", "qk_norm_rope_fw", "qk_norm_rope_bw", "qk_norm_rope_workspace",
+    "grad_norm", "grad_clip", "grad_norm_workspace",
+    "ls_softmax_fw_relpos", "ls_softmax_bw_relpos", "ls_softmax_bw_relpos_workspace_size",
+    "ls_qk_norm_rope_fw", "ls_qk_norm_rope_bw", "ls_qk_norm_rope_bw_workspace_size",
+    "ls_grad_norm", "ls_grad_clip", "ls_grad_norm_workspace_size",
 ]
 
 
@@ -95,7 +106,11 @@ def _ok(status: int, where: str):
 def _call(where: str, dev, fn, *args):
     """Run one library call with ``dev`` as the current device (the library
     launches on the current device, on the stream it is given)."""
-    with _torch().cuda.device(dev):
+    torch = _torch()
+    if dev.index == torch.cuda.current_device():
+        _ok(fn(*args), where)
+        return
+    with torch.cuda.device(dev):
         _ok(fn(*args), where)
 
 
@@ -338,3 +353,329 @@ def cross_entropy_bw(logits, target, lse, dloss, dlogits=None):
     _call("ls_cross_entropy_bw", dev, ls_cross_entropy_bw, _ptr(dlogits), _ptr(logits),
           _ptr(target), _ptr(lse), _ptr(dloss), rows, vocab, ls_dtype(logits), _stream(logits))
     return dlogits
+
+
+# ----------------------------------------------------------------------------
+# softmax with a learned relative position bias
+# ----------------------------------------------------------------------------
+def relpos_buckets(num_buckets: int = 32, max_distance: int = 128, bidirectional: bool = True,
+                   device="cuda"):
+    """The usual bucket map: int32 [2 * max_distance + 1], the bucket of each
+    clipped distance -max_distance ... max_distance from query to key.  Near
+    distances have buckets of their own, farther ones share them in ratios up
+    to max_distance; with ``bidirectional`` half of the buckets are for keys
+    after the query, otherwise those keys share bucket 0 (distance 0).
+
+    Found in whole numbers: distance n is past step t of the k wide buckets
+    when log(n/e) / log(max_distance/e) * k >= t, that is when
+    n^k e^t >= max_distance^t e^k (e: the distances with their own bucket).
+    Any other int32 map of this length can be given to the softmax instead."""
+    torch = _torch()
+    half = num_buckets // 2 if bidirectional else num_buckets
+    e = half // 2
+    if e < 1 or max_distance <= e:
+        raise ValueError("relpos_buckets needs num_buckets >= 4 (2 without bidirectional) and "
+                         "max_distance above the number of single distances")
+    k = half - e
+    side, t = [], 0
+    for n in range(max_distance + 1):
+        if n < e:
+            side.append(n)
+            continue
+        while t + 1 < k and n ** k * e ** (t + 1) >= max_distance ** (t + 1) * e ** k:
+            t += 1
+        side.append(e + t)
+    after = [half + b for b in side[1:]] if bidirectional else [0] * max_distance
+    return torch.tensor(side[::-1] + after, dtype=torch.int32, device=device)
+
+
+def _relpos(bucket):
+    torch = _torch()
+    if bucket.dim() != 1 or bucket.dtype != torch.int32 or bucket.numel() % 2 == 0:
+        raise ValueError("buckets must be a 1-D int32 tensor of 2 * max_distance + 1 ids")
+    return bucket.numel() // 2
+
+
+def softmax_fw_relpos(scores, table, buckets, mask=None, causal: bool = False, scale=None,
+                      out=None):
+    """Softmax over the last axis of scale * scores [B,H,Tq,Tk] plus the learned
+    bias ``table[buckets[r + R], h]`` of the clipped distance r = j - (i + Tk -
+    Tq) in [-R, R], plus an additive mask [B,Tk]; future keys masked when
+    ``causal``.  ``table`` is [num_buckets, H] in the scores' dtype, ``buckets``
+    int32 [2R + 1] (see relpos_buckets).  ``out`` may be ``scores``."""
+    torch = _torch()
+    if scores.dim() != 4:
+        raise ValueError("scores must be [B, H, Tq, Tk]")
+    B, H, Tq, Tk = scores.shape
+    if table.dim() != 2:
+        raise ValueError("table must be [num_buckets, H]")
+    _want("table", table, (table.shape[0], H), scores.dtype)
+    R = _relpos(buckets)
+    _want("mask", mask, (B, Tk), scores.dtype)
+    _want("out", out, scores.shape, scores.dtype)
+    out = torch.empty_like(scores) if out is None else out
+    dev = _dev(scores, table, buckets, mask, out)
+    _call("ls_softmax_fw_relpos", dev, ls_softmax_fw_relpos, _ptr(out), _ptr(scores), _ptr(mask),
+          _ptr(table), _ptr(buckets), B, H, Tq, Tk, table.shape[0], R, causal,
+          1.0 if scale is None else float(scale), ls_dtype(scores), _stream(scores))
+    return out
+
+
+def softmax_relpos_workspace(H: int, max_distance: int, device):
+    """A workspace tensor of the size ls_softmax_bw_relpos needs."""
+    n = ls_softmax_bw_relpos_workspace_size(H, max_distance)
+    return _torch().empty(max(n, 16) // 4, device=device, dtype=_torch().float32)
+
+
+def softmax_bw_relpos(dout, out_fw, buckets, num_buckets: int, mask=None, causal: bool = False,
+                      scale=None, workspace=None, dinp=None, dtable=None):
+    """Gradients of ``softmax_fw_relpos``: (dscores, dtable), dtable fp32
+    [num_buckets, H] in a fixed summation order.  Reads only visible keys;
+    ``dinp`` may be ``dout``."""
+    torch = _torch()
+    if dout.dim() != 4:
+        raise ValueError("dout must be [B, H, Tq, Tk]")
+    B, H, Tq, Tk = dout.shape
+    _want("out_fw", out_fw, dout.shape, dout.dtype)
+    R = _relpos(buckets)
+    _want("mask", mask, (B, Tk), dout.dtype)
+    _want("dinp", dinp, dout.shape, dout.dtype)
+    _want("dtable", dtable, (num_buckets, H), torch.float32)
+    if workspace is None:
+        workspace = softmax_relpos_workspace(H, R, dout.device)
+    _workspace("workspace", workspace)
+    dinp = torch.empty_like(dout) if dinp is None else dinp
+    if dtable is None:
+        dtable = torch.empty(num_buckets, H, device=dout.device, dtype=torch.float32)
+    dev = _dev(dout, out_fw, buckets, mask, workspace, dinp, dtable)
+    _call("ls_softmax_bw_relpos", dev, ls_softmax_bw_relpos, _ptr(dinp), _ptr(dtable), _ptr(dout),
+          _ptr(out_fw), _ptr(mask), _ptr(buckets), B, H, Tq, Tk, num_buckets, R, causal,
+          1.0 if scale is None else float(scale), _ptr(workspace),
+          workspace.numel() * workspace.element_size(), ls_dtype(dout), _stream(dout))
+    return dinp, dtable
+
+
+# ----------------------------------------------------------------------------
+# per-head norm of queries and keys with the position rotation
+# ----------------------------------------------------------------------------
+def rope_tables(max_pos: int, rot: int, base: float = 10000.0, device="cuda"):
+    """Cosine and sine tables, fp32 [max_pos, rot / 2], of the angles
+    position * base^(-2p / rot), computed in float64 and rounded once."""
+    torch = _torch()
+    if rot < 2 or rot % 2:
+        raise ValueError("rot must be even and at least 2")
+    p = torch.arange(0, rot, 2, device=device, dtype=torch.float64)
+    angle = torch.arange(max_pos, device=device, dtype=torch.float64)[:, None] * base ** (-p / rot)
+    return angle.cos().float(), angle.sin().float()
+
+
+def _heads(name, t, tokens=None, D=None, dtype=None):
+    """Token stride of a [tokens, heads, D] tensor whose heads and features are
+    dense (a slice of a packed projection is)."""
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [tokens, heads, D]")
+    n, h, d = t.shape
+    if (tokens is not None and n != tokens) or (D is not None and d != D) or \
+            (dtype is not None and t.dtype != dtype):
+        raise ValueError(f"{name} must be {dtype} of shape [{tokens}, heads, {D}], "
+                         f"got {t.dtype} of shape {list(t.shape)}")
+    s = t.stride()
+    if (d > 1 and s[2] != 1) or (h > 1 and s[1] != d):
+        raise ValueError(f"{name} must have dense heads and features")
+    if n <= 1 or h == 0:
+        return h * d
+    if s[0] < h * d:
+        raise ValueError(f"{name} must not overlap itself (token stride {s[0]} < {h * d})")
+    return s[0]
+
+
+def _like_heads(name, t, x):
+    """As _heads, for a tensor that has to have x's shape and dtype."""
+    if t.shape != x.shape or t.dtype != x.dtype:
+        raise ValueError(f"{name} must be {x.dtype} of shape {list(x.shape)}, "
+                         f"got {t.dtype} of shape {list(t.shape)}")
+    return _heads(name, t)
+
+
+def _rotation(cos, sin, positions, tokens, D):
+    """(rot, max_pos) of the rotation tables; (0, 0) without them."""
+    torch = _torch()
+    if cos is None and sin is None and positions is None:
+        return 0, 0
+    if cos is None or sin is None or positions is None:
+        raise ValueError("cos, sin and positions go together")
+    if cos.dim() != 2 or 2 * cos.shape[1] > D:
+        raise ValueError(f"cos must be [max_pos, rot / 2] with rot <= {D}")
+    _want("cos", cos, cos.shape, torch.float32)
+    _want("sin", sin, cos.shape, torch.float32)
+    _want("positions", positions, (tokens,), torch.int32)
+    return 2 * cos.shape[1], cos.shape[0]
+
+
+def _one_device(strided, dense):
+    """The one device of all tensors; the dense ones must be contiguous."""
+    dev = _dev(*dense)
+    for t in strided:
+        if not t.is_cuda:
+            raise ValueError("tensors must live on a CUDA device (there is no CPU path)")
+        if t.device != dev:
+            raise ValueError(f"tensors on different devices ({dev} and {t.device})")
+    return dev
+
+
+def qk_norm_rope_fw(q, k, gamma_q, gamma_k, cos=None, sin=None, positions=None,
+                    interleaved: bool = False, eps: float = 1e-6, q_out=None, k_out=None,
+                    q_rstd=None, k_rstd=None):
+    """RMSNorm of every head of q [tokens, Hq, D] and k [tokens, Hk, D] (gamma_q
+    and gamma_k [D]) and, with ``cos`` / ``sin`` (fp32 [max_pos, rot / 2], see
+    rope_tables) and ``positions`` (int32 [tokens]), the rotation of the first
+    rot features; pairs are (p, p + rot / 2), or neighbours when
+    ``interleaved``.  Returns (q_out, k_out, q_rstd, k_rstd), the statistics
+    fp32.  Tokens may be strided (slices of a packed projection); the outputs
+    may be the inputs (in place, same strides)."""
+    torch = _torch()
+    qs = _heads("q", q)
+    tokens, Hq, D = q.shape
+    ks = _heads("k", k, tokens, D, q.dtype)
+    Hk = k.shape[1]
+    _want("gamma_q", gamma_q, (D,), q.dtype)
+    _want("gamma_k", gamma_k, (D,), q.dtype)
+    rot, max_pos = _rotation(cos, sin, positions, tokens, D)
+    _want("q_rstd", q_rstd, (tokens, Hq), torch.float32)
+    _want("k_rstd", k_rstd, (tokens, Hk), torch.float32)
+    new = dict(device=q.device, dtype=q.dtype)
+    q_out = torch.empty((tokens, Hq, D), **new) if q_out is None else q_out
+    k_out = torch.empty((tokens, Hk, D), **new) if k_out is None else k_out
+    qos, kos = _like_heads("q_out", q_out, q), _like_heads("k_out", k_out, k)
+    new["dtype"] = torch.float32
+    q_rstd = torch.empty((tokens, Hq), **new) if q_rstd is None else q_rstd
+    k_rstd = torch.empty((tokens, Hk), **new) if k_rstd is None else k_rstd
+    dev = _one_device((q, k, q_out, k_out),
+                      (gamma_q, gamma_k, cos, sin, positions, q_rstd, k_rstd))
+    _call("ls_qk_norm_rope_fw", dev, ls_qk_norm_rope_fw, _ptr(q_out), _ptr(k_out), _ptr(q_rstd),
+          _ptr(k_rstd), _ptr(q), _ptr(k), _ptr(gamma_q), _ptr(gamma_k), _ptr(cos), _ptr(sin),
+          _ptr(positions), tokens, Hq, Hk, D, rot, max_pos, qos, kos, qs, ks, interleaved,
+          float(eps), ls_dtype(q), _stream(q))
+    return q_out, k_out, q_rstd, k_rstd
+
+
+def qk_norm_rope_workspace(tokens: int, Hq: int, Hk: int, D: int, device):
+    """A workspace tensor of the size ls_qk_norm_rope_bw needs."""
+    n = ls_qk_norm_rope_bw_workspace_size(tokens, Hq, Hk, D)
+    return _torch().empty(max(n, 16) // 4, device=device, dtype=_torch().float32)
+
+
+def qk_norm_rope_bw(dq_out, dk_out, q, k, gamma_q, gamma_k, q_rstd, k_rstd, cos=None, sin=None,
+                    positions=None, interleaved: bool = False, workspace=None, dq=None, dk=None,
+                    dgamma_q=None, dgamma_k=None):
+    """Gradients of ``qk_norm_rope_fw`` from those of its outputs, its inputs and
+    its saved statistics: (dq, dk, dgamma_q, dgamma_k), the gamma gradients
+    fp32 [D] in a fixed summation order.  ``dq`` and ``dk`` may be ``dq_out``
+    and ``dk_out``, or slices of a packed gradient."""
+    torch = _torch()
+    qs = _heads("q", q)
+    tokens, Hq, D = q.shape
+    ks = _heads("k", k, tokens, D, q.dtype)
+    Hk = k.shape[1]
+    dqos, dkos = _like_heads("dq_out", dq_out, q), _like_heads("dk_out", dk_out, k)
+    _want("gamma_q", gamma_q, (D,), q.dtype)
+    _want("gamma_k", gamma_k, (D,), q.dtype)
+    _want("q_rstd", q_rstd, (tokens, Hq), torch.float32)
+    _want("k_rstd", k_rstd, (tokens, Hk), torch.float32)
+    rot, max_pos = _rotation(cos, sin, positions, tokens, D)
+    _want("dgamma_q", dgamma_q, (D,), torch.float32)
+    _want("dgamma_k", dgamma_k, (D,), torch.float32)
+    if workspace is None:
+        workspace = qk_norm_rope_workspace(tokens, Hq, Hk, D, q.device)
+    _workspace("workspace", workspace)
+    new = dict(device=q.device, dtype=q.dtype)
+    dq = torch.empty((tokens, Hq, D), **new) if dq is None else dq
+    dk = torch.empty((tokens, Hk, D), **new) if dk is None else dk
+    dqs, dks = _like_heads("dq", dq, q), _like_heads("dk", dk, k)
+    # a side without heads has no gradient to sum: its gamma gradient is zero
+    make = torch.empty if Hq and Hk else torch.zeros
+    new["dtype"] = torch.float32
+    dgamma_q = make(D, **new) if dgamma_q is None else dgamma_q
+    dgamma_k = make(D, **new) if dgamma_k is None else dgamma_k
+    dev = _one_device((q, k, dq_out, dk_out, dq, dk),
+                      (gamma_q, gamma_k, q_rstd, k_rstd, cos, sin, positions, workspace,
+                       dgamma_q, dgamma_k))
+    _call("ls_qk_norm_rope_bw", dev, ls_qk_norm_rope_bw, _ptr(dq), _ptr(dk), _ptr(dgamma_q),
+          _ptr(dgamma_k), _ptr(dq_out), _ptr(dk_out), _ptr(q), _ptr(k), _ptr(gamma_q),
+          _ptr(gamma_k), _ptr(q_rstd), _ptr(k_rstd), _ptr(cos), _ptr(sin), _ptr(positions),
+          tokens, Hq, Hk, D, rot, max_pos, dqs, dks, dqos, dkos, qs, ks, interleaved,
+          _ptr(workspace), workspace.numel() * workspace.element_size(), ls_dtype(q), _stream(q))
+    return dq, dk, dgamma_q, dgamma_k
+
+
+# ----------------------------------------------------------------------------
+# global gradient norm and clipping
+# ----------------------------------------------------------------------------
+def _grad_lists(grads):
+    """(device, pointers, sizes, dtype codes) of a list of dense tensors."""
+    grads = list(grads)
+    if not grads:
+        raise ValueError("an empty list has no device: give at least one gradient")
+    dev = _dev(*grads)
+    n = len(grads)
+    ptrs = (ctypes.c_void_p * n)(*[t.data_ptr() for t in grads])
+    sizes = (ctypes.c_int64 * n)(*[t.numel() for t in grads])
+    return grads, dev, ptrs, sizes, (ctypes.c_int32 * n)(*[ls_dtype(t) for t in grads])
+
+
+def grad_norm_workspace(count: int, device):
+    """A workspace tensor of the size ls_grad_norm and ls_grad_clip need for
+    ``count`` gradients."""
+    n = ls_grad_norm_workspace_size(count)
+    return _torch().empty(max(n, 16) // 4, device=device, dtype=_torch().float32)
+
+
+def _norm_outputs(grads, dev, workspace, norm):
+    torch = _torch()
+    _want("norm", norm, (1,), torch.float32)
+    if workspace is None:
+        workspace = grad_norm_workspace(len(grads), dev)
+    _workspace("workspace", workspace)
+    norm = torch.empty(1, device=dev, dtype=torch.float32) if norm is None else norm
+    if _dev(workspace, norm) != dev:
+        raise ValueError(f"workspace and norm must be on {dev}")
+    return workspace, norm
+
+
+def grad_norm(grads, workspace=None, norm=None):
+    """Global norm sqrt(sum g^2) over a list of gradients (fp32, fp16 and bf16
+    may be mixed), fp32 [1] on their device."""
+    grads, dev, ptrs, sizes, dts = _grad_lists(grads)
+    workspace, norm = _norm_outputs(grads, dev, workspace, norm)
+    _call("ls_grad_norm", dev, ls_grad_norm, _ptr(norm), ptrs, sizes, dts, len(grads),
+          _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(norm))
+    return norm
+
+
+def grad_clip(grads, max_norm: float, out=None, eps: float = 1e-6, workspace=None, norm=None):
+    """Multiplies a list of gradients by min(1, max_norm / (norm + eps)), norm
+    being ``grad_norm(grads)``; returns (out, norm).  ``out`` None clips in
+    place; otherwise it is a list of tensors of the gradients' shapes and
+    dtypes.  No tensor may be in ``out`` twice."""
+    grads, dev, ptrs, sizes, dts = _grad_lists(grads)
+    if out is None:
+        out, optrs = grads, ptrs
+    else:
+        out = list(out)
+        if len(out) != len(grads):
+            raise ValueError(f"out must hold {len(grads)} tensors, got {len(out)}")
+        for i, (o, g) in enumerate(zip(out, grads)):
+            if o.shape != g.shape or o.dtype != g.dtype:
+                _want(f"out[{i}]", o, g.shape, g.dtype)
+        if _dev(*out) != dev:
+            raise ValueError(f"out must be on {dev}")
+        optrs = (ctypes.c_void_p * len(out))(*[t.data_ptr() for t in out])
+    if len(set(optrs)) < len(out):
+        held = [t.data_ptr() for t in out if t.numel()]
+        if len(set(held)) < len(held):
+            raise ValueError("a tensor is in out twice")
+    workspace, norm = _norm_outputs(grads, dev, workspace, norm)
+    _call("ls_grad_clip", dev, ls_grad_clip, _ptr(norm), optrs, ptrs, sizes, dts, len(grads),
+          float(max_norm), float(eps), _ptr(workspace),
+          workspace.numel() * workspace.element_size(), _stream(norm))
+    return out, norm

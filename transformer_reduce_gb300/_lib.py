@@ -45,6 +45,15 @@ SIGNATURES = {
     "ls_rmsnorm_bw_dgamma": ([_VP, _VP, _VP, _VP, _I64, _I64, _VP, _SZ, _INT, _VP], _INT),
     "ls_cross_entropy_fw": ([_VP, _VP, _VP, _VP, _I64, _I64, _INT, _VP], _INT),
     "ls_cross_entropy_bw": ([_VP, _VP, _VP, _VP, _VP, _I64, _I64, _INT, _VP], _INT),
+    "ls_softmax_fw_relpos": ([_VP] * 5 + [_I64] * 6 + [_INT, _F32, _INT, _VP], _INT),
+    "ls_softmax_bw_relpos_workspace_size": ([_I64, _I64], _SZ),
+    "ls_softmax_bw_relpos": ([_VP] * 6 + [_I64] * 6 + [_INT, _F32, _VP, _SZ, _INT, _VP], _INT),
+    "ls_qk_norm_rope_fw": ([_VP] * 11 + [_I64] * 10 + [_INT, _F32, _INT, _VP], _INT),
+    "ls_qk_norm_rope_bw_workspace_size": ([_I64] * 4, _SZ),
+    "ls_qk_norm_rope_bw": ([_VP] * 15 + [_I64] * 12 + [_INT, _VP, _SZ, _INT, _VP], _INT),
+    "ls_grad_norm_workspace_size": ([_I64], _SZ),
+    "ls_grad_norm": ([_VP] * 4 + [_I64, _VP, _SZ, _VP], _INT),
+    "ls_grad_clip": ([_VP] * 5 + [_I64, _F32, _F32, _VP, _SZ, _VP], _INT),
     "ls_status_string": ([_INT], ctypes.c_char_p),
 }
 
@@ -161,3 +170,63 @@ def ls_softmax_bw_masked_scaled(dinp, dout, out_fw, mask, B, H, Tq, Tk, causal, 
                                 stream=0) -> int:
     return load().ls_softmax_bw_masked_scaled(dinp, dout, out_fw, mask, B, H, Tq, Tk, causal,
                                               scale, dt, stream)
+
+
+def ls_softmax_fw_relpos(out, inp, mask, table, bucket, B, H, Tq, Tk, num_buckets, max_distance,
+                         causal, scale, dt, stream=0) -> int:
+    return load().ls_softmax_fw_relpos(out, inp, mask, table, bucket, B, H, Tq, Tk, num_buckets,
+                                       max_distance, int(bool(causal)), scale, dt, stream)
+
+
+def ls_softmax_bw_relpos_workspace_size(H, max_distance) -> int:
+    return load().ls_softmax_bw_relpos_workspace_size(H, max_distance)
+
+
+def ls_softmax_bw_relpos(dinp, dtable, dout, out_fw, mask, bucket, B, H, Tq, Tk, num_buckets,
+                         max_distance, causal, scale, workspace, workspace_bytes, dt,
+                         stream=0) -> int:
+    return load().ls_softmax_bw_relpos(dinp, dtable, dout, out_fw, mask, bucket, B, H, Tq, Tk,
+                                       num_buckets, max_distance, int(bool(causal)), scale,
+                                       workspace, workspace_bytes, dt, stream)
+
+
+def ls_qk_norm_rope_fw(q_out, k_out, q_rstd, k_rstd, q, k, gamma_q, gamma_k, cos, sin, positions,
+                       tokens, Hq, Hk, D, rot, max_pos, q_out_stride, k_out_stride, q_stride,
+                       k_stride, interleaved, eps, dt, stream=0) -> int:
+    return load().ls_qk_norm_rope_fw(q_out, k_out, q_rstd, k_rstd, q, k, gamma_q, gamma_k, cos,
+                                     sin, positions, tokens, Hq, Hk, D, rot, max_pos,
+                                     q_out_stride, k_out_stride, q_stride, k_stride,
+                                     int(bool(interleaved)), eps, dt, stream)
+
+
+def ls_qk_norm_rope_bw_workspace_size(tokens, Hq, Hk, D) -> int:
+    return load().ls_qk_norm_rope_bw_workspace_size(tokens, Hq, Hk, D)
+
+
+def ls_qk_norm_rope_bw(dq, dk, dgamma_q, dgamma_k, dq_out, dk_out, q, k, gamma_q, gamma_k, q_rstd,
+                       k_rstd, cos, sin, positions, tokens, Hq, Hk, D, rot, max_pos, dq_stride,
+                       dk_stride, dq_out_stride, dk_out_stride, q_stride, k_stride, interleaved,
+                       workspace, workspace_bytes, dt, stream=0) -> int:
+    return load().ls_qk_norm_rope_bw(dq, dk, dgamma_q, dgamma_k, dq_out, dk_out, q, k, gamma_q,
+                                     gamma_k, q_rstd, k_rstd, cos, sin, positions, tokens, Hq, Hk,
+                                     D, rot, max_pos, dq_stride, dk_stride, dq_out_stride,
+                                     dk_out_stride, q_stride, k_stride, int(bool(interleaved)),
+                                     workspace, workspace_bytes, dt, stream)
+
+
+def ls_grad_norm_workspace_size(count) -> int:
+    return load().ls_grad_norm_workspace_size(count)
+
+
+def ls_grad_norm(norm, grads, sizes, dtypes, count, workspace, workspace_bytes, stream=0) -> int:
+    """``grads``, ``sizes`` and ``dtypes`` are ctypes arrays (void pointers,
+    int64, int32) of ``count`` entries, or None for an empty list."""
+    return load().ls_grad_norm(norm, grads, sizes, dtypes, count, workspace, workspace_bytes,
+                               stream)
+
+
+def ls_grad_clip(norm, out, grads, sizes, dtypes, count, max_norm, eps, workspace,
+                 workspace_bytes, stream=0) -> int:
+    """As ls_grad_norm; ``out`` is a ctypes array of void pointers too."""
+    return load().ls_grad_clip(norm, out, grads, sizes, dtypes, count, max_norm, eps, workspace,
+                               workspace_bytes, stream)

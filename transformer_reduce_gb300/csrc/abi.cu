@@ -85,6 +85,26 @@ bool vec_ok(int64_t row_len, size_t es, std::initializer_list<const void *> ptrs
 
 ls_status from_cuda(cudaError_t e) { return e == cudaSuccess ? LS_OK : LS_ERR_CUDA; }
 
+// One side (queries or keys) of the per-head norm with its typed pointers.
+template <typename T>
+lsr::QkSide<T> qk_side(void *out, const void *x, const void *dout, const void *gamma,
+                              float *rstd_out, const float *rstd, float *dgamma, int64_t heads,
+                              int64_t x_stride, int64_t out_stride, int64_t dout_stride) {
+    lsr::QkSide<T> s = {};
+    s.out = static_cast<T *>(out);
+    s.x = static_cast<const T *>(x);
+    s.dout = static_cast<const T *>(dout);
+    s.gamma = static_cast<const T *>(gamma);
+    s.rstd_out = rstd_out;
+    s.rstd = rstd;
+    s.dgamma = dgamma;
+    s.heads = heads;
+    s.x_stride = x_stride;
+    s.out_stride = out_stride;
+    s.dout_stride = dout_stride;
+    return s;
+}
+
 }  // namespace
 
 extern "C" {
@@ -543,6 +563,328 @@ ls_status ls_cross_entropy_bw(void *dlogits, const void *logits, const int32_t *
                 vocab, vec, st));
     }
     return LS_ERR_UNSUPPORTED;
+}
+
+// ----------------------------------------------------------------------------
+// softmax with a relative position bias
+// ----------------------------------------------------------------------------
+// Shared checks; sets `empty` when there is no score at all.
+static ls_status relpos_check(int64_t B, int64_t H, int64_t Tq, int64_t Tk, int64_t num_buckets,
+                              int64_t max_distance, int causal, float scale, bool *empty) {
+    if (B < 0 || H < 0 || Tq < 0 || Tk < 0 || num_buckets < 1 || max_distance < 1)
+        return LS_ERR_INVALID_ARG;
+    if (!scale_ok(scale) || (causal && Tq > Tk)) return LS_ERR_INVALID_ARG;
+    if (Tk > LS_MAX_ROW_LENGTH || Tq > LS_MAX_ROW_LENGTH ||
+        max_distance > LS_MAX_RELPOS_DISTANCE || num_buckets > LS_MAX_RELPOS_BUCKETS ||
+        H > INT32_MAX || H > INT64_MAX / 8 / num_buckets)
+        return LS_ERR_UNSUPPORTED;
+    *empty = B == 0 || H == 0 || Tq == 0 || Tk == 0;
+    if (!*empty && (H > INT64_MAX / B || Tq > INT64_MAX / (B * H) || Tk > INT64_MAX / (B * H * Tq)))
+        return LS_ERR_UNSUPPORTED;
+    return LS_OK;
+}
+
+static lsr::RelposShape relpos_shape(int64_t B, int64_t H, int64_t Tq, int64_t Tk,
+                                     int64_t num_buckets, int64_t max_distance, int causal,
+                                     float scale, bool empty) {
+    lsr::RelposShape p = {};
+    p.rows_per_head = empty ? 0 : B * Tq;
+    p.rows = empty ? 0 : B * Tq * H;
+    p.per = 1;
+    p.H = H;
+    p.Tq = Tq;
+    p.Tk = Tk;
+    p.qoff = Tk - Tq;
+    p.num_buckets = num_buckets;
+    p.R = (int)max_distance;
+    p.causal = causal ? 1 : 0;
+    p.scale = scale;
+    return p;
+}
+
+ls_status ls_softmax_fw_relpos(void *out, const void *inp, const void *mask, const void *table,
+                               const int32_t *bucket, int64_t B, int64_t H, int64_t Tq,
+                               int64_t Tk, int64_t num_buckets, int64_t max_distance, int causal,
+                               float scale, ls_dtype dt, void *stream) {
+    const size_t es = elem_size(dt);
+    if (es == 0) return LS_ERR_UNSUPPORTED;
+    bool empty = false;
+    const ls_status s =
+        relpos_check(B, H, Tq, Tk, num_buckets, max_distance, causal, scale, &empty);
+    if (s != LS_OK) return s;
+    if (empty) return LS_OK;
+    if (!out || !inp || !table || !bucket) return LS_ERR_INVALID_ARG;
+    if (!aligned(out, es) || !aligned(inp, es) || !aligned(table, es) || !aligned(bucket, 4) ||
+        (mask && !aligned(mask, es)))
+        return LS_ERR_MISALIGNED;
+    const lsr::RelposShape p =
+        relpos_shape(B, H, Tq, Tk, num_buckets, max_distance, causal, scale, empty);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    switch (dt) {
+        case LS_F32:
+            return from_cuda(lsr::launch_relpos_fw<float>((float *)out, (const float *)inp,
+                                                          (const float *)mask,
+                                                          (const float *)table, bucket, p, st));
+        case LS_F16:
+            return from_cuda(lsr::launch_relpos_fw<__half>((__half *)out, (const __half *)inp,
+                                                           (const __half *)mask,
+                                                           (const __half *)table, bucket, p, st));
+        case LS_BF16:
+            return from_cuda(lsr::launch_relpos_fw<__nv_bfloat16>(
+                (__nv_bfloat16 *)out, (const __nv_bfloat16 *)inp, (const __nv_bfloat16 *)mask,
+                (const __nv_bfloat16 *)table, bucket, p, st));
+    }
+    return LS_ERR_UNSUPPORTED;
+}
+
+size_t ls_softmax_bw_relpos_workspace_size(int64_t H, int64_t max_distance) {
+    if (H <= 0 || max_distance <= 0 || max_distance > LS_MAX_RELPOS_DISTANCE || H > INT32_MAX)
+        return 0;
+    return (size_t)lsr::relpos_bw_slots(H) * (size_t)(2 * max_distance + 1) * sizeof(float);
+}
+
+ls_status ls_softmax_bw_relpos(void *dinp, float *dtable, const void *dout, const void *out_fw,
+                               const void *mask, const int32_t *bucket, int64_t B, int64_t H,
+                               int64_t Tq, int64_t Tk, int64_t num_buckets, int64_t max_distance,
+                               int causal, float scale, void *workspace, size_t workspace_bytes,
+                               ls_dtype dt, void *stream) {
+    const size_t es = elem_size(dt);
+    if (es == 0) return LS_ERR_UNSUPPORTED;
+    bool empty = false;
+    const ls_status s =
+        relpos_check(B, H, Tq, Tk, num_buckets, max_distance, causal, scale, &empty);
+    if (s != LS_OK) return s;
+    if (H == 0) return LS_OK;
+    if (!dtable || !bucket || (!empty && (!dinp || !dout || !out_fw))) return LS_ERR_INVALID_ARG;
+    if ((dinp && !aligned(dinp, es)) || (dout && !aligned(dout, es)) ||
+        (out_fw && !aligned(out_fw, es)) || (mask && !aligned(mask, es)) || !aligned(dtable, 4) ||
+        !aligned(bucket, 4))
+        return LS_ERR_MISALIGNED;
+    const size_t need = ls_softmax_bw_relpos_workspace_size(H, max_distance);
+    if (!empty && (!workspace || workspace_bytes < need || !aligned(workspace, 16)))
+        return LS_ERR_WORKSPACE;
+    const lsr::RelposShape p =
+        relpos_shape(B, H, Tq, Tk, num_buckets, max_distance, causal, scale, empty);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    float *part = static_cast<float *>(workspace);
+    switch (dt) {
+        case LS_F32:
+            return from_cuda(lsr::launch_relpos_bw<float>((float *)dinp, dtable,
+                                                          (const float *)dout,
+                                                          (const float *)out_fw,
+                                                          (const float *)mask, bucket, p, part,
+                                                          st));
+        case LS_F16:
+            return from_cuda(lsr::launch_relpos_bw<__half>(
+                (__half *)dinp, dtable, (const __half *)dout, (const __half *)out_fw,
+                (const __half *)mask, bucket, p, part, st));
+        case LS_BF16:
+            return from_cuda(lsr::launch_relpos_bw<__nv_bfloat16>(
+                (__nv_bfloat16 *)dinp, dtable, (const __nv_bfloat16 *)dout,
+                (const __nv_bfloat16 *)out_fw, (const __nv_bfloat16 *)mask, bucket, p, part, st));
+    }
+    return LS_ERR_UNSUPPORTED;
+}
+
+// ----------------------------------------------------------------------------
+// per-head norm of queries and keys with the position rotation
+// ----------------------------------------------------------------------------
+static ls_status qk_check(int64_t tokens, int64_t Hq, int64_t Hk, int64_t D, int64_t rot,
+                          int64_t max_pos, const float *cos, const float *sin,
+                          const int32_t *positions) {
+    if (tokens < 0 || Hq < 0 || Hk < 0 || D < 1 || rot < 0 || rot > D || rot % 2 != 0)
+        return LS_ERR_INVALID_ARG;
+    if (D > LS_MAX_HEAD_DIM || Hq > INT32_MAX || Hk > INT32_MAX) return LS_ERR_UNSUPPORTED;
+    if (tokens > 0 && (Hq + Hk + 1) * D > INT64_MAX / tokens) return LS_ERR_UNSUPPORTED;
+    if (rot > 0 && tokens > 0 && Hq + Hk > 0) {
+        if (!cos || !sin || !positions || max_pos < 1) return LS_ERR_INVALID_ARG;
+        if (max_pos > INT64_MAX / rot) return LS_ERR_UNSUPPORTED;
+        if (!aligned(cos, 4) || !aligned(sin, 4) || !aligned(positions, 4))
+            return LS_ERR_MISALIGNED;
+    }
+    return LS_OK;
+}
+
+// A tensor of one side: dense heads, tokens `stride` elements apart.
+static ls_status qk_tensor(const void *p, int64_t tokens, int64_t heads, int64_t D,
+                           int64_t stride, size_t es) {
+    if (tokens == 0 || heads == 0) return LS_OK;
+    if (!p || stride < heads * D) return LS_ERR_INVALID_ARG;
+    if (stride > INT64_MAX / tokens) return LS_ERR_UNSUPPORTED;
+    return aligned(p, es) ? LS_OK : LS_ERR_MISALIGNED;
+}
+
+static lsr::QkRope qk_rope(const float *cos, const float *sin, const int32_t *positions,
+                           int64_t tokens, int64_t max_pos, int64_t D, int64_t rot,
+                           int interleaved, float eps) {
+    lsr::QkRope r = {};
+    r.cos = cos;
+    r.sin = sin;
+    r.positions = positions;
+    r.tokens = tokens;
+    r.max_pos = max_pos;
+    r.D = (int)D;
+    r.rot = (int)rot;
+    r.interleaved = interleaved ? 1 : 0;
+    r.eps = eps;
+    return r;
+}
+
+ls_status ls_qk_norm_rope_fw(void *q_out, void *k_out, float *q_rstd, float *k_rstd,
+                             const void *q, const void *k, const void *gamma_q,
+                             const void *gamma_k, const float *cos, const float *sin,
+                             const int32_t *positions, int64_t tokens, int64_t Hq, int64_t Hk,
+                             int64_t D, int64_t rot, int64_t max_pos, int64_t q_out_stride,
+                             int64_t k_out_stride, int64_t q_stride, int64_t k_stride,
+                             int interleaved, float eps, ls_dtype dt, void *stream) {
+    const size_t es = elem_size(dt);
+    if (es == 0) return LS_ERR_UNSUPPORTED;
+    ls_status s = qk_check(tokens, Hq, Hk, D, rot, max_pos, cos, sin, positions);
+    if (s != LS_OK) return s;
+    if (!(eps >= 0.f) || !std::isfinite(eps)) return LS_ERR_INVALID_ARG;
+    if (tokens == 0 || Hq + Hk == 0) return LS_OK;
+    if ((s = qk_tensor(q_out, tokens, Hq, D, q_out_stride, es)) != LS_OK ||
+        (s = qk_tensor(k_out, tokens, Hk, D, k_out_stride, es)) != LS_OK ||
+        (s = qk_tensor(q, tokens, Hq, D, q_stride, es)) != LS_OK ||
+        (s = qk_tensor(k, tokens, Hk, D, k_stride, es)) != LS_OK)
+        return s;
+    if ((Hq > 0 && !gamma_q) || (Hk > 0 && !gamma_k)) return LS_ERR_INVALID_ARG;
+    if ((gamma_q && !aligned(gamma_q, es)) || (gamma_k && !aligned(gamma_k, es)) ||
+        (q_rstd && !aligned(q_rstd, 4)) || (k_rstd && !aligned(k_rstd, 4)))
+        return LS_ERR_MISALIGNED;
+    const lsr::QkRope r =
+        qk_rope(cos, sin, positions, tokens, max_pos, D, rot, interleaved, eps);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    auto launch = [&](auto zero) {
+        using T = decltype(zero);
+        return from_cuda(lsr::launch_qk_fw<T>(
+            qk_side<T>(q_out, q, nullptr, gamma_q, q_rstd, nullptr, nullptr, Hq, q_stride,
+                       q_out_stride, 0),
+            qk_side<T>(k_out, k, nullptr, gamma_k, k_rstd, nullptr, nullptr, Hk, k_stride,
+                       k_out_stride, 0),
+            r, st));
+    };
+    switch (dt) {
+        case LS_F32: return launch(float());
+        case LS_F16: return launch(__half());
+        case LS_BF16: return launch(__nv_bfloat16());
+    }
+    return LS_ERR_UNSUPPORTED;
+}
+
+size_t ls_qk_norm_rope_bw_workspace_size(int64_t tokens, int64_t Hq, int64_t Hk, int64_t D) {
+    if (tokens <= 0 || Hq < 0 || Hk < 0 || Hq > INT32_MAX || Hk > INT32_MAX || D <= 0 ||
+        D > LS_MAX_HEAD_DIM)
+        return 0;
+    return (size_t)lsr::qk_bw_parts(tokens, Hq, Hk) * (size_t)D * sizeof(float);
+}
+
+ls_status ls_qk_norm_rope_bw(void *dq, void *dk, float *dgamma_q, float *dgamma_k,
+                             const void *dq_out, const void *dk_out, const void *q, const void *k,
+                             const void *gamma_q, const void *gamma_k, const float *q_rstd,
+                             const float *k_rstd, const float *cos, const float *sin,
+                             const int32_t *positions, int64_t tokens, int64_t Hq, int64_t Hk,
+                             int64_t D, int64_t rot, int64_t max_pos, int64_t dq_stride,
+                             int64_t dk_stride, int64_t dq_out_stride, int64_t dk_out_stride,
+                             int64_t q_stride, int64_t k_stride, int interleaved, void *workspace,
+                             size_t workspace_bytes, ls_dtype dt, void *stream) {
+    const size_t es = elem_size(dt);
+    if (es == 0) return LS_ERR_UNSUPPORTED;
+    ls_status s = qk_check(tokens, Hq, Hk, D, rot, max_pos, cos, sin, positions);
+    if (s != LS_OK) return s;
+    if ((Hq > 0 && !dgamma_q) || (Hk > 0 && !dgamma_k)) return LS_ERR_INVALID_ARG;
+    if (Hq + Hk == 0) return LS_OK;
+    if ((s = qk_tensor(dq, tokens, Hq, D, dq_stride, es)) != LS_OK ||
+        (s = qk_tensor(dk, tokens, Hk, D, dk_stride, es)) != LS_OK ||
+        (s = qk_tensor(dq_out, tokens, Hq, D, dq_out_stride, es)) != LS_OK ||
+        (s = qk_tensor(dk_out, tokens, Hk, D, dk_out_stride, es)) != LS_OK ||
+        (s = qk_tensor(q, tokens, Hq, D, q_stride, es)) != LS_OK ||
+        (s = qk_tensor(k, tokens, Hk, D, k_stride, es)) != LS_OK)
+        return s;
+    if (tokens > 0 && ((Hq > 0 && (!gamma_q || !q_rstd)) || (Hk > 0 && (!gamma_k || !k_rstd))))
+        return LS_ERR_INVALID_ARG;
+    if ((gamma_q && !aligned(gamma_q, es)) || (gamma_k && !aligned(gamma_k, es)) ||
+        (q_rstd && !aligned(q_rstd, 4)) || (k_rstd && !aligned(k_rstd, 4)) ||
+        (dgamma_q && !aligned(dgamma_q, 4)) || (dgamma_k && !aligned(dgamma_k, 4)))
+        return LS_ERR_MISALIGNED;
+    const size_t need = ls_qk_norm_rope_bw_workspace_size(tokens, Hq, Hk, D);
+    if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 16)))
+        return LS_ERR_WORKSPACE;
+    const lsr::QkRope r =
+        qk_rope(cos, sin, positions, tokens, max_pos, D, rot, interleaved, 0.f);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    float *part = static_cast<float *>(workspace);
+    auto launch = [&](auto zero) {
+        using T = decltype(zero);
+        return from_cuda(lsr::launch_qk_bw<T>(
+            qk_side<T>(dq, q, dq_out, gamma_q, nullptr, q_rstd, Hq > 0 ? dgamma_q : nullptr, Hq,
+                       q_stride, dq_stride, dq_out_stride),
+            qk_side<T>(dk, k, dk_out, gamma_k, nullptr, k_rstd, Hk > 0 ? dgamma_k : nullptr, Hk,
+                       k_stride, dk_stride, dk_out_stride),
+            r, part, st));
+    };
+    switch (dt) {
+        case LS_F32: return launch(float());
+        case LS_F16: return launch(__half());
+        case LS_BF16: return launch(__nv_bfloat16());
+    }
+    return LS_ERR_UNSUPPORTED;
+}
+
+// ----------------------------------------------------------------------------
+// global gradient norm and clipping
+// ----------------------------------------------------------------------------
+// Checks the host lists (out NULL: a norm alone).
+static ls_status grad_check(const float *norm, void *const *out, bool clip,
+                            const void *const *grads, const int64_t *sizes,
+                            const int32_t *dtypes, int64_t count, const void *workspace,
+                            size_t workspace_bytes) {
+    if (count < 0 || !norm) return LS_ERR_INVALID_ARG;
+    if (count > 0 && (!grads || !sizes || !dtypes || (clip && !out))) return LS_ERR_INVALID_ARG;
+    if (!aligned(norm, 4)) return LS_ERR_MISALIGNED;
+    int64_t total = 0;
+    for (int64_t i = 0; i < count; ++i) {
+        const size_t es = elem_size((ls_dtype)dtypes[i]);
+        if (es == 0) return LS_ERR_UNSUPPORTED;
+        if (sizes[i] < 0) return LS_ERR_INVALID_ARG;
+        if (sizes[i] == 0) continue;
+        if (!grads[i] || (clip && !out[i])) return LS_ERR_INVALID_ARG;
+        if (!aligned(grads[i], es) || (clip && !aligned(out[i], es))) return LS_ERR_MISALIGNED;
+        if (sizes[i] > (INT64_MAX / 8 - total)) return LS_ERR_UNSUPPORTED;
+        total += sizes[i];
+    }
+    const size_t need = ls_grad_norm_workspace_size(count);
+    if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 16)))
+        return LS_ERR_WORKSPACE;
+    return LS_OK;
+}
+
+size_t ls_grad_norm_workspace_size(int64_t count) {
+    return (size_t)lsr::grad_parts(count) * sizeof(double);
+}
+
+ls_status ls_grad_norm(float *norm, const void *const *grads, const int64_t *sizes,
+                       const int32_t *dtypes, int64_t count, void *workspace,
+                       size_t workspace_bytes, void *stream) {
+    const ls_status s = grad_check(norm, nullptr, false, grads, sizes, dtypes, count, workspace,
+                                   workspace_bytes);
+    if (s != LS_OK) return s;
+    return from_cuda(lsr::launch_grad_norm(norm, grads, sizes, dtypes, count,
+                                           static_cast<double *>(workspace),
+                                           static_cast<cudaStream_t>(stream)));
+}
+
+ls_status ls_grad_clip(float *norm, void *const *out, const void *const *grads,
+                       const int64_t *sizes, const int32_t *dtypes, int64_t count, float max_norm,
+                       float eps, void *workspace, size_t workspace_bytes, void *stream) {
+    if (!std::isfinite(max_norm) || !(max_norm > 0.f) || !std::isfinite(eps) || !(eps >= 0.f))
+        return LS_ERR_INVALID_ARG;
+    const ls_status s = grad_check(norm, out, true, grads, sizes, dtypes, count, workspace,
+                                   workspace_bytes);
+    if (s != LS_OK) return s;
+    return from_cuda(lsr::launch_grad_clip(norm, out, grads, sizes, dtypes, count, max_norm, eps,
+                                           static_cast<double *>(workspace),
+                                           static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -78,4 +78,66 @@ template <typename T>
 cudaError_t launch_ce_bw(T *dz, const T *z, const int32_t *target, const float *lse,
                          const float *dloss, int64_t rows, int64_t V, bool vec, cudaStream_t st);
 
+// Softmax with a relative position bias: the problem and its cut into runs of
+// `per` rows in head-major order (h, b, i), one run per block.
+struct RelposShape {
+    int64_t rows_per_head;  // B * Tq
+    int64_t rows;           // H * B * Tq
+    int64_t per;            // rows of a block's run
+    int64_t H, Tq, Tk, qoff;
+    int64_t num_buckets;
+    int R;
+    int causal;
+    float scale;
+};
+
+constexpr int kRelposMaxDistance = 2048;
+// Workspace slots of 2R + 1 floats that the backward may use.
+int64_t relpos_bw_slots(int64_t H);
+template <typename T>
+cudaError_t launch_relpos_fw(T *out, const T *inp, const T *mask, const T *table,
+                             const int32_t *bucket, RelposShape p, cudaStream_t st);
+template <typename T>
+cudaError_t launch_relpos_bw(T *dinp, float *dtable, const T *dout, const T *y, const T *mask,
+                             const int32_t *bucket, RelposShape p, float *part,
+                             cudaStream_t st);
+
+// Per-head norm of queries and keys with the position rotation.  One side
+// (queries or keys) of a call: x and out are [tokens, heads, D] with a stride
+// between tokens.
+template <typename T>
+struct QkSide {
+    T *out;            // forward: the rotated norm; backward: dx
+    const T *x;        // forward input
+    const T *dout;     // backward only
+    const T *gamma;    // [D]
+    float *rstd_out;   // forward: written unless NULL
+    const float *rstd;  // backward: as saved
+    float *dgamma;     // backward
+    int64_t heads, x_stride, out_stride, dout_stride;
+};
+struct QkRope {
+    const float *cos, *sin;    // [max_pos, rot / 2]
+    const int32_t *positions;  // [tokens]
+    int64_t tokens, max_pos;
+    int D, rot, interleaved;
+    float eps;
+};
+constexpr int kQkMaxHeadDim = 1024;
+// Blocks of the backward, each with one partial gamma gradient of D floats.
+int64_t qk_bw_parts(int64_t tokens, int64_t Hq, int64_t Hk);
+template <typename T>
+cudaError_t launch_qk_fw(QkSide<T> q, QkSide<T> k, QkRope r, cudaStream_t st);
+template <typename T>
+cudaError_t launch_qk_bw(QkSide<T> q, QkSide<T> k, QkRope r, float *part, cudaStream_t st);
+
+// Global norm of many tensors, and the tensors times min(1, max_norm / (norm
+// + eps)); host arrays of `count` entries; dts holds ls_dtype codes.
+int64_t grad_parts(int64_t count);
+cudaError_t launch_grad_norm(float *norm, const void *const *grads, const int64_t *sizes,
+                             const int32_t *dts, int64_t count, double *part, cudaStream_t st);
+cudaError_t launch_grad_clip(float *norm, void *const *out, const void *const *grads,
+                             const int64_t *sizes, const int32_t *dts, int64_t count,
+                             float max_norm, float eps, double *part, cudaStream_t st);
+
 }  // namespace lsr
