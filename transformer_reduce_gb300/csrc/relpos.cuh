@@ -311,26 +311,27 @@ struct RelposCursor {
 };
 
 // Windows of the batch entries of rows [r0, r1) of a head (r0 < r1), into wtab;
-// false if there are too many of them or they are not worth finding.
+// false if there are too many of them or they are not worth finding.  BLOCK:
+// the threads of the block, 0 where the launch decides.
 template <typename T, bool ADDS, int BLOCK>
 __device__ __forceinline__ bool relpos_find_windows(int2 *wtab, const T *mask, const RelposShape &p,
                                                     int r0, int r1) {
     const int Tq = (int)p.Tq;
     const int b0 = r0 / Tq, nb = (r1 - 1) / Tq - b0 + 1;
     if (!mask || Tq < kRelposWindowTq || nb > kRelposWinMax) return false;
-    for (int k = threadIdx.x >> 5; k < nb; k += BLOCK / 32) {
+    for (int k = threadIdx.x >> 5; k < nb; k += (BLOCK ? BLOCK : (int)blockDim.x) / 32) {
         const int2 w = relpos_mask_window<T, ADDS>(mask + (int64_t)(b0 + k) * p.Tk, (int)p.Tk);
         if ((threadIdx.x & 31) == 0) wtab[k] = w;
     }
     return true;
 }
 
-// Chunk of V elements at element offset `at` of a tensor of `total` elements;
-// only the elements with bits set are wanted, and at least one of them is.
-template <typename T>
+// Chunk of V elements at element offset `at` of a tensor of `total` elements.
+// AL: chunks never leave their row.
+template <typename T, bool AL>
 __device__ __forceinline__ uint4 relpos_load(const T *base, int64_t at, int64_t total) {
     constexpr int V = Traits<T>::kVec;
-    if (at >= 0 && at + V <= total) return ld_stream16(base + at);
+    if (AL || (at >= 0 && at + V <= total)) return ld_stream16(base + at);
     float f[V];
 #pragma unroll
     for (int e = 0; e < V; ++e)
@@ -340,10 +341,10 @@ __device__ __forceinline__ uint4 relpos_load(const T *base, int64_t at, int64_t 
 
 // Store of a chunk whose first key is j0; keys outside [0, Tk) belong to other
 // rows.
-template <typename T>
+template <typename T, bool AL>
 __device__ __forceinline__ void relpos_store(T *row, int j0, int Tk, const uint4 &u) {
     constexpr int V = Traits<T>::kVec;
-    if (j0 >= 0 && j0 + V <= Tk) {
+    if (AL || (j0 >= 0 && j0 + V <= Tk)) {
         st_stream16(row + j0, u);
         return;
     }
@@ -354,33 +355,98 @@ __device__ __forceinline__ void relpos_store(T *row, int j0, int Tk, const uint4
         if (j0 + e >= 0 && j0 + e < Tk) Traits<T>::store1(row + j0 + e, f[e]);
 }
 
-// Bits of the chunk's visible keys.
+// Bits of the chunk's visible keys: inside [lo, hi), and not masked with -inf
+// in mrow if that is given.
 template <typename T>
 __device__ __forceinline__ uint32_t relpos_bits(const T *mrow, int j0, int lo, int hi) {
-    uint32_t bits = 0u;
+    constexpr int V = Traits<T>::kVec;
+    const int a = min(max(lo - j0, 0), V), b = min(max(hi - j0, 0), V);
+    uint32_t bits = ((1u << b) - 1u) & ~((1u << a) - 1u);
+    if (mrow) {
 #pragma unroll
-    for (int e = 0; e < Traits<T>::kVec; ++e) {
-        bool see = j0 + e >= lo && j0 + e < hi;
-        if (mrow && see) see = Traits<T>::load1_cached(mrow + j0 + e) != -INFINITY;
-        bits |= (see ? 1u : 0u) << e;
+        for (int e = 0; e < V; ++e)
+            if ((bits >> e) & 1u)
+                if (Traits<T>::load1_cached(mrow + j0 + e) == -INFINITY) bits &= ~(1u << e);
     }
     return bits;
 }
 
-// The bias by distance in shared memory: four copies of the 2R + 1 values with
-// both ends repeated, copy k shifted by k, so that the V values from any
-// distance on start at a 16-byte address of one of them.
-template <int V>
-__host__ __device__ constexpr int relpos_lut_stride(int R) { return (2 * R + 2 * V + 7) / 4 * 4; }
-template <int V>
-constexpr size_t relpos_fw_smem(int R) { return (size_t)4 * relpos_lut_stride<V>(R) * 4; }
-
-template <int TPR, int CPT>
-constexpr int relpos_fw_min_blocks() {
-    return TPR > 256 ? 1 : (CPT <= 1 ? 4 : CPT <= 2 ? 3 : 2);
+// What a row group needs of one row.
+struct RelposRow {
+    int64_t off;  // element offset of the row
+    int q;        // the query's key position
+    int s;        // elements from a 16-byte address to the row's start
+    int lo, hi;   // window of visible keys; empty for a row that is not there
+    int b;        // batch entry whose mask is added element by element, or -1
+};
+template <bool AL, int V>
+__device__ __forceinline__ RelposRow relpos_row(const RelposShape &p, const RelposCursor &cur,
+                                                int64_t h, bool valid, bool masked,
+                                                const int2 *wtab, int b0, int phase) {
+    RelposRow w;
+    w.off = (((int64_t)cur.b * p.H + h) * (int)p.Tq + cur.i) * (int)p.Tk;
+    w.q = cur.i + (int)p.qoff;
+    w.s = AL ? 0 : (int)((w.off + phase) & (V - 1));
+    w.lo = 0;
+    w.hi = valid ? (int)p.Tk : 0;
+    w.b = -1;
+    if (masked && valid) {
+        const int2 win = wtab ? wtab[cur.b - b0] : make_int2(-1, 0);
+        if (win.x < 0) {
+            w.b = cur.b;
+        } else {
+            w.lo = win.x;
+            w.hi = win.y;
+        }
+    }
+    if (p.causal) w.hi = min(w.hi, w.q + 1);
+    return w;
 }
 
-template <typename T, int TPR, int CPT>
+// The bias by distance in shared memory, as seen by chunks.  A[x] is the bias
+// of distance x - R - kLutPad, both ends repeated; copy k (of four) holds A
+// shifted by k, so that the values from any distance on start at a 16-byte
+// address of the copy of its phase.  All chunks of a row have the same phase,
+// and far chunks are clamped by whole 16-byte steps into the repeated ends.
+constexpr int kLutPad = 12;  // a chunk clamped at either end lies in it at any phase
+__host__ __device__ constexpr int relpos_lut_stride(int R) {
+    return (2 * R + 1 + 2 * kLutPad + 8 + 3) / 4 * 4;
+}
+
+// Resident blocks per SM asked of ptxas, and stages of the row pipeline (rows
+// in flight per group: one less).
+template <int TPR, int CPT>
+constexpr int relpos_fw_min_blocks() {
+    return TPR > 256 ? 1 : (CPT <= 2 ? 4 : 3);
+}
+constexpr int kRelposFwStages = 3;
+template <int TPR, int CPT>
+constexpr size_t relpos_fw_smem(int R) {
+    return (size_t)4 * relpos_lut_stride(R) * 4 +
+           (size_t)kRelposFwStages * CPT * relpos_block<TPR>() * 16;
+}
+
+// Mask elements of a chunk, -inf outside [lo, hi).
+template <typename T, bool VEC>
+__device__ __forceinline__ void relpos_mask(const T *mrow, int j0, int lo, int hi,
+                                            float (&mv)[Traits<T>::kVec]) {
+    constexpr int V = Traits<T>::kVec;
+    if (j0 >= lo && j0 + V <= hi) {
+        if (VEC) {
+            Traits<T>::unpack(ld_cached16(mrow + j0), mv);
+        } else {
+#pragma unroll
+            for (int e = 0; e < V; ++e) mv[e] = Traits<T>::load1_cached(mrow + j0 + e);
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < V; ++e)
+            mv[e] = j0 + e >= lo && j0 + e < hi ? Traits<T>::load1_cached(mrow + j0 + e)
+                                                : -INFINITY;
+    }
+}
+
+template <typename T, int TPR, int CPT, bool AL>
 __global__ void __launch_bounds__(relpos_block<TPR>(), (relpos_fw_min_blocks<TPR, CPT>()))
 relpos_fw_vec(T *out, const T *inp, const T *mask, const T *table, const int32_t *bucket,
               const RelposShape p, int mask_vec) {
@@ -390,17 +456,21 @@ relpos_fw_vec(T *out, const T *inp, const T *mask, const T *table, const int32_t
     constexpr int H2 = V / 2;
     constexpr int BLOCK = relpos_block<TPR>();
     constexpr int G = BLOCK / TPR;
-    extern __shared__ float4 lut4[];
-    float *lut = reinterpret_cast<float *>(lut4);
+    constexpr int S = kRelposFwStages;
+    extern __shared__ uint4 dsmem[];
+    uint4 *stage = dsmem + threadIdx.x;  // [S][CPT][BLOCK], a thread's own slots
+    const float4 *lut4 = reinterpret_cast<const float4 *>(dsmem + S * CPT * BLOCK);
+    float *lut = reinterpret_cast<float *>(dsmem + S * CPT * BLOCK);
     __shared__ float red_max[BLOCK / 32], red_sum[BLOCK / 32];
     __shared__ int2 wtab[kRelposWinMax];
     const int lane = threadIdx.x % TPR;
     const int grp = threadIdx.x / TPR;
     const int sub = TPR < 32 ? grp % (32 / (TPR < 32 ? TPR : 32)) : 0;  // group of the warp
-    const int Tk = (int)p.Tk, stride = relpos_lut_stride<V>(p.R);
+    const int Tk = (int)p.Tk, stride = relpos_lut_stride(p.R);
+    const int top = (2 * p.R + kLutPad + 4) / 4;  // last 16-byte step a chunk may start at
     const int64_t total = p.rows * p.Tk;
     const int Tq = (int)p.Tq, gq = G / Tq, gr = G - gq * Tq;
-    const int base_phase = (int)((reinterpret_cast<uintptr_t>(inp) / sizeof(T)) % V);
+    const int phase = (int)((reinterpret_cast<uintptr_t>(inp) / sizeof(T)) % V);
     const float2 sc = f2(p.scale);
 
     const int64_t beg = (int64_t)blockIdx.x * p.per;
@@ -410,160 +480,179 @@ relpos_fw_vec(T *out, const T *inp, const T *mask, const T *table, const int32_t
         const int r0 = (int)(t0 - h * p.rows_per_head);
         const int r1 = (int)min(end - h * p.rows_per_head, p.rows_per_head);
         __syncthreads();  // the last segment's bias and windows are no longer read
+        const bool windows = relpos_find_windows<T, true, BLOCK>(wtab, mask, p, r0, r1);
+        const int b0 = r0 / Tq;
+        if (windows) __syncthreads();
+        // Copies of a row's visible chunks into a stage: each thread its own
+        // slots.  A chunk that reaches past the tensor is put there by hand.
+        int r_issue = r0 + grp;
+        RelposCursor ci(Tq, r_issue);
+        auto issue = [&](int s) {
+            if (r_issue < r1) {
+                const RelposRow w = relpos_row<AL, V>(p, ci, h, true, mask != nullptr,
+                                                      windows ? wtab : nullptr, b0, phase);
+#pragma unroll
+                for (int k = 0; k < CPT; ++k) {
+                    const int j0 = (k * TPR + lane) * V - w.s;
+                    if (j0 < w.hi && j0 + V > w.lo) {
+                        const int64_t at = w.off + j0;
+                        if (AL || (at >= 0 && at + V <= total))
+                            cp_async16(&stage[(s * CPT + k) * BLOCK], inp + at);
+                        else
+                            stage[(s * CPT + k) * BLOCK] = relpos_load<T, AL>(inp, at, total);
+                    }
+                }
+                r_issue += G;
+                ci.advance(Tq, gq, gr);
+            }
+            cp_async_commit();
+        };
+#pragma unroll
+        for (int s = 0; s < S - 1; ++s) issue(s);
+        // the bias, while the first rows are on their way
         for (int x = threadIdx.x; x < stride; x += BLOCK) {
-            const float v = relpos_bias<T>(table, bucket, p, h,
-                                           min(max(x - V, 0), 2 * p.R));
+            const float v =
+                relpos_bias<T>(table, bucket, p, h, min(max(x - kLutPad, 0), 2 * p.R));
 #pragma unroll
             for (int k = 0; k < 4; ++k)
                 if (x >= k) lut[k * stride + x - k] = v;
         }
-        const bool windows = relpos_find_windows<T, true, BLOCK>(wtab, mask, p, r0, r1);
-        const int b0 = r0 / Tq;
         __syncthreads();
+        int s_cur = 0, s_iss = S - 1;
         RelposCursor cur(Tq, r0 + grp);
         // groups that share a warp take the same number of turns (shuffles)
         for (int rw = r0 + grp - sub; rw < r1; rw += G, cur.advance(Tq, gq, gr)) {
+            issue(s_iss);
+            s_iss = s_iss + 1 == S ? 0 : s_iss + 1;
+            cp_async_wait<S - 1>();  // this thread's copies of the row have landed
             const bool valid = rw + sub < r1;
-            const int64_t off = (((int64_t)cur.b * p.H + h) * Tq + cur.i) * Tk;
-            const int q = cur.i + (int)p.qoff;  // the query's key position
-            const int s = (int)((off + base_phase) & (V - 1));
-            int lo = 0, hi = valid ? Tk : 0;
-            const T *mrow = nullptr;  // set: add the mask element by element
-            if (mask && valid) {
-                const int2 w = windows ? wtab[cur.b - b0] : make_int2(-1, 0);
-                if (w.x < 0) {
-                    mrow = mask + (int64_t)cur.b * Tk;
-                } else {
-                    lo = w.x;
-                    hi = w.y;
-                }
-            }
-            if (p.causal) hi = min(hi, q + 1);
-
-            uint4 raw[CPT];
-#pragma unroll
-            for (int k = 0; k < CPT; ++k) {
-                const int j0 = (k * TPR + lane) * V - s;
-                if (j0 < hi && j0 + V > lo) raw[k] = relpos_load<T>(inp, off + j0, total);
-            }
+            const RelposRow w = relpos_row<AL, V>(p, cur, h, valid, mask != nullptr,
+                                                  windows ? wtab : nullptr, b0, phase);
+            const int lo = w.lo, hi = w.hi, j_lane = lane * V - w.s;
+            // keys of the warp's part of chunk k: [k * TPR * V + wj, ... + WK)
+            const int wj = (TPR > 32 ? (lane & ~31) * V : 0) - w.s;
+            constexpr int WK = (TPR < 32 ? TPR : 32) * V;
+            // distance of the lane's first key, in elements from A[0]
+            const int x_lane = j_lane - w.q + p.R + kLutPad;
+            const float4 *lut_row = lut4 + (x_lane & 3) * (stride / 4);
             float2 v[CPT][H2];
             float m = -INFINITY;
 #pragma unroll
             for (int k = 0; k < CPT; ++k) {
-                const int j0 = (k * TPR + lane) * V - s;
-                if (j0 < hi && j0 + V > lo) {
-                    unpack2<T>(raw[k], v[k]);
-                    const int u = min(max(j0 - q, -p.R - V), p.R + 1) + p.R + V;
-                    const float4 *bias = lut4 + ((u & 3) * stride + (u & ~3)) / 4;
-                    float2 bv[H2];
+                const int j0 = k * TPR * V + j_lane;
+                if (!(k * TPR * V + wj < hi && k * TPR * V + wj + WK > lo)) continue;
+                unpack2<T>(stage[(s_cur * CPT + k) * BLOCK], v[k]);
+                const float4 *bias =
+                    lut_row + min(max((x_lane >> 2) + k * (TPR * V / 4), 0), top);
 #pragma unroll
-                    for (int h2 = 0; h2 < H2; h2 += 2) {
-                        const float4 b4 = bias[h2 / 2];
-                        bv[h2] = make_float2(b4.x, b4.y);
-                        bv[h2 + 1] = make_float2(b4.z, b4.w);
-                    }
-#pragma unroll
-                    for (int h2 = 0; h2 < H2; ++h2) v[k][h2] = fma2(v[k][h2], sc, bv[h2]);
-                    if (mrow) {
-                        float mv[V];
-                        if (mask_vec && j0 >= 0 && j0 + V <= Tk) {
-                            Tr::unpack(ld_cached16(mrow + j0), mv);
-                        } else {
-#pragma unroll
-                            for (int e = 0; e < V; ++e)
-                                mv[e] = j0 + e >= lo && j0 + e < hi
-                                            ? Tr::load1_cached(mrow + j0 + e) : -INFINITY;
-                        }
-#pragma unroll
-                        for (int h2 = 0; h2 < H2; ++h2) {
-                            v[k][h2].x = mv[2 * h2] == -INFINITY ? -INFINITY
-                                                                 : v[k][h2].x + mv[2 * h2];
-                            v[k][h2].y = mv[2 * h2 + 1] == -INFINITY ? -INFINITY
-                                                                     : v[k][h2].y + mv[2 * h2 + 1];
-                        }
-                    }
-                    if (j0 < lo || j0 + V > hi) {
-#pragma unroll
-                        for (int h2 = 0; h2 < H2; ++h2) {
-                            const int j = j0 + 2 * h2;
-                            if (j < lo || j >= hi) v[k][h2].x = -INFINITY;
-                            if (j + 1 < lo || j + 1 >= hi) v[k][h2].y = -INFINITY;
-                        }
-                    }
-#pragma unroll
-                    for (int h2 = 0; h2 < H2; ++h2) m = fmax3(m, v[k][h2].x, v[k][h2].y);
+                for (int h2 = 0; h2 < H2; h2 += 2) {
+                    const float4 b4 = bias[h2 / 2];
+                    v[k][h2] = fma2(v[k][h2], sc, make_float2(b4.x, b4.y));
+                    v[k][h2 + 1] = fma2(v[k][h2 + 1], sc, make_float2(b4.z, b4.w));
                 }
+                if (w.b >= 0) {
+                    const T *mrow = mask + (int64_t)w.b * Tk;
+                    float mv[V];
+                    if (AL && mask_vec)
+                        relpos_mask<T, true>(mrow, j0, lo, hi, mv);
+                    else
+                        relpos_mask<T, false>(mrow, j0, lo, hi, mv);
+                    // -inf decides whatever the score (NaN too)
+#pragma unroll
+                    for (int h2 = 0; h2 < H2; ++h2) {
+                        v[k][h2].x = mv[2 * h2] == -INFINITY ? -INFINITY : v[k][h2].x + mv[2 * h2];
+                        v[k][h2].y = mv[2 * h2 + 1] == -INFINITY ? -INFINITY
+                                                                 : v[k][h2].y + mv[2 * h2 + 1];
+                    }
+                } else if (j0 < lo || j0 + V > hi) {
+                    const int a = lo - j0, b = hi - j0;
+#pragma unroll
+                    for (int h2 = 0; h2 < H2; ++h2) {
+                        if (2 * h2 < a || 2 * h2 >= b) v[k][h2].x = -INFINITY;
+                        if (2 * h2 + 1 < a || 2 * h2 + 1 >= b) v[k][h2].y = -INFINITY;
+                    }
+                }
+#pragma unroll
+                for (int h2 = 0; h2 < H2; ++h2) m = fmax3(m, v[k][h2].x, v[k][h2].y);
             }
             m = relpos_reduce<TPR, BLOCK, OpMax>(m, red_max, grp);
-            // e^(z - m): as one fused multiply-add where m * log2 e is finite,
-            // else (a row of the type's lowest values) the difference first
-            const bool far = !(fabsf(m) < 1e30f);
-            const float mm = m == -INFINITY ? 0.f : m;  // nothing visible: all weights 0
-            const float2 nmL = f2(-mm * kLog2e), nm = f2(-mm), L2e = f2(kLog2e);
+            // e^(z - m) as one fused multiply-add where m * log2 e is finite;
+            // else (a row of the type's lowest values, an infinite or missing
+            // maximum) the difference is taken first
+            float2 nmL = f2(-m * kLog2e);
+            if (!(fabsf(m) < 1e30f)) {
+                const float2 nm = f2(m == -INFINITY ? 0.f : -m);
+#pragma unroll
+                for (int k = 0; k < CPT; ++k)
+#pragma unroll
+                    for (int h2 = 0; h2 < H2; ++h2) v[k][h2] = add2(v[k][h2], nm);
+                nmL = f2(0.f);
+            }
             float2 sum2 = f2(0.f);
 #pragma unroll
             for (int k = 0; k < CPT; ++k) {
-                const int j0 = (k * TPR + lane) * V - s;
-                if (j0 < hi && j0 + V > lo) {
+                if (!(k * TPR * V + wj < hi && k * TPR * V + wj + WK > lo)) continue;
 #pragma unroll
-                    for (int h2 = 0; h2 < H2; ++h2) {
-                        float2 w = far ? mul2(add2(v[k][h2], nm), L2e) : fma2(v[k][h2], L2e, nmL);
-                        w.x = fast_exp2(w.x);
-                        w.y = fast_exp2(w.y);
-                        v[k][h2] = w;
-                        sum2 = add2(sum2, w);
-                    }
+                for (int h2 = 0; h2 < H2; ++h2) {
+                    float2 e = fma2(v[k][h2], f2(kLog2e), nmL);
+                    e.x = fast_exp2(e.x);
+                    e.y = fast_exp2(e.y);
+                    v[k][h2] = e;
+                    sum2 = add2(sum2, e);
                 }
             }
-            const float sum =
-                relpos_reduce<TPR, BLOCK, OpSum>(sum2.x + sum2.y, red_sum, grp);
+            const float sum = relpos_reduce<TPR, BLOCK, OpSum>(sum2.x + sum2.y, red_sum, grp);
             const float inv = sum == 0.f ? 0.f : fast_rcp(sum);
-            T *orow = out + off;
+            T *orow = out + w.off;
 #pragma unroll
             for (int k = 0; k < CPT; ++k) {
-                const int j0 = (k * TPR + lane) * V - s;
-                if (valid && j0 < Tk) {
-                    uint4 o = make_uint4(0u, 0u, 0u, 0u);
-                    if (j0 < hi && j0 + V > lo) {
-                        float2 yv[H2];
+                const int j0 = k * TPR * V + j_lane;
+                uint4 o = make_uint4(0u, 0u, 0u, 0u);
+                if (k * TPR * V + wj < hi && k * TPR * V + wj + WK > lo) {
+                    float2 yv[H2];
 #pragma unroll
-                        for (int h2 = 0; h2 < H2; ++h2) yv[h2] = mul2(v[k][h2], f2(inv));
-                        if (inv != inv) {  // NaN or +inf among the scores: only visible keys
-                            const uint32_t bits = relpos_bits<T>(mrow, j0, lo, hi);
+                    for (int h2 = 0; h2 < H2; ++h2) yv[h2] = mul2(v[k][h2], f2(inv));
+                    if (inv != inv) {  // NaN or +inf among the scores: only visible keys
+                        const uint32_t bits = relpos_bits<T>(
+                            w.b >= 0 ? mask + (int64_t)w.b * Tk : nullptr, j0, lo, hi);
 #pragma unroll
-                            for (int h2 = 0; h2 < H2; ++h2) {
-                                if (!((bits >> (2 * h2)) & 1u)) yv[h2].x = 0.f;
-                                if (!((bits >> (2 * h2 + 1)) & 1u)) yv[h2].y = 0.f;
-                            }
+                        for (int h2 = 0; h2 < H2; ++h2) {
+                            if (!((bits >> (2 * h2)) & 1u)) yv[h2].x = 0.f;
+                            if (!((bits >> (2 * h2 + 1)) & 1u)) yv[h2].y = 0.f;
                         }
-                        o = pack2<T>(yv);
                     }
-                    relpos_store<T>(orow, j0, Tk, o);
+                    o = pack2<T>(yv);
                 }
+                if (valid && j0 < Tk) relpos_store<T, AL>(orow, j0, Tk, o);
             }
+            s_cur = s_cur + 1 == S ? 0 : s_cur + 1;
         }
+        cp_async_wait<0>();  // (only empty groups are left)
         t0 = h * p.rows_per_head + r1;
     }
 }
 
 // ----------------------------------------------------------------------------
 // Register-resident backward.  Each row group adds its rows' dz by distance
-// into its own array of the distances [rmin, rmin + width) that are not
-// clipped and can occur, index x stored at x + x / 32: a lane's V keys are
-// neighbours, so lanes access with a stride of V, which the gap spreads over
-// the banks.
+// into its own array.  As the bias in the forward, the array exists in four
+// copies, one for each phase of a row's chunks, so that a chunk is added with
+// two 16-byte loads and stores; it covers the distances [first, first +
+// width) that are not clipped and can occur and a chunk more on either side,
+// so that a chunk is either wholly inside or wholly clipped.
 // ----------------------------------------------------------------------------
 struct RelposBand {
-    int rmin, width, stride;  // stride: floats of a group's array
+    int first;   // distance of entry 0
+    int stride;  // entries of a copy, a multiple of 4
 };
+template <int V>
 __host__ __device__ inline RelposBand relpos_band(const RelposShape &p) {
     const int64_t last = p.causal ? 0 : p.Tq - 1;  // the largest j - q
     const int rmin = (int)(-p.R + 1 > 1 - p.Tk ? -p.R + 1 : 1 - p.Tk);
     const int rmax = (int)(p.R - 1 < last ? p.R - 1 : last);
     RelposBand b;
-    b.rmin = rmin;
-    b.width = rmax >= rmin ? rmax - rmin + 1 : 0;
-    b.stride = b.width + b.width / 32 + 1;
+    b.first = rmin - V;
+    // entries first ... rmax + V, and what the copies' shift leaves over
+    b.stride = (((rmax > rmin ? rmax - rmin : 0) + 1 + 2 * V + 3) / 4 + 1) * 4;
     return b;
 }
 
@@ -572,7 +661,9 @@ constexpr int relpos_bw_resident() {
     return TPR > 256 ? 1 : (CPT <= 1 ? 4 : CPT <= 2 ? 3 : 2);
 }
 
-template <typename T, int TPR, int CPT>
+// blockDim.x: relpos_block<TPR>() threads, or fewer (whole warps and row
+// groups) where the groups' arrays would not fit.
+template <typename T, int TPR, int CPT, bool AL>
 __global__ void __launch_bounds__(relpos_block<TPR>(), (relpos_bw_resident<TPR, CPT>()))
 relpos_bw_vec(T *dinp, float *part, const T *dout, const T *y, const T *mask,
               const RelposShape p) {
@@ -581,20 +672,21 @@ relpos_bw_vec(T *dinp, float *part, const T *dout, const T *y, const T *mask,
     constexpr int V = Tr::kVec;
     constexpr int H2 = V / 2;
     constexpr int BLOCK = relpos_block<TPR>();
-    constexpr int G = BLOCK / TPR;
-    extern __shared__ float acc[];  // [G][band.stride]
+    extern __shared__ float4 acc4[];  // [G][4][band.stride / 4]
+    float *acc = reinterpret_cast<float *>(acc4);
     __shared__ float red[2][BLOCK / 32];
-    __shared__ float ends[2][G];
+    __shared__ float ends[2][BLOCK / 32];
     __shared__ int2 wtab[kRelposWinMax];
+    const int G = blockDim.x / TPR;
     const int lane = threadIdx.x % TPR;
     const int grp = threadIdx.x / TPR;
     const int sub = TPR < 32 ? grp % (32 / (TPR < 32 ? TPR : 32)) : 0;  // group of the warp
     const int Tk = (int)p.Tk;
-    const RelposBand band = relpos_band(p);
-    float *mine = acc + grp * band.stride;
+    const RelposBand band = relpos_band<V>(p);
+    float4 *mine = acc4 + grp * band.stride;
     const int64_t total = p.rows * p.Tk;
     const int Tq = (int)p.Tq, gq = G / Tq, gr = G - gq * Tq;
-    const int base_phase = (int)((reinterpret_cast<uintptr_t>(y) / sizeof(T)) % V);
+    const int phase = (int)((reinterpret_cast<uintptr_t>(y) / sizeof(T)) % V);
 
     const int64_t beg = (int64_t)blockIdx.x * p.per;
     const int64_t end = min(beg + p.per, p.rows);
@@ -602,54 +694,44 @@ relpos_bw_vec(T *dinp, float *part, const T *dout, const T *y, const T *mask,
         const int64_t h = t0 / p.rows_per_head;
         const int r0 = (int)(t0 - h * p.rows_per_head);
         const int r1 = (int)min(end - h * p.rows_per_head, p.rows_per_head);
-        for (int x = threadIdx.x; x < G * band.stride; x += BLOCK) acc[x] = 0.f;
-        const bool windows = relpos_find_windows<T, false, BLOCK>(wtab, mask, p, r0, r1);
+        for (int x = threadIdx.x; x < G * band.stride; x += blockDim.x)
+            acc4[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+        const bool windows = relpos_find_windows<T, false, 0>(wtab, mask, p, r0, r1);
         const int b0 = r0 / Tq;
         __syncthreads();
-        float lo_sum = 0.f, hi_sum = 0.f;  // the clipped ends
+        float2 lo2 = f2(0.f), hi2 = f2(0.f);  // the clipped ends
         int turn = 0;
         RelposCursor cur(Tq, r0 + grp);
         // groups that share a warp take the same number of turns (shuffles)
         for (int rw = r0 + grp - sub; rw < r1; rw += G, cur.advance(Tq, gq, gr)) {
             const bool valid = rw + sub < r1;
-            const int64_t off = (((int64_t)cur.b * p.H + h) * Tq + cur.i) * Tk;
-            const int q = cur.i + (int)p.qoff;
-            const int s0 = (int)((off + base_phase) & (V - 1));
-            int lo = 0, hi = valid ? Tk : 0;
-            const T *mrow = nullptr;
-            if (mask && valid) {
-                const int2 w = windows ? wtab[cur.b - b0] : make_int2(-1, 0);
-                if (w.x < 0) {
-                    mrow = mask + (int64_t)cur.b * Tk;
-                } else {
-                    lo = w.x;
-                    hi = w.y;
-                }
-            }
-            if (p.causal) hi = min(hi, q + 1);
+            const RelposRow w = relpos_row<AL, V>(p, cur, h, valid, mask != nullptr,
+                                                  windows ? wtab : nullptr, b0, phase);
+            const int lo = w.lo, hi = w.hi, j_lane = lane * V - w.s;
+            const int wj = (TPR > 32 ? (lane & ~31) * V : 0) - w.s;
+            constexpr int WK = (TPR < 32 ? TPR : 32) * V;
+            const T *mrow = w.b >= 0 ? mask + (int64_t)w.b * Tk : nullptr;
 
             uint4 yr[CPT], gr4[CPT];
 #pragma unroll
             for (int k = 0; k < CPT; ++k) {
-                const int j0 = (k * TPR + lane) * V - s0;
+                const int j0 = k * TPR * V + j_lane;
                 yr[k] = gr4[k] = make_uint4(0u, 0u, 0u, 0u);
                 if (j0 < hi && j0 + V > lo) {
-                    yr[k] = relpos_load<T>(y, off + j0, total);
-                    gr4[k] = relpos_load<T>(dout, off + j0, total);
-                }
-            }
-#pragma unroll
-            for (int k = 0; k < CPT; ++k) {
-                const int j0 = (k * TPR + lane) * V - s0;
-                if (j0 < hi && j0 + V > lo && (mrow || j0 < lo || j0 + V > hi)) {
-                    const uint32_t bits = relpos_bits<T>(mrow, j0, lo, hi);
-                    keep_elements<T>(yr[k], bits);
-                    keep_elements<T>(gr4[k], bits);
+                    yr[k] = relpos_load<T, AL>(y, w.off + j0, total);
+                    gr4[k] = relpos_load<T, AL>(dout, w.off + j0, total);
                 }
             }
             float2 s2 = f2(0.f);
 #pragma unroll
             for (int k = 0; k < CPT; ++k) {
+                const int j0 = k * TPR * V + j_lane;
+                if (!(k * TPR * V + wj < hi && k * TPR * V + wj + WK > lo)) continue;
+                if (mrow || j0 < lo || j0 + V > hi) {
+                    const uint32_t bits = relpos_bits<T>(mrow, j0, lo, hi);
+                    keep_elements<T>(yr[k], bits);
+                    keep_elements<T>(gr4[k], bits);
+                }
                 float2 yv[H2], gv[H2];
                 unpack2<T>(yr[k], yv);
                 unpack2<T>(gr4[k], gv);
@@ -658,102 +740,97 @@ relpos_bw_vec(T *dinp, float *part, const T *dout, const T *y, const T *mask,
             }
             // the group's barrier also orders this row's additions after the
             // last row's; `red` alternates so that one barrier is enough
-            const float s =
-                relpos_reduce<TPR, BLOCK, OpSum>(s2.x + s2.y, red[turn], grp);
+            const float s = relpos_reduce<TPR, 0, OpSum>(s2.x + s2.y, red[turn], grp);
             turn ^= 1;
+            const int x_lane = j_lane - w.q - band.first;  // entry of the lane's first key
+            float4 *acc_row = mine + (x_lane & 3) * (band.stride / 4);
 #pragma unroll
             for (int k = 0; k < CPT; ++k) {
-                const int j0 = (k * TPR + lane) * V - s0;
-                if (!valid || j0 >= Tk) continue;
-                float2 yv[H2], gv[H2], dz[H2], dx[H2];
-                unpack2<T>(yr[k], yv);
-                unpack2<T>(gr4[k], gv);
+                const int j0 = k * TPR * V + j_lane;
+                uint4 o = make_uint4(0u, 0u, 0u, 0u);
+                if (k * TPR * V + wj < hi && k * TPR * V + wj + WK > lo) {
+                    float2 yv[H2], gv[H2], dz[H2], dx[H2];
+                    unpack2<T>(yr[k], yv);
+                    unpack2<T>(gr4[k], gv);
 #pragma unroll
-                for (int h2 = 0; h2 < H2; ++h2)
-                    dz[h2] = mul2(yv[h2], add2(gv[h2], f2(-s)));
-                const bool see = j0 < hi && j0 + V > lo;
-                if (!(fabsf(s) < INFINITY)) {  // 0 * NaN: invisible keys stay 0
-                    const uint32_t bits = see ? relpos_bits<T>(mrow, j0, lo, hi) : 0u;
+                    for (int h2 = 0; h2 < H2; ++h2)
+                        dz[h2] = mul2(yv[h2], add2(gv[h2], f2(-s)));
+                    if (!(fabsf(s) < INFINITY)) {  // 0 * NaN: invisible keys stay 0
+                        const uint32_t bits = relpos_bits<T>(mrow, j0, lo, hi);
 #pragma unroll
-                    for (int h2 = 0; h2 < H2; ++h2) {
-                        if (!((bits >> (2 * h2)) & 1u)) dz[h2].x = 0.f;
-                        if (!((bits >> (2 * h2 + 1)) & 1u)) dz[h2].y = 0.f;
+                        for (int h2 = 0; h2 < H2; ++h2) {
+                            if (!((bits >> (2 * h2)) & 1u)) dz[h2].x = 0.f;
+                            if (!((bits >> (2 * h2 + 1)) & 1u)) dz[h2].y = 0.f;
+                        }
+                    }
+#pragma unroll
+                    for (int h2 = 0; h2 < H2; ++h2) dx[h2] = mul2(dz[h2], f2(p.scale));
+                    o = pack2<T>(dx);
+                    if (j0 < hi && j0 + V > lo) {
+                        const int d0 = j0 - w.q;
+                        if (d0 <= -p.R - V + 1) {
+#pragma unroll
+                            for (int h2 = 0; h2 < H2; ++h2) lo2 = add2(lo2, dz[h2]);
+                        } else if (d0 >= p.R) {
+#pragma unroll
+                            for (int h2 = 0; h2 < H2; ++h2) hi2 = add2(hi2, dz[h2]);
+                        } else {
+                            float4 *at = acc_row + (x_lane >> 2) + k * (TPR * V / 4);
+                            float4 a[H2 / 2];
+#pragma unroll
+                            for (int h2 = 0; h2 < H2 / 2; ++h2) a[h2] = at[h2];
+#pragma unroll
+                            for (int h2 = 0; h2 < H2 / 2; ++h2) {
+                                const float2 u = add2(make_float2(a[h2].x, a[h2].y), dz[2 * h2]);
+                                const float2 t =
+                                    add2(make_float2(a[h2].z, a[h2].w), dz[2 * h2 + 1]);
+                                at[h2] = make_float4(u.x, u.y, t.x, t.y);
+                            }
+                        }
                     }
                 }
-#pragma unroll
-                for (int h2 = 0; h2 < H2; ++h2) dx[h2] = mul2(dz[h2], f2(p.scale));
-                relpos_store<T>(dinp + off, j0, Tk, pack2<T>(dx));
-                if (!see) continue;
-                const int d0 = j0 - q, x0 = d0 - band.rmin;
-                if (x0 >= 0 && x0 + V <= band.width) {
-                    float a[V];
-#pragma unroll
-                    for (int e = 0; e < V; ++e) a[e] = mine[x0 + e + (x0 + e) / 32];
-#pragma unroll
-                    for (int h2 = 0; h2 < H2; ++h2) {
-                        a[2 * h2] += dz[h2].x;
-                        a[2 * h2 + 1] += dz[h2].y;
-                    }
-#pragma unroll
-                    for (int e = 0; e < V; ++e) mine[x0 + e + (x0 + e) / 32] = a[e];
-                } else if (d0 + V - 1 <= -p.R || d0 >= p.R) {
-                    float2 t = dz[0];
-#pragma unroll
-                    for (int h2 = 1; h2 < H2; ++h2) t = add2(t, dz[h2]);
-                    if (d0 < 0)
-                        lo_sum += t.x + t.y;
-                    else
-                        hi_sum += t.x + t.y;
-                } else {
-#pragma unroll
-                    for (int e = 0; e < V; ++e) {
-                        const float d = e % 2 ? dz[e / 2].y : dz[e / 2].x;
-                        const int x = x0 + e;
-                        if (x >= 0 && x < band.width)
-                            mine[x + x / 32] += d;
-                        else if (d0 + e <= -p.R)
-                            lo_sum += d;
-                        else if (d0 + e >= p.R)
-                            hi_sum += d;
-                    }
-                }
+                if (valid && j0 < Tk) relpos_store<T, AL>(dinp + w.off, j0, Tk, o);
             }
             if constexpr (TPR <= 32) __syncwarp();
         }
-        // the groups' ends: lanes of a group, then its warps
-        __shared__ float wends[2][BLOCK / 32];
-        constexpr int W = TPR < 32 ? TPR : 32;
+        // the block's sum of each distance: entries of all groups and copies
+        // in order, and at both ends the lanes' registers and the entries of
+        // clipped distances
         __syncwarp();
+        float lo_sum = lo2.x + lo2.y, hi_sum = hi2.x + hi2.y;
 #pragma unroll
-        for (int o = W / 2; o > 0; o >>= 1) {
+        for (int o = 16; o > 0; o >>= 1) {
             lo_sum += __shfl_xor_sync(0xffffffffu, lo_sum, o);
             hi_sum += __shfl_xor_sync(0xffffffffu, hi_sum, o);
         }
-        if constexpr (TPR > 32) {
-            if ((threadIdx.x & 31) == 0) {
-                wends[0][threadIdx.x >> 5] = lo_sum;
-                wends[1][threadIdx.x >> 5] = hi_sum;
-            }
-            __syncthreads();
-            if (lane < 2) {
-                float v = 0.f;
-                for (int w = 0; w < TPR / 32; ++w) v += wends[lane][grp * (TPR / 32) + w];
-                ends[lane][grp] = v;
-            }
-        } else if (lane == 0) {
-            ends[0][grp] = lo_sum;
-            ends[1][grp] = hi_sum;
+        if ((threadIdx.x & 31) == 0) {
+            ends[0][threadIdx.x >> 5] = lo_sum;
+            ends[1][threadIdx.x >> 5] = hi_sum;
         }
         __syncthreads();
         const int W2 = 2 * p.R + 1;
         float *slot = part + ((int64_t)blockIdx.x + h) * W2;
-        for (int d = threadIdx.x; d < W2; d += BLOCK) {
+        // entry `x` of the distances from band.first on
+        auto entry = [&](int x) {
+            float t = 0.f;
+            for (int g = 0; g < G; ++g)
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    if (x >= c && x - c < band.stride)
+                        t += acc[(g * 4 + c) * band.stride + x - c];
+            return t;
+        };
+        for (int d = threadIdx.x; d < W2; d += blockDim.x) {
             float v = 0.f;
-            const int x = d - p.R - band.rmin;
+            const int x = d - p.R - band.first;
             if (d == 0 || d == 2 * p.R) {
-                for (int g = 0; g < G; ++g) v += ends[d ? 1 : 0][g];
-            } else if (x >= 0 && x < band.width) {
-                for (int g = 0; g < G; ++g) v += acc[g * band.stride + x + x / 32];
+                for (int g = 0; g < (int)blockDim.x / 32; ++g) v += ends[d ? 1 : 0][g];
+                for (int e = 0; e < V; ++e) {  // distances -R - e, R + e
+                    const int xe = d ? x + e : x - e;
+                    if (xe >= 0 && xe < band.stride + 3) v += entry(xe);
+                }
+            } else if (x >= 0 && x < band.stride + 3) {
+                v = entry(x);
             }
             slot[d] = v;
         }

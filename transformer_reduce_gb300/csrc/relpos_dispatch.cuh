@@ -55,9 +55,12 @@ constexpr size_t relpos_sums_bytes(int R) { return (size_t)(2 * R + 1) * 4; }
 // Bucket of the register-resident kernels; false: the row is too long
 // (or a head's rows pass 32 bits).
 // `phase`: elements by which the tensors start past a 16-byte address.
-inline bool pick_relpos_bucket(const RelposShape &p, int V, int phase, int *tpr, int *cpt) {
+// dense: as many chunks per thread as allowed (the row's own costs are then
+// shared by more elements), else as few.
+inline bool pick_relpos_bucket(bool dense, const RelposShape &p, int V, int phase, int *tpr, int *cpt) {
     if (p.Tk > (int64_t)512 * 4 * V || p.rows_per_head > INT32_MAX - 512) return false;
     const int64_t chunks = p.Tk % V == 0 && phase == 0 ? p.Tk / V : (p.Tk + 2 * V - 2) / V;
+    if (dense) return pick_bucket_dense(chunks, 4, 512, tpr, cpt);
     if (!pick_bucket(chunks, 4, 512, tpr, cpt)) return false;
     if (*tpr > 32) *cpt = (int)ceil_div(chunks, *tpr);
     return true;
@@ -68,27 +71,37 @@ int relpos_phase(const void *p) {
     return (int)(reinterpret_cast<uintptr_t>(p) % 16 / sizeof(T));
 }
 
+template <typename T, int TPR, int CPT, bool AL>
+cudaError_t launch_relpos_fw_vec(T *out, const T *inp, const T *mask, const T *table,
+                                 const int32_t *bucket, RelposShape p, int mask_vec,
+                                 cudaStream_t st) {
+    constexpr auto K = relpos_fw_vec<T, TPR, CPT, AL>;
+    const size_t smem = relpos_fw_smem<TPR, CPT>(p.R);
+    const cudaError_t e = relpos_allow_smem<K>(relpos_fw_smem<TPR, CPT>(kRelposMaxDistance));
+    if (e != cudaSuccess) return e;
+    const int64_t blocks =
+        device_sm_count() * relpos_resident(relpos_fw_min_blocks<TPR, CPT>(), smem);
+    const unsigned grid = relpos_cut(p, blocks, relpos_block<TPR>() / TPR);
+    return launch_pdl(K, dim3(grid), dim3(relpos_block<TPR>()), smem, st, out, inp, mask, table,
+                      bucket, p, mask_vec);
+}
+
 template <typename T>
 cudaError_t launch_relpos_fw(T *out, const T *inp, const T *mask, const T *table,
                              const int32_t *bucket, RelposShape p, cudaStream_t st) {
     constexpr int V = Traits<T>::kVec;
     const int phase = relpos_phase<T>(inp);
     int tpr = 0, cpt = 0;
-    if (relpos_phase<T>(out) == phase && pick_relpos_bucket(p, V, phase, &tpr, &cpt)) {
-        const int mask_vec = p.Tk % V == 0 && phase == 0 && relpos_phase<T>(mask) == 0;
-        const size_t smem = relpos_fw_smem<V>(p.R);
-#define X(TPR_, CPT_)                                                                        \
-    if (tpr == TPR_ && cpt == CPT_) {                                                        \
-        const cudaError_t e = relpos_allow_smem<relpos_fw_vec<T, TPR_, CPT_>>(               \
-            relpos_fw_smem<V>(kRelposMaxDistance));                                          \
-        if (e != cudaSuccess) return e;                                                      \
-        const int64_t blocks =                                                               \
-            device_sm_count() * relpos_resident(relpos_fw_min_blocks<TPR_, CPT_>(), smem);   \
-        const unsigned grid = relpos_cut(p, blocks, relpos_block<TPR_>() / TPR_);            \
-        return launch_pdl(relpos_fw_vec<T, TPR_, CPT_>, dim3(grid), dim3(relpos_block<TPR_>()), \
-                          smem, st, out, inp, mask, table, bucket, p, mask_vec);             \
-    }
-        LSR_RELPOS_BUCKETS(X)
+    if (relpos_phase<T>(out) == phase && pick_relpos_bucket(true, p, V, phase, &tpr, &cpt)) {
+        const bool al = p.Tk % V == 0 && phase == 0;
+        const int mask_vec = relpos_phase<T>(mask) == 0;
+#define X(TPR_, CPT_)                                                                     \
+    if (tpr == TPR_ && cpt == CPT_)                                                       \
+        return al ? launch_relpos_fw_vec<T, TPR_, CPT_, true>(out, inp, mask, table,      \
+                                                              bucket, p, mask_vec, st)    \
+                  : launch_relpos_fw_vec<T, TPR_, CPT_, false>(out, inp, mask, table,     \
+                                                               bucket, p, mask_vec, st);
+        LSR_DENSE4_BUCKETS(X)
 #undef X
     }
     const size_t smem = relpos_sums_bytes(p.R);
@@ -103,6 +116,29 @@ cudaError_t launch_relpos_fw(T *out, const T *inp, const T *mask, const T *table
                       table, bucket, p);
 }
 
+// Threads of a backward block whose row groups' arrays fit, 0: not even one
+// warp's.
+template <int TPR>
+int relpos_bw_threads(size_t group_bytes) {
+    for (int n = relpos_block<TPR>(); n >= (TPR < 32 ? 32 : TPR); n /= 2)
+        if (group_bytes * (n / TPR) <= kRelposBandMax) return n;
+    return 0;
+}
+
+template <typename T, int TPR, int CPT, bool AL>
+cudaError_t launch_relpos_bw_vec(T *dinp, const T *dout, const T *y, const T *mask,
+                                 RelposShape &p, float *part, int threads, cudaStream_t st) {
+    constexpr auto K = relpos_bw_vec<T, TPR, CPT, AL>;
+    const cudaError_t e = relpos_allow_smem<K>(kRelposBandMax);
+    if (e != cudaSuccess) return e;
+    const int G = threads / TPR;
+    const size_t smem = (size_t)relpos_band<Traits<T>::kVec>(p).stride * 16 * G;
+    const int64_t blocks =
+        kRelposSms * relpos_resident(relpos_bw_resident<TPR, CPT>(), smem);
+    const unsigned grid = relpos_cut(p, blocks, G);
+    return launch_pdl(K, dim3(grid), dim3(threads), smem, st, dinp, part, dout, y, mask, p);
+}
+
 template <typename T>
 cudaError_t launch_relpos_bw_rows(T *dinp, const T *dout, const T *y, const T *mask,
                                   RelposShape &p, float *part, cudaStream_t st) {
@@ -110,19 +146,17 @@ cudaError_t launch_relpos_bw_rows(T *dinp, const T *dout, const T *y, const T *m
     const int phase = relpos_phase<T>(y);
     int tpr = 0, cpt = 0;
     if (relpos_phase<T>(dout) == phase && relpos_phase<T>(dinp) == phase &&
-        pick_relpos_bucket(p, V, phase, &tpr, &cpt)) {
-        const size_t band = (size_t)relpos_band(p).stride * 4;
-#define X(TPR_, CPT_)                                                                        \
-    if (tpr == TPR_ && cpt == CPT_ && band * (relpos_block<TPR_>() / TPR_) <= kRelposBandMax) { \
-        constexpr int G = relpos_block<TPR_>() / TPR_;                                       \
-        const cudaError_t e =                                                                \
-            relpos_allow_smem<relpos_bw_vec<T, TPR_, CPT_>>(kRelposBandMax);                 \
-        if (e != cudaSuccess) return e;                                                      \
-        const int64_t blocks =                                                               \
-            kRelposSms * relpos_resident(relpos_bw_resident<TPR_, CPT_>(), band * G);        \
-        const unsigned grid = relpos_cut(p, blocks, G);                                      \
-        return launch_pdl(relpos_bw_vec<T, TPR_, CPT_>, dim3(grid), dim3(relpos_block<TPR_>()), \
-                          band * G, st, dinp, part, dout, y, mask, p);                       \
+        pick_relpos_bucket(false, p, V, phase, &tpr, &cpt)) {
+        const bool al = p.Tk % V == 0 && phase == 0;
+        const size_t group_bytes = (size_t)relpos_band<V>(p).stride * 16;
+#define X(TPR_, CPT_)                                                                       \
+    if (tpr == TPR_ && cpt == CPT_) {                                                       \
+        const int n = relpos_bw_threads<TPR_>(group_bytes);                                 \
+        if (n > 0)                                                                          \
+            return al ? launch_relpos_bw_vec<T, TPR_, CPT_, true>(dinp, dout, y, mask, p,   \
+                                                                  part, n, st)              \
+                      : launch_relpos_bw_vec<T, TPR_, CPT_, false>(dinp, dout, y, mask, p,  \
+                                                                   part, n, st);            \
     }
         LSR_RELPOS_BUCKETS(X)
 #undef X
