@@ -400,6 +400,10 @@ __device__ __forceinline__ RelposRow relpos_row(const RelposShape &p, const Relp
         }
     }
     if (p.causal) w.hi = min(w.hi, w.q + 1);
+    if (w.hi <= w.lo) {  // no chunk, not even one that begins before the row, meets it
+        w.lo = 0;
+        w.hi = -V;
+    }
     return w;
 }
 
@@ -633,12 +637,19 @@ relpos_fw_vec(T *out, const T *inp, const T *mask, const T *table, const int32_t
 }
 
 // ----------------------------------------------------------------------------
-// Register-resident backward.  Each row group adds its rows' dz by distance
-// into its own array.  As the bias in the forward, the array exists in four
-// copies, one for each phase of a row's chunks, so that a chunk is added with
-// two 16-byte loads and stores; it covers the distances [first, first +
-// width) that are not clipped and can occur and a chunk more on either side,
-// so that a chunk is either wholly inside or wholly clipped.
+// Register-resident backward.  Rows are staged one ahead, y and dout.  dz is
+// added by distance into arrays of the block.  As the bias in the forward, an
+// array exists in four copies, one for each phase of a row's chunks, so that a
+// chunk is added with two 16-byte loads and stores; it covers the distances
+// [first, first + stride) that are not clipped and can occur and a chunk more
+// on either side, so that a chunk is either wholly inside or wholly clipped.
+//
+// A row of several warps has one array (its keys have distinct distances, and
+// the barrier of the row's sum keeps rows apart).  A warp of whole rows has an
+// array for every four of its row groups.  Groups that share one work on consecutive queries, whose phases usually differ:
+// they then add to different copies at the same time.  Where two phases agree
+// (rows of odd lengths, the last query of a batch entry beside the next one's
+// first) the groups take turns.
 // ----------------------------------------------------------------------------
 struct RelposBand {
     int first;   // distance of entry 0
@@ -656,15 +667,25 @@ __host__ __device__ inline RelposBand relpos_band(const RelposShape &p) {
     return b;
 }
 
+// Arrays of a warp (rows within it), arrays and shared memory of a block of n
+// threads.
+template <int TPR>
+constexpr int relpos_warp_arrays() { return TPR >= 8 ? 1 : 8 / TPR; }
+template <int TPR>
+__host__ __device__ constexpr int relpos_bw_arrays(int n) {
+    return TPR <= 32 ? n / 32 * relpos_warp_arrays<TPR>() : n / TPR;
+}
+constexpr int kRelposBwStages = 2;
 template <int TPR, int CPT>
-constexpr int relpos_bw_resident() {
-    return TPR > 256 ? 1 : (CPT <= 1 ? 4 : CPT <= 2 ? 3 : 2);
+__host__ __device__ constexpr size_t relpos_bw_smem(int n, int band_stride) {
+    return (size_t)relpos_bw_arrays<TPR>(n) * band_stride * 16 +
+           (size_t)kRelposBwStages * 2 * CPT * n * 16;
 }
 
 // blockDim.x: relpos_block<TPR>() threads, or fewer (whole warps and row
-// groups) where the groups' arrays would not fit.
+// groups) where the arrays would not fit.
 template <typename T, int TPR, int CPT, bool AL>
-__global__ void __launch_bounds__(relpos_block<TPR>(), (relpos_bw_resident<TPR, CPT>()))
+__global__ void __launch_bounds__(relpos_block<TPR>(), 512 / relpos_block<TPR>())
 relpos_bw_vec(T *dinp, float *part, const T *dout, const T *y, const T *mask,
               const RelposShape p) {
     pdl_begin();
@@ -672,18 +693,26 @@ relpos_bw_vec(T *dinp, float *part, const T *dout, const T *y, const T *mask,
     constexpr int V = Tr::kVec;
     constexpr int H2 = V / 2;
     constexpr int BLOCK = relpos_block<TPR>();
-    extern __shared__ float4 acc4[];  // [G][4][band.stride / 4]
-    float *acc = reinterpret_cast<float *>(acc4);
+    constexpr int S = kRelposBwStages;
+    constexpr int TW = TPR < 32 ? TPR : 32;  // threads of a group in one warp
+    extern __shared__ uint4 dsmem[];
+    const int n = blockDim.x;
+    uint4 *stage = dsmem + threadIdx.x;  // [S][CPT][2][n], a thread's own slots
+    float4 *acc4 = reinterpret_cast<float4 *>(dsmem + S * CPT * 2 * n);
+    float *acc = reinterpret_cast<float *>(acc4);  // [arrays][4][band.stride]
     __shared__ float red[2][BLOCK / 32];
     __shared__ float ends[2][BLOCK / 32];
     __shared__ int2 wtab[kRelposWinMax];
-    const int G = blockDim.x / TPR;
+    const int G = n / TPR;
     const int lane = threadIdx.x % TPR;
     const int grp = threadIdx.x / TPR;
-    const int sub = TPR < 32 ? grp % (32 / (TPR < 32 ? TPR : 32)) : 0;  // group of the warp
+    const int sub = grp % (32 / TW);  // group of the warp
     const int Tk = (int)p.Tk;
     const RelposBand band = relpos_band<V>(p);
-    float4 *mine = acc4 + grp * band.stride;
+    const int arrays = relpos_bw_arrays<TPR>(n);
+    float4 *mine =
+        acc4 + (TPR <= 32 ? (threadIdx.x >> 5) * relpos_warp_arrays<TPR>() + sub / 4 : grp) *
+                   band.stride;
     const int64_t total = p.rows * p.Tk;
     const int Tq = (int)p.Tq, gq = G / Tq, gr = G - gq * Tq;
     const int phase = (int)((reinterpret_cast<uintptr_t>(y) / sizeof(T)) % V);
@@ -694,39 +723,65 @@ relpos_bw_vec(T *dinp, float *part, const T *dout, const T *y, const T *mask,
         const int64_t h = t0 / p.rows_per_head;
         const int r0 = (int)(t0 - h * p.rows_per_head);
         const int r1 = (int)min(end - h * p.rows_per_head, p.rows_per_head);
-        for (int x = threadIdx.x; x < G * band.stride; x += blockDim.x)
-            acc4[x] = make_float4(0.f, 0.f, 0.f, 0.f);
         const bool windows = relpos_find_windows<T, false, 0>(wtab, mask, p, r0, r1);
         const int b0 = r0 / Tq;
+        if (windows) __syncthreads();
+        int r_issue = r0 + grp;
+        RelposCursor ci(Tq, r_issue);
+        auto issue = [&](int s) {
+            if (r_issue < r1) {
+                const RelposRow w = relpos_row<AL, V>(p, ci, h, true, mask != nullptr,
+                                                      windows ? wtab : nullptr, b0, phase);
+#pragma unroll
+                for (int k = 0; k < CPT; ++k) {
+                    const int j0 = (k * TPR + lane) * V - w.s;
+                    if (j0 < w.hi && j0 + V > w.lo) {
+                        const int64_t at = w.off + j0;
+                        uint4 *slot = &stage[(s * CPT + k) * 2 * n];
+                        if (AL || (at >= 0 && at + V <= total)) {
+                            cp_async16(slot, y + at);
+                            cp_async16(slot + n, dout + at);
+                        } else {
+                            slot[0] = relpos_load<T, AL>(y, at, total);
+                            slot[n] = relpos_load<T, AL>(dout, at, total);
+                        }
+                    }
+                }
+                r_issue += G;
+                ci.advance(Tq, gq, gr);
+            }
+            cp_async_commit();
+        };
+#pragma unroll
+        for (int s = 0; s < S - 1; ++s) issue(s);
+        for (int x = threadIdx.x; x < arrays * band.stride; x += n)
+            acc4[x] = make_float4(0.f, 0.f, 0.f, 0.f);
         __syncthreads();
         float2 lo2 = f2(0.f), hi2 = f2(0.f);  // the clipped ends
-        int turn = 0;
+        int turn = 0, s_cur = 0, s_iss = S - 1;
         RelposCursor cur(Tq, r0 + grp);
         // groups that share a warp take the same number of turns (shuffles)
         for (int rw = r0 + grp - sub; rw < r1; rw += G, cur.advance(Tq, gq, gr)) {
+            issue(s_iss);
+            s_iss = s_iss + 1 == S ? 0 : s_iss + 1;
+            cp_async_wait<S - 1>();  // this thread's copies of the row have landed
             const bool valid = rw + sub < r1;
             const RelposRow w = relpos_row<AL, V>(p, cur, h, valid, mask != nullptr,
                                                   windows ? wtab : nullptr, b0, phase);
             const int lo = w.lo, hi = w.hi, j_lane = lane * V - w.s;
             const int wj = (TPR > 32 ? (lane & ~31) * V : 0) - w.s;
-            constexpr int WK = (TPR < 32 ? TPR : 32) * V;
+            constexpr int WK = TW * V;
             const T *mrow = w.b >= 0 ? mask + (int64_t)w.b * Tk : nullptr;
 
             uint4 yr[CPT], gr4[CPT];
-#pragma unroll
-            for (int k = 0; k < CPT; ++k) {
-                const int j0 = k * TPR * V + j_lane;
-                yr[k] = gr4[k] = make_uint4(0u, 0u, 0u, 0u);
-                if (j0 < hi && j0 + V > lo) {
-                    yr[k] = relpos_load<T, AL>(y, w.off + j0, total);
-                    gr4[k] = relpos_load<T, AL>(dout, w.off + j0, total);
-                }
-            }
             float2 s2 = f2(0.f);
 #pragma unroll
             for (int k = 0; k < CPT; ++k) {
                 const int j0 = k * TPR * V + j_lane;
                 if (!(k * TPR * V + wj < hi && k * TPR * V + wj + WK > lo)) continue;
+                const uint4 *slot = &stage[(s_cur * CPT + k) * 2 * n];
+                yr[k] = slot[0];
+                gr4[k] = slot[n];
                 if (mrow || j0 < lo || j0 + V > hi) {
                     const uint32_t bits = relpos_bits<T>(mrow, j0, lo, hi);
                     keep_elements<T>(yr[k], bits);
@@ -744,56 +799,72 @@ relpos_bw_vec(T *dinp, float *part, const T *dout, const T *y, const T *mask,
             turn ^= 1;
             const int x_lane = j_lane - w.q - band.first;  // entry of the lane's first key
             float4 *acc_row = mine + (x_lane & 3) * (band.stride / 4);
+            // groups before this one with the same array and copy go first
+            int rank = 0;
+            if constexpr (TPR < 32) {
+                const unsigned same = __match_any_sync(
+                    0xffffffffu, valid ? (sub / 4) * 4 + (x_lane & 3) : 32 + sub);
+                rank = __popc(same & ((1u << (sub * TPR)) - 1u)) / TPR;
+            }
+            for (int go = 0;; ++go) {
 #pragma unroll
-            for (int k = 0; k < CPT; ++k) {
-                const int j0 = k * TPR * V + j_lane;
-                uint4 o = make_uint4(0u, 0u, 0u, 0u);
-                if (k * TPR * V + wj < hi && k * TPR * V + wj + WK > lo) {
-                    float2 yv[H2], gv[H2], dz[H2], dx[H2];
-                    unpack2<T>(yr[k], yv);
-                    unpack2<T>(gr4[k], gv);
+                for (int k = 0; k < CPT; ++k) {
+                    const int j0 = k * TPR * V + j_lane;
+                    uint4 o = make_uint4(0u, 0u, 0u, 0u);
+                    if (k * TPR * V + wj < hi && k * TPR * V + wj + WK > lo) {
+                        float2 yv[H2], gv[H2], dz[H2], dx[H2];
+                        unpack2<T>(yr[k], yv);
+                        unpack2<T>(gr4[k], gv);
 #pragma unroll
-                    for (int h2 = 0; h2 < H2; ++h2)
-                        dz[h2] = mul2(yv[h2], add2(gv[h2], f2(-s)));
-                    if (!(fabsf(s) < INFINITY)) {  // 0 * NaN: invisible keys stay 0
-                        const uint32_t bits = relpos_bits<T>(mrow, j0, lo, hi);
+                        for (int h2 = 0; h2 < H2; ++h2)
+                            dz[h2] = mul2(yv[h2], add2(gv[h2], f2(-s)));
+                        if (!(fabsf(s) < INFINITY)) {  // 0 * NaN: invisible keys stay 0
+                            const uint32_t bits = relpos_bits<T>(mrow, j0, lo, hi);
 #pragma unroll
-                        for (int h2 = 0; h2 < H2; ++h2) {
-                            if (!((bits >> (2 * h2)) & 1u)) dz[h2].x = 0.f;
-                            if (!((bits >> (2 * h2 + 1)) & 1u)) dz[h2].y = 0.f;
+                            for (int h2 = 0; h2 < H2; ++h2) {
+                                if (!((bits >> (2 * h2)) & 1u)) dz[h2].x = 0.f;
+                                if (!((bits >> (2 * h2 + 1)) & 1u)) dz[h2].y = 0.f;
+                            }
                         }
-                    }
 #pragma unroll
-                    for (int h2 = 0; h2 < H2; ++h2) dx[h2] = mul2(dz[h2], f2(p.scale));
-                    o = pack2<T>(dx);
-                    if (j0 < hi && j0 + V > lo) {
-                        const int d0 = j0 - w.q;
-                        if (d0 <= -p.R - V + 1) {
+                        for (int h2 = 0; h2 < H2; ++h2) dx[h2] = mul2(dz[h2], f2(p.scale));
+                        o = pack2<T>(dx);
+                        if (rank == go && j0 < hi && j0 + V > lo) {
+                            const int d0 = j0 - w.q;
+                            if (d0 <= -p.R - V + 1) {
 #pragma unroll
-                            for (int h2 = 0; h2 < H2; ++h2) lo2 = add2(lo2, dz[h2]);
-                        } else if (d0 >= p.R) {
+                                for (int h2 = 0; h2 < H2; ++h2) lo2 = add2(lo2, dz[h2]);
+                            } else if (d0 >= p.R) {
 #pragma unroll
-                            for (int h2 = 0; h2 < H2; ++h2) hi2 = add2(hi2, dz[h2]);
-                        } else {
-                            float4 *at = acc_row + (x_lane >> 2) + k * (TPR * V / 4);
-                            float4 a[H2 / 2];
+                                for (int h2 = 0; h2 < H2; ++h2) hi2 = add2(hi2, dz[h2]);
+                            } else {
+                                float4 *at = acc_row + (x_lane >> 2) + k * (TPR * V / 4);
+                                float4 a[H2 / 2];
 #pragma unroll
-                            for (int h2 = 0; h2 < H2 / 2; ++h2) a[h2] = at[h2];
+                                for (int h2 = 0; h2 < H2 / 2; ++h2) a[h2] = at[h2];
 #pragma unroll
-                            for (int h2 = 0; h2 < H2 / 2; ++h2) {
-                                const float2 u = add2(make_float2(a[h2].x, a[h2].y), dz[2 * h2]);
-                                const float2 t =
-                                    add2(make_float2(a[h2].z, a[h2].w), dz[2 * h2 + 1]);
-                                at[h2] = make_float4(u.x, u.y, t.x, t.y);
+                                for (int h2 = 0; h2 < H2 / 2; ++h2) {
+                                    const float2 u =
+                                        add2(make_float2(a[h2].x, a[h2].y), dz[2 * h2]);
+                                    const float2 t =
+                                        add2(make_float2(a[h2].z, a[h2].w), dz[2 * h2 + 1]);
+                                    at[h2] = make_float4(u.x, u.y, t.x, t.y);
+                                }
                             }
                         }
                     }
+                    if (go == 0 && valid && j0 < Tk)
+                        relpos_store<T, AL>(dinp + w.off, j0, Tk, o);
                 }
-                if (valid && j0 < Tk) relpos_store<T, AL>(dinp + w.off, j0, Tk, o);
+                if constexpr (TPR > 32) break;
+                __syncwarp();
+                if constexpr (TPR == 32) break;
+                if (!__any_sync(0xffffffffu, rank > go)) break;
             }
-            if constexpr (TPR <= 32) __syncwarp();
+            s_cur = s_cur + 1 == S ? 0 : s_cur + 1;
         }
-        // the block's sum of each distance: entries of all groups and copies
+        cp_async_wait<0>();  // (only empty groups are left)
+        // the block's sum of each distance: entries of all arrays and copies
         // in order, and at both ends the lanes' registers and the entries of
         // clipped distances
         __syncwarp();
@@ -813,18 +884,18 @@ relpos_bw_vec(T *dinp, float *part, const T *dout, const T *y, const T *mask,
         // entry `x` of the distances from band.first on
         auto entry = [&](int x) {
             float t = 0.f;
-            for (int g = 0; g < G; ++g)
+            for (int g = 0; g < arrays; ++g)
 #pragma unroll
                 for (int c = 0; c < 4; ++c)
                     if (x >= c && x - c < band.stride)
                         t += acc[(g * 4 + c) * band.stride + x - c];
             return t;
         };
-        for (int d = threadIdx.x; d < W2; d += blockDim.x) {
+        for (int d = threadIdx.x; d < W2; d += n) {
             float v = 0.f;
             const int x = d - p.R - band.first;
             if (d == 0 || d == 2 * p.R) {
-                for (int g = 0; g < (int)blockDim.x / 32; ++g) v += ends[d ? 1 : 0][g];
+                for (int g = 0; g < n / 32; ++g) v += ends[d ? 1 : 0][g];
                 for (int e = 0; e < V; ++e) {  // distances -R - e, R + e
                     const int xe = d ? x + e : x - e;
                     if (xe >= 0 && xe < band.stride + 3) v += entry(xe);

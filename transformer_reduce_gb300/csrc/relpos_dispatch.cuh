@@ -13,9 +13,8 @@ namespace lsr {
 // depends only on the problem.
 constexpr int64_t kRelposSms = 152;
 constexpr int64_t kRelposBwBlocks = 4 * kRelposSms;
-// Shared memory of an SM that blocks can have, and of a block at most.
+// Shared memory of an SM that the blocks can have.
 constexpr size_t kRelposSmSmem = 220 * 1024;
-constexpr size_t kRelposBandMax = 100 * 1024;
 
 // Opt in, once per device, to the most dynamic shared memory a kernel may ask
 // for at the largest max_distance.
@@ -47,23 +46,22 @@ inline int64_t relpos_resident(int most, size_t smem) {
 
 constexpr size_t relpos_sums_bytes(int R) { return (size_t)(2 * R + 1) * 4; }
 
-// Threads per row and chunks per thread that pick_relpos_bucket can return.
-#define LSR_RELPOS_BUCKETS(X)                                                     \
-    X(1, 1) X(2, 1) X(4, 1) X(8, 1) X(16, 1) X(32, 1) X(32, 2) X(32, 3) X(32, 4) \
+// Threads per row and chunks per thread of the backward (those of
+// LSR_DENSE4_BUCKETS with at least four threads).
+#define LSR_RELPOS_BW_BUCKETS(X)                                                        \
+    X(4, 1) X(4, 2) X(4, 3) X(4, 4) X(8, 3) X(8, 4) X(16, 3) X(16, 4) X(32, 3) X(32, 4) \
     X(64, 3) X(64, 4) X(128, 3) X(128, 4) X(256, 3) X(256, 4) X(512, 3) X(512, 4)
 
 // Bucket of the register-resident kernels; false: the row is too long
 // (or a head's rows pass 32 bits).
 // `phase`: elements by which the tensors start past a 16-byte address.
-// dense: as many chunks per thread as allowed (the row's own costs are then
-// shared by more elements), else as few.
-inline bool pick_relpos_bucket(bool dense, const RelposShape &p, int V, int phase, int *tpr, int *cpt) {
+// As many chunks per thread as allowed, so that the row's own costs are shared
+// by more elements ([32,16,512,512] bf16 forward: 322 instructions per row and
+// warp at one row per warp and two chunks, 92 us at two rows and four).
+inline bool pick_relpos_bucket(const RelposShape &p, int V, int phase, int *tpr, int *cpt) {
     if (p.Tk > (int64_t)512 * 4 * V || p.rows_per_head > INT32_MAX - 512) return false;
     const int64_t chunks = p.Tk % V == 0 && phase == 0 ? p.Tk / V : (p.Tk + 2 * V - 2) / V;
-    if (dense) return pick_bucket_dense(chunks, 4, 512, tpr, cpt);
-    if (!pick_bucket(chunks, 4, 512, tpr, cpt)) return false;
-    if (*tpr > 32) *cpt = (int)ceil_div(chunks, *tpr);
-    return true;
+    return pick_bucket_dense(chunks, 4, 512, tpr, cpt);
 }
 
 template <typename T>
@@ -92,7 +90,7 @@ cudaError_t launch_relpos_fw(T *out, const T *inp, const T *mask, const T *table
     constexpr int V = Traits<T>::kVec;
     const int phase = relpos_phase<T>(inp);
     int tpr = 0, cpt = 0;
-    if (relpos_phase<T>(out) == phase && pick_relpos_bucket(true, p, V, phase, &tpr, &cpt)) {
+    if (relpos_phase<T>(out) == phase && pick_relpos_bucket(p, V, phase, &tpr, &cpt)) {
         const bool al = p.Tk % V == 0 && phase == 0;
         const int mask_vec = relpos_phase<T>(mask) == 0;
 #define X(TPR_, CPT_)                                                                     \
@@ -116,27 +114,31 @@ cudaError_t launch_relpos_fw(T *out, const T *inp, const T *mask, const T *table
                       table, bucket, p);
 }
 
-// Threads of a backward block whose row groups' arrays fit, 0: not even one
-// warp's.
-template <int TPR>
-int relpos_bw_threads(size_t group_bytes) {
-    for (int n = relpos_block<TPR>(); n >= (TPR < 32 ? 32 : TPR); n /= 2)
-        if (group_bytes * (n / TPR) <= kRelposBandMax) return n;
-    return 0;
+// Threads of a backward block: as many as let two blocks share an SM, at
+// least a warp or a row group.  (The largest arrays, max_distance 2048 with
+// two of them in one warp, still fit kRelposSmSmem.)
+template <int TPR, int CPT>
+int relpos_bw_threads(int band_stride) {
+    int n = relpos_block<TPR>();
+    while (n / 2 >= (TPR < 32 ? 32 : TPR) &&
+           relpos_bw_smem<TPR, CPT>(n, band_stride) > kRelposSmSmem / 2 - 4096)
+        n /= 2;
+    return n;
 }
 
 template <typename T, int TPR, int CPT, bool AL>
 cudaError_t launch_relpos_bw_vec(T *dinp, const T *dout, const T *y, const T *mask,
-                                 RelposShape &p, float *part, int threads, cudaStream_t st) {
+                                 RelposShape &p, float *part, cudaStream_t st) {
     constexpr auto K = relpos_bw_vec<T, TPR, CPT, AL>;
-    const cudaError_t e = relpos_allow_smem<K>(kRelposBandMax);
+    const cudaError_t e = relpos_allow_smem<K>(kRelposSmSmem);
     if (e != cudaSuccess) return e;
-    const int G = threads / TPR;
-    const size_t smem = (size_t)relpos_band<Traits<T>::kVec>(p).stride * 16 * G;
-    const int64_t blocks =
-        kRelposSms * relpos_resident(relpos_bw_resident<TPR, CPT>(), smem);
-    const unsigned grid = relpos_cut(p, blocks, G);
-    return launch_pdl(K, dim3(grid), dim3(threads), smem, st, dinp, part, dout, y, mask, p);
+    const int stride = relpos_band<Traits<T>::kVec>(p).stride;
+    const int n = relpos_bw_threads<TPR, CPT>(stride);
+    const size_t smem = relpos_bw_smem<TPR, CPT>(n, stride);
+    int64_t blocks = kRelposSms * relpos_resident(512 / n, smem);
+    if (blocks > kRelposBwBlocks) blocks = kRelposBwBlocks;
+    const unsigned grid = relpos_cut(p, blocks, n / TPR);
+    return launch_pdl(K, dim3(grid), dim3(n), smem, st, dinp, part, dout, y, mask, p);
 }
 
 template <typename T>
@@ -146,19 +148,19 @@ cudaError_t launch_relpos_bw_rows(T *dinp, const T *dout, const T *y, const T *m
     const int phase = relpos_phase<T>(y);
     int tpr = 0, cpt = 0;
     if (relpos_phase<T>(dout) == phase && relpos_phase<T>(dinp) == phase &&
-        pick_relpos_bucket(false, p, V, phase, &tpr, &cpt)) {
+        pick_relpos_bucket(p, V, phase, &tpr, &cpt)) {
         const bool al = p.Tk % V == 0 && phase == 0;
-        const size_t group_bytes = (size_t)relpos_band<V>(p).stride * 16;
+        if (tpr < 4) {  // groups of one or two threads would need too many arrays
+            cpt = (int)ceil_div(tpr * cpt, 4);
+            tpr = 4;
+        }
 #define X(TPR_, CPT_)                                                                       \
-    if (tpr == TPR_ && cpt == CPT_) {                                                       \
-        const int n = relpos_bw_threads<TPR_>(group_bytes);                                 \
-        if (n > 0)                                                                          \
-            return al ? launch_relpos_bw_vec<T, TPR_, CPT_, true>(dinp, dout, y, mask, p,   \
-                                                                  part, n, st)              \
-                      : launch_relpos_bw_vec<T, TPR_, CPT_, false>(dinp, dout, y, mask, p,  \
-                                                                   part, n, st);            \
-    }
-        LSR_RELPOS_BUCKETS(X)
+    if (tpr == TPR_ && cpt == CPT_)                                                         \
+        return al ? launch_relpos_bw_vec<T, TPR_, CPT_, true>(dinp, dout, y, mask, p, part, \
+                                                              st)                           \
+                  : launch_relpos_bw_vec<T, TPR_, CPT_, false>(dinp, dout, y, mask, p,      \
+                                                               part, st);
+        LSR_RELPOS_BW_BUCKETS(X)
 #undef X
     }
     if (p.Tk <= kLoopWarpRowMax) {
