@@ -294,18 +294,33 @@ __device__ __forceinline__ float relpos_reduce(float v, float *red, int grp) {
 
 // Position of a row group in its segment, advanced by G rows without division.
 // (The launcher keeps a head's rows below 2^31 - 512, so 32 bits hold them.)
+struct RelposStep {
+    int gq, gr;             // G = gq * Tq + gr
+    int64_t step, wrap;     // elements of G rows within the tensor, and of a batch entry's end
+    __device__ __forceinline__ RelposStep(const RelposShape &p, int G) {
+        const int Tq = (int)p.Tq;
+        gq = G / Tq;
+        gr = G - gq * Tq;
+        step = ((int64_t)gq * p.H * Tq + gr) * p.Tk;
+        wrap = (p.H - 1) * Tq * p.Tk;
+    }
+};
 struct RelposCursor {
     int b, i;
-    __device__ __forceinline__ RelposCursor(int Tq, int bi) {
-        b = bi / Tq;
-        i = bi - b * Tq;
+    int64_t off;  // element offset of the row
+    __device__ __forceinline__ RelposCursor(const RelposShape &p, int64_t h, int bi) {
+        b = bi / (int)p.Tq;
+        i = bi - b * (int)p.Tq;
+        off = (((int64_t)b * p.H + h) * p.Tq + i) * p.Tk;
     }
-    __device__ __forceinline__ void advance(int Tq, int gq, int gr) {
-        b += gq;
-        i += gr;
+    __device__ __forceinline__ void advance(int Tq, const RelposStep &g) {
+        b += g.gq;
+        i += g.gr;
+        off += g.step;
         if (i >= Tq) {
             i -= Tq;
             ++b;
+            off += g.wrap;
         }
     }
 };
@@ -381,10 +396,10 @@ struct RelposRow {
 };
 template <bool AL, int V>
 __device__ __forceinline__ RelposRow relpos_row(const RelposShape &p, const RelposCursor &cur,
-                                                int64_t h, bool valid, bool masked,
-                                                const int2 *wtab, int b0, int phase) {
+                                                bool valid, bool masked, const int2 *wtab, int b0,
+                                                int phase) {
     RelposRow w;
-    w.off = (((int64_t)cur.b * p.H + h) * (int)p.Tq + cur.i) * (int)p.Tk;
+    w.off = cur.off;
     w.q = cur.i + (int)p.qoff;
     w.s = AL ? 0 : (int)((w.off + phase) & (V - 1));
     w.lo = 0;
@@ -417,13 +432,13 @@ __host__ __device__ constexpr int relpos_lut_stride(int R) {
     return (2 * R + 1 + 2 * kLutPad + 8 + 3) / 4 * 4;
 }
 
-// Resident blocks per SM asked of ptxas, and stages of the row pipeline (rows
-// in flight per group: one less).
+// Resident blocks per SM asked of ptxas, and stages of the row pipeline (the
+// current row and the next).
 template <int TPR, int CPT>
 constexpr int relpos_fw_min_blocks() {
     return TPR > 256 ? 1 : (CPT <= 2 ? 4 : 3);
 }
-constexpr int kRelposFwStages = 3;
+constexpr int kRelposFwStages = 2;
 template <int TPR, int CPT>
 constexpr size_t relpos_fw_smem(int R) {
     return (size_t)4 * relpos_lut_stride(R) * 4 +
@@ -461,6 +476,7 @@ relpos_fw_vec(T *out, const T *inp, const T *mask, const T *table, const int32_t
     constexpr int BLOCK = relpos_block<TPR>();
     constexpr int G = BLOCK / TPR;
     constexpr int S = kRelposFwStages;
+    static_assert(S == 2, "the row in flight is carried in registers");
     extern __shared__ uint4 dsmem[];
     uint4 *stage = dsmem + threadIdx.x;  // [S][CPT][BLOCK], a thread's own slots
     const float4 *lut4 = reinterpret_cast<const float4 *>(dsmem + S * CPT * BLOCK);
@@ -473,7 +489,8 @@ relpos_fw_vec(T *out, const T *inp, const T *mask, const T *table, const int32_t
     const int Tk = (int)p.Tk, stride = relpos_lut_stride(p.R);
     const int top = (2 * p.R + kLutPad + 4) / 4;  // last 16-byte step a chunk may start at
     const int64_t total = p.rows * p.Tk;
-    const int Tq = (int)p.Tq, gq = G / Tq, gr = G - gq * Tq;
+    const int Tq = (int)p.Tq;
+    const RelposStep step(p, G);
     const int phase = (int)((reinterpret_cast<uintptr_t>(inp) / sizeof(T)) % V);
     const float2 sc = f2(p.scale);
 
@@ -490,16 +507,17 @@ relpos_fw_vec(T *out, const T *inp, const T *mask, const T *table, const int32_t
         // Copies of a row's visible chunks into a stage: each thread its own
         // slots.  A chunk that reaches past the tensor is put there by hand.
         int r_issue = r0 + grp;
-        RelposCursor ci(Tq, r_issue);
+        RelposCursor ci(p, h, r_issue);
+        RelposRow next;  // the row issued last
         auto issue = [&](int s) {
+            next = relpos_row<AL, V>(p, ci, r_issue < r1, mask != nullptr,
+                                     windows ? wtab : nullptr, b0, phase);
             if (r_issue < r1) {
-                const RelposRow w = relpos_row<AL, V>(p, ci, h, true, mask != nullptr,
-                                                      windows ? wtab : nullptr, b0, phase);
 #pragma unroll
                 for (int k = 0; k < CPT; ++k) {
-                    const int j0 = (k * TPR + lane) * V - w.s;
-                    if (j0 < w.hi && j0 + V > w.lo) {
-                        const int64_t at = w.off + j0;
+                    const int j0 = (k * TPR + lane) * V - next.s;
+                    if (j0 < next.hi && j0 + V > next.lo) {
+                        const int64_t at = next.off + j0;
                         if (AL || (at >= 0 && at + V <= total))
                             cp_async16(&stage[(s * CPT + k) * BLOCK], inp + at);
                         else
@@ -507,12 +525,11 @@ relpos_fw_vec(T *out, const T *inp, const T *mask, const T *table, const int32_t
                     }
                 }
                 r_issue += G;
-                ci.advance(Tq, gq, gr);
+                ci.advance(Tq, step);
             }
             cp_async_commit();
         };
-#pragma unroll
-        for (int s = 0; s < S - 1; ++s) issue(s);
+        issue(0);
         // the bias, while the first rows are on their way
         for (int x = threadIdx.x; x < stride; x += BLOCK) {
             const float v =
@@ -522,16 +539,13 @@ relpos_fw_vec(T *out, const T *inp, const T *mask, const T *table, const int32_t
                 if (x >= k) lut[k * stride + x - k] = v;
         }
         __syncthreads();
-        int s_cur = 0, s_iss = S - 1;
-        RelposCursor cur(Tq, r0 + grp);
+        int turn = 0;  // stage of the current row
         // groups that share a warp take the same number of turns (shuffles)
-        for (int rw = r0 + grp - sub; rw < r1; rw += G, cur.advance(Tq, gq, gr)) {
-            issue(s_iss);
-            s_iss = s_iss + 1 == S ? 0 : s_iss + 1;
-            cp_async_wait<S - 1>();  // this thread's copies of the row have landed
+        for (int rw = r0 + grp - sub; rw < r1; rw += G, turn ^= 1) {
+            const RelposRow w = next;
             const bool valid = rw + sub < r1;
-            const RelposRow w = relpos_row<AL, V>(p, cur, h, valid, mask != nullptr,
-                                                  windows ? wtab : nullptr, b0, phase);
+            issue(turn ^ 1);
+            cp_async_wait<1>();  // this thread's copies of the row have landed
             const int lo = w.lo, hi = w.hi, j_lane = lane * V - w.s;
             // keys of the warp's part of chunk k: [k * TPR * V + wj, ... + WK)
             const int wj = (TPR > 32 ? (lane & ~31) * V : 0) - w.s;
@@ -545,7 +559,7 @@ relpos_fw_vec(T *out, const T *inp, const T *mask, const T *table, const int32_t
             for (int k = 0; k < CPT; ++k) {
                 const int j0 = k * TPR * V + j_lane;
                 if (!(k * TPR * V + wj < hi && k * TPR * V + wj + WK > lo)) continue;
-                unpack2<T>(stage[(s_cur * CPT + k) * BLOCK], v[k]);
+                unpack2<T>(stage[(turn * CPT + k) * BLOCK], v[k]);
                 const float4 *bias =
                     lut_row + min(max((x_lane >> 2) + k * (TPR * V / 4), 0), top);
 #pragma unroll
@@ -629,7 +643,6 @@ relpos_fw_vec(T *out, const T *inp, const T *mask, const T *table, const int32_t
                 }
                 if (valid && j0 < Tk) relpos_store<T, AL>(orow, j0, Tk, o);
             }
-            s_cur = s_cur + 1 == S ? 0 : s_cur + 1;
         }
         cp_async_wait<0>();  // (only empty groups are left)
         t0 = h * p.rows_per_head + r1;
@@ -675,7 +688,7 @@ template <int TPR>
 __host__ __device__ constexpr int relpos_bw_arrays(int n) {
     return TPR <= 32 ? n / 32 * relpos_warp_arrays<TPR>() : n / TPR;
 }
-constexpr int kRelposBwStages = 2;
+constexpr int kRelposBwStages = 2;  // the current row and the next
 template <int TPR, int CPT>
 __host__ __device__ constexpr size_t relpos_bw_smem(int n, int band_stride) {
     return (size_t)relpos_bw_arrays<TPR>(n) * band_stride * 16 +
@@ -694,6 +707,7 @@ relpos_bw_vec(T *dinp, float *part, const T *dout, const T *y, const T *mask,
     constexpr int H2 = V / 2;
     constexpr int BLOCK = relpos_block<TPR>();
     constexpr int S = kRelposBwStages;
+    static_assert(S == 2, "the row in flight is carried in registers");
     constexpr int TW = TPR < 32 ? TPR : 32;  // threads of a group in one warp
     extern __shared__ uint4 dsmem[];
     const int n = blockDim.x;
@@ -714,7 +728,8 @@ relpos_bw_vec(T *dinp, float *part, const T *dout, const T *y, const T *mask,
         acc4 + (TPR <= 32 ? (threadIdx.x >> 5) * relpos_warp_arrays<TPR>() + sub / 4 : grp) *
                    band.stride;
     const int64_t total = p.rows * p.Tk;
-    const int Tq = (int)p.Tq, gq = G / Tq, gr = G - gq * Tq;
+    const int Tq = (int)p.Tq;
+    const RelposStep step(p, G);
     const int phase = (int)((reinterpret_cast<uintptr_t>(y) / sizeof(T)) % V);
 
     const int64_t beg = (int64_t)blockIdx.x * p.per;
@@ -727,16 +742,17 @@ relpos_bw_vec(T *dinp, float *part, const T *dout, const T *y, const T *mask,
         const int b0 = r0 / Tq;
         if (windows) __syncthreads();
         int r_issue = r0 + grp;
-        RelposCursor ci(Tq, r_issue);
+        RelposCursor ci(p, h, r_issue);
+        RelposRow next;  // the row issued last
         auto issue = [&](int s) {
+            next = relpos_row<AL, V>(p, ci, r_issue < r1, mask != nullptr,
+                                     windows ? wtab : nullptr, b0, phase);
             if (r_issue < r1) {
-                const RelposRow w = relpos_row<AL, V>(p, ci, h, true, mask != nullptr,
-                                                      windows ? wtab : nullptr, b0, phase);
 #pragma unroll
                 for (int k = 0; k < CPT; ++k) {
-                    const int j0 = (k * TPR + lane) * V - w.s;
-                    if (j0 < w.hi && j0 + V > w.lo) {
-                        const int64_t at = w.off + j0;
+                    const int j0 = (k * TPR + lane) * V - next.s;
+                    if (j0 < next.hi && j0 + V > next.lo) {
+                        const int64_t at = next.off + j0;
                         uint4 *slot = &stage[(s * CPT + k) * 2 * n];
                         if (AL || (at >= 0 && at + V <= total)) {
                             cp_async16(slot, y + at);
@@ -748,26 +764,22 @@ relpos_bw_vec(T *dinp, float *part, const T *dout, const T *y, const T *mask,
                     }
                 }
                 r_issue += G;
-                ci.advance(Tq, gq, gr);
+                ci.advance(Tq, step);
             }
             cp_async_commit();
         };
-#pragma unroll
-        for (int s = 0; s < S - 1; ++s) issue(s);
+        issue(0);
         for (int x = threadIdx.x; x < arrays * band.stride; x += n)
             acc4[x] = make_float4(0.f, 0.f, 0.f, 0.f);
         __syncthreads();
         float2 lo2 = f2(0.f), hi2 = f2(0.f);  // the clipped ends
-        int turn = 0, s_cur = 0, s_iss = S - 1;
-        RelposCursor cur(Tq, r0 + grp);
+        int turn = 0;  // also the stage of the current row
         // groups that share a warp take the same number of turns (shuffles)
-        for (int rw = r0 + grp - sub; rw < r1; rw += G, cur.advance(Tq, gq, gr)) {
-            issue(s_iss);
-            s_iss = s_iss + 1 == S ? 0 : s_iss + 1;
-            cp_async_wait<S - 1>();  // this thread's copies of the row have landed
+        for (int rw = r0 + grp - sub; rw < r1; rw += G) {
+            const RelposRow w = next;
             const bool valid = rw + sub < r1;
-            const RelposRow w = relpos_row<AL, V>(p, cur, h, valid, mask != nullptr,
-                                                  windows ? wtab : nullptr, b0, phase);
+            issue(turn ^ 1);
+            cp_async_wait<1>();  // this thread's copies of the row have landed
             const int lo = w.lo, hi = w.hi, j_lane = lane * V - w.s;
             const int wj = (TPR > 32 ? (lane & ~31) * V : 0) - w.s;
             constexpr int WK = TW * V;
@@ -779,7 +791,7 @@ relpos_bw_vec(T *dinp, float *part, const T *dout, const T *y, const T *mask,
             for (int k = 0; k < CPT; ++k) {
                 const int j0 = k * TPR * V + j_lane;
                 if (!(k * TPR * V + wj < hi && k * TPR * V + wj + WK > lo)) continue;
-                const uint4 *slot = &stage[(s_cur * CPT + k) * 2 * n];
+                const uint4 *slot = &stage[(turn * CPT + k) * 2 * n];
                 yr[k] = slot[0];
                 gr4[k] = slot[n];
                 if (mrow || j0 < lo || j0 + V > hi) {
@@ -806,62 +818,73 @@ relpos_bw_vec(T *dinp, float *part, const T *dout, const T *y, const T *mask,
                     0xffffffffu, valid ? (sub / 4) * 4 + (x_lane & 3) : 32 + sub);
                 rank = __popc(same & ((1u << (sub * TPR)) - 1u)) / TPR;
             }
-            for (int go = 0;; ++go) {
+            auto dz_of = [&](int k, float2(&dz)[H2]) {
+                float2 yv[H2], gv[H2];
+                unpack2<T>(yr[k], yv);
+                unpack2<T>(gr4[k], gv);
 #pragma unroll
-                for (int k = 0; k < CPT; ++k) {
-                    const int j0 = k * TPR * V + j_lane;
-                    uint4 o = make_uint4(0u, 0u, 0u, 0u);
-                    if (k * TPR * V + wj < hi && k * TPR * V + wj + WK > lo) {
-                        float2 yv[H2], gv[H2], dz[H2], dx[H2];
-                        unpack2<T>(yr[k], yv);
-                        unpack2<T>(gr4[k], gv);
+                for (int h2 = 0; h2 < H2; ++h2) dz[h2] = mul2(yv[h2], add2(gv[h2], f2(-s)));
+                if (!(fabsf(s) < INFINITY)) {  // 0 * NaN: invisible keys stay 0
+                    const uint32_t bits =
+                        relpos_bits<T>(mrow, k * TPR * V + j_lane, lo, hi);
 #pragma unroll
-                        for (int h2 = 0; h2 < H2; ++h2)
-                            dz[h2] = mul2(yv[h2], add2(gv[h2], f2(-s)));
-                        if (!(fabsf(s) < INFINITY)) {  // 0 * NaN: invisible keys stay 0
-                            const uint32_t bits = relpos_bits<T>(mrow, j0, lo, hi);
+                    for (int h2 = 0; h2 < H2; ++h2) {
+                        if (!((bits >> (2 * h2)) & 1u)) dz[h2].x = 0.f;
+                        if (!((bits >> (2 * h2 + 1)) & 1u)) dz[h2].y = 0.f;
+                    }
+                }
+            };
+            auto add = [&](int k, const float2(&dz)[H2]) {
+                const int d0 = k * TPR * V + j_lane - w.q;
+                if (d0 <= -p.R - V + 1) {
 #pragma unroll
-                            for (int h2 = 0; h2 < H2; ++h2) {
-                                if (!((bits >> (2 * h2)) & 1u)) dz[h2].x = 0.f;
-                                if (!((bits >> (2 * h2 + 1)) & 1u)) dz[h2].y = 0.f;
-                            }
-                        }
+                    for (int h2 = 0; h2 < H2; ++h2) lo2 = add2(lo2, dz[h2]);
+                } else if (d0 >= p.R) {
 #pragma unroll
-                        for (int h2 = 0; h2 < H2; ++h2) dx[h2] = mul2(dz[h2], f2(p.scale));
-                        o = pack2<T>(dx);
+                    for (int h2 = 0; h2 < H2; ++h2) hi2 = add2(hi2, dz[h2]);
+                } else {
+                    float4 *at = acc_row + (x_lane >> 2) + k * (TPR * V / 4);
+                    float4 a[H2 / 2];
+#pragma unroll
+                    for (int h2 = 0; h2 < H2 / 2; ++h2) a[h2] = at[h2];
+#pragma unroll
+                    for (int h2 = 0; h2 < H2 / 2; ++h2) {
+                        const float2 u = add2(make_float2(a[h2].x, a[h2].y), dz[2 * h2]);
+                        const float2 t = add2(make_float2(a[h2].z, a[h2].w), dz[2 * h2 + 1]);
+                        at[h2] = make_float4(u.x, u.y, t.x, t.y);
+                    }
+                }
+            };
+#pragma unroll
+            for (int k = 0; k < CPT; ++k) {
+                const int j0 = k * TPR * V + j_lane;
+                uint4 o = make_uint4(0u, 0u, 0u, 0u);
+                if (k * TPR * V + wj < hi && k * TPR * V + wj + WK > lo) {
+                    float2 dz[H2], dx[H2];
+                    dz_of(k, dz);
+#pragma unroll
+                    for (int h2 = 0; h2 < H2; ++h2) dx[h2] = mul2(dz[h2], f2(p.scale));
+                    o = pack2<T>(dx);
+                    if (rank == 0 && j0 < hi && j0 + V > lo) add(k, dz);
+                }
+                if (valid && j0 < Tk) relpos_store<T, AL>(dinp + w.off, j0, Tk, o);
+            }
+            if constexpr (TPR <= 32) __syncwarp();
+            if constexpr (TPR < 32) {
+#pragma unroll 1
+                for (int go = 1; __any_sync(0xffffffffu, rank >= go); ++go) {
+#pragma unroll
+                    for (int k = 0; k < CPT; ++k) {
+                        const int j0 = k * TPR * V + j_lane;
                         if (rank == go && j0 < hi && j0 + V > lo) {
-                            const int d0 = j0 - w.q;
-                            if (d0 <= -p.R - V + 1) {
-#pragma unroll
-                                for (int h2 = 0; h2 < H2; ++h2) lo2 = add2(lo2, dz[h2]);
-                            } else if (d0 >= p.R) {
-#pragma unroll
-                                for (int h2 = 0; h2 < H2; ++h2) hi2 = add2(hi2, dz[h2]);
-                            } else {
-                                float4 *at = acc_row + (x_lane >> 2) + k * (TPR * V / 4);
-                                float4 a[H2 / 2];
-#pragma unroll
-                                for (int h2 = 0; h2 < H2 / 2; ++h2) a[h2] = at[h2];
-#pragma unroll
-                                for (int h2 = 0; h2 < H2 / 2; ++h2) {
-                                    const float2 u =
-                                        add2(make_float2(a[h2].x, a[h2].y), dz[2 * h2]);
-                                    const float2 t =
-                                        add2(make_float2(a[h2].z, a[h2].w), dz[2 * h2 + 1]);
-                                    at[h2] = make_float4(u.x, u.y, t.x, t.y);
-                                }
-                            }
+                            float2 dz[H2];
+                            dz_of(k, dz);
+                            add(k, dz);
                         }
                     }
-                    if (go == 0 && valid && j0 < Tk)
-                        relpos_store<T, AL>(dinp + w.off, j0, Tk, o);
+                    __syncwarp();
                 }
-                if constexpr (TPR > 32) break;
-                __syncwarp();
-                if constexpr (TPR == 32) break;
-                if (!__any_sync(0xffffffffu, rank > go)) break;
             }
-            s_cur = s_cur + 1 == S ? 0 : s_cur + 1;
         }
         cp_async_wait<0>();  // (only empty groups are left)
         // the block's sum of each distance: entries of all arrays and copies
