@@ -743,29 +743,31 @@ relpos_bw_vec(T *dinp, float *part, const T *dout, const T *y, const T *mask,
         if (windows) __syncthreads();
         int r_issue = r0 + grp;
         RelposCursor ci(p, h, r_issue);
-        RelposRow next;  // the row issued last
+        RelposRow next;  // the row issued last, and bit k: the thread's chunk k has a visible
+        uint32_t next_see, next_edge;  // key (see), and an invisible one by the window (edge)
         auto issue = [&](int s) {
             next = relpos_row<AL, V>(p, ci, r_issue < r1, mask != nullptr,
                                      windows ? wtab : nullptr, b0, phase);
-            if (r_issue < r1) {
+            next_see = next_edge = 0u;
 #pragma unroll
-                for (int k = 0; k < CPT; ++k) {
-                    const int j0 = (k * TPR + lane) * V - next.s;
-                    if (j0 < next.hi && j0 + V > next.lo) {
-                        const int64_t at = next.off + j0;
-                        uint4 *slot = &stage[(s * CPT + k) * 2 * n];
-                        if (AL || (at >= 0 && at + V <= total)) {
-                            cp_async16(slot, y + at);
-                            cp_async16(slot + n, dout + at);
-                        } else {
-                            slot[0] = relpos_load<T, AL>(y, at, total);
-                            slot[n] = relpos_load<T, AL>(dout, at, total);
-                        }
+            for (int k = 0; k < CPT; ++k) {
+                const int j0 = (k * TPR + lane) * V - next.s;
+                if (j0 < next.hi && j0 + V > next.lo) {
+                    next_see |= 1u << k;
+                    if (j0 < next.lo || j0 + V > next.hi) next_edge |= 1u << k;
+                    const int64_t at = next.off + j0;
+                    uint4 *slot = &stage[(s * CPT + k) * 2 * n];
+                    if (AL || (at >= 0 && at + V <= total)) {
+                        cp_async16(slot, y + at);
+                        cp_async16(slot + n, dout + at);
+                    } else {
+                        slot[0] = relpos_load<T, AL>(y, at, total);
+                        slot[n] = relpos_load<T, AL>(dout, at, total);
                     }
                 }
-                r_issue += G;
-                ci.advance(Tq, step);
             }
+            r_issue += G;
+            ci.advance(Tq, step);
             cp_async_commit();
         };
         issue(0);
@@ -777,53 +779,53 @@ relpos_bw_vec(T *dinp, float *part, const T *dout, const T *y, const T *mask,
         // groups that share a warp take the same number of turns (shuffles)
         for (int rw = r0 + grp - sub; rw < r1; rw += G) {
             const RelposRow w = next;
+            const uint32_t see = next_see, edge = next_edge;
             const bool valid = rw + sub < r1;
             issue(turn ^ 1);
             cp_async_wait<1>();  // this thread's copies of the row have landed
             const int lo = w.lo, hi = w.hi, j_lane = lane * V - w.s;
-            const int wj = (TPR > 32 ? (lane & ~31) * V : 0) - w.s;
-            constexpr int WK = TW * V;
             const T *mrow = w.b >= 0 ? mask + (int64_t)w.b * Tk : nullptr;
 
-            uint4 yr[CPT], gr4[CPT];
+            // y and dout of chunk k, 0 at invisible keys
+            auto load = [&](int k, float2(&yv)[H2], float2(&gv)[H2]) {
+                const uint4 *slot = &stage[(turn * CPT + k) * 2 * n];
+                uint4 yr = slot[0], gr4 = slot[n];
+                if (mrow || ((edge >> k) & 1u)) {
+                    const uint32_t bits = relpos_bits<T>(mrow, k * TPR * V + j_lane, lo, hi);
+                    keep_elements<T>(yr, bits);
+                    keep_elements<T>(gr4, bits);
+                }
+                unpack2<T>(yr, yv);
+                unpack2<T>(gr4, gv);
+            };
+            float2 yv[CPT][H2], gv[CPT][H2];
             float2 s2 = f2(0.f);
 #pragma unroll
             for (int k = 0; k < CPT; ++k) {
-                const int j0 = k * TPR * V + j_lane;
-                if (!(k * TPR * V + wj < hi && k * TPR * V + wj + WK > lo)) continue;
-                const uint4 *slot = &stage[(turn * CPT + k) * 2 * n];
-                yr[k] = slot[0];
-                gr4[k] = slot[n];
-                if (mrow || j0 < lo || j0 + V > hi) {
-                    const uint32_t bits = relpos_bits<T>(mrow, j0, lo, hi);
-                    keep_elements<T>(yr[k], bits);
-                    keep_elements<T>(gr4[k], bits);
-                }
-                float2 yv[H2], gv[H2];
-                unpack2<T>(yr[k], yv);
-                unpack2<T>(gr4[k], gv);
+                if (!((see >> k) & 1u)) continue;
+                load(k, yv[k], gv[k]);
 #pragma unroll
-                for (int h2 = 0; h2 < H2; ++h2) s2 = fma2(yv[h2], gv[h2], s2);
+                for (int h2 = 0; h2 < H2; ++h2) s2 = fma2(yv[k][h2], gv[k][h2], s2);
             }
             // the group's barrier also orders this row's additions after the
             // last row's; `red` alternates so that one barrier is enough
             const float s = relpos_reduce<TPR, 0, OpSum>(s2.x + s2.y, red[turn], grp);
-            turn ^= 1;
             const int x_lane = j_lane - w.q - band.first;  // entry of the lane's first key
             float4 *acc_row = mine + (x_lane & 3) * (band.stride / 4);
             // groups before this one with the same array and copy go first
             int rank = 0;
-            if constexpr (TPR < 32) {
-                const unsigned same = __match_any_sync(
-                    0xffffffffu, valid ? (sub / 4) * 4 + (x_lane & 3) : 32 + sub);
-                rank = __popc(same & ((1u << (sub * TPR)) - 1u)) / TPR;
-            }
-            auto dz_of = [&](int k, float2(&dz)[H2]) {
-                float2 yv[H2], gv[H2];
-                unpack2<T>(yr[k], yv);
-                unpack2<T>(gr4[k], gv);
+            if constexpr (TPR < 32 && !AL) {
+                const int copy = x_lane & 3;
 #pragma unroll
-                for (int h2 = 0; h2 < H2; ++h2) dz[h2] = mul2(yv[h2], add2(gv[h2], f2(-s)));
+                for (int d = 1; d < 4 && d < 32 / TPR; ++d) {
+                    const int other = __shfl_up_sync(0xffffffffu, copy, d * TPR);
+                    rank += sub % 4 >= d && other == copy;
+                }
+            }
+            auto dz_of = [&](int k, const float2(&yk)[H2], const float2(&gk)[H2],
+                             float2(&dz)[H2]) {
+#pragma unroll
+                for (int h2 = 0; h2 < H2; ++h2) dz[h2] = mul2(yk[h2], add2(gk[h2], f2(-s)));
                 if (!(fabsf(s) < INFINITY)) {  // 0 * NaN: invisible keys stay 0
                     const uint32_t bits =
                         relpos_bits<T>(mrow, k * TPR * V + j_lane, lo, hi);
@@ -859,32 +861,33 @@ relpos_bw_vec(T *dinp, float *part, const T *dout, const T *y, const T *mask,
             for (int k = 0; k < CPT; ++k) {
                 const int j0 = k * TPR * V + j_lane;
                 uint4 o = make_uint4(0u, 0u, 0u, 0u);
-                if (k * TPR * V + wj < hi && k * TPR * V + wj + WK > lo) {
+                if ((see >> k) & 1u) {
                     float2 dz[H2], dx[H2];
-                    dz_of(k, dz);
+                    dz_of(k, yv[k], gv[k], dz);
 #pragma unroll
                     for (int h2 = 0; h2 < H2; ++h2) dx[h2] = mul2(dz[h2], f2(p.scale));
                     o = pack2<T>(dx);
-                    if (rank == 0 && j0 < hi && j0 + V > lo) add(k, dz);
+                    if (rank == 0) add(k, dz);
                 }
                 if (valid && j0 < Tk) relpos_store<T, AL>(dinp + w.off, j0, Tk, o);
             }
             if constexpr (TPR <= 32) __syncwarp();
-            if constexpr (TPR < 32) {
+            if constexpr (TPR < 32 && !AL) {
 #pragma unroll 1
                 for (int go = 1; __any_sync(0xffffffffu, rank >= go); ++go) {
 #pragma unroll
                     for (int k = 0; k < CPT; ++k) {
-                        const int j0 = k * TPR * V + j_lane;
-                        if (rank == go && j0 < hi && j0 + V > lo) {
-                            float2 dz[H2];
-                            dz_of(k, dz);
+                        if (rank == go && ((see >> k) & 1u)) {
+                            float2 ya[H2], ga[H2], dz[H2];
+                            load(k, ya, ga);
+                            dz_of(k, ya, ga, dz);
                             add(k, dz);
                         }
                     }
                     __syncwarp();
                 }
             }
+            turn ^= 1;
         }
         cp_async_wait<0>();  // (only empty groups are left)
         // the block's sum of each distance: entries of all arrays and copies

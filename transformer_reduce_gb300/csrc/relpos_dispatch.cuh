@@ -149,7 +149,7 @@ cudaError_t launch_relpos_bw_rows(T *dinp, const T *dout, const T *y, const T *m
     int tpr = 0, cpt = 0;
     if (relpos_phase<T>(dout) == phase && relpos_phase<T>(dinp) == phase &&
         pick_relpos_bucket(p, V, phase, &tpr, &cpt)) {
-        const bool al = p.Tk % V == 0 && phase == 0;
+        const bool al = p.Tk % V == 0 && phase == 0 && p.Tq % 4 == 0;
         if (tpr < 4) {  // groups of one or two threads would need too many arrays
             cpt = (int)ceil_div(tpr * cpt, 4);
             tpr = 4;
