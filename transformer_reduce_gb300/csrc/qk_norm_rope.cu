@@ -22,26 +22,103 @@ static void qk_bw_split(int64_t tokens, int64_t Hq, int64_t Hk, int64_t &nq, int
 }
 
 int64_t qk_bw_parts(int64_t tokens, int64_t Hq, int64_t Hk) {
-    if (tokens <= 0) return 0;
-    int64_t nq, nk;
-    qk_bw_split(tokens, Hq, Hk, nq, nk);
-    return nq + nk;
+    return tokens > 0 && Hq + Hk > 0 ? kQkBwBlocks + 1 : 0;
+}
+
+// Whether every head is a whole number of 16-byte vectors, partners included,
+// at 16-byte addresses, and the angles of a vector lie at 8-byte ones.
+template <typename T>
+static bool qk_side_vec(const QkSide<T> &s) {
+    const auto bits = reinterpret_cast<uintptr_t>(s.out) | reinterpret_cast<uintptr_t>(s.x) |
+                      reinterpret_cast<uintptr_t>(s.dout) | reinterpret_cast<uintptr_t>(s.gamma);
+    const int64_t strides = s.x_stride | s.out_stride | s.dout_stride;
+    return s.heads == 0 || (bits % 16 == 0 && strides % Traits<T>::kVec == 0);
+}
+template <typename T>
+static int qk_lanes_vec(const QkSide<T> &q, const QkSide<T> &k, const QkRope &r) {
+    constexpr int V = Traits<T>::kVec;
+    const auto angles = reinterpret_cast<uintptr_t>(r.cos) | reinterpret_cast<uintptr_t>(r.sin);
+    if (r.D % V || r.rot % (r.interleaved ? V : 2 * V) || angles % 8 || !qk_side_vec(q) ||
+        !qk_side_vec(k) || q.heads + k.heads > (1 << 24))
+        return 0;
+    int lanes = 2;
+    while (lanes < qk_lanes(r.D, r.rot, V, r.interleaved)) lanes *= 2;
+    return lanes <= 32 ? lanes : 0;
+}
+
+#define LSR_QK_LANES(X) X(2) X(4) X(8) X(16) X(32)
+
+template <typename T, int LPR, bool INTER>
+static cudaError_t launch_qk_fw_vec(const QkSide<T> &q, const QkSide<T> &k, const QkRope &r,
+                                    cudaStream_t st) {
+    constexpr int RPW = 32 / LPR;
+    const int ngq = (int)ceil_div(q.heads, RPW), ngk = (int)ceil_div(k.heads, RPW);
+    // as many groups of a token per warp as leave a warp for every warp slot
+    // (three blocks of eight on each SM)
+    const int64_t slots = (int64_t)device_sm_count() * 24;
+    int64_t per_item = r.tokens * (ngq + ngk) / slots;
+    per_item = per_item < 1 ? 1 : (per_item > ngq + ngk ? ngq + ngk : per_item);
+    const int64_t items = r.tokens * ceil_div(ngq + ngk, per_item);
+    return launch_persistent<qk_fw_vec<T, LPR, INTER>>(256, 0, ceil_div(items, 8), st, q, k, r,
+                                                       ngq, ngk, (int)per_item);
 }
 
 template <typename T>
 cudaError_t launch_qk_fw(QkSide<T> q, QkSide<T> k, QkRope r, cudaStream_t st) {
+    const int lanes = qk_lanes_vec(q, k, r);
+#define X(L)                                                                        \
+    if (lanes == L)                                                                 \
+        return r.interleaved ? launch_qk_fw_vec<T, L, true>(q, k, r, st)            \
+                             : launch_qk_fw_vec<T, L, false>(q, k, r, st);
+    LSR_QK_LANES(X)
+#undef X
     const int64_t rows = r.tokens * (q.heads + k.heads);
     return launch_persistent<qk_fw_loop<T>>(256, 0, ceil_div(rows, 8), st, q, k, r);
+}
+
+// Blocks of the vector kernel: two on each SM, in proportion to the sides'
+// groups of heads, each side with at most one block per eight tokens.
+static void qk_bw_vec_split(int64_t tokens, int64_t gq, int64_t gk, int64_t &nq, int64_t &nk) {
+    constexpr int64_t blocks = 2 * 152;
+    static_assert(blocks <= kQkBwBlocks, "the workspace holds kQkBwBlocks parts");
+    nq = blocks * gq / (gq + gk);
+    if (gq > 0 && nq < 1) nq = 1;
+    if (gk > 0 && nq > blocks - 1) nq = blocks - 1;
+    nk = gk > 0 ? blocks - nq : 0;
+    const int64_t most = ceil_div(tokens, 8);
+    if (nq > most) nq = most;
+    if (nk > most) nk = most;
+}
+
+template <typename T, int LPR, bool INTER>
+static cudaError_t launch_qk_bw_vec(const QkSide<T> &q, const QkSide<T> &k, const QkRope &r,
+                                    float *part, int64_t &nq, int64_t &nk, cudaStream_t st) {
+    constexpr int RPW = 32 / LPR;
+    qk_bw_vec_split(r.tokens, ceil_div(q.heads, RPW), ceil_div(k.heads, RPW), nq, nk);
+    return launch_pdl(qk_bw_vec<T, LPR, INTER>, dim3((unsigned)(nq + nk)), dim3(256), 0, st, q, k,
+                      r, part, (int)nq);
+}
+
+template <typename T>
+static cudaError_t launch_qk_bw_rows(const QkSide<T> &q, const QkSide<T> &k, const QkRope &r,
+                                     float *part, int64_t &nq, int64_t &nk, cudaStream_t st) {
+    const int lanes = qk_lanes_vec(q, k, r);
+#define X(L)                                                                               \
+    if (lanes == L)                                                                        \
+        return r.interleaved ? launch_qk_bw_vec<T, L, true>(q, k, r, part, nq, nk, st)      \
+                             : launch_qk_bw_vec<T, L, false>(q, k, r, part, nq, nk, st);
+    LSR_QK_LANES(X)
+#undef X
+    qk_bw_split(r.tokens, q.heads, k.heads, nq, nk);
+    return launch_pdl(qk_bw_loop<T>, dim3((unsigned)(nq + nk)), dim3(256), (size_t)8 * r.D * 4, st,
+                      q, k, r, part, (int)nq);
 }
 
 template <typename T>
 cudaError_t launch_qk_bw(QkSide<T> q, QkSide<T> k, QkRope r, float *part, cudaStream_t st) {
     int64_t nq = 0, nk = 0;
     if (r.tokens > 0) {
-        qk_bw_split(r.tokens, q.heads, k.heads, nq, nk);
-        const cudaError_t e =
-            launch_pdl(qk_bw_loop<T>, dim3((unsigned)(nq + nk)), dim3(256),
-                       (size_t)8 * r.D * 4, st, q, k, r, part, (int)nq);
+        const cudaError_t e = launch_qk_bw_rows(q, k, r, part, nq, nk, st);
         if (e != cudaSuccess) return e;
     }
     return launch_pdl(qk_fold, dim3((unsigned)ceil_div(r.D, 32), 2), dim3(256), 0, st, q.dgamma,

@@ -163,6 +163,304 @@ qk_bw_loop(const QkSide<T> qs, const QkSide<T> ks, const QkRope r, float *part, 
     }
 }
 
+// ----------------------------------------------------------------------------
+// Heads of whole 16-byte vectors.  LPR lanes hold a head, two vectors each:
+//   halves       lane l < rot / 2V holds vectors l and l + rot / 2V, whose
+//                elements are each other's partners; the other lanes hold the
+//                unrotated vectors two by two;
+//   interleaved  lane l holds vectors 2l and 2l + 1, with their pairs inside.
+// Either way a lane needs V angles of its token's position, the same for every
+// head of the token: a warp takes one token, loads them once, and goes through
+// the heads of both sides, 32 / LPR at a time, the next heads' vectors loading
+// while it works on the current ones.
+// ----------------------------------------------------------------------------
+struct QkLane {
+    int va, vb;   // vectors
+    bool ha, hb;  // there are such vectors
+    bool ra, rb;  // they are rotated
+};
+template <int V, bool INTER>
+__device__ __forceinline__ QkLane qk_lane(const QkRope &r, int l) {
+    const int nv = r.D / V;
+    QkLane q;
+    if (INTER) {
+        q.va = 2 * l;
+        q.vb = 2 * l + 1;
+        q.ra = q.va * V < r.rot;
+        q.rb = q.vb * V < r.rot;
+    } else {
+        const int hv = r.rot / 2 / V;
+        q.ra = q.rb = l < hv;
+        q.va = q.ra ? l : 2 * l;
+        q.vb = q.ra ? l + hv : 2 * l + 1;
+    }
+    q.ha = q.va < nv;
+    q.hb = q.vb < nv;
+    return q;
+}
+// Lanes that hold a head (INTER as above).
+inline int qk_lanes(int D, int rot, int V, bool inter) {
+    const int nv = D / V, hv = inter ? 0 : rot / 2 / V;
+    return hv + (nv - 2 * hv + 1) / 2;
+}
+
+// Cosines and sines of the lane's V angles (1 and 0 where nothing is rotated).
+template <int V, bool INTER>
+__device__ __forceinline__ void qk_angles(const QkRope &r, const QkLane &q, int64_t tok,
+                                          float (&c)[V], float (&s)[V]) {
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+        c[e] = 1.f;
+        s[e] = 0.f;
+    }
+    if (!q.ra) return;  // (vector vb is rotated only if va is)
+    const int64_t pos = __ldg(r.positions + tok);
+    const int half = r.rot / 2;
+    if (pos < 0 || pos >= r.max_pos) {
+#pragma unroll
+        for (int e = 0; e < V; ++e) c[e] = s[e] = __int_as_float(0x7fc00000);
+        return;
+    }
+    const float *cp = r.cos + pos * half + (INTER ? q.va * (V / 2) : q.va * V);
+    const float *sp = r.sin + pos * half + (INTER ? q.va * (V / 2) : q.va * V);
+    // interleaved: vector vb = va + 1 takes the V / 2 angles after va's
+    const int n = INTER && !q.rb ? V / 2 : V;
+#pragma unroll
+    for (int e = 0; e < V; e += 2) {
+        if (e < n) {
+            const float2 cv = __ldg(reinterpret_cast<const float2 *>(cp + e));
+            const float2 sv = __ldg(reinterpret_cast<const float2 *>(sp + e));
+            c[e] = cv.x;
+            c[e + 1] = cv.y;
+            s[e] = sv.x;
+            s[e + 1] = sv.y;
+        }
+    }
+}
+
+// Rotates the lane's two vectors (SIGN -1: back).
+template <int V, bool INTER>
+__device__ __forceinline__ void qk_turn(const QkLane &q, const float (&c)[V], const float (&s)[V],
+                                        float sign, float (&a)[V], float (&b)[V]) {
+    if (!q.ra) return;
+    if (INTER) {
+#pragma unroll
+        for (int e = 0; e < V / 2; ++e) {
+            const float se = sign * s[e], x = a[2 * e], y = a[2 * e + 1];
+            a[2 * e] = x * c[e] - y * se;
+            a[2 * e + 1] = y * c[e] + x * se;
+        }
+        if (q.rb) {
+#pragma unroll
+            for (int e = 0; e < V / 2; ++e) {
+                const float ce = c[V / 2 + e], se = sign * s[V / 2 + e];
+                const float x = b[2 * e], y = b[2 * e + 1];
+                b[2 * e] = x * ce - y * se;
+                b[2 * e + 1] = y * ce + x * se;
+            }
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            const float se = sign * s[e], x = a[e], y = b[e];
+            a[e] = x * c[e] - y * se;
+            b[e] = y * c[e] + x * se;
+        }
+    }
+}
+
+// Sum over the LPR lanes of a head.
+template <int LPR>
+__device__ __forceinline__ float qk_sum(float v) {
+#pragma unroll
+    for (int o = LPR / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+// A group is the 32 / LPR heads of one side that a warp takes at once; an item
+// is up to `per_item` groups of one token (all of them, unless that would
+// leave too few items for the GPU).  ngq, ngk: groups of the two sides.
+template <typename T, int LPR, bool INTER>
+__global__ void __launch_bounds__(256, 3)
+qk_fw_vec(const QkSide<T> qs, const QkSide<T> ks, const QkRope r, int ngq, int ngk, int per_item) {
+    pdl_begin();
+    using Tr = Traits<T>;
+    constexpr int V = Tr::kVec;
+    constexpr int RPW = 32 / LPR;
+    const int lane = threadIdx.x & 31, l = lane % LPR, sub = lane / LPR;
+    const QkLane q = qk_lane<V, INTER>(r, l);
+    const int ng = ngq + ngk, per_token = (ng + per_item - 1) / per_item;
+    const int64_t items = r.tokens * per_token;
+    const float invD = 1.f / (float)r.D;
+    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+    for (int64_t item = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); item < items;
+         item += (int64_t)gridDim.x * 8) {
+        const int64_t tok = per_token == 1 ? item : item / per_token;
+        const int f0 = (int)(item - tok * per_token) * per_item, f1 = min(f0 + per_item, ng);
+        uint4 ra = zero, rb = zero;
+        auto load = [&](int f) {
+            const bool isq = f < ngq;
+            const int h = (isq ? f : f - ngq) * RPW + sub;
+            ra = rb = zero;
+            if (h < (isq ? qs.heads : ks.heads)) {
+                const T *x = (isq ? qs.x + tok * qs.x_stride : ks.x + tok * ks.x_stride) +
+                             (int64_t)h * r.D;
+                if (q.ha) ra = ld_stream16(x + q.va * V);
+                if (q.hb) rb = ld_stream16(x + q.vb * V);
+            }
+        };
+        load(f0);
+        float c[V], s[V];
+        qk_angles<V, INTER>(r, q, tok, c, s);
+        for (int f = f0; f < f1; ++f) {
+            const bool isq = f < ngq;
+            const QkSide<T> &sd = isq ? qs : ks;
+            const int h = (isq ? f : f - ngq) * RPW + sub;
+            float a[V], b[V], ga[V], gb[V];
+            Tr::unpack(ra, a);
+            Tr::unpack(rb, b);
+            const uint4 wa = q.ha ? ld_cached16(sd.gamma + q.va * V) : zero;
+            const uint4 wb = q.hb ? ld_cached16(sd.gamma + q.vb * V) : zero;
+            if (f + 1 < f1) load(f + 1);
+            float ss = 0.f;
+#pragma unroll
+            for (int e = 0; e < V; ++e) ss = fmaf(a[e], a[e], fmaf(b[e], b[e], ss));
+            ss = qk_sum<LPR>(ss);
+            const float rstd = 1.f / sqrtf(fmaf(ss, invD, r.eps));
+            Tr::unpack(wa, ga);
+            Tr::unpack(wb, gb);
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                a[e] *= rstd * ga[e];
+                b[e] *= rstd * gb[e];
+            }
+            qk_turn<V, INTER>(q, c, s, 1.f, a, b);
+            if (h < sd.heads) {
+                T *o = sd.out + tok * sd.out_stride + (int64_t)h * r.D;
+                if (q.ha) st_stream16(o + q.va * V, Tr::pack(a));
+                if (q.hb) st_stream16(o + q.vb * V, Tr::pack(b));
+                if (l == 0 && sd.rstd_out) sd.rstd_out[tok * sd.heads + h] = rstd;
+            }
+        }
+    }
+}
+
+// Backward.  Blocks b < q_blocks work on query heads, the others on key heads,
+// so that a lane has the gamma gradients of its 2V features of one side in
+// registers; they are added over a warp's heads by shuffles and over the
+// block's warps in shared memory at the end.  ng: groups of a token, by side.
+template <typename T, int LPR, bool INTER>
+__global__ void __launch_bounds__(256, 2)
+qk_bw_vec(const QkSide<T> qs, const QkSide<T> ks, const QkRope r, float *part, int q_blocks) {
+    pdl_begin();
+    using Tr = Traits<T>;
+    constexpr int V = Tr::kVec;
+    constexpr int RPW = 32 / LPR;
+    __shared__ float sum[8][LPR * 2 * V + 1];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane % LPR, sub = lane / LPR;
+    const QkLane q = qk_lane<V, INTER>(r, l);
+    const bool isq = (int)blockIdx.x < q_blocks;
+    const QkSide<T> &sd = isq ? qs : ks;
+    const int64_t nblk = isq ? q_blocks : (int)gridDim.x - q_blocks;
+    const int64_t blk = isq ? blockIdx.x : (int)blockIdx.x - q_blocks;
+    const int heads = (int)sd.heads, ng = (heads + RPW - 1) / RPW;
+    const float invD = 1.f / (float)r.D;
+    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+    const uint4 wa = q.ha ? ld_cached16(sd.gamma + q.va * V) : zero;
+    const uint4 wb = q.hb ? ld_cached16(sd.gamma + q.vb * V) : zero;
+    float da[V], db[V];  // gamma gradients
+#pragma unroll
+    for (int e = 0; e < V; ++e) da[e] = db[e] = 0.f;
+    for (int64_t tok = blk * 8 + warp; tok < r.tokens; tok += nblk * 8) {
+        uint4 xa, xb, ya, yb;
+        float rs;
+        auto load = [&](int f) {
+            const int h = f * RPW + sub;
+            xa = xb = ya = yb = zero;
+            rs = 0.f;
+            if (h < heads) {
+                const T *x = sd.x + tok * sd.x_stride + (int64_t)h * r.D;
+                const T *dy = sd.dout + tok * sd.dout_stride + (int64_t)h * r.D;
+                rs = __ldg(sd.rstd + tok * heads + h);
+                if (q.ha) {
+                    xa = ld_stream16(x + q.va * V);
+                    ya = ld_stream16(dy + q.va * V);
+                }
+                if (q.hb) {
+                    xb = ld_stream16(x + q.vb * V);
+                    yb = ld_stream16(dy + q.vb * V);
+                }
+            }
+        };
+        load(0);
+        float c[V], s[V];
+        qk_angles<V, INTER>(r, q, tok, c, s);
+        for (int f = 0; f < ng; ++f) {
+            const int h = f * RPW + sub;
+            float a[V], b[V], g[V], x[V], u[V];
+            const float rstd = rs;
+            Tr::unpack(ya, a);
+            Tr::unpack(yb, b);
+            qk_turn<V, INTER>(q, c, s, -1.f, a, b);  // dn
+            Tr::unpack(xa, x);
+            Tr::unpack(xb, u);
+            if (f + 1 < ng) load(f + 1);
+            float t = 0.f;
+            Tr::unpack(wa, g);
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                x[e] *= rstd;  // xhat
+                da[e] = fmaf(a[e], x[e], da[e]);
+                a[e] *= g[e];
+                t = fmaf(a[e], x[e], t);
+            }
+            Tr::unpack(wb, g);
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                u[e] *= rstd;
+                db[e] = fmaf(b[e], u[e], db[e]);
+                b[e] *= g[e];
+                t = fmaf(b[e], u[e], t);
+            }
+            t = qk_sum<LPR>(t) * invD;
+            if (h < heads) {
+                T *dx = sd.out + tok * sd.out_stride + (int64_t)h * r.D;
+#pragma unroll
+                for (int e = 0; e < V; ++e) {
+                    a[e] = rstd * fmaf(-x[e], t, a[e]);
+                    b[e] = rstd * fmaf(-u[e], t, b[e]);
+                }
+                if (q.ha) st_stream16(dx + q.va * V, Tr::pack(a));
+                if (q.hb) st_stream16(dx + q.vb * V, Tr::pack(b));
+            }
+        }
+    }
+    // the warp's heads: lanes l of all subs; then the block's warps
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+#pragma unroll
+        for (int o = 16; o >= LPR; o >>= 1) {
+            da[e] += __shfl_xor_sync(0xffffffffu, da[e], o);
+            db[e] += __shfl_xor_sync(0xffffffffu, db[e], o);
+        }
+        if (sub == 0) {
+            sum[warp][l * 2 * V + e] = da[e];
+            sum[warp][l * 2 * V + V + e] = db[e];
+        }
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < LPR * 2 * V; i += 256) {
+        const QkLane w = qk_lane<V, INTER>(r, i / (2 * V));
+        const bool second = i % (2 * V) >= V;
+        if (second ? w.hb : w.ha) {
+            float v = sum[0][i];
+#pragma unroll
+            for (int k = 1; k < 8; ++k) v += sum[k][i];
+            part[(int64_t)blockIdx.x * r.D + (second ? w.vb : w.va) * V + i % V] = v;
+        }
+    }
+}
+
 // dgamma of both sides: the blocks' sums added in order.  blockIdx.y: side.
 __global__ void __launch_bounds__(256)
 qk_fold(float *dgq, float *dgk, const float *part, int D, int q_blocks, int blocks) {
