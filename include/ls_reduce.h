@@ -568,6 +568,9 @@ ls_status ls_qk_norm_rope_bw(void *dq, void *dk, float *dgamma_q, float *dgamma_
                              int64_t q_stride, int64_t k_stride, int interleaved, void *workspace,
                              size_t workspace_bytes, ls_dtype dt, void *stream);
 
+/* Most elements of a list of gradients. */
+#define LS_MAX_GRAD_ELEMENTS ((int64_t)1 << 40)
+
 /*
  * Bytes of device workspace ls_grad_norm and ls_grad_clip need for a list of
  * `count` tensors, whatever their sizes.  Host-only; launches nothing.
@@ -591,8 +594,8 @@ size_t ls_grad_norm_workspace_size(int64_t count);
  *           bytes, 16-byte aligned, contents ignored; may be NULL for an
  *           empty list.  Calls that overlap on the GPU must not share it.
  * Errors: LS_ERR_INVALID_ARG for NULL pointers, negative counts or sizes;
- * LS_ERR_UNSUPPORTED for an unknown dtype; LS_ERR_MISALIGNED;
- * LS_ERR_WORKSPACE; LS_ERR_CUDA.
+ * LS_ERR_UNSUPPORTED for an unknown dtype or more than LS_MAX_GRAD_ELEMENTS;
+ * LS_ERR_MISALIGNED; LS_ERR_WORKSPACE; LS_ERR_CUDA.
  */
 ls_status ls_grad_norm(float *norm, const void *const *grads, const int64_t *sizes,
                        const int32_t *dtypes, int64_t count, void *workspace,

@@ -10,8 +10,10 @@ if the library is missing or a call fails, they raise.
 """
 from __future__ import annotations
 
-import ctypes
+import array
+import operator
 
+from . import _lib as _lib_module
 from ._lib import (LS_BF16, LS_ERR_CUDA, ls_cross_entropy_bw, ls_cross_entropy_fw,
                    ls_softmax_bw_masked_scaled, ls_softmax_fw_scaled, LS_ERR_INVALID_ARG, LS_ERR_MISALIGNED,  # noqa: F401
                    LS_ERR_UNSUPPORTED, LS_ERR_WORKSPACE, LS_F16, LS_F32, LS_OK, LsError,
@@ -42,17 +44,29 @@ __all__ = [
 ]
 
 
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
+
+
+_DTYPE_CODES = {}
 
 
 def ls_dtype(t) -> int:
-    torch = _torch()
-    m = {torch.float32: LS_F32, torch.float16: LS_F16, torch.bfloat16: LS_BF16}
-    if t.dtype not in m:
+    if not _DTYPE_CODES:
+        torch = _torch()
+        _DTYPE_CODES.update({torch.float32: LS_F32, torch.float16: LS_F16,
+                             torch.bfloat16: LS_BF16})
+    code = _DTYPE_CODES.get(t.dtype)
+    if code is None:
         raise TypeError(f"unsupported storage dtype {t.dtype} (float32, float16, bfloat16)")
-    return m[t.dtype]
+    return code
 
 
 def _stream(t) -> int:
@@ -83,7 +97,7 @@ def _want(name, t, shape, dtype):
     read or write through its pointer (they trust the sizes they are given)."""
     if t is None:
         return
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
+    if t.shape != shape or t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype} of shape {list(shape)}, "
                          f"got {t.dtype} of shape {list(t.shape)}")
 
@@ -112,6 +126,41 @@ def _call(where: str, dev, fn, *args):
         return
     with torch.cuda.device(dev):
         _ok(fn(*args), where)
+
+
+def _same_device(*ts):
+    """The index of the one CUDA device of all given tensors (None skipped), all
+    contiguous; as _dev, in one call per tensor and property."""
+    index = -1
+    for t in ts:
+        if t is not None:
+            i = t.get_device()
+            if i < 0 or (index >= 0 and i != index) or not t.is_contiguous():
+                return _dev(*ts).index  # says which of them is wrong
+            index = i
+    return index
+
+
+def _launch(where: str, index: int, *args):
+    """Calls the library on device ``index``'s current stream, which is passed
+    after the given arguments, with that device current."""
+    torch = _torch()
+    fn = getattr(_lib_module._lib or load(), where)
+    if index == torch.cuda.current_device():
+        status = fn(*args, _raw_stream(index))
+    else:
+        with torch.cuda.device(index):
+            status = fn(*args, _raw_stream(index))
+    if status != LS_OK:
+        raise LsError(status, where)
+
+
+def _raw_stream(index: int) -> int:
+    """Handle of the current stream of device ``index`` (without building a
+    Stream object where torch can say it directly)."""
+    torch = _torch()
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return raw(index) if raw is not None else torch.cuda.current_stream(index).cuda_stream
 
 
 def _rows_hidden(x, name="x"):
@@ -406,18 +455,22 @@ def softmax_fw_relpos(scores, table, buckets, mask=None, causal: bool = False, s
     torch = _torch()
     if scores.dim() != 4:
         raise ValueError("scores must be [B, H, Tq, Tk]")
-    B, H, Tq, Tk = scores.shape
+    B, H, Tq, Tk = shape = scores.shape
+    dtype = scores.dtype
     if table.dim() != 2:
         raise ValueError("table must be [num_buckets, H]")
-    _want("table", table, (table.shape[0], H), scores.dtype)
+    nb = table.shape[0]
+    _want("table", table, (nb, H), dtype)
     R = _relpos(buckets)
-    _want("mask", mask, (B, Tk), scores.dtype)
-    _want("out", out, scores.shape, scores.dtype)
-    out = torch.empty_like(scores) if out is None else out
-    dev = _dev(scores, table, buckets, mask, out)
-    _call("ls_softmax_fw_relpos", dev, ls_softmax_fw_relpos, _ptr(out), _ptr(scores), _ptr(mask),
-          _ptr(table), _ptr(buckets), B, H, Tq, Tk, table.shape[0], R, causal,
-          1.0 if scale is None else float(scale), ls_dtype(scores), _stream(scores))
+    _want("mask", mask, (B, Tk), dtype)
+    if out is None:
+        out = torch.empty_like(scores)
+    else:
+        _want("out", out, shape, dtype)
+    dev = _same_device(scores, table, buckets, mask, out)
+    _launch("ls_softmax_fw_relpos", dev, _ptr(out), _ptr(scores), _ptr(mask), _ptr(table),
+            _ptr(buckets), B, H, Tq, Tk, nb, R, 1 if causal else 0,
+            1.0 if scale is None else float(scale), ls_dtype(scores))
     return out
 
 
@@ -446,12 +499,12 @@ def softmax_bw_relpos(dout, out_fw, buckets, num_buckets: int, mask=None, causal
     _workspace("workspace", workspace)
     dinp = torch.empty_like(dout) if dinp is None else dinp
     if dtable is None:
-        dtable = torch.empty(num_buckets, H, device=dout.device, dtype=torch.float32)
-    dev = _dev(dout, out_fw, buckets, mask, workspace, dinp, dtable)
-    _call("ls_softmax_bw_relpos", dev, ls_softmax_bw_relpos, _ptr(dinp), _ptr(dtable), _ptr(dout),
-          _ptr(out_fw), _ptr(mask), _ptr(buckets), B, H, Tq, Tk, num_buckets, R, causal,
-          1.0 if scale is None else float(scale), _ptr(workspace),
-          workspace.numel() * workspace.element_size(), ls_dtype(dout), _stream(dout))
+        dtable = dout.new_empty((num_buckets, H), dtype=torch.float32)
+    dev = _same_device(dout, out_fw, buckets, mask, workspace, dinp, dtable)
+    _launch("ls_softmax_bw_relpos", dev, _ptr(dinp), _ptr(dtable), _ptr(dout), _ptr(out_fw),
+            _ptr(mask), _ptr(buckets), B, H, Tq, Tk, num_buckets, R, 1 if causal else 0,
+            1.0 if scale is None else float(scale), _ptr(workspace),
+            workspace.numel() * 4, ls_dtype(dout))
     return dinp, dtable
 
 
@@ -506,21 +559,25 @@ def _rotation(cos, sin, positions, tokens, D):
         raise ValueError("cos, sin and positions go together")
     if cos.dim() != 2 or 2 * cos.shape[1] > D:
         raise ValueError(f"cos must be [max_pos, rot / 2] with rot <= {D}")
-    _want("cos", cos, cos.shape, torch.float32)
-    _want("sin", sin, cos.shape, torch.float32)
-    _want("positions", positions, (tokens,), torch.int32)
-    return 2 * cos.shape[1], cos.shape[0]
+    max_pos, half = shape = cos.shape
+    f32 = torch.float32
+    if cos.dtype != f32 or sin.dtype != f32 or sin.shape != shape or \
+            positions.dtype != torch.int32 or positions.shape != (tokens,):
+        _want("cos", cos, shape, f32)
+        _want("sin", sin, shape, f32)
+        _want("positions", positions, (tokens,), torch.int32)
+    return 2 * half, max_pos
 
 
 def _one_device(strided, dense):
-    """The one device of all tensors; the dense ones must be contiguous."""
-    dev = _dev(*dense)
+    """The one device (its index) of all tensors; the dense ones must be contiguous."""
+    index = _same_device(*dense)
     for t in strided:
-        if not t.is_cuda:
-            raise ValueError("tensors must live on a CUDA device (there is no CPU path)")
-        if t.device != dev:
-            raise ValueError(f"tensors on different devices ({dev} and {t.device})")
-    return dev
+        if t.get_device() != index:
+            if not t.is_cuda:
+                raise ValueError("tensors must live on a CUDA device (there is no CPU path)")
+            raise ValueError(f"tensors on different devices (cuda:{index} and {t.device})")
+    return index
 
 
 def qk_norm_rope_fw(q, k, gamma_q, gamma_k, cos=None, sin=None, positions=None,
@@ -536,26 +593,35 @@ def qk_norm_rope_fw(q, k, gamma_q, gamma_k, cos=None, sin=None, positions=None,
     torch = _torch()
     qs = _heads("q", q)
     tokens, Hq, D = q.shape
-    ks = _heads("k", k, tokens, D, q.dtype)
+    dtype = q.dtype
+    ks = _heads("k", k, tokens, D, dtype)
     Hk = k.shape[1]
-    _want("gamma_q", gamma_q, (D,), q.dtype)
-    _want("gamma_k", gamma_k, (D,), q.dtype)
+    _want("gamma_q", gamma_q, (D,), dtype)
+    _want("gamma_k", gamma_k, (D,), dtype)
     rot, max_pos = _rotation(cos, sin, positions, tokens, D)
-    _want("q_rstd", q_rstd, (tokens, Hq), torch.float32)
-    _want("k_rstd", k_rstd, (tokens, Hk), torch.float32)
-    new = dict(device=q.device, dtype=q.dtype)
-    q_out = torch.empty((tokens, Hq, D), **new) if q_out is None else q_out
-    k_out = torch.empty((tokens, Hk, D), **new) if k_out is None else k_out
-    qos, kos = _like_heads("q_out", q_out, q), _like_heads("k_out", k_out, k)
-    new["dtype"] = torch.float32
-    q_rstd = torch.empty((tokens, Hq), **new) if q_rstd is None else q_rstd
-    k_rstd = torch.empty((tokens, Hk), **new) if k_rstd is None else k_rstd
+    qos, kos = Hq * D, Hk * D
+    if q_out is None:
+        q_out = q.new_empty((tokens, Hq, D))
+    else:
+        qos = _like_heads("q_out", q_out, q)
+    if k_out is None:
+        k_out = k.new_empty((tokens, Hk, D))
+    else:
+        kos = _like_heads("k_out", k_out, k)
+    if q_rstd is None:
+        q_rstd = q.new_empty((tokens, Hq), dtype=torch.float32)
+    else:
+        _want("q_rstd", q_rstd, (tokens, Hq), torch.float32)
+    if k_rstd is None:
+        k_rstd = q.new_empty((tokens, Hk), dtype=torch.float32)
+    else:
+        _want("k_rstd", k_rstd, (tokens, Hk), torch.float32)
     dev = _one_device((q, k, q_out, k_out),
                       (gamma_q, gamma_k, cos, sin, positions, q_rstd, k_rstd))
-    _call("ls_qk_norm_rope_fw", dev, ls_qk_norm_rope_fw, _ptr(q_out), _ptr(k_out), _ptr(q_rstd),
-          _ptr(k_rstd), _ptr(q), _ptr(k), _ptr(gamma_q), _ptr(gamma_k), _ptr(cos), _ptr(sin),
-          _ptr(positions), tokens, Hq, Hk, D, rot, max_pos, qos, kos, qs, ks, interleaved,
-          float(eps), ls_dtype(q), _stream(q))
+    _launch("ls_qk_norm_rope_fw", dev, _ptr(q_out), _ptr(k_out), _ptr(q_rstd), _ptr(k_rstd),
+            _ptr(q), _ptr(k), _ptr(gamma_q), _ptr(gamma_k), _ptr(cos), _ptr(sin), _ptr(positions),
+            tokens, Hq, Hk, D, rot, max_pos, qos, kos, qs, ks, 1 if interleaved else 0,
+            float(eps), ls_dtype(q))
     return q_out, k_out, q_rstd, k_rstd
 
 
@@ -588,39 +654,60 @@ def qk_norm_rope_bw(dq_out, dk_out, q, k, gamma_q, gamma_k, q_rstd, k_rstd, cos=
     if workspace is None:
         workspace = qk_norm_rope_workspace(tokens, Hq, Hk, D, q.device)
     _workspace("workspace", workspace)
-    new = dict(device=q.device, dtype=q.dtype)
-    dq = torch.empty((tokens, Hq, D), **new) if dq is None else dq
-    dk = torch.empty((tokens, Hk, D), **new) if dk is None else dk
+    dq = q.new_empty((tokens, Hq, D)) if dq is None else dq
+    dk = k.new_empty((tokens, Hk, D)) if dk is None else dk
     dqs, dks = _like_heads("dq", dq, q), _like_heads("dk", dk, k)
     # a side without heads has no gradient to sum: its gamma gradient is zero
-    make = torch.empty if Hq and Hk else torch.zeros
-    new["dtype"] = torch.float32
-    dgamma_q = make(D, **new) if dgamma_q is None else dgamma_q
-    dgamma_k = make(D, **new) if dgamma_k is None else dgamma_k
+    make = q.new_empty if Hq and Hk else q.new_zeros
+    dgamma_q = make(D, dtype=torch.float32) if dgamma_q is None else dgamma_q
+    dgamma_k = make(D, dtype=torch.float32) if dgamma_k is None else dgamma_k
     dev = _one_device((q, k, dq_out, dk_out, dq, dk),
                       (gamma_q, gamma_k, q_rstd, k_rstd, cos, sin, positions, workspace,
                        dgamma_q, dgamma_k))
-    _call("ls_qk_norm_rope_bw", dev, ls_qk_norm_rope_bw, _ptr(dq), _ptr(dk), _ptr(dgamma_q),
-          _ptr(dgamma_k), _ptr(dq_out), _ptr(dk_out), _ptr(q), _ptr(k), _ptr(gamma_q),
-          _ptr(gamma_k), _ptr(q_rstd), _ptr(k_rstd), _ptr(cos), _ptr(sin), _ptr(positions),
-          tokens, Hq, Hk, D, rot, max_pos, dqs, dks, dqos, dkos, qs, ks, interleaved,
-          _ptr(workspace), workspace.numel() * workspace.element_size(), ls_dtype(q), _stream(q))
+    _launch("ls_qk_norm_rope_bw", dev, _ptr(dq), _ptr(dk), _ptr(dgamma_q), _ptr(dgamma_k),
+            _ptr(dq_out), _ptr(dk_out), _ptr(q), _ptr(k), _ptr(gamma_q), _ptr(gamma_k),
+            _ptr(q_rstd), _ptr(k_rstd), _ptr(cos), _ptr(sin), _ptr(positions), tokens, Hq, Hk, D,
+            rot, max_pos, dqs, dks, dqos, dkos, qs, ks, 1 if interleaved else 0, _ptr(workspace),
+            workspace.numel() * 4, ls_dtype(q))
     return dq, dk, dgamma_q, dgamma_k
 
 
 # ----------------------------------------------------------------------------
 # global gradient norm and clipping
 # ----------------------------------------------------------------------------
+_DTYPE = operator.attrgetter("dtype")
+
+
+def _list_device(tensors):
+    """The index of the one CUDA device of a list's dense tensors."""
+    Tensor = _torch().Tensor
+    try:
+        devices = set(map(Tensor.get_device, tensors))
+        if len(devices) == 1 and all(map(Tensor.is_contiguous, tensors)):
+            index = devices.pop()
+            if index >= 0:
+                return index
+    except TypeError:
+        pass  # something that only looks like a tensor
+    return _dev(*tensors).index  # says what is wrong
+
+
 def _grad_lists(grads):
-    """(device, pointers, sizes, dtype codes) of a list of dense tensors."""
+    """(tensors, device index, pointers, element counts, and dtype codes) of a
+    list of dense tensors, the last as a host array."""
     grads = list(grads)
     if not grads:
         raise ValueError("an empty list has no device: give at least one gradient")
-    dev = _dev(*grads)
-    n = len(grads)
-    ptrs = (ctypes.c_void_p * n)(*[t.data_ptr() for t in grads])
-    sizes = (ctypes.c_int64 * n)(*[t.numel() for t in grads])
-    return grads, dev, ptrs, sizes, (ctypes.c_int32 * n)(*[ls_dtype(t) for t in grads])
+    index = _list_device(grads)
+    try:
+        codes = array.array("i", map(_DTYPE_CODES.__getitem__, map(_DTYPE, grads)))
+    except KeyError:  # the first call, or an unsupported dtype
+        codes = array.array("i", map(ls_dtype, grads))
+    return grads, index, [t.data_ptr() for t in grads], [t.numel() for t in grads], codes
+
+
+def _at(a) -> int:
+    return a.buffer_info()[0]
 
 
 def grad_norm_workspace(count: int, device):
@@ -630,52 +717,57 @@ def grad_norm_workspace(count: int, device):
     return _torch().empty(max(n, 16) // 4, device=device, dtype=_torch().float32)
 
 
-def _norm_outputs(grads, dev, workspace, norm):
-    torch = _torch()
-    _want("norm", norm, (1,), torch.float32)
+def _norm_outputs(grads, index, workspace, norm):
+    f32 = _torch().float32
+    _want("norm", norm, (1,), f32)
     if workspace is None:
-        workspace = grad_norm_workspace(len(grads), dev)
+        n = ls_grad_norm_workspace_size(len(grads))
+        workspace = grads[0].new_empty(max(n, 16) // 4, dtype=f32)
     _workspace("workspace", workspace)
-    norm = torch.empty(1, device=dev, dtype=torch.float32) if norm is None else norm
-    if _dev(workspace, norm) != dev:
-        raise ValueError(f"workspace and norm must be on {dev}")
+    norm = grads[0].new_empty(1, dtype=f32) if norm is None else norm
+    if _same_device(workspace, norm) != index:
+        raise ValueError(f"workspace and norm must be on {grads[0].device}")
     return workspace, norm
 
 
 def grad_norm(grads, workspace=None, norm=None):
     """Global norm sqrt(sum g^2) over a list of gradients (fp32, fp16 and bf16
     may be mixed), fp32 [1] on their device."""
-    grads, dev, ptrs, sizes, dts = _grad_lists(grads)
-    workspace, norm = _norm_outputs(grads, dev, workspace, norm)
-    _call("ls_grad_norm", dev, ls_grad_norm, _ptr(norm), ptrs, sizes, dts, len(grads),
-          _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(norm))
+    grads, index, ptrs, sizes, codes = _grad_lists(grads)
+    workspace, norm = _norm_outputs(grads, index, workspace, norm)
+    ptrs, sizes = array.array("Q", ptrs), array.array("q", sizes)
+    _launch("ls_grad_norm", index, _ptr(norm), _at(ptrs), _at(sizes), _at(codes), len(grads),
+            _ptr(workspace), workspace.numel() * 4)
     return norm
 
 
 def grad_clip(grads, max_norm: float, out=None, eps: float = 1e-6, workspace=None, norm=None):
     """Multiplies a list of gradients by min(1, max_norm / (norm + eps)), norm
     being ``grad_norm(grads)``; returns (out, norm).  ``out`` None clips in
-    place; otherwise it is a list of tensors of the gradients' shapes and
-    dtypes.  No tensor may be in ``out`` twice."""
-    grads, dev, ptrs, sizes, dts = _grad_lists(grads)
+    place; otherwise it is a list of tensors with the gradients' element counts
+    and dtypes.  No tensor may be in ``out`` twice."""
+    grads, index, ptrs, sizes, codes = _grad_lists(grads)
     if out is None:
         out, optrs = grads, ptrs
     else:
         out = list(out)
         if len(out) != len(grads):
             raise ValueError(f"out must hold {len(grads)} tensors, got {len(out)}")
-        for i, (o, g) in enumerate(zip(out, grads)):
-            if o.shape != g.shape or o.dtype != g.dtype:
+        if [t.numel() for t in out] != sizes or \
+                list(map(_DTYPE, out)) != list(map(_DTYPE, grads)):
+            for i, (o, g) in enumerate(zip(out, grads)):
                 _want(f"out[{i}]", o, g.shape, g.dtype)
-        if _dev(*out) != dev:
-            raise ValueError(f"out must be on {dev}")
-        optrs = (ctypes.c_void_p * len(out))(*[t.data_ptr() for t in out])
+        if _list_device(out) != index:
+            raise ValueError(f"out must be on {grads[0].device}")
+        optrs = [t.data_ptr() for t in out]
     if len(set(optrs)) < len(out):
-        held = [t.data_ptr() for t in out if t.numel()]
+        held = [p for p, n in zip(optrs, sizes) if n]
         if len(set(held)) < len(held):
             raise ValueError("a tensor is in out twice")
-    workspace, norm = _norm_outputs(grads, dev, workspace, norm)
-    _call("ls_grad_clip", dev, ls_grad_clip, _ptr(norm), optrs, ptrs, sizes, dts, len(grads),
-          float(max_norm), float(eps), _ptr(workspace),
-          workspace.numel() * workspace.element_size(), _stream(norm))
+    workspace, norm = _norm_outputs(grads, index, workspace, norm)
+    same = optrs is ptrs
+    ptrs, sizes = array.array("Q", ptrs), array.array("q", sizes)
+    optrs = ptrs if same else array.array("Q", optrs)
+    _launch("ls_grad_clip", index, _ptr(norm), _at(optrs), _at(ptrs), _at(sizes), _at(codes),
+            len(grads), float(max_norm), float(eps), _ptr(workspace), workspace.numel() * 4)
     return out, norm

@@ -219,14 +219,15 @@ def ls_grad_norm_workspace_size(count) -> int:
 
 
 def ls_grad_norm(norm, grads, sizes, dtypes, count, workspace, workspace_bytes, stream=0) -> int:
-    """``grads``, ``sizes`` and ``dtypes`` are ctypes arrays (void pointers,
-    int64, int32) of ``count`` entries, or None for an empty list."""
+    """``grads``, ``sizes`` and ``dtypes`` are host arrays (void pointers, int64,
+    int32) of ``count`` entries: ctypes arrays or their addresses, or None for
+    an empty list."""
     return load().ls_grad_norm(norm, grads, sizes, dtypes, count, workspace, workspace_bytes,
                                stream)
 
 
 def ls_grad_clip(norm, out, grads, sizes, dtypes, count, max_norm, eps, workspace,
                  workspace_bytes, stream=0) -> int:
-    """As ls_grad_norm; ``out`` is a ctypes array of void pointers too."""
+    """As ls_grad_norm; ``out`` is a host array of void pointers too."""
     return load().ls_grad_clip(norm, out, grads, sizes, dtypes, count, max_norm, eps, workspace,
                                workspace_bytes, stream)

@@ -850,7 +850,7 @@ static ls_status grad_check(const float *norm, void *const *out, bool clip,
         if (sizes[i] == 0) continue;
         if (!grads[i] || (clip && !out[i])) return LS_ERR_INVALID_ARG;
         if (!aligned(grads[i], es) || (clip && !aligned(out[i], es))) return LS_ERR_MISALIGNED;
-        if (sizes[i] > (INT64_MAX / 8 - total)) return LS_ERR_UNSUPPORTED;
+        if (sizes[i] > LS_MAX_GRAD_ELEMENTS - total) return LS_ERR_UNSUPPORTED;
         total += sizes[i];
     }
     const size_t need = ls_grad_norm_workspace_size(count);

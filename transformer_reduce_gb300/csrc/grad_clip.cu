@@ -4,11 +4,12 @@
 //     norm = sqrt(sum over all tensors and elements of g^2)
 //     out  = g * min(1, max_norm / (norm + eps))
 //
-// The list of tensors travels in the kernel's parameters (40 bytes a tensor,
+// The list of tensors travels in the kernel's parameters (29 bytes a tensor,
 // up to kGradCap of them a launch), so nothing is copied to the device and a
-// captured graph carries its list.  Tensors are cut into chunks of 2048
-// 16-byte slots; a block of 256 threads takes a chunk at a time, eight slots
-// per thread in flight together, and finds the chunk's tensor by bisection.
+// captured graph carries its list.  Tensors are cut into chunks of 16-byte
+// slots; a block of 256 threads takes a chunk at a time, eight slots per
+// thread in flight together (two for short lists, which would not fill the GPU
+// otherwise), and finds the chunk's tensor by bisection.
 // Slots lie on 16-byte addresses whatever the tensor's own alignment; the
 // first and last slot of a tensor are taken element by element.
 //
@@ -21,6 +22,8 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <type_traits>
+
 #include "dispatch.cuh"
 #include "launch.h"
 #include "ls_device.cuh"
@@ -30,24 +33,29 @@ namespace lsr {
 namespace {
 
 constexpr int kGradBlock = 256;
-constexpr int kGradSlots = 8;                              // 16-byte slots per thread
-constexpr int64_t kGradChunk = kGradBlock * kGradSlots;    // slots per chunk
+// 16-byte slots per thread and chunk: eight, so that a thread has 128 bytes in
+// flight, or two where eight would leave blocks of the norm without a chunk.
+constexpr int kGradSlots = 8, kGradFewSlots = 2;
 constexpr int64_t kGradBlocks = 4 * 152;  // partial sums of a launch, a constant of the library
 constexpr int kGradCap = 512;             // tensors of a launch
 constexpr int kGradSmallCap = 48;         // a shorter list has a parameter block of its own
 
+template <int CAP>
+struct GradList {
+    int32_t count, chunks;
+    int32_t chunk0[CAP];  // first chunk of each tensor (read by the bisection: close together)
+    uint8_t dt[CAP];
+    const void *g[CAP];
+    void *o[CAP];
+    int64_t n[CAP];
+};
+// One tensor's part of a list.
 struct GradSpan {
     const void *g;
     void *o;
     int64_t n;
-    int64_t chunk0;  // first chunk of the tensor
-    int32_t dt;
-};
-template <int CAP>
-struct GradList {
-    GradSpan s[CAP];
-    int64_t chunks;
-    int32_t count;
+    int dt;
+    int64_t chunk;  // of the tensor
 };
 
 // Element at the 16-byte address at or below p, relative to p.
@@ -56,24 +64,25 @@ __device__ __forceinline__ int64_t grad_first_element(const void *p) {
     return -(int64_t)((reinterpret_cast<uintptr_t>(p) & 15u) / sizeof(T));
 }
 
-int64_t grad_chunks(const void *p, int64_t n, int es) {
-    const int64_t bytes = n * es + (int64_t)(reinterpret_cast<uintptr_t>(p) & 15u);
-    return n > 0 ? ceil_div(ceil_div(bytes, 16), kGradChunk) : 0;
+int64_t grad_slots(const void *p, int64_t n, int es) {
+    return n > 0 ? ceil_div(n * es + (int64_t)(reinterpret_cast<uintptr_t>(p) & 15u), 16) : 0;
 }
 
 int grad_es(int dt) { return dt == LS_F32 ? 4 : 2; }
 
+// The tensor of a chunk: the last one whose chunk0 <= chunk (tensors without
+// elements share their successor's chunk0 and are never the last).
 template <int CAP>
-__device__ __forceinline__ int grad_find(const GradList<CAP> &L, int64_t chunk) {
-    int lo = 0, hi = L.count;  // the last tensor whose chunk0 <= chunk
+__device__ __forceinline__ GradSpan grad_find(const GradList<CAP> &L, int chunk) {
+    int lo = 0, hi = L.count;
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (L.s[mid].chunk0 <= chunk)
+        if (L.chunk0[mid] <= chunk)
             lo = mid;
         else
             hi = mid;
     }
-    return lo;
+    return GradSpan{L.g[lo], L.o[lo], L.n[lo], L.dt[lo], chunk - L.chunk0[lo]};
 }
 
 // The slot whose first element is e0 (elements outside [0, n) read as 0).
@@ -92,22 +101,22 @@ __device__ __forceinline__ uint4 grad_load(const T *g, int64_t e0, int64_t n) {
 // leave the range where that is exact enough (a sum below 2^-90 may have lost
 // denormal squares, one that overflowed may be finite), and then in FP64;
 // slots of zeros, which a sparse gradient is full of, never take that path.
-template <typename T>
-__device__ __forceinline__ double grad_chunk_squares(const GradSpan &sp, int64_t chunk) {
+template <typename T, int U>
+__device__ __forceinline__ double grad_chunk_squares(const GradSpan &sp) {
     constexpr int V = Traits<T>::kVec;
     const T *g = static_cast<const T *>(sp.g);
     const int64_t e0 =
         grad_first_element<T>(sp.g) +
-        ((chunk - sp.chunk0) * kGradChunk + threadIdx.x) * V;
-    uint4 raw[kGradSlots];
+        (sp.chunk * (kGradBlock * U) + threadIdx.x) * V;
+    uint4 raw[U];
 #pragma unroll
-    for (int u = 0; u < kGradSlots; ++u) {
+    for (int u = 0; u < U; ++u) {
         const int64_t e = e0 + (int64_t)u * kGradBlock * V;
         raw[u] = e < sp.n ? grad_load<T>(g, e, sp.n) : make_uint4(0u, 0u, 0u, 0u);
     }
     float2 s2 = f2(0.f);
 #pragma unroll
-    for (int u = 0; u < kGradSlots; ++u) {
+    for (int u = 0; u < U; ++u) {
         float2 v[V / 2];
         unpack2<T>(raw[u], v);
 #pragma unroll
@@ -117,11 +126,11 @@ __device__ __forceinline__ double grad_chunk_squares(const GradSpan &sp, int64_t
     if (s > 0x1p-90f && s < INFINITY) return (double)s;
     uint32_t any = 0u;
 #pragma unroll
-    for (int u = 0; u < kGradSlots; ++u) any |= raw[u].x | raw[u].y | raw[u].z | raw[u].w;
+    for (int u = 0; u < U; ++u) any |= raw[u].x | raw[u].y | raw[u].z | raw[u].w;
     if (any == 0u) return 0.0;
     double d = 0.0;
 #pragma unroll 1
-    for (int u = 0; u < kGradSlots; ++u) {
+    for (int u = 0; u < U; ++u) {
         const int64_t e = e0 + (int64_t)u * kGradBlock * V;
         for (int i = 0; i < V; ++i)
             if (e + i >= 0 && e + i < sp.n) {
@@ -144,19 +153,19 @@ __device__ __forceinline__ double grad_block_sum(double v) {
     return v;
 }
 
-template <int CAP>
+template <int CAP, int U>
 __global__ void __launch_bounds__(kGradBlock)
 grad_squares(double *part, const __grid_constant__ GradList<CAP> L) {
     pdl_begin();
     double d = 0.0;
-    for (int64_t c = blockIdx.x; c < L.chunks; c += gridDim.x) {
-        const GradSpan &sp = L.s[grad_find(L, c)];
+    for (int c = blockIdx.x; c < L.chunks; c += gridDim.x) {
+        const GradSpan sp = grad_find(L, c);
         if (sp.dt == LS_F32)
-            d += grad_chunk_squares<float>(sp, c);
+            d += grad_chunk_squares<float, U>(sp);
         else if (sp.dt == LS_F16)
-            d += grad_chunk_squares<__half>(sp, c);
+            d += grad_chunk_squares<__half, U>(sp);
         else
-            d += grad_chunk_squares<__nv_bfloat16>(sp, c);
+            d += grad_chunk_squares<__nv_bfloat16, U>(sp);
     }
     d = grad_block_sum(d);
     if (threadIdx.x == 0) part[blockIdx.x] = d;
@@ -176,8 +185,8 @@ grad_norm_final(float *norm, const double *part, int parts) {
     if (threadIdx.x == 0) *norm = v;
 }
 
-template <typename T>
-__device__ __forceinline__ void grad_chunk_scale(const GradSpan &sp, int64_t chunk, float coef) {
+template <typename T, int U>
+__device__ __forceinline__ void grad_chunk_scale(const GradSpan &sp, float coef) {
     constexpr int V = Traits<T>::kVec;
     const T *g = static_cast<const T *>(sp.g);
     T *o = static_cast<T *>(sp.o);
@@ -185,10 +194,10 @@ __device__ __forceinline__ void grad_chunk_scale(const GradSpan &sp, int64_t chu
         ((reinterpret_cast<uintptr_t>(g) ^ reinterpret_cast<uintptr_t>(o)) & 15u) == 0;
     const int64_t e0 =
         grad_first_element<T>(sp.g) +
-        ((chunk - sp.chunk0) * kGradChunk + threadIdx.x) * V;
-    uint4 raw[kGradSlots];
+        (sp.chunk * (kGradBlock * U) + threadIdx.x) * V;
+    uint4 raw[U];
 #pragma unroll
-    for (int u = 0; u < kGradSlots; ++u) {
+    for (int u = 0; u < U; ++u) {
         const int64_t e = e0 + (int64_t)u * kGradBlock * V;
         if (e < sp.n) {
             if (e >= 0 && e + V <= sp.n)
@@ -198,7 +207,7 @@ __device__ __forceinline__ void grad_chunk_scale(const GradSpan &sp, int64_t chu
         }
     }
 #pragma unroll
-    for (int u = 0; u < kGradSlots; ++u) {
+    for (int u = 0; u < U; ++u) {
         const int64_t e = e0 + (int64_t)u * kGradBlock * V;
         if (e >= sp.n) continue;
         float f[V];
@@ -215,7 +224,7 @@ __device__ __forceinline__ void grad_chunk_scale(const GradSpan &sp, int64_t chu
     }
 }
 
-template <int CAP>
+template <int CAP, int U>
 __global__ void __launch_bounds__(kGradBlock)
 grad_scale(float *norm, const double *part, int parts, float max_norm, float eps,
            const __grid_constant__ GradList<CAP> L) {
@@ -224,76 +233,103 @@ grad_scale(float *norm, const double *part, int parts, float max_norm, float eps
     if (blockIdx.x == 0 && threadIdx.x == 0) *norm = total;
     const float ratio = max_norm / (total + eps);
     const float coef = ratio >= 1.f ? 1.f : ratio;  // a NaN norm gives NaN
-    for (int64_t k = blockIdx.x; k < L.chunks; k += gridDim.x) {
-        const int64_t c = L.chunks - 1 - k;
-        const GradSpan &sp = L.s[grad_find(L, c)];
+    for (int k = blockIdx.x; k < L.chunks; k += gridDim.x) {
+        const GradSpan sp = grad_find(L, L.chunks - 1 - k);
         if (coef == 1.f && sp.o == sp.g) continue;  // in place and nothing to clip
         if (sp.dt == LS_F32)
-            grad_chunk_scale<float>(sp, c, coef);
+            grad_chunk_scale<float, U>(sp, coef);
         else if (sp.dt == LS_F16)
-            grad_chunk_scale<__half>(sp, c, coef);
+            grad_chunk_scale<__half, U>(sp, coef);
         else
-            grad_chunk_scale<__nv_bfloat16>(sp, c, coef);
+            grad_chunk_scale<__nv_bfloat16, U>(sp, coef);
     }
 }
 
-// One launch's list from tensors [beg, end) of the caller's arrays.
+// A caller's list on the host.
+struct GradHost {
+    void *const *out;  // NULL: a norm alone
+    const void *const *grads;
+    const int64_t *sizes;
+    const int32_t *dts;
+    int64_t count;
+};
+
+// One launch's list from tensors [beg, end), cut into chunks of U slots per
+// thread.  (The ABI bounds the elements of a list, so chunks fit 31 bits.)
 template <int CAP>
-void grad_fill(GradList<CAP> &L, void *const *out, const void *const *grads, const int64_t *sizes,
-               const int32_t *dts, int64_t beg, int64_t end) {
+void grad_fill(GradList<CAP> &L, const GradHost &a, int64_t beg, int64_t end, int U) {
     L.count = (int)(end - beg);
     int64_t chunks = 0;
     for (int64_t i = beg; i < end; ++i) {
-        GradSpan &s = L.s[i - beg];
-        s.g = grads[i];
-        s.o = out ? out[i] : nullptr;
-        s.n = sizes[i];
-        s.dt = dts[i];
-        s.chunk0 = chunks;
-        chunks += grad_chunks(s.g, s.n, grad_es(s.dt));
+        const int64_t k = i - beg;
+        L.g[k] = a.grads[i];
+        L.o[k] = a.out ? a.out[i] : nullptr;
+        L.n[k] = a.sizes[i];
+        L.dt[k] = (uint8_t)a.dts[i];
+        L.chunk0[k] = (int32_t)chunks;
+        chunks += ceil_div(grad_slots(a.grads[i], a.sizes[i], grad_es(a.dts[i])),
+                           (int64_t)kGradBlock * U);
     }
-    L.chunks = chunks;
+    L.chunks = (int32_t)chunks;
 }
 
-template <int CAP>
-cudaError_t grad_squares_launch(double *part, const void *const *grads, const int64_t *sizes,
-                                const int32_t *dts, int64_t beg, int64_t end, int *parts,
-                                cudaStream_t st) {
+template <int CAP, int U>
+cudaError_t grad_squares_launch(double *part, const GradHost &a, int64_t beg, int64_t end,
+                                int *parts, cudaStream_t st) {
     GradList<CAP> L;
-    grad_fill<CAP>(L, nullptr, grads, sizes, dts, beg, end);
+    grad_fill<CAP>(L, a, beg, end, U);
     *parts = (int)(L.chunks < kGradBlocks ? L.chunks : kGradBlocks);
     if (*parts == 0) return cudaSuccess;
-    return launch_pdl(grad_squares<CAP>, dim3((unsigned)*parts), dim3(kGradBlock), 0, st, part, L);
+    return launch_pdl(grad_squares<CAP, U>, dim3((unsigned)*parts), dim3(kGradBlock), 0, st, part,
+                      L);
 }
 
-template <int CAP>
+template <int CAP, int U>
 cudaError_t grad_scale_launch(float *norm, const double *part, int parts, float max_norm,
-                              float eps, void *const *out, const void *const *grads,
-                              const int64_t *sizes, const int32_t *dts, int64_t beg, int64_t end,
+                              float eps, const GradHost &a, int64_t beg, int64_t end,
                               cudaStream_t st) {
     GradList<CAP> L;
-    grad_fill<CAP>(L, out, grads, sizes, dts, beg, end);
-    return launch_persistent<grad_scale<CAP>>(kGradBlock, 0, L.chunks, st, norm, part, parts,
-                                              max_norm, eps, L);
+    grad_fill<CAP>(L, a, beg, end, U);
+    return launch_persistent<grad_scale<CAP, U>>(kGradBlock, 0, L.chunks, st, norm, part, parts,
+                                                 max_norm, eps, L);
+}
+
+// Whether the list is small enough for chunks of few slots.
+bool grad_few(const GradHost &a) {
+    int64_t slots = 0;
+    for (int64_t i = 0; i < a.count; ++i)
+        slots += grad_slots(a.grads[i], a.sizes[i], grad_es(a.dts[i]));
+    return slots < kGradBlocks * kGradBlock * kGradSlots;
+}
+
+// Calls f(beg, end, list capacity, slots per thread) for every launch.
+template <typename F>
+cudaError_t grad_launches(const GradHost &a, F f) {
+    const bool few = grad_few(a);
+    using Few = std::integral_constant<int, kGradFewSlots>;
+    using Many = std::integral_constant<int, kGradSlots>;
+    using Small = std::integral_constant<int, kGradSmallCap>;
+    using Full = std::integral_constant<int, kGradCap>;
+    for (int64_t beg = 0; beg < a.count; beg += kGradCap) {
+        const int64_t end = beg + kGradCap < a.count ? beg + kGradCap : a.count;
+        const bool small = end - beg <= kGradSmallCap;
+        const cudaError_t e = small ? (few ? f(beg, end, Small(), Few()) : f(beg, end, Small(), Many()))
+                                    : (few ? f(beg, end, Full(), Few()) : f(beg, end, Full(), Many()));
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
 }
 
 // Partials of every tensor; *parts: how many were left at `part`.
-cudaError_t grad_all_squares(const void *const *grads, const int64_t *sizes, const int32_t *dts,
-                             int64_t count, double *part, int *parts, cudaStream_t st) {
+cudaError_t grad_all_squares(const GradHost &a, double *part, int *parts, cudaStream_t st) {
     *parts = 0;
-    for (int64_t beg = 0; beg < count;) {
-        const int64_t end = beg + kGradCap < count ? beg + kGradCap : count;
+    return grad_launches(a, [&](int64_t beg, int64_t end, auto cap, auto slots) {
         int n = 0;
-        const cudaError_t e =
-            end - beg <= kGradSmallCap
-                ? grad_squares_launch<kGradSmallCap>(part + *parts, grads, sizes, dts, beg, end,
-                                                     &n, st)
-                : grad_squares_launch<kGradCap>(part + *parts, grads, sizes, dts, beg, end, &n, st);
-        if (e != cudaSuccess) return e;
+        const cudaError_t e = grad_squares_launch<decltype(cap)::value, decltype(slots)::value>(
+            part + *parts, a, beg, end, &n, st);
         *parts += n;
-        beg = end;
-    }
-    return cudaSuccess;
+        return e;
+    });
 }
 
 }  // namespace
@@ -304,8 +340,9 @@ int64_t grad_parts(int64_t count) {
 
 cudaError_t launch_grad_norm(float *norm, const void *const *grads, const int64_t *sizes,
                              const int32_t *dts, int64_t count, double *part, cudaStream_t st) {
+    const GradHost a = {nullptr, grads, sizes, dts, count};
     int parts = 0;
-    const cudaError_t e = grad_all_squares(grads, sizes, dts, count, part, &parts, st);
+    const cudaError_t e = grad_all_squares(a, part, &parts, st);
     if (e != cudaSuccess) return e;
     return launch_pdl(grad_norm_final, dim3(1), dim3(kGradBlock), 0, st, norm,
                       (const double *)part, parts);
@@ -314,23 +351,17 @@ cudaError_t launch_grad_norm(float *norm, const void *const *grads, const int64_
 cudaError_t launch_grad_clip(float *norm, void *const *out, const void *const *grads,
                              const int64_t *sizes, const int32_t *dts, int64_t count,
                              float max_norm, float eps, double *part, cudaStream_t st) {
+    const GradHost a = {out, grads, sizes, dts, count};
     int parts = 0;
-    cudaError_t e = grad_all_squares(grads, sizes, dts, count, part, &parts, st);
+    const cudaError_t e = grad_all_squares(a, part, &parts, st);
     if (e != cudaSuccess) return e;
     if (parts == 0)
         return launch_pdl(grad_norm_final, dim3(1), dim3(kGradBlock), 0, st, norm,
                           (const double *)part, 0);
-    for (int64_t beg = 0; beg < count;) {
-        const int64_t end = beg + kGradCap < count ? beg + kGradCap : count;
-        e = end - beg <= kGradSmallCap
-                ? grad_scale_launch<kGradSmallCap>(norm, part, parts, max_norm, eps, out, grads,
-                                                   sizes, dts, beg, end, st)
-                : grad_scale_launch<kGradCap>(norm, part, parts, max_norm, eps, out, grads, sizes,
-                                              dts, beg, end, st);
-        if (e != cudaSuccess) return e;
-        beg = end;
-    }
-    return cudaSuccess;
+    return grad_launches(a, [&](int64_t beg, int64_t end, auto cap, auto slots) {
+        return grad_scale_launch<decltype(cap)::value, decltype(slots)::value>(
+            norm, part, parts, max_norm, eps, a, beg, end, st);
+    });
 }
 
 }  // namespace lsr

@@ -204,67 +204,69 @@ inline int qk_lanes(int D, int rot, int V, bool inter) {
     return hv + (nv - 2 * hv + 1) / 2;
 }
 
-// Cosines and sines of the lane's V angles (1 and 0 where nothing is rotated).
+// Cosines and sines of the lane's V angles, as pairs of neighbours (halves) or
+// for one pair of features each (interleaved: c[h].x of vector va's pairs 2h,
+// c[h].y of 2h + 1, then vb's); 1 and 0 where nothing is rotated.
 template <int V, bool INTER>
 __device__ __forceinline__ void qk_angles(const QkRope &r, const QkLane &q, int64_t tok,
-                                          float (&c)[V], float (&s)[V]) {
+                                          float2 (&c)[V / 2], float2 (&s)[V / 2]) {
 #pragma unroll
-    for (int e = 0; e < V; ++e) {
-        c[e] = 1.f;
-        s[e] = 0.f;
+    for (int h = 0; h < V / 2; ++h) {
+        c[h] = f2(1.f);
+        s[h] = f2(0.f);
     }
     if (!q.ra) return;  // (vector vb is rotated only if va is)
     const int64_t pos = __ldg(r.positions + tok);
     const int half = r.rot / 2;
     if (pos < 0 || pos >= r.max_pos) {
 #pragma unroll
-        for (int e = 0; e < V; ++e) c[e] = s[e] = __int_as_float(0x7fc00000);
+        for (int h = 0; h < V / 2; ++h) c[h] = s[h] = f2(__int_as_float(0x7fc00000));
         return;
     }
-    const float *cp = r.cos + pos * half + (INTER ? q.va * (V / 2) : q.va * V);
-    const float *sp = r.sin + pos * half + (INTER ? q.va * (V / 2) : q.va * V);
+    const int64_t at = pos * half + (INTER ? q.va * (V / 2) : q.va * V);
     // interleaved: vector vb = va + 1 takes the V / 2 angles after va's
-    const int n = INTER && !q.rb ? V / 2 : V;
+    const int n = INTER && !q.rb ? V / 4 : V / 2;
 #pragma unroll
-    for (int e = 0; e < V; e += 2) {
-        if (e < n) {
-            const float2 cv = __ldg(reinterpret_cast<const float2 *>(cp + e));
-            const float2 sv = __ldg(reinterpret_cast<const float2 *>(sp + e));
-            c[e] = cv.x;
-            c[e + 1] = cv.y;
-            s[e] = sv.x;
-            s[e + 1] = sv.y;
+    for (int h = 0; h < V / 2; ++h)
+        if (h < n) {
+            c[h] = __ldg(reinterpret_cast<const float2 *>(r.cos + at + 2 * h));
+            s[h] = __ldg(reinterpret_cast<const float2 *>(r.sin + at + 2 * h));
         }
-    }
 }
 
-// Rotates the lane's two vectors (SIGN -1: back).
-template <int V, bool INTER>
-__device__ __forceinline__ void qk_turn(const QkLane &q, const float (&c)[V], const float (&s)[V],
-                                        float sign, float (&a)[V], float (&b)[V]) {
+// One pair of features turned by (c, s).
+__device__ __forceinline__ float2 qk_turn1(float2 v, float c, float s) {
+    return make_float2(fmaf(v.x, c, -(v.y * s)), fmaf(v.y, c, v.x * s));
+}
+
+// Turns the lane's two vectors (BACK: by the opposite angles).
+template <int V, bool INTER, bool BACK>
+__device__ __forceinline__ void qk_turn(const QkLane &q, const float2 (&c)[V / 2],
+                                        const float2 (&s)[V / 2], float2 (&a)[V / 2],
+                                        float2 (&b)[V / 2]) {
     if (!q.ra) return;
-    if (INTER) {
+    if constexpr (INTER) {
 #pragma unroll
-        for (int e = 0; e < V / 2; ++e) {
-            const float se = sign * s[e], x = a[2 * e], y = a[2 * e + 1];
-            a[2 * e] = x * c[e] - y * se;
-            a[2 * e + 1] = y * c[e] + x * se;
+        for (int h = 0; h < V / 4; ++h) {
+            a[2 * h] = qk_turn1(a[2 * h], c[h].x, BACK ? -s[h].x : s[h].x);
+            a[2 * h + 1] = qk_turn1(a[2 * h + 1], c[h].y, BACK ? -s[h].y : s[h].y);
         }
         if (q.rb) {
 #pragma unroll
-            for (int e = 0; e < V / 2; ++e) {
-                const float ce = c[V / 2 + e], se = sign * s[V / 2 + e];
-                const float x = b[2 * e], y = b[2 * e + 1];
-                b[2 * e] = x * ce - y * se;
-                b[2 * e + 1] = y * ce + x * se;
+            for (int h = 0; h < V / 4; ++h) {
+                const float2 ch = c[V / 4 + h], sh = s[V / 4 + h];
+                b[2 * h] = qk_turn1(b[2 * h], ch.x, BACK ? -sh.x : sh.x);
+                b[2 * h + 1] = qk_turn1(b[2 * h + 1], ch.y, BACK ? -sh.y : sh.y);
             }
         }
     } else {
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-            const float se = sign * s[e], x = a[e], y = b[e];
-            a[e] = x * c[e] - y * se;
-            b[e] = y * c[e] + x * se;
+        for (int h = 0; h < V / 2; ++h) {
+            const float2 up = BACK ? make_float2(-s[h].x, -s[h].y) : s[h];
+            const float2 down = BACK ? s[h] : make_float2(-s[h].x, -s[h].y);
+            const float2 x = a[h], y = b[h];
+            a[h] = fma2(x, c[h], mul2(y, down));
+            b[h] = fma2(y, c[h], mul2(x, up));
         }
     }
 }
@@ -286,6 +288,7 @@ qk_fw_vec(const QkSide<T> qs, const QkSide<T> ks, const QkRope r, int ngq, int n
     pdl_begin();
     using Tr = Traits<T>;
     constexpr int V = Tr::kVec;
+    constexpr int H2 = V / 2;
     constexpr int RPW = 32 / LPR;
     const int lane = threadIdx.x & 31, l = lane % LPR, sub = lane / LPR;
     const QkLane q = qk_lane<V, INTER>(r, l);
@@ -297,49 +300,54 @@ qk_fw_vec(const QkSide<T> qs, const QkSide<T> ks, const QkRope r, int ngq, int n
          item += (int64_t)gridDim.x * 8) {
         const int64_t tok = per_token == 1 ? item : item / per_token;
         const int f0 = (int)(item - tok * per_token) * per_item, f1 = min(f0 + per_item, ng);
-        uint4 ra = zero, rb = zero;
+        uint4 ra, rb;
         auto load = [&](int f) {
             const bool isq = f < ngq;
             const int h = (isq ? f : f - ngq) * RPW + sub;
             ra = rb = zero;
-            if (h < (isq ? qs.heads : ks.heads)) {
-                const T *x = (isq ? qs.x + tok * qs.x_stride : ks.x + tok * ks.x_stride) +
-                             (int64_t)h * r.D;
+            if (h < (int)(isq ? qs.heads : ks.heads)) {
+                const T *x = (isq ? qs.x + tok * qs.x_stride : ks.x + tok * ks.x_stride) + h * r.D;
                 if (q.ha) ra = ld_stream16(x + q.va * V);
                 if (q.hb) rb = ld_stream16(x + q.vb * V);
             }
         };
         load(f0);
-        float c[V], s[V];
+        float2 c[H2], s[H2];
         qk_angles<V, INTER>(r, q, tok, c, s);
-        for (int f = f0; f < f1; ++f) {
+        for (int f = f0; f < f1;) {  // one side at a time
             const bool isq = f < ngq;
-            const QkSide<T> &sd = isq ? qs : ks;
-            const int h = (isq ? f : f - ngq) * RPW + sub;
-            float a[V], b[V], ga[V], gb[V];
-            Tr::unpack(ra, a);
-            Tr::unpack(rb, b);
-            const uint4 wa = q.ha ? ld_cached16(sd.gamma + q.va * V) : zero;
-            const uint4 wb = q.hb ? ld_cached16(sd.gamma + q.vb * V) : zero;
-            if (f + 1 < f1) load(f + 1);
-            float ss = 0.f;
+            const T *gamma = isq ? qs.gamma : ks.gamma;
+            T *out = (isq ? qs.out + tok * qs.out_stride : ks.out + tok * ks.out_stride);
+            float *rstd_out = isq ? qs.rstd_out : ks.rstd_out;
+            const int heads = (int)(isq ? qs.heads : ks.heads);
+            const int g0 = isq ? 0 : ngq, g1 = isq ? min(f1, ngq) : f1;
+            if (rstd_out) rstd_out += tok * heads;
+            float2 ga[H2], gb[H2];
+            unpack2<T>(q.ha ? ld_cached16(gamma + q.va * V) : zero, ga);
+            unpack2<T>(q.hb ? ld_cached16(gamma + q.vb * V) : zero, gb);
+            for (; f < g1; ++f) {
+                const int h = (f - g0) * RPW + sub;
+                float2 a[H2], b[H2];
+                unpack2<T>(ra, a);
+                unpack2<T>(rb, b);
+                if (f + 1 < f1) load(f + 1);
+                float2 ss = f2(0.f);
 #pragma unroll
-            for (int e = 0; e < V; ++e) ss = fmaf(a[e], a[e], fmaf(b[e], b[e], ss));
-            ss = qk_sum<LPR>(ss);
-            const float rstd = 1.f / sqrtf(fmaf(ss, invD, r.eps));
-            Tr::unpack(wa, ga);
-            Tr::unpack(wb, gb);
+                for (int e = 0; e < H2; ++e) ss = fma2(a[e], a[e], fma2(b[e], b[e], ss));
+                // rsqrt.approx: at most 2 units in the last place off
+                const float rstd = rsqrtf(fmaf(qk_sum<LPR>(ss.x + ss.y), invD, r.eps));
 #pragma unroll
-            for (int e = 0; e < V; ++e) {
-                a[e] *= rstd * ga[e];
-                b[e] *= rstd * gb[e];
-            }
-            qk_turn<V, INTER>(q, c, s, 1.f, a, b);
-            if (h < sd.heads) {
-                T *o = sd.out + tok * sd.out_stride + (int64_t)h * r.D;
-                if (q.ha) st_stream16(o + q.va * V, Tr::pack(a));
-                if (q.hb) st_stream16(o + q.vb * V, Tr::pack(b));
-                if (l == 0 && sd.rstd_out) sd.rstd_out[tok * sd.heads + h] = rstd;
+                for (int e = 0; e < H2; ++e) {
+                    a[e] = mul2(mul2(a[e], f2(rstd)), ga[e]);
+                    b[e] = mul2(mul2(b[e], f2(rstd)), gb[e]);
+                }
+                qk_turn<V, INTER, false>(q, c, s, a, b);
+                if (h < heads) {
+                    T *o = out + h * r.D;
+                    if (q.ha) st_stream16(o + q.va * V, pack2<T>(a));
+                    if (q.hb) st_stream16(o + q.vb * V, pack2<T>(b));
+                    if (l == 0 && rstd_out) rstd_out[h] = rstd;
+                }
             }
         }
     }
@@ -348,13 +356,16 @@ qk_fw_vec(const QkSide<T> qs, const QkSide<T> ks, const QkRope r, int ngq, int n
 // Backward.  Blocks b < q_blocks work on query heads, the others on key heads,
 // so that a lane has the gamma gradients of its 2V features of one side in
 // registers; they are added over a warp's heads by shuffles and over the
-// block's warps in shared memory at the end.  ng: groups of a token, by side.
+// block's warps in shared memory at the end.  With p = dn * x and
+// S = sum gamma p (x not normed): dgamma += rstd p and
+// dx = rstd gamma dn - x rstd^3 S / D.
 template <typename T, int LPR, bool INTER>
 __global__ void __launch_bounds__(256, 2)
 qk_bw_vec(const QkSide<T> qs, const QkSide<T> ks, const QkRope r, float *part, int q_blocks) {
     pdl_begin();
     using Tr = Traits<T>;
     constexpr int V = Tr::kVec;
+    constexpr int H2 = V / 2;
     constexpr int RPW = 32 / LPR;
     __shared__ float sum[8][LPR * 2 * V + 1];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane % LPR, sub = lane / LPR;
@@ -366,22 +377,24 @@ qk_bw_vec(const QkSide<T> qs, const QkSide<T> ks, const QkRope r, float *part, i
     const int heads = (int)sd.heads, ng = (heads + RPW - 1) / RPW;
     const float invD = 1.f / (float)r.D;
     const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-    const uint4 wa = q.ha ? ld_cached16(sd.gamma + q.va * V) : zero;
-    const uint4 wb = q.hb ? ld_cached16(sd.gamma + q.vb * V) : zero;
-    float da[V], db[V];  // gamma gradients
+    float2 ga[H2], gb[H2], da[H2], db[H2];  // gamma and its gradients
+    unpack2<T>(q.ha ? ld_cached16(sd.gamma + q.va * V) : zero, ga);
+    unpack2<T>(q.hb ? ld_cached16(sd.gamma + q.vb * V) : zero, gb);
 #pragma unroll
-    for (int e = 0; e < V; ++e) da[e] = db[e] = 0.f;
+    for (int e = 0; e < H2; ++e) da[e] = db[e] = f2(0.f);
     for (int64_t tok = blk * 8 + warp; tok < r.tokens; tok += nblk * 8) {
         uint4 xa, xb, ya, yb;
         float rs;
+        const T *xt = sd.x + tok * sd.x_stride, *yt = sd.dout + tok * sd.dout_stride;
+        const float *rt = sd.rstd + tok * heads;
+        T *dt = sd.out + tok * sd.out_stride;
         auto load = [&](int f) {
             const int h = f * RPW + sub;
             xa = xb = ya = yb = zero;
             rs = 0.f;
             if (h < heads) {
-                const T *x = sd.x + tok * sd.x_stride + (int64_t)h * r.D;
-                const T *dy = sd.dout + tok * sd.dout_stride + (int64_t)h * r.D;
-                rs = __ldg(sd.rstd + tok * heads + h);
+                const T *x = xt + h * r.D, *dy = yt + h * r.D;
+                rs = __ldg(rt + h);
                 if (q.ha) {
                     xa = ld_stream16(x + q.va * V);
                     ya = ld_stream16(dy + q.va * V);
@@ -393,59 +406,57 @@ qk_bw_vec(const QkSide<T> qs, const QkSide<T> ks, const QkRope r, float *part, i
             }
         };
         load(0);
-        float c[V], s[V];
+        float2 c[H2], s[H2];
         qk_angles<V, INTER>(r, q, tok, c, s);
         for (int f = 0; f < ng; ++f) {
             const int h = f * RPW + sub;
-            float a[V], b[V], g[V], x[V], u[V];
+            float2 a[H2], b[H2], x[H2], u[H2];
             const float rstd = rs;
-            Tr::unpack(ya, a);
-            Tr::unpack(yb, b);
-            qk_turn<V, INTER>(q, c, s, -1.f, a, b);  // dn
-            Tr::unpack(xa, x);
-            Tr::unpack(xb, u);
+            unpack2<T>(ya, a);
+            unpack2<T>(yb, b);
+            unpack2<T>(xa, x);
+            unpack2<T>(xb, u);
             if (f + 1 < ng) load(f + 1);
-            float t = 0.f;
-            Tr::unpack(wa, g);
+            qk_turn<V, INTER, true>(q, c, s, a, b);  // dn
+            float2 t = f2(0.f);
 #pragma unroll
-            for (int e = 0; e < V; ++e) {
-                x[e] *= rstd;  // xhat
-                da[e] = fmaf(a[e], x[e], da[e]);
-                a[e] *= g[e];
-                t = fmaf(a[e], x[e], t);
+            for (int e = 0; e < H2; ++e) {
+                const float2 p = mul2(a[e], x[e]), w = mul2(b[e], u[e]);
+                da[e] = fma2(p, f2(rstd), da[e]);
+                db[e] = fma2(w, f2(rstd), db[e]);
+                t = fma2(p, ga[e], fma2(w, gb[e], t));
             }
-            Tr::unpack(wb, g);
-#pragma unroll
-            for (int e = 0; e < V; ++e) {
-                u[e] *= rstd;
-                db[e] = fmaf(b[e], u[e], db[e]);
-                b[e] *= g[e];
-                t = fmaf(b[e], u[e], t);
-            }
-            t = qk_sum<LPR>(t) * invD;
+            const float S = qk_sum<LPR>(t.x + t.y);
             if (h < heads) {
-                T *dx = sd.out + tok * sd.out_stride + (int64_t)h * r.D;
+                // x rstd first: rstd^3 alone could leave fp32's range
+                const float k = -(S * invD) * rstd;
+                T *dx = dt + h * r.D;
 #pragma unroll
-                for (int e = 0; e < V; ++e) {
-                    a[e] = rstd * fmaf(-x[e], t, a[e]);
-                    b[e] = rstd * fmaf(-u[e], t, b[e]);
+                for (int e = 0; e < H2; ++e) {
+                    a[e] = mul2(f2(rstd), fma2(mul2(x[e], f2(rstd)), f2(k), mul2(a[e], ga[e])));
+                    b[e] = mul2(f2(rstd), fma2(mul2(u[e], f2(rstd)), f2(k), mul2(b[e], gb[e])));
                 }
-                if (q.ha) st_stream16(dx + q.va * V, Tr::pack(a));
-                if (q.hb) st_stream16(dx + q.vb * V, Tr::pack(b));
+                if (q.ha) st_stream16(dx + q.va * V, pack2<T>(a));
+                if (q.hb) st_stream16(dx + q.vb * V, pack2<T>(b));
             }
         }
     }
     // the warp's heads: lanes l of all subs; then the block's warps
 #pragma unroll
-    for (int e = 0; e < V; ++e) {
+    for (int e = 0; e < H2; ++e) {
 #pragma unroll
         for (int o = 16; o >= LPR; o >>= 1) {
-            da[e] += __shfl_xor_sync(0xffffffffu, da[e], o);
-            db[e] += __shfl_xor_sync(0xffffffffu, db[e], o);
+            da[e].x += __shfl_xor_sync(0xffffffffu, da[e].x, o);
+            da[e].y += __shfl_xor_sync(0xffffffffu, da[e].y, o);
+            db[e].x += __shfl_xor_sync(0xffffffffu, db[e].x, o);
+            db[e].y += __shfl_xor_sync(0xffffffffu, db[e].y, o);
         }
         if (sub == 0) {
-            sum[warp][l * 2 * V + e] = da[e];
-            sum[warp][l * 2 * V + V + e] = db[e];
+            float *to = &sum[warp][l * 2 * V + 2 * e];
+            to[0] = da[e].x;
+            to[1] = da[e].y;
+            to[V] = db[e].x;
+            to[V + 1] = db[e].y;
         }
     }
     __syncthreads();
