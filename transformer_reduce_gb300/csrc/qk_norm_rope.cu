@@ -95,8 +95,9 @@ static cudaError_t launch_qk_bw_vec(const QkSide<T> &q, const QkSide<T> &k, cons
                                     float *part, int64_t &nq, int64_t &nk, cudaStream_t st) {
     constexpr int RPW = 32 / LPR;
     qk_bw_vec_split(r.tokens, ceil_div(q.heads, RPW), ceil_div(k.heads, RPW), nq, nk);
-    return launch_pdl(qk_bw_vec<T, LPR, INTER>, dim3((unsigned)(nq + nk)), dim3(256), 0, st, q, k,
-                      r, part, (int)nq);
+    ensure_dynamic_smem<qk_bw_vec<T, LPR, INTER>>(kQkBwSmem);
+    return launch_pdl(qk_bw_vec<T, LPR, INTER>, dim3((unsigned)(nq + nk)), dim3(256), kQkBwSmem,
+                      st, q, k, r, part, (int)nq);
 }
 
 template <typename T>

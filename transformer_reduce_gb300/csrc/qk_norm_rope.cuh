@@ -167,8 +167,11 @@ qk_bw_loop(const QkSide<T> qs, const QkSide<T> ks, const QkRope r, float *part, 
 // Heads of whole 16-byte vectors.  LPR lanes hold a head, two vectors each:
 //   halves       lane l < rot / 2V holds vectors l and l + rot / 2V, whose
 //                elements are each other's partners; the other lanes hold the
-//                unrotated vectors two by two;
-//   interleaved  lane l holds vectors 2l and 2l + 1, with their pairs inside.
+//                unrotated vectors in the same manner;
+//   interleaved  lane l holds vectors l and l + (half of the vectors), with
+//                their pairs inside.
+// (Neighbouring lanes hold neighbouring vectors: a 16-byte copy of every other
+// vector would fetch each 32-byte sector twice.)
 // Either way a lane needs V angles of its token's position, the same for every
 // head of the token: a warp takes one token, loads them once, and goes through
 // the heads of both sides, 32 / LPR at a time, the next heads' vectors loading
@@ -181,21 +184,15 @@ struct QkLane {
 };
 template <int V, bool INTER>
 __device__ __forceinline__ QkLane qk_lane(const QkRope &r, int l) {
-    const int nv = r.D / V;
+    const int nv = r.D / V, hv = INTER ? 0 : r.rot / 2 / V;
+    const int rest = (nv - 2 * hv + 1) / 2;  // lanes of the vectors that have no partner
     QkLane q;
-    if (INTER) {
-        q.va = 2 * l;
-        q.vb = 2 * l + 1;
-        q.ra = q.va * V < r.rot;
-        q.rb = q.vb * V < r.rot;
-    } else {
-        const int hv = r.rot / 2 / V;
-        q.ra = q.rb = l < hv;
-        q.va = q.ra ? l : 2 * l;
-        q.vb = q.ra ? l + hv : 2 * l + 1;
-    }
-    q.ha = q.va < nv;
-    q.hb = q.vb < nv;
+    q.va = l < hv ? l : hv + l;
+    q.vb = l < hv ? l + hv : hv + l + rest;
+    q.ha = l < hv + rest;
+    q.hb = q.ha && q.vb < nv;
+    q.ra = INTER ? q.ha && q.va * V < r.rot : l < hv;
+    q.rb = INTER ? q.hb && q.vb * V < r.rot : l < hv;
     return q;
 }
 // Lanes that hold a head (INTER as above).
@@ -208,7 +205,7 @@ inline int qk_lanes(int D, int rot, int V, bool inter) {
 // for one pair of features each (interleaved: c[h].x of vector va's pairs 2h,
 // c[h].y of 2h + 1, then vb's); 1 and 0 where nothing is rotated.
 template <int V, bool INTER>
-__device__ __forceinline__ void qk_angles(const QkRope &r, const QkLane &q, int64_t tok,
+__device__ __forceinline__ void qk_angles(const QkRope &r, const QkLane &q, int64_t pos,
                                           float2 (&c)[V / 2], float2 (&s)[V / 2]) {
 #pragma unroll
     for (int h = 0; h < V / 2; ++h) {
@@ -216,22 +213,22 @@ __device__ __forceinline__ void qk_angles(const QkRope &r, const QkLane &q, int6
         s[h] = f2(0.f);
     }
     if (!q.ra) return;  // (vector vb is rotated only if va is)
-    const int64_t pos = __ldg(r.positions + tok);
     const int half = r.rot / 2;
     if (pos < 0 || pos >= r.max_pos) {
 #pragma unroll
         for (int h = 0; h < V / 2; ++h) c[h] = s[h] = f2(__int_as_float(0x7fc00000));
         return;
     }
-    const int64_t at = pos * half + (INTER ? q.va * (V / 2) : q.va * V);
-    // interleaved: vector vb = va + 1 takes the V / 2 angles after va's
-    const int n = INTER && !q.rb ? V / 4 : V / 2;
 #pragma unroll
-    for (int h = 0; h < V / 2; ++h)
-        if (h < n) {
-            c[h] = __ldg(reinterpret_cast<const float2 *>(r.cos + at + 2 * h));
-            s[h] = __ldg(reinterpret_cast<const float2 *>(r.sin + at + 2 * h));
+    for (int h = 0; h < V / 2; ++h) {
+        // halves: the V angles of vector va; interleaved: V / 2 of each vector
+        const bool second = INTER && h >= V / 4;
+        const int p = INTER ? (second ? q.vb * (V / 2) - V / 2 : q.va * (V / 2)) : q.va * V;
+        if (!second || q.rb) {
+            c[h] = __ldg(reinterpret_cast<const float2 *>(r.cos + pos * half + p + 2 * h));
+            s[h] = __ldg(reinterpret_cast<const float2 *>(r.sin + pos * half + p + 2 * h));
         }
+    }
 }
 
 // One pair of features turned by (c, s).
@@ -279,11 +276,14 @@ __device__ __forceinline__ float qk_sum(float v) {
     return v;
 }
 
+constexpr int kQkStages = 3;  // the current group and two on their way
+constexpr size_t kQkBwSmem = (size_t)kQkStages * 256 * (4 * 16 + 4);
+
 // A group is the 32 / LPR heads of one side that a warp takes at once; an item
 // is up to `per_item` groups of one token (all of them, unless that would
 // leave too few items for the GPU).  ngq, ngk: groups of the two sides.
 template <typename T, int LPR, bool INTER>
-__global__ void __launch_bounds__(256, 3)
+__global__ void __launch_bounds__(256, 2)
 qk_fw_vec(const QkSide<T> qs, const QkSide<T> ks, const QkRope r, int ngq, int ngk, int per_item) {
     pdl_begin();
     using Tr = Traits<T>;
@@ -296,24 +296,46 @@ qk_fw_vec(const QkSide<T> qs, const QkSide<T> ks, const QkRope r, int ngq, int n
     const int64_t items = r.tokens * per_token;
     const float invD = 1.f / (float)r.D;
     const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-    for (int64_t item = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); item < items;
-         item += (int64_t)gridDim.x * 8) {
-        const int64_t tok = per_token == 1 ? item : item / per_token;
-        const int f0 = (int)(item - tok * per_token) * per_item, f1 = min(f0 + per_item, ng);
-        uint4 ra, rb;
-        auto load = [&](int f) {
-            const bool isq = f < ngq;
-            const int h = (isq ? f : f - ngq) * RPW + sub;
-            ra = rb = zero;
-            if (h < (int)(isq ? qs.heads : ks.heads)) {
-                const T *x = (isq ? qs.x + tok * qs.x_stride : ks.x + tok * ks.x_stride) + h * r.D;
-                if (q.ha) ra = ld_stream16(x + q.va * V);
-                if (q.hb) rb = ld_stream16(x + q.vb * V);
+    const int64_t hop = (int64_t)gridDim.x * 8;
+    // The warp's groups in order, copied kQkStages - 1 ahead: each thread its
+    // own two vectors into its own slots.
+    __shared__ uint4 stage[kQkStages][2][256];
+    int64_t i_item = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+    int64_t i_tok = per_token == 1 ? i_item : i_item / per_token;
+    int i_f = (int)(i_item - i_tok * per_token) * per_item, i_end = min(i_f + per_item, ng);
+    auto issue = [&](int st) {
+        if (i_item < items) {
+            const bool isq = i_f < ngq;
+            const int h = (isq ? i_f : i_f - ngq) * RPW + sub;
+            uint4 *slot = &stage[st][0][threadIdx.x];
+            const bool there = h < (int)(isq ? qs.heads : ks.heads);
+            const T *x = (isq ? qs.x + i_tok * qs.x_stride : ks.x + i_tok * ks.x_stride) + h * r.D;
+            if (there && q.ha) cp_async16(slot, x + q.va * V);
+            else *slot = zero;
+            if (there && q.hb) cp_async16(slot + 256, x + q.vb * V);
+            else slot[256] = zero;
+            if (++i_f == i_end) {
+                i_item += hop;
+                i_tok = per_token == 1 ? i_item : i_item / per_token;
+                i_f = (int)(i_item - i_tok * per_token) * per_item;
+                i_end = min(i_f + per_item, ng);
             }
-        };
-        load(f0);
+        }
+        cp_async_commit();
+    };
+#pragma unroll
+    for (int st = 0; st < kQkStages - 1; ++st) issue(st);
+    int st_cur = 0;
+    int64_t item = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+    int64_t tok = per_token == 1 ? item : item / per_token;
+    int pos = r.rot && item < items ? __ldg(r.positions + tok) : 0;
+    for (int64_t next; item < items; item = next) {
+        next = item + hop;
+        const int64_t tok_next = per_token == 1 ? next : next / per_token;
+        const int f0 = (int)(item - tok * per_token) * per_item, f1 = min(f0 + per_item, ng);
         float2 c[H2], s[H2];
-        qk_angles<V, INTER>(r, q, tok, c, s);
+        qk_angles<V, INTER>(r, q, pos, c, s);
+        if (r.rot && next < items) pos = __ldg(r.positions + tok_next);
         for (int f = f0; f < f1;) {  // one side at a time
             const bool isq = f < ngq;
             const T *gamma = isq ? qs.gamma : ks.gamma;
@@ -328,9 +350,11 @@ qk_fw_vec(const QkSide<T> qs, const QkSide<T> ks, const QkRope r, int ngq, int n
             for (; f < g1; ++f) {
                 const int h = (f - g0) * RPW + sub;
                 float2 a[H2], b[H2];
-                unpack2<T>(ra, a);
-                unpack2<T>(rb, b);
-                if (f + 1 < f1) load(f + 1);
+                issue(st_cur == 0 ? kQkStages - 1 : st_cur - 1);
+                cp_async_wait<kQkStages - 1>();  // this thread's copies of the group have landed
+                unpack2<T>(stage[st_cur][0][threadIdx.x], a);
+                unpack2<T>(stage[st_cur][1][threadIdx.x], b);
+                st_cur = st_cur + 1 == kQkStages ? 0 : st_cur + 1;
                 float2 ss = f2(0.f);
 #pragma unroll
                 for (int e = 0; e < H2; ++e) ss = fma2(a[e], a[e], fma2(b[e], b[e], ss));
@@ -350,6 +374,7 @@ qk_fw_vec(const QkSide<T> qs, const QkSide<T> ks, const QkRope r, int ngq, int n
                 }
             }
         }
+        tok = tok_next;
     }
 }
 
@@ -382,41 +407,60 @@ qk_bw_vec(const QkSide<T> qs, const QkSide<T> ks, const QkRope r, float *part, i
     unpack2<T>(q.hb ? ld_cached16(sd.gamma + q.vb * V) : zero, gb);
 #pragma unroll
     for (int e = 0; e < H2; ++e) da[e] = db[e] = f2(0.f);
-    for (int64_t tok = blk * 8 + warp; tok < r.tokens; tok += nblk * 8) {
-        uint4 xa, xb, ya, yb;
-        float rs;
-        const T *xt = sd.x + tok * sd.x_stride, *yt = sd.dout + tok * sd.dout_stride;
-        const float *rt = sd.rstd + tok * heads;
-        T *dt = sd.out + tok * sd.out_stride;
-        auto load = [&](int f) {
-            const int h = f * RPW + sub;
-            xa = xb = ya = yb = zero;
-            rs = 0.f;
-            if (h < heads) {
-                const T *x = xt + h * r.D, *dy = yt + h * r.D;
-                rs = __ldg(rt + h);
-                if (q.ha) {
-                    xa = ld_stream16(x + q.va * V);
-                    ya = ld_stream16(dy + q.va * V);
-                }
-                if (q.hb) {
-                    xb = ld_stream16(x + q.vb * V);
-                    yb = ld_stream16(dy + q.vb * V);
-                }
+    extern __shared__ uint4 dsmem[];  // [kQkStages][4][256], then the rows' rstd
+    float *rs = reinterpret_cast<float *>(dsmem + kQkStages * 4 * 256) + threadIdx.x;
+    const int64_t hop = nblk * 8;
+    int64_t i_tok = blk * 8 + warp;
+    int i_f = 0;
+    auto issue = [&](int st) {
+        if (i_tok < r.tokens) {
+            const int h = i_f * RPW + sub;
+            uint4 *slot = dsmem + st * 4 * 256 + threadIdx.x;
+            const bool there = h < heads;
+            const T *x = sd.x + i_tok * sd.x_stride + h * r.D;
+            const T *dy = sd.dout + i_tok * sd.dout_stride + h * r.D;
+            if (there && q.ha) {
+                cp_async16(slot, x + q.va * V);
+                cp_async16(slot + 256, dy + q.va * V);
+            } else {
+                slot[0] = slot[256] = zero;
             }
-        };
-        load(0);
+            if (there && q.hb) {
+                cp_async16(slot + 512, x + q.vb * V);
+                cp_async16(slot + 768, dy + q.vb * V);
+            } else {
+                slot[512] = slot[768] = zero;
+            }
+            if (there) cp_async4(rs + st * 256, sd.rstd + i_tok * heads + h);
+            else rs[st * 256] = 0.f;
+            if (++i_f == ng) {
+                i_f = 0;
+                i_tok += hop;
+            }
+        }
+        cp_async_commit();
+    };
+#pragma unroll
+    for (int st = 0; st < kQkStages - 1; ++st) issue(st);
+    int st_cur = 0;
+    int pos = r.rot && blk * 8 + warp < r.tokens ? __ldg(r.positions + blk * 8 + warp) : 0;
+    for (int64_t tok = blk * 8 + warp; tok < r.tokens; tok += hop) {
+        T *dt = sd.out + tok * sd.out_stride;
         float2 c[H2], s[H2];
-        qk_angles<V, INTER>(r, q, tok, c, s);
+        qk_angles<V, INTER>(r, q, pos, c, s);
+        if (r.rot && tok + hop < r.tokens) pos = __ldg(r.positions + tok + hop);
         for (int f = 0; f < ng; ++f) {
             const int h = f * RPW + sub;
             float2 a[H2], b[H2], x[H2], u[H2];
-            const float rstd = rs;
-            unpack2<T>(ya, a);
-            unpack2<T>(yb, b);
-            unpack2<T>(xa, x);
-            unpack2<T>(xb, u);
-            if (f + 1 < ng) load(f + 1);
+            issue(st_cur == 0 ? kQkStages - 1 : st_cur - 1);
+            cp_async_wait<kQkStages - 1>();  // this thread's copies of the group have landed
+            const uint4 *slot = dsmem + st_cur * 4 * 256 + threadIdx.x;
+            const float rstd = rs[st_cur * 256];
+            unpack2<T>(slot[0], x);
+            unpack2<T>(slot[256], a);
+            unpack2<T>(slot[512], u);
+            unpack2<T>(slot[768], b);
+            st_cur = st_cur + 1 == kQkStages ? 0 : st_cur + 1;
             qk_turn<V, INTER, true>(q, c, s, a, b);  // dn
             float2 t = f2(0.f);
 #pragma unroll
