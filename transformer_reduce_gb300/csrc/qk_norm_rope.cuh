@@ -299,7 +299,7 @@ qk_fw_vec(const QkSide<T> qs, const QkSide<T> ks, const QkRope r, int ngq, int n
     const int64_t hop = (int64_t)gridDim.x * 8;
     // The warp's groups in order, copied kQkStages - 1 ahead: each thread its
     // own two vectors into its own slots.
-    __shared__ uint4 stage[kQkStages][2][256];
+    __shared__ __align__(128) uint4 stage[kQkStages][2][256];
     int64_t i_item = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
     int64_t i_tok = per_token == 1 ? i_item : i_item / per_token;
     int i_f = (int)(i_item - i_tok * per_token) * per_item, i_end = min(i_f + per_item, ng);
@@ -407,7 +407,7 @@ qk_bw_vec(const QkSide<T> qs, const QkSide<T> ks, const QkRope r, float *part, i
     unpack2<T>(q.hb ? ld_cached16(sd.gamma + q.vb * V) : zero, gb);
 #pragma unroll
     for (int e = 0; e < H2; ++e) da[e] = db[e] = f2(0.f);
-    extern __shared__ uint4 dsmem[];  // [kQkStages][4][256], then the rows' rstd
+    extern __shared__ __align__(128) uint4 dsmem[];  // [kQkStages][4][256], then the rows' rstd
     float *rs = reinterpret_cast<float *>(dsmem + kQkStages * 4 * 256) + threadIdx.x;
     const int64_t hop = nblk * 8;
     int64_t i_tok = blk * 8 + warp;

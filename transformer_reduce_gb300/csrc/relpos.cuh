@@ -355,7 +355,7 @@ __device__ __forceinline__ uint4 relpos_load(const T *base, int64_t at, int64_t 
 }
 
 // Store of a chunk whose first key is j0; keys outside [0, Tk) belong to other
-// rows.
+// rows: a partial chunk is stored by words, and by halves at its border.
 template <typename T, bool AL>
 __device__ __forceinline__ void relpos_store(T *row, int j0, int Tk, const uint4 &u) {
     constexpr int V = Traits<T>::kVec;
@@ -363,11 +363,38 @@ __device__ __forceinline__ void relpos_store(T *row, int j0, int Tk, const uint4
         st_stream16(row + j0, u);
         return;
     }
-    float f[V];
-    Traits<T>::unpack(u, f);
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-    for (int e = 0; e < V; ++e)
-        if (j0 + e >= 0 && j0 + e < Tk) Traits<T>::store1(row + j0 + e, f[e]);
+    for (int i = 0; i < 4; ++i) {
+        if constexpr (V == 4) {
+            if (j0 + i >= 0 && j0 + i < Tk)
+                __stcs(reinterpret_cast<uint32_t *>(row + j0 + i), w[i]);
+        } else {
+            const int j = j0 + 2 * i;  // (a chunk starts at a 16-byte address)
+            if (j >= 0 && j + 1 < Tk)
+                __stcs(reinterpret_cast<uint32_t *>(row + j), w[i]);
+            else if (j >= 0 && j < Tk)
+                __stcs(reinterpret_cast<unsigned short *>(row + j), (unsigned short)w[i]);
+            else if (j == -1 && j + 1 < Tk)
+                __stcs(reinterpret_cast<unsigned short *>(row + j + 1),
+                       (unsigned short)(w[i] >> 16));
+        }
+    }
+}
+
+// The elements [0, n) of a chunk as a mask, for n = 0 ... V, in shared memory.
+template <typename T>
+__device__ __forceinline__ void relpos_keep_table(uint4 *keep) {
+    constexpr int V = Traits<T>::kVec;
+    if (threadIdx.x <= V) {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int n = (int)threadIdx.x - i * (V / 4);  // elements of word i
+            w[i] = n >= V / 4 ? 0xffffffffu : (V == 8 && n == 1 ? 0xffffu : 0u);
+        }
+        keep[threadIdx.x] = make_uint4(w[0], w[1], w[2], w[3]);
+    }
 }
 
 // Bits of the chunk's visible keys: inside [lo, hi), and not masked with -inf
@@ -477,7 +504,7 @@ relpos_fw_vec(T *out, const T *inp, const T *mask, const T *table, const int32_t
     constexpr int G = BLOCK / TPR;
     constexpr int S = kRelposFwStages;
     static_assert(S == 2, "the row in flight is carried in registers");
-    extern __shared__ uint4 dsmem[];
+    extern __shared__ __align__(128) uint4 dsmem[];
     uint4 *stage = dsmem + threadIdx.x;  // [S][CPT][BLOCK], a thread's own slots
     const float4 *lut4 = reinterpret_cast<const float4 *>(dsmem + S * CPT * BLOCK);
     float *lut = reinterpret_cast<float *>(dsmem + S * CPT * BLOCK);
@@ -709,7 +736,7 @@ relpos_bw_vec(T *dinp, float *part, const T *dout, const T *y, const T *mask,
     constexpr int S = kRelposBwStages;
     static_assert(S == 2, "the row in flight is carried in registers");
     constexpr int TW = TPR < 32 ? TPR : 32;  // threads of a group in one warp
-    extern __shared__ uint4 dsmem[];
+    extern __shared__ __align__(128) uint4 dsmem[];
     const int n = blockDim.x;
     uint4 *stage = dsmem + threadIdx.x;  // [S][CPT][2][n], a thread's own slots
     float4 *acc4 = reinterpret_cast<float4 *>(dsmem + S * CPT * 2 * n);
@@ -717,6 +744,8 @@ relpos_bw_vec(T *dinp, float *part, const T *dout, const T *y, const T *mask,
     __shared__ float red[2][BLOCK / 32];
     __shared__ float ends[2][BLOCK / 32];
     __shared__ int2 wtab[kRelposWinMax];
+    __shared__ uint4 keep[V + 1];
+    relpos_keep_table<T>(keep);  // (seen after the first segment's barrier)
     const int G = n / TPR;
     const int lane = threadIdx.x % TPR;
     const int grp = threadIdx.x / TPR;
@@ -790,10 +819,21 @@ relpos_bw_vec(T *dinp, float *part, const T *dout, const T *y, const T *mask,
             auto load = [&](int k, float2(&yv)[H2], float2(&gv)[H2]) {
                 const uint4 *slot = &stage[(turn * CPT + k) * 2 * n];
                 uint4 yr = slot[0], gr4 = slot[n];
-                if (mrow || ((edge >> k) & 1u)) {
-                    const uint32_t bits = relpos_bits<T>(mrow, k * TPR * V + j_lane, lo, hi);
+                const int j0 = k * TPR * V + j_lane;
+                if (mrow) {
+                    const uint32_t bits = relpos_bits<T>(mrow, j0, lo, hi);
                     keep_elements<T>(yr, bits);
                     keep_elements<T>(gr4, bits);
+                } else if ((edge >> k) & 1u) {
+                    const uint4 b = keep[min(hi - j0, V)], a = keep[max(lo - j0, 0)];
+                    yr.x &= b.x & ~a.x;
+                    yr.y &= b.y & ~a.y;
+                    yr.z &= b.z & ~a.z;
+                    yr.w &= b.w & ~a.w;
+                    gr4.x &= b.x & ~a.x;
+                    gr4.y &= b.y & ~a.y;
+                    gr4.z &= b.z & ~a.z;
+                    gr4.w &= b.w & ~a.w;
                 }
                 unpack2<T>(yr, yv);
                 unpack2<T>(gr4, gv);
