@@ -439,10 +439,11 @@ def relpos_buckets(num_buckets: int = 32, max_distance: int = 128, bidirectional
 
 
 def _relpos(bucket):
-    torch = _torch()
-    if bucket.dim() != 1 or bucket.dtype != torch.int32 or bucket.numel() % 2 == 0:
+    """max_distance of a bucket map."""
+    n = bucket.numel()
+    if bucket.dim() != 1 or n % 2 == 0 or bucket.dtype != _torch().int32:
         raise ValueError("buckets must be a 1-D int32 tensor of 2 * max_distance + 1 ids")
-    return bucket.numel() // 2
+    return n // 2
 
 
 def softmax_fw_relpos(scores, table, buckets, mask=None, causal: bool = False, scale=None,
@@ -452,24 +453,25 @@ def softmax_fw_relpos(scores, table, buckets, mask=None, causal: bool = False, s
     Tq) in [-R, R], plus an additive mask [B,Tk]; future keys masked when
     ``causal``.  ``table`` is [num_buckets, H] in the scores' dtype, ``buckets``
     int32 [2R + 1] (see relpos_buckets).  ``out`` may be ``scores``."""
-    torch = _torch()
     if scores.dim() != 4:
         raise ValueError("scores must be [B, H, Tq, Tk]")
-    B, H, Tq, Tk = shape = scores.shape
+    B, H, Tq, Tk = scores.shape
     dtype = scores.dtype
     if table.dim() != 2:
         raise ValueError("table must be [num_buckets, H]")
-    nb = table.shape[0]
-    _want("table", table, (nb, H), dtype)
+    nb, heads = table.shape
+    if heads != H or table.dtype != dtype:
+        _want("table", table, (nb, H), dtype)
     R = _relpos(buckets)
-    _want("mask", mask, (B, Tk), dtype)
+    if mask is not None and (mask.dtype != dtype or mask.shape != (B, Tk)):
+        _want("mask", mask, (B, Tk), dtype)
     if out is None:
-        out = torch.empty_like(scores)
+        out = _torch().empty_like(scores)
     else:
-        _want("out", out, shape, dtype)
+        _want("out", out, scores.shape, dtype)
     dev = _same_device(scores, table, buckets, mask, out)
-    _launch("ls_softmax_fw_relpos", dev, _ptr(out), _ptr(scores), _ptr(mask), _ptr(table),
-            _ptr(buckets), B, H, Tq, Tk, nb, R, 1 if causal else 0,
+    _launch("ls_softmax_fw_relpos", dev, out.data_ptr(), scores.data_ptr(), _ptr(mask),
+            table.data_ptr(), buckets.data_ptr(), B, H, Tq, Tk, nb, R, 1 if causal else 0,
             1.0 if scale is None else float(scale), ls_dtype(scores))
     return out
 
@@ -485,26 +487,35 @@ def softmax_bw_relpos(dout, out_fw, buckets, num_buckets: int, mask=None, causal
     """Gradients of ``softmax_fw_relpos``: (dscores, dtable), dtable fp32
     [num_buckets, H] in a fixed summation order.  Reads only visible keys;
     ``dinp`` may be ``dout``."""
-    torch = _torch()
+    f32 = _torch().float32
     if dout.dim() != 4:
         raise ValueError("dout must be [B, H, Tq, Tk]")
-    B, H, Tq, Tk = dout.shape
-    _want("out_fw", out_fw, dout.shape, dout.dtype)
+    B, H, Tq, Tk = shape = dout.shape
+    dtype = dout.dtype
+    if out_fw.shape != shape or out_fw.dtype != dtype:
+        _want("out_fw", out_fw, shape, dtype)
     R = _relpos(buckets)
-    _want("mask", mask, (B, Tk), dout.dtype)
-    _want("dinp", dinp, dout.shape, dout.dtype)
-    _want("dtable", dtable, (num_buckets, H), torch.float32)
+    if mask is not None and (mask.dtype != dtype or mask.shape != (B, Tk)):
+        _want("mask", mask, (B, Tk), dtype)
     if workspace is None:
-        workspace = softmax_relpos_workspace(H, R, dout.device)
-    _workspace("workspace", workspace)
-    dinp = torch.empty_like(dout) if dinp is None else dinp
+        n = max(ls_softmax_bw_relpos_workspace_size(H, R), 16) // 4
+        workspace = dout.new_empty(n, dtype=f32)
+    else:
+        _workspace("workspace", workspace)
+        n = workspace.numel()
+    if dinp is None:
+        dinp = _torch().empty_like(dout)
+    else:
+        _want("dinp", dinp, shape, dtype)
     if dtable is None:
-        dtable = dout.new_empty((num_buckets, H), dtype=torch.float32)
+        dtable = dout.new_empty((num_buckets, H), dtype=f32)
+    else:
+        _want("dtable", dtable, (num_buckets, H), f32)
     dev = _same_device(dout, out_fw, buckets, mask, workspace, dinp, dtable)
-    _launch("ls_softmax_bw_relpos", dev, _ptr(dinp), _ptr(dtable), _ptr(dout), _ptr(out_fw),
-            _ptr(mask), _ptr(buckets), B, H, Tq, Tk, num_buckets, R, 1 if causal else 0,
-            1.0 if scale is None else float(scale), _ptr(workspace),
-            workspace.numel() * 4, ls_dtype(dout))
+    _launch("ls_softmax_bw_relpos", dev, dinp.data_ptr(), dtable.data_ptr(), dout.data_ptr(),
+            out_fw.data_ptr(), _ptr(mask), buckets.data_ptr(), B, H, Tq, Tk, num_buckets, R,
+            1 if causal else 0, 1.0 if scale is None else float(scale), workspace.data_ptr(),
+            4 * n, ls_dtype(dout))
     return dinp, dtable
 
 
@@ -522,32 +533,44 @@ def rope_tables(max_pos: int, rot: int, base: float = 10000.0, device="cuda"):
     return angle.cos().float(), angle.sin().float()
 
 
-def _heads(name, t, tokens=None, D=None, dtype=None):
-    """Token stride of a [tokens, heads, D] tensor whose heads and features are
-    dense (a slice of a packed projection is)."""
+def _heads(name, t):
+    """Shape and token stride of a [tokens, heads, D] tensor whose heads and
+    features are dense (a slice of a packed projection is)."""
     if t.dim() != 3:
         raise ValueError(f"{name} must be [tokens, heads, D]")
     n, h, d = t.shape
-    if (tokens is not None and n != tokens) or (D is not None and d != D) or \
-            (dtype is not None and t.dtype != dtype):
-        raise ValueError(f"{name} must be {dtype} of shape [{tokens}, heads, {D}], "
-                         f"got {t.dtype} of shape {list(t.shape)}")
-    s = t.stride()
-    if (d > 1 and s[2] != 1) or (h > 1 and s[1] != d):
+    st, sh, sd = t.stride()
+    if (d > 1 and sd != 1) or (h > 1 and sh != d):
         raise ValueError(f"{name} must have dense heads and features")
     if n <= 1 or h == 0:
-        return h * d
-    if s[0] < h * d:
-        raise ValueError(f"{name} must not overlap itself (token stride {s[0]} < {h * d})")
-    return s[0]
+        return n, h, d, h * d
+    if st < h * d:
+        raise ValueError(f"{name} must not overlap itself (token stride {st} < {h * d})")
+    return n, h, d, st
 
 
 def _like_heads(name, t, x):
-    """As _heads, for a tensor that has to have x's shape and dtype."""
+    """Token stride of t, which has to have x's shape and dtype."""
     if t.shape != x.shape or t.dtype != x.dtype:
         raise ValueError(f"{name} must be {x.dtype} of shape {list(x.shape)}, "
                          f"got {t.dtype} of shape {list(t.shape)}")
-    return _heads(name, t)
+    return _heads(name, t)[3]
+
+
+def _both_heads(q, k, gamma_q, gamma_k):
+    """(tokens, Hq, Hk, D, token strides of q and k) of the two sides."""
+    tokens, Hq, D, qs = _heads("q", q)
+    dtype, shape = q.dtype, k.shape
+    if len(shape) != 3 or shape[0] != tokens or shape[2] != D or k.dtype != dtype:
+        raise ValueError(f"k must be {dtype} of shape [{tokens}, heads, {D}], "
+                         f"got {k.dtype} of shape {list(shape)}")
+    _, Hk, _, ks = _heads("k", k)
+    want = (D,)
+    if gamma_q.shape != want or gamma_q.dtype != dtype or \
+            gamma_k.shape != want or gamma_k.dtype != dtype:
+        _want("gamma_q", gamma_q, want, dtype)
+        _want("gamma_k", gamma_k, want, dtype)
+    return tokens, Hq, Hk, D, qs, ks
 
 
 def _rotation(cos, sin, positions, tokens, D):
@@ -590,14 +613,8 @@ def qk_norm_rope_fw(q, k, gamma_q, gamma_k, cos=None, sin=None, positions=None,
     ``interleaved``.  Returns (q_out, k_out, q_rstd, k_rstd), the statistics
     fp32.  Tokens may be strided (slices of a packed projection); the outputs
     may be the inputs (in place, same strides)."""
-    torch = _torch()
-    qs = _heads("q", q)
-    tokens, Hq, D = q.shape
-    dtype = q.dtype
-    ks = _heads("k", k, tokens, D, dtype)
-    Hk = k.shape[1]
-    _want("gamma_q", gamma_q, (D,), dtype)
-    _want("gamma_k", gamma_k, (D,), dtype)
+    f32 = _torch().float32
+    tokens, Hq, Hk, D, qs, ks = _both_heads(q, k, gamma_q, gamma_k)
     rot, max_pos = _rotation(cos, sin, positions, tokens, D)
     qos, kos = Hq * D, Hk * D
     if q_out is None:
@@ -609,18 +626,18 @@ def qk_norm_rope_fw(q, k, gamma_q, gamma_k, cos=None, sin=None, positions=None,
     else:
         kos = _like_heads("k_out", k_out, k)
     if q_rstd is None:
-        q_rstd = q.new_empty((tokens, Hq), dtype=torch.float32)
+        q_rstd = q.new_empty((tokens, Hq), dtype=f32)
     else:
-        _want("q_rstd", q_rstd, (tokens, Hq), torch.float32)
+        _want("q_rstd", q_rstd, (tokens, Hq), f32)
     if k_rstd is None:
-        k_rstd = q.new_empty((tokens, Hk), dtype=torch.float32)
+        k_rstd = q.new_empty((tokens, Hk), dtype=f32)
     else:
-        _want("k_rstd", k_rstd, (tokens, Hk), torch.float32)
+        _want("k_rstd", k_rstd, (tokens, Hk), f32)
     dev = _one_device((q, k, q_out, k_out),
                       (gamma_q, gamma_k, cos, sin, positions, q_rstd, k_rstd))
-    _launch("ls_qk_norm_rope_fw", dev, _ptr(q_out), _ptr(k_out), _ptr(q_rstd), _ptr(k_rstd),
-            _ptr(q), _ptr(k), _ptr(gamma_q), _ptr(gamma_k), _ptr(cos), _ptr(sin), _ptr(positions),
-            tokens, Hq, Hk, D, rot, max_pos, qos, kos, qs, ks, 1 if interleaved else 0,
+    _launch("ls_qk_norm_rope_fw", dev, q_out.data_ptr(), k_out.data_ptr(), q_rstd.data_ptr(),
+            k_rstd.data_ptr(), q.data_ptr(), k.data_ptr(), gamma_q.data_ptr(),
+            gamma_k.data_ptr(), _ptr(cos), _ptr(sin), _ptr(positions), tokens, Hq, Hk, D, rot, max_pos, qos, kos, qs, ks, 1 if interleaved else 0,
             float(eps), ls_dtype(q))
     return q_out, k_out, q_rstd, k_rstd
 
@@ -638,37 +655,47 @@ def qk_norm_rope_bw(dq_out, dk_out, q, k, gamma_q, gamma_k, q_rstd, k_rstd, cos=
     its saved statistics: (dq, dk, dgamma_q, dgamma_k), the gamma gradients
     fp32 [D] in a fixed summation order.  ``dq`` and ``dk`` may be ``dq_out``
     and ``dk_out``, or slices of a packed gradient."""
-    torch = _torch()
-    qs = _heads("q", q)
-    tokens, Hq, D = q.shape
-    ks = _heads("k", k, tokens, D, q.dtype)
-    Hk = k.shape[1]
+    f32 = _torch().float32
+    tokens, Hq, Hk, D, qs, ks = _both_heads(q, k, gamma_q, gamma_k)
     dqos, dkos = _like_heads("dq_out", dq_out, q), _like_heads("dk_out", dk_out, k)
-    _want("gamma_q", gamma_q, (D,), q.dtype)
-    _want("gamma_k", gamma_k, (D,), q.dtype)
-    _want("q_rstd", q_rstd, (tokens, Hq), torch.float32)
-    _want("k_rstd", k_rstd, (tokens, Hk), torch.float32)
+    if q_rstd.shape != (tokens, Hq) or q_rstd.dtype != f32 or \
+            k_rstd.shape != (tokens, Hk) or k_rstd.dtype != f32:
+        _want("q_rstd", q_rstd, (tokens, Hq), f32)
+        _want("k_rstd", k_rstd, (tokens, Hk), f32)
     rot, max_pos = _rotation(cos, sin, positions, tokens, D)
-    _want("dgamma_q", dgamma_q, (D,), torch.float32)
-    _want("dgamma_k", dgamma_k, (D,), torch.float32)
     if workspace is None:
-        workspace = qk_norm_rope_workspace(tokens, Hq, Hk, D, q.device)
-    _workspace("workspace", workspace)
-    dq = q.new_empty((tokens, Hq, D)) if dq is None else dq
-    dk = k.new_empty((tokens, Hk, D)) if dk is None else dk
-    dqs, dks = _like_heads("dq", dq, q), _like_heads("dk", dk, k)
+        n = max(ls_qk_norm_rope_bw_workspace_size(tokens, Hq, Hk, D), 16) // 4
+        workspace = q.new_empty(n, dtype=f32)
+    else:
+        _workspace("workspace", workspace)
+        n = workspace.numel()
+    dqs, dks = Hq * D, Hk * D
+    if dq is None:
+        dq = q.new_empty((tokens, Hq, D))
+    else:
+        dqs = _like_heads("dq", dq, q)
+    if dk is None:
+        dk = k.new_empty((tokens, Hk, D))
+    else:
+        dks = _like_heads("dk", dk, k)
     # a side without heads has no gradient to sum: its gamma gradient is zero
     make = q.new_empty if Hq and Hk else q.new_zeros
-    dgamma_q = make(D, dtype=torch.float32) if dgamma_q is None else dgamma_q
-    dgamma_k = make(D, dtype=torch.float32) if dgamma_k is None else dgamma_k
+    if dgamma_q is None:
+        dgamma_q = make(D, dtype=f32)
+    else:
+        _want("dgamma_q", dgamma_q, (D,), f32)
+    if dgamma_k is None:
+        dgamma_k = make(D, dtype=f32)
+    else:
+        _want("dgamma_k", dgamma_k, (D,), f32)
     dev = _one_device((q, k, dq_out, dk_out, dq, dk),
                       (gamma_q, gamma_k, q_rstd, k_rstd, cos, sin, positions, workspace,
                        dgamma_q, dgamma_k))
-    _launch("ls_qk_norm_rope_bw", dev, _ptr(dq), _ptr(dk), _ptr(dgamma_q), _ptr(dgamma_k),
-            _ptr(dq_out), _ptr(dk_out), _ptr(q), _ptr(k), _ptr(gamma_q), _ptr(gamma_k),
-            _ptr(q_rstd), _ptr(k_rstd), _ptr(cos), _ptr(sin), _ptr(positions), tokens, Hq, Hk, D,
-            rot, max_pos, dqs, dks, dqos, dkos, qs, ks, 1 if interleaved else 0, _ptr(workspace),
-            workspace.numel() * 4, ls_dtype(q))
+    _launch("ls_qk_norm_rope_bw", dev, dq.data_ptr(), dk.data_ptr(), dgamma_q.data_ptr(),
+            dgamma_k.data_ptr(), dq_out.data_ptr(), dk_out.data_ptr(), q.data_ptr(), k.data_ptr(),
+            gamma_q.data_ptr(), gamma_k.data_ptr(), q_rstd.data_ptr(), k_rstd.data_ptr(),
+            _ptr(cos), _ptr(sin), _ptr(positions), tokens, Hq, Hk, D, rot, max_pos, dqs, dks,
+            dqos, dkos, qs, ks, 1 if interleaved else 0, workspace.data_ptr(), 4 * n, ls_dtype(q))
     return dq, dk, dgamma_q, dgamma_k
 
 
