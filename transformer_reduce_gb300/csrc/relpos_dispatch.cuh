@@ -1,6 +1,6 @@
 // relpos_dispatch.cuh -- launchers of the softmax with a relative position
-// bias (instantiated per storage dtype in relpos_f32.cu, relpos_f16.cu and
-// relpos_bf16.cu, so that the build compiles them in parallel).
+// bias (instantiated per direction and storage dtype in relpos_fw_f32.cu ...
+// relpos_bw_bf16.cu, so that the build compiles them in parallel).
 #pragma once
 
 #include "dispatch.cuh"
@@ -69,11 +69,11 @@ int relpos_phase(const void *p) {
     return (int)(reinterpret_cast<uintptr_t>(p) % 16 / sizeof(T));
 }
 
-template <typename T, int TPR, int CPT, bool AL>
+template <typename T, int TPR, int CPT, bool AL, bool MASKED>
 cudaError_t launch_relpos_fw_vec(T *out, const T *inp, const T *mask, const T *table,
                                  const int32_t *bucket, RelposShape p, int mask_vec,
                                  cudaStream_t st) {
-    constexpr auto K = relpos_fw_vec<T, TPR, CPT, AL>;
+    constexpr auto K = relpos_fw_vec<T, TPR, CPT, AL, MASKED>;
     const size_t smem = relpos_fw_smem<TPR, CPT>(p.R);
     const cudaError_t e = relpos_allow_smem<K>(relpos_fw_smem<TPR, CPT>(kRelposMaxDistance));
     if (e != cudaSuccess) return e;
@@ -93,14 +93,15 @@ cudaError_t launch_relpos_fw(T *out, const T *inp, const T *mask, const T *table
     if (relpos_phase<T>(out) == phase && pick_relpos_bucket(p, V, phase, &tpr, &cpt)) {
         const bool al = p.Tk % V == 0 && phase == 0;
         const int mask_vec = relpos_phase<T>(mask) == 0;
-#define X(TPR_, CPT_)                                                                     \
-    if (tpr == TPR_ && cpt == CPT_)                                                       \
-        return al ? launch_relpos_fw_vec<T, TPR_, CPT_, true>(out, inp, mask, table,      \
-                                                              bucket, p, mask_vec, st)    \
-                  : launch_relpos_fw_vec<T, TPR_, CPT_, false>(out, inp, mask, table,     \
-                                                               bucket, p, mask_vec, st);
+#define F(TPR_, CPT_, AL_, M_) \
+    launch_relpos_fw_vec<T, TPR_, CPT_, AL_, M_>(out, inp, mask, table, bucket, p, mask_vec, st)
+#define X(TPR_, CPT_)                                                              \
+    if (tpr == TPR_ && cpt == CPT_)                                                \
+        return mask ? (al ? F(TPR_, CPT_, true, true) : F(TPR_, CPT_, false, true)) \
+                    : (al ? F(TPR_, CPT_, true, false) : F(TPR_, CPT_, false, false));
         LSR_DENSE4_BUCKETS(X)
 #undef X
+#undef F
     }
     const size_t smem = relpos_sums_bytes(p.R);
     const int64_t blocks = (int64_t)device_sm_count() * 8;
@@ -126,10 +127,10 @@ int relpos_bw_threads(int band_stride) {
     return n;
 }
 
-template <typename T, int TPR, int CPT, bool AL>
+template <typename T, int TPR, int CPT, bool AL, bool MASKED>
 cudaError_t launch_relpos_bw_vec(T *dinp, const T *dout, const T *y, const T *mask,
                                  RelposShape &p, float *part, cudaStream_t st) {
-    constexpr auto K = relpos_bw_vec<T, TPR, CPT, AL>;
+    constexpr auto K = relpos_bw_vec<T, TPR, CPT, AL, MASKED>;
     const cudaError_t e = relpos_allow_smem<K>(kRelposSmSmem);
     if (e != cudaSuccess) return e;
     const int stride = relpos_band<Traits<T>::kVec>(p).stride;
@@ -154,14 +155,15 @@ cudaError_t launch_relpos_bw_rows(T *dinp, const T *dout, const T *y, const T *m
             cpt = (int)ceil_div(tpr * cpt, 4);
             tpr = 4;
         }
-#define X(TPR_, CPT_)                                                                       \
-    if (tpr == TPR_ && cpt == CPT_)                                                         \
-        return al ? launch_relpos_bw_vec<T, TPR_, CPT_, true>(dinp, dout, y, mask, p, part, \
-                                                              st)                           \
-                  : launch_relpos_bw_vec<T, TPR_, CPT_, false>(dinp, dout, y, mask, p,      \
-                                                               part, st);
+#define F(TPR_, CPT_, AL_, M_) \
+    launch_relpos_bw_vec<T, TPR_, CPT_, AL_, M_>(dinp, dout, y, mask, p, part, st)
+#define X(TPR_, CPT_)                                                              \
+    if (tpr == TPR_ && cpt == CPT_)                                                \
+        return mask ? (al ? F(TPR_, CPT_, true, true) : F(TPR_, CPT_, false, true)) \
+                    : (al ? F(TPR_, CPT_, true, false) : F(TPR_, CPT_, false, false));
         LSR_RELPOS_BW_BUCKETS(X)
 #undef X
+#undef F
     }
     if (p.Tk <= kLoopWarpRowMax) {
         const cudaError_t e =
@@ -190,11 +192,12 @@ cudaError_t launch_relpos_bw(T *dinp, float *dtable, const T *dout, const T *y, 
                       (const float *)part, bucket, p);
 }
 
-#define LSR_RELPOS_INSTANTIATE(T)                                                              \
-    template cudaError_t launch_relpos_fw<T>(T *, const T *, const T *, const T *,             \
-                                             const int32_t *, RelposShape, cudaStream_t);      \
-    template cudaError_t launch_relpos_bw<T>(T *, float *, const T *, const T *, const T *,    \
-                                             const int32_t *, RelposShape, float *,            \
+#define LSR_RELPOS_FW_INSTANTIATE(T)                                                        \
+    template cudaError_t launch_relpos_fw<T>(T *, const T *, const T *, const T *,          \
+                                             const int32_t *, RelposShape, cudaStream_t);
+#define LSR_RELPOS_BW_INSTANTIATE(T)                                                        \
+    template cudaError_t launch_relpos_bw<T>(T *, float *, const T *, const T *, const T *, \
+                                             const int32_t *, RelposShape, float *,         \
                                              cudaStream_t);
 
 }  // namespace lsr
