@@ -149,7 +149,7 @@ def test_relpos_one_bucket_per_distance_and_ids_outside(lib):
 
 
 @pytest.mark.parametrize("dt", list(DT))
-@pytest.mark.parametrize("Tk", [40, 45, 512, 2049])
+@pytest.mark.parametrize("Tk", [40, 45, 512, 2049, 17000])
 def test_relpos_infinities_and_nan(lib, dt, Tk):
     """NaN and infinities at invisible keys never matter; at visible ones the
     row follows the formula: +inf or NaN make it NaN, -inf gets weight 0, a
@@ -201,7 +201,7 @@ def test_relpos_infinities_and_nan(lib, dt, Tk):
 
 
 @pytest.mark.parametrize("dt", list(DT))
-@pytest.mark.parametrize("Tk", [24, 100, 512, 1001, 5000])
+@pytest.mark.parametrize("Tk", [24, 100, 512, 1001, 5000, 20000])
 def test_relpos_lowest_value_everywhere(lib, dt, Tk):
     """A row whose every key carries the type's lowest value is still a softmax."""
     L, dtype = lib, DT[dt]
@@ -244,6 +244,43 @@ def test_relpos_in_place_and_misaligned(lib, dt, Tk, shifts):
     dx, dtab = L.softmax_bw_relpos(g, y, buckets, 32, m, dinp=g)
     R.check(g, wx, tx, "dx in place")
     R.check(dtab, wt, tt, "table in place")
+
+
+@pytest.mark.parametrize("Tk", [45, 2100])
+def test_relpos_looped_path_infinities_and_nan(lib, Tk):
+    """The looped kernels (tensors at different offsets within 16 bytes)."""
+    L = lib
+    shape = (2, 2, 12, Tk)
+    x, table, buckets, _ = _relpos(L, shape, "f16", nb=8, dist=16)
+    mask = torch.zeros(2, Tk, device=DEV, dtype=torch.float16)
+    mask[:, Tk // 2:] = -INF
+    x[0, 0, 0, 1] = float("nan")
+    x[0, 0, 1, 2] = INF
+    x[0, 0, 2, :] = -INF
+    x[0, 0, 3, ::2] = -INF
+    x[..., Tk // 2:] = float("nan")
+    out = _shifted(torch.zeros_like(x), 1)
+    y = L.softmax_fw_relpos(x, table, buckets, mask, out=out)
+    seen = mask[0] == 0
+    assert torch.all(y[0, 0, 0][seen].isnan()) and torch.all(y[0, 0, 1][seen].isnan())
+    assert torch.all(y[..., ~seen] == 0) and torch.all(y[0, 0, 2] == 0)
+    want, tol = R.relpos_fw(x, table, buckets, mask, False, 1.0)
+    R.check(y[0, 0, 3:], want[0, 0, 3:], tol[0, 0, 3:], "rows after")
+    dout = _randn(shape, torch.float16, 9)
+    good = y.nan_to_num()
+    d1, t1 = L.softmax_bw_relpos(_shifted(dout, 1), good, buckets, 8, mask)
+    bad = dout.clone()
+    bad[..., Tk // 2:] = float("nan")
+    d2, t2 = L.softmax_bw_relpos(_shifted(bad, 1), good, buckets, 8, mask)
+    assert torch.equal(d1, d2) and torch.equal(t1, t2) and torch.all(d1[..., ~seen] == 0)
+
+
+def test_relpos_bw_many_rows_per_block_and_few_buckets(lib):
+    """Long runs of rows of every alignment, whose phases change with the batch entry."""
+    for shape, causal in (((7, 3, 701, 40), False), ((9, 2, 333, 130), False),
+                          ((5, 4, 257, 257), True), ((40, 3, 17, 66), False)):
+        for dt in ("bf16", "f32"):
+            _check_relpos(lib, shape, dt, nb=8, dist=60, mask="pad", causal=causal)
 
 
 def test_relpos_empty_problems(lib):

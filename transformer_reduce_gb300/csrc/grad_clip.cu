@@ -174,7 +174,7 @@ grad_squares(double *part, const __grid_constant__ GradList<CAP> L) {
 // The norm from all partials, the same in every block that asks.
 __device__ __forceinline__ float grad_total_norm(const double *part, int parts) {
     double d = 0.0;
-    for (int i = threadIdx.x; i < parts; i += kGradBlock) d += part[i];
+    for (int i = threadIdx.x; i < parts; i += kGradBlock) d += __ldcg(part + i);
     return (float)sqrt(grad_block_sum(d));
 }
 

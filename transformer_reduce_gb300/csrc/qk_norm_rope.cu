@@ -39,7 +39,7 @@ static int qk_lanes_vec(const QkSide<T> &q, const QkSide<T> &k, const QkRope &r)
     constexpr int V = Traits<T>::kVec;
     const auto angles = reinterpret_cast<uintptr_t>(r.cos) | reinterpret_cast<uintptr_t>(r.sin);
     if (r.D % V || r.rot % (r.interleaved ? V : 2 * V) || angles % 8 || !qk_side_vec(q) ||
-        !qk_side_vec(k) || q.heads + k.heads > (1 << 24))
+        !qk_side_vec(k) || q.heads + k.heads > (1 << 20))  // (a token's elements fit 31 bits)
         return 0;
     int lanes = 2;
     while (lanes < qk_lanes(r.D, r.rot, V, r.interleaved)) lanes *= 2;

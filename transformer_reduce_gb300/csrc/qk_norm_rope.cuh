@@ -527,7 +527,7 @@ qk_fold(float *dgq, float *dgk, const float *part, int D, int q_blocks, int bloc
     float v = 0.f;
     if (j < D) {
 #pragma unroll 8
-        for (int b = beg + ty; b < end; b += 8) v += __ldg(part + (int64_t)b * D + j);
+        for (int b = beg + ty; b < end; b += 8) v += __ldcg(part + (int64_t)b * D + j);
     }
     sum[ty][tx] = v;
     __syncthreads();

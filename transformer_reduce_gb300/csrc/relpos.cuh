@@ -996,7 +996,7 @@ relpos_fold(float *dtable, const float *part, const int32_t *bucket, const Relpo
     for (int d = threadIdx.x; d < W; d += 256) {
         float v = 0.f;
 #pragma unroll 8
-        for (int64_t k = first; k <= last; ++k) v += __ldg(part + (k + h) * W + d);
+        for (int64_t k = first; k <= last; ++k) v += __ldcg(part + (k + h) * W + d);
         dist[d] = v;
     }
     __syncthreads();
