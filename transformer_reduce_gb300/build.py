@@ -27,7 +27,7 @@ LIB_PATH = os.path.join(PKG, LIB_NAME)
 SOURCES = ["abi.cu", "kernels_f32.cu", "kernels_f16.cu", "kernels_bf16.cu", "noalloc.cu",
            "cross_entropy.cu", "relpos_fw_f32.cu", "relpos_fw_f16.cu",
            "relpos_fw_bf16.cu", "relpos_bw_f32.cu", "relpos_bw_f16.cu", "relpos_bw_bf16.cu",
-           "qk_norm_rope.cu", "grad_clip.cu"]
+           "qk_norm_rope_f32.cu", "qk_norm_rope_f16.cu", "qk_norm_rope_bf16.cu", "grad_clip.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-O2",
               "--expt-relaxed-constexpr"]

@@ -14,6 +14,8 @@
 // not rounded before the rotation.
 #pragma once
 
+#include <type_traits>
+
 #include "launch.h"
 #include "ls_device.cuh"
 
@@ -164,7 +166,9 @@ qk_bw_loop(const QkSide<T> qs, const QkSide<T> ks, const QkRope r, float *part, 
 }
 
 // ----------------------------------------------------------------------------
-// Heads of whole 16-byte vectors.  LPR lanes hold a head, two vectors each:
+// Heads of whole vectors of V elements: 16 bytes where the head size, the
+// rotated part, the pointers and the strides are multiples of them, else 8 or 4
+// bytes.  LPR lanes hold a head, two vectors each:
 //   halves       lane l < rot / 2V holds vectors l and l + rot / 2V, whose
 //                elements are each other's partners; the other lanes hold the
 //                unrotated vectors in the same manner;
@@ -177,6 +181,85 @@ qk_bw_loop(const QkSide<T> qs, const QkSide<T> ks, const QkRope r, float *part, 
 // the heads of both sides, 32 / LPR at a time, the next heads' vectors loading
 // while it works on the current ones.
 // ----------------------------------------------------------------------------
+// A vector of V elements as it lies in memory.
+template <typename T, int V>
+struct alignas(V * sizeof(T)) QkRaw {
+    static constexpr int N = V * (int)sizeof(T) / 4;  // words
+    uint32_t w[N];
+};
+template <typename T, int V>
+__device__ __forceinline__ QkRaw<T, V> qk_zero() {
+    QkRaw<T, V> r;
+#pragma unroll
+    for (int i = 0; i < QkRaw<T, V>::N; ++i) r.w[i] = 0u;
+    return r;
+}
+// Gamma's vector at p, or zeros.
+template <typename T, int V>
+__device__ __forceinline__ QkRaw<T, V> qk_gamma(const T *p, bool there) {
+    constexpr int N = QkRaw<T, V>::N;
+    QkRaw<T, V> r = qk_zero<T, V>();
+    if (there) {
+        if constexpr (N == 4) {
+            const uint4 u = ld_cached16(p);
+            r.w[0] = u.x;
+            r.w[1] = u.y;
+            r.w[2] = u.z;
+            r.w[3] = u.w;
+        } else if constexpr (N == 2) {
+            const uint2 u = __ldg(reinterpret_cast<const uint2 *>(p));
+            r.w[0] = u.x;
+            r.w[1] = u.y;
+        } else {
+            r.w[0] = __ldg(reinterpret_cast<const uint32_t *>(p));
+        }
+    }
+    return r;
+}
+template <typename T, int V>
+__device__ __forceinline__ void qk_unpack(const QkRaw<T, V> &r, float2 (&f)[V / 2]) {
+#pragma unroll
+    for (int h = 0; h < V / 2; ++h) {
+        if constexpr (sizeof(T) == 4)
+            f[h] = make_float2(__uint_as_float(r.w[2 * h]), __uint_as_float(r.w[2 * h + 1]));
+        else if constexpr (std::is_same<T, __half>::value)
+            f[h] = Traits<__half>::two(r.w[h]);
+        else
+            f[h] = bf16x2_to_float2(r.w[h]);
+    }
+}
+template <typename T, int V>
+__device__ __forceinline__ void qk_store(T *p, const float2 (&f)[V / 2]) {
+    constexpr int N = QkRaw<T, V>::N;
+    uint32_t w[N];
+#pragma unroll
+    for (int h = 0; h < V / 2; ++h) {
+        if constexpr (sizeof(T) == 4) {
+            w[2 * h] = __float_as_uint(f[h].x);
+            w[2 * h + 1] = __float_as_uint(f[h].y);
+        } else {
+            w[h] = Traits<T>::word(f[h].x, f[h].y);
+        }
+    }
+    if constexpr (N == 4)
+        __stcs(reinterpret_cast<uint4 *>(p), make_uint4(w[0], w[1], w[2], w[3]));
+    else if constexpr (N == 2)
+        __stcs(reinterpret_cast<uint2 *>(p), make_uint2(w[0], w[1]));
+    else
+        __stcs(reinterpret_cast<uint32_t *>(p), w[0]);
+}
+// Asynchronous copy of one vector into the thread's slot.
+template <typename T, int V>
+__device__ __forceinline__ void qk_copy(QkRaw<T, V> *slot, const T *p) {
+    if constexpr (QkRaw<T, V>::N == 4)
+        cp_async16(slot, p);
+    else if constexpr (QkRaw<T, V>::N == 2)
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_addr(slot)), "l"(p)
+                     : "memory");
+    else
+        cp_async4(slot, p);
+}
+
 struct QkLane {
     int va, vb;   // vectors
     bool ha, hb;  // there are such vectors
@@ -201,9 +284,9 @@ inline int qk_lanes(int D, int rot, int V, bool inter) {
     return hv + (nv - 2 * hv + 1) / 2;
 }
 
-// Cosines and sines of the lane's V angles, as pairs of neighbours (halves) or
-// for one pair of features each (interleaved: c[h].x of vector va's pairs 2h,
-// c[h].y of 2h + 1, then vb's); 1 and 0 where nothing is rotated.
+// Cosines and sines of the lane's V angles, two by two (halves: those of
+// vector va's features; interleaved: V / 2 for the pairs of vector va, then V / 2
+// for vb's); 1 and 0 where nothing is rotated.
 template <int V, bool INTER>
 __device__ __forceinline__ void qk_angles(const QkRope &r, const QkLane &q, int64_t pos,
                                           float2 (&c)[V / 2], float2 (&s)[V / 2]) {
@@ -219,14 +302,23 @@ __device__ __forceinline__ void qk_angles(const QkRope &r, const QkLane &q, int6
         for (int h = 0; h < V / 2; ++h) c[h] = s[h] = f2(__int_as_float(0x7fc00000));
         return;
     }
+    const float *cp = r.cos + pos * half, *sp = r.sin + pos * half;
+    if constexpr (INTER && V == 2) {
+        c[0].x = __ldg(cp + q.va);
+        s[0].x = __ldg(sp + q.va);
+        if (q.rb) {
+            c[0].y = __ldg(cp + q.vb);
+            s[0].y = __ldg(sp + q.vb);
+        }
+    } else {
 #pragma unroll
-    for (int h = 0; h < V / 2; ++h) {
-        // halves: the V angles of vector va; interleaved: V / 2 of each vector
-        const bool second = INTER && h >= V / 4;
-        const int p = INTER ? (second ? q.vb * (V / 2) - V / 2 : q.va * (V / 2)) : q.va * V;
-        if (!second || q.rb) {
-            c[h] = __ldg(reinterpret_cast<const float2 *>(r.cos + pos * half + p + 2 * h));
-            s[h] = __ldg(reinterpret_cast<const float2 *>(r.sin + pos * half + p + 2 * h));
+        for (int h = 0; h < V / 2; ++h) {
+            const bool second = INTER && h >= V / 4;
+            const int p = INTER ? (second ? q.vb * (V / 2) - V / 2 : q.va * (V / 2)) : q.va * V;
+            if (!second || q.rb) {
+                c[h] = __ldg(reinterpret_cast<const float2 *>(cp + p + 2 * h));
+                s[h] = __ldg(reinterpret_cast<const float2 *>(sp + p + 2 * h));
+            }
         }
     }
 }
@@ -243,17 +335,15 @@ __device__ __forceinline__ void qk_turn(const QkLane &q, const float2 (&c)[V / 2
                                         float2 (&b)[V / 2]) {
     if (!q.ra) return;
     if constexpr (INTER) {
+        auto at = [](const float2(&v)[V / 2], int i) { return i & 1 ? v[i / 2].y : v[i / 2].x; };
 #pragma unroll
-        for (int h = 0; h < V / 4; ++h) {
-            a[2 * h] = qk_turn1(a[2 * h], c[h].x, BACK ? -s[h].x : s[h].x);
-            a[2 * h + 1] = qk_turn1(a[2 * h + 1], c[h].y, BACK ? -s[h].y : s[h].y);
-        }
+        for (int h = 0; h < V / 2; ++h)
+            a[h] = qk_turn1(a[h], at(c, h), BACK ? -at(s, h) : at(s, h));
         if (q.rb) {
 #pragma unroll
-            for (int h = 0; h < V / 4; ++h) {
-                const float2 ch = c[V / 4 + h], sh = s[V / 4 + h];
-                b[2 * h] = qk_turn1(b[2 * h], ch.x, BACK ? -sh.x : sh.x);
-                b[2 * h + 1] = qk_turn1(b[2 * h + 1], ch.y, BACK ? -sh.y : sh.y);
+            for (int h = 0; h < V / 2; ++h) {
+                const int i = V / 2 + h;
+                b[h] = qk_turn1(b[h], at(c, i), BACK ? -at(s, i) : at(s, i));
             }
         }
     } else {
@@ -277,17 +367,17 @@ __device__ __forceinline__ float qk_sum(float v) {
 }
 
 constexpr int kQkStages = 3;  // the current group and two on their way
-constexpr size_t kQkBwSmem = (size_t)kQkStages * 256 * (4 * 16 + 4);
+template <typename T, int V>
+constexpr size_t qk_bw_smem() { return (size_t)kQkStages * 256 * (4 * sizeof(QkRaw<T, V>) + 4); }
 
 // A group is the 32 / LPR heads of one side that a warp takes at once; an item
 // is up to `per_item` groups of one token (all of them, unless that would
 // leave too few items for the GPU).  ngq, ngk: groups of the two sides.
-template <typename T, int LPR, bool INTER>
+template <typename T, int V, int LPR, bool INTER>
 __global__ void __launch_bounds__(256, 2)
 qk_fw_vec(const QkSide<T> qs, const QkSide<T> ks, const QkRope r, int ngq, int ngk, int per_item) {
     pdl_begin();
-    using Tr = Traits<T>;
-    constexpr int V = Tr::kVec;
+    using Raw = QkRaw<T, V>;
     constexpr int H2 = V / 2;
     constexpr int RPW = 32 / LPR;
     const int lane = threadIdx.x & 31, l = lane % LPR, sub = lane / LPR;
@@ -295,11 +385,11 @@ qk_fw_vec(const QkSide<T> qs, const QkSide<T> ks, const QkRope r, int ngq, int n
     const int ng = ngq + ngk, per_token = (ng + per_item - 1) / per_item;
     const int64_t items = r.tokens * per_token;
     const float invD = 1.f / (float)r.D;
-    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+    const Raw zero = qk_zero<T, V>();
     const int64_t hop = (int64_t)gridDim.x * 8;
     // The warp's groups in order, copied kQkStages - 1 ahead: each thread its
     // own two vectors into its own slots.
-    __shared__ __align__(128) uint4 stage[kQkStages][2][256];
+    __shared__ __align__(128) Raw stage[kQkStages][2][256];
     int64_t i_item = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
     int64_t i_tok = per_token == 1 ? i_item : i_item / per_token;
     int i_f = (int)(i_item - i_tok * per_token) * per_item, i_end = min(i_f + per_item, ng);
@@ -307,13 +397,17 @@ qk_fw_vec(const QkSide<T> qs, const QkSide<T> ks, const QkRope r, int ngq, int n
         if (i_item < items) {
             const bool isq = i_f < ngq;
             const int h = (isq ? i_f : i_f - ngq) * RPW + sub;
-            uint4 *slot = &stage[st][0][threadIdx.x];
+            Raw *slot = &stage[st][0][threadIdx.x];
             const bool there = h < (int)(isq ? qs.heads : ks.heads);
             const T *x = (isq ? qs.x + i_tok * qs.x_stride : ks.x + i_tok * ks.x_stride) + h * r.D;
-            if (there && q.ha) cp_async16(slot, x + q.va * V);
-            else *slot = zero;
-            if (there && q.hb) cp_async16(slot + 256, x + q.vb * V);
-            else slot[256] = zero;
+            if (there && q.ha)
+                qk_copy<T, V>(slot, x + q.va * V);
+            else
+                slot[0] = zero;
+            if (there && q.hb)
+                qk_copy<T, V>(slot + 256, x + q.vb * V);
+            else
+                slot[256] = zero;
             if (++i_f == i_end) {
                 i_item += hop;
                 i_tok = per_token == 1 ? i_item : i_item / per_token;
@@ -345,15 +439,15 @@ qk_fw_vec(const QkSide<T> qs, const QkSide<T> ks, const QkRope r, int ngq, int n
             const int g0 = isq ? 0 : ngq, g1 = isq ? min(f1, ngq) : f1;
             if (rstd_out) rstd_out += tok * heads;
             float2 ga[H2], gb[H2];
-            unpack2<T>(q.ha ? ld_cached16(gamma + q.va * V) : zero, ga);
-            unpack2<T>(q.hb ? ld_cached16(gamma + q.vb * V) : zero, gb);
+            qk_unpack<T, V>(qk_gamma<T, V>(gamma + q.va * V, q.ha), ga);
+            qk_unpack<T, V>(qk_gamma<T, V>(gamma + q.vb * V, q.hb), gb);
             for (; f < g1; ++f) {
                 const int h = (f - g0) * RPW + sub;
                 float2 a[H2], b[H2];
                 issue(st_cur == 0 ? kQkStages - 1 : st_cur - 1);
                 cp_async_wait<kQkStages - 1>();  // this thread's copies of the group have landed
-                unpack2<T>(stage[st_cur][0][threadIdx.x], a);
-                unpack2<T>(stage[st_cur][1][threadIdx.x], b);
+                qk_unpack<T, V>(stage[st_cur][0][threadIdx.x], a);
+                qk_unpack<T, V>(stage[st_cur][1][threadIdx.x], b);
                 st_cur = st_cur + 1 == kQkStages ? 0 : st_cur + 1;
                 float2 ss = f2(0.f);
 #pragma unroll
@@ -368,8 +462,8 @@ qk_fw_vec(const QkSide<T> qs, const QkSide<T> ks, const QkRope r, int ngq, int n
                 qk_turn<V, INTER, false>(q, c, s, a, b);
                 if (h < heads) {
                     T *o = out + h * r.D;
-                    if (q.ha) st_stream16(o + q.va * V, pack2<T>(a));
-                    if (q.hb) st_stream16(o + q.vb * V, pack2<T>(b));
+                    if (q.ha) qk_store<T, V>(o + q.va * V, a);
+                    if (q.hb) qk_store<T, V>(o + q.vb * V, b);
                     if (l == 0 && rstd_out) rstd_out[h] = rstd;
                 }
             }
@@ -384,12 +478,11 @@ qk_fw_vec(const QkSide<T> qs, const QkSide<T> ks, const QkRope r, int ngq, int n
 // block's warps in shared memory at the end.  With p = dn * x and
 // S = sum gamma p (x not normed): dgamma += rstd p and
 // dx = rstd gamma dn - x rstd^3 S / D.
-template <typename T, int LPR, bool INTER>
+template <typename T, int V, int LPR, bool INTER>
 __global__ void __launch_bounds__(256, 2)
 qk_bw_vec(const QkSide<T> qs, const QkSide<T> ks, const QkRope r, float *part, int q_blocks) {
     pdl_begin();
-    using Tr = Traits<T>;
-    constexpr int V = Tr::kVec;
+    using Raw = QkRaw<T, V>;
     constexpr int H2 = V / 2;
     constexpr int RPW = 32 / LPR;
     __shared__ float sum[8][LPR * 2 * V + 1];
@@ -401,33 +494,34 @@ qk_bw_vec(const QkSide<T> qs, const QkSide<T> ks, const QkRope r, float *part, i
     const int64_t blk = isq ? blockIdx.x : (int)blockIdx.x - q_blocks;
     const int heads = (int)sd.heads, ng = (heads + RPW - 1) / RPW;
     const float invD = 1.f / (float)r.D;
-    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+    const Raw zero = qk_zero<T, V>();
     float2 ga[H2], gb[H2], da[H2], db[H2];  // gamma and its gradients
-    unpack2<T>(q.ha ? ld_cached16(sd.gamma + q.va * V) : zero, ga);
-    unpack2<T>(q.hb ? ld_cached16(sd.gamma + q.vb * V) : zero, gb);
+    qk_unpack<T, V>(qk_gamma<T, V>(sd.gamma + q.va * V, q.ha), ga);
+    qk_unpack<T, V>(qk_gamma<T, V>(sd.gamma + q.vb * V, q.hb), gb);
 #pragma unroll
     for (int e = 0; e < H2; ++e) da[e] = db[e] = f2(0.f);
-    extern __shared__ __align__(128) uint4 dsmem[];  // [kQkStages][4][256], then the rows' rstd
-    float *rs = reinterpret_cast<float *>(dsmem + kQkStages * 4 * 256) + threadIdx.x;
+    extern __shared__ __align__(128) uint4 dsmem[];
+    Raw *stage = reinterpret_cast<Raw *>(dsmem);  // [kQkStages][4][256], then the rows' rstd
+    float *rs = reinterpret_cast<float *>(stage + kQkStages * 4 * 256) + threadIdx.x;
     const int64_t hop = nblk * 8;
     int64_t i_tok = blk * 8 + warp;
     int i_f = 0;
     auto issue = [&](int st) {
         if (i_tok < r.tokens) {
             const int h = i_f * RPW + sub;
-            uint4 *slot = dsmem + st * 4 * 256 + threadIdx.x;
+            Raw *slot = stage + st * 4 * 256 + threadIdx.x;
             const bool there = h < heads;
             const T *x = sd.x + i_tok * sd.x_stride + h * r.D;
             const T *dy = sd.dout + i_tok * sd.dout_stride + h * r.D;
             if (there && q.ha) {
-                cp_async16(slot, x + q.va * V);
-                cp_async16(slot + 256, dy + q.va * V);
+                qk_copy<T, V>(slot, x + q.va * V);
+                qk_copy<T, V>(slot + 256, dy + q.va * V);
             } else {
                 slot[0] = slot[256] = zero;
             }
             if (there && q.hb) {
-                cp_async16(slot + 512, x + q.vb * V);
-                cp_async16(slot + 768, dy + q.vb * V);
+                qk_copy<T, V>(slot + 512, x + q.vb * V);
+                qk_copy<T, V>(slot + 768, dy + q.vb * V);
             } else {
                 slot[512] = slot[768] = zero;
             }
@@ -454,12 +548,12 @@ qk_bw_vec(const QkSide<T> qs, const QkSide<T> ks, const QkRope r, float *part, i
             float2 a[H2], b[H2], x[H2], u[H2];
             issue(st_cur == 0 ? kQkStages - 1 : st_cur - 1);
             cp_async_wait<kQkStages - 1>();  // this thread's copies of the group have landed
-            const uint4 *slot = dsmem + st_cur * 4 * 256 + threadIdx.x;
+            const Raw *slot = stage + st_cur * 4 * 256 + threadIdx.x;
             const float rstd = rs[st_cur * 256];
-            unpack2<T>(slot[0], x);
-            unpack2<T>(slot[256], a);
-            unpack2<T>(slot[512], u);
-            unpack2<T>(slot[768], b);
+            qk_unpack<T, V>(slot[0], x);
+            qk_unpack<T, V>(slot[256], a);
+            qk_unpack<T, V>(slot[512], u);
+            qk_unpack<T, V>(slot[768], b);
             st_cur = st_cur + 1 == kQkStages ? 0 : st_cur + 1;
             qk_turn<V, INTER, true>(q, c, s, a, b);  // dn
             float2 t = f2(0.f);
@@ -480,8 +574,8 @@ qk_bw_vec(const QkSide<T> qs, const QkSide<T> ks, const QkRope r, float *part, i
                     a[e] = mul2(f2(rstd), fma2(mul2(x[e], f2(rstd)), f2(k), mul2(a[e], ga[e])));
                     b[e] = mul2(f2(rstd), fma2(mul2(u[e], f2(rstd)), f2(k), mul2(b[e], gb[e])));
                 }
-                if (q.ha) st_stream16(dx + q.va * V, pack2<T>(a));
-                if (q.hb) st_stream16(dx + q.vb * V, pack2<T>(b));
+                if (q.ha) qk_store<T, V>(dx + q.va * V, a);
+                if (q.hb) qk_store<T, V>(dx + q.vb * V, b);
             }
         }
     }
@@ -517,7 +611,7 @@ qk_bw_vec(const QkSide<T> qs, const QkSide<T> ks, const QkRope r, float *part, i
 }
 
 // dgamma of both sides: the blocks' sums added in order.  blockIdx.y: side.
-__global__ void __launch_bounds__(256)
+static __global__ void __launch_bounds__(256)
 qk_fold(float *dgq, float *dgk, const float *part, int D, int q_blocks, int blocks) {
     pdl_begin();
     __shared__ float sum[8][33];
