@@ -143,7 +143,7 @@ cudaError_t launch_qk_bw(QkSide<T> q, QkSide<T> k, QkRope r, float *part, cudaSt
         const cudaError_t e = launch_qk_bw_rows(q, k, r, part, nq, nk, st);
         if (e != cudaSuccess) return e;
     }
-    return launch_pdl(qk_fold, dim3((unsigned)ceil_div(r.D, 32), 2), dim3(256), 0, st, q.dgamma,
+    return launch_pdl(qk_fold, dim3((unsigned)ceil_div(r.D, 32), 2), dim3(1024), 0, st, q.dgamma,
                       k.dgamma, (const float *)part, r.D, (int)nq, (int)(nq + nk));
 }
 

@@ -610,27 +610,28 @@ qk_bw_vec(const QkSide<T> qs, const QkSide<T> ks, const QkRope r, float *part, i
     }
 }
 
-// dgamma of both sides: the blocks' sums added in order.  blockIdx.y: side.
-static __global__ void __launch_bounds__(256)
+// dgamma of both sides: the blocks' sums, 32 threads per feature, in a fixed
+// order.  blockIdx.y: side.
+static __global__ void __launch_bounds__(1024)
 qk_fold(float *dgq, float *dgk, const float *part, int D, int q_blocks, int blocks) {
     pdl_begin();
-    __shared__ float sum[8][33];
+    __shared__ float sum[32][33];
     const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
     const int j = blockIdx.x * 32 + tx;
     const int beg = blockIdx.y ? q_blocks : 0, end = blockIdx.y ? blocks : q_blocks;
     float v = 0.f;
     if (j < D) {
 #pragma unroll 8
-        for (int b = beg + ty; b < end; b += 8) v += __ldcg(part + (int64_t)b * D + j);
+        for (int b = beg + ty; b < end; b += 32) v += __ldcg(part + (int64_t)b * D + j);
     }
     sum[ty][tx] = v;
     __syncthreads();
     float *out = blockIdx.y ? dgk : dgq;
-    if (ty == 0 && j < D && out) {
+    v = sum[tx][ty];  // one warp per feature
 #pragma unroll
-        for (int t = 1; t < 8; ++t) v += sum[t][tx];
-        out[j] = v;
-    }
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    const int jo = blockIdx.x * 32 + ty;
+    if (tx == 0 && jo < D && out) out[jo] = v;
 }
 
 }  // namespace lsr

@@ -981,36 +981,48 @@ relpos_bw_vec(T *dinp, float *part, const T *dout, const T *y, const T *mask_or_
     }
 }
 
-// dtable[k, h] for one head h = blockIdx.x and the buckets of blockIdx.y:
-// segment sums of each distance in order, then each bucket's distances.
+// dtable[k, h] for one head h = blockIdx.x and the buckets of blockIdx.y: the
+// segment sums of each distance (four threads per distance, every fourth
+// segment each, so that a long chain of loads does not set the time), then
+// each bucket's distances, one warp per bucket.  All in a fixed order.
 constexpr int kRelposFoldBuckets = 32;
-static __global__ void __launch_bounds__(256)
+constexpr int kRelposFoldThreads = 1024;
+constexpr size_t relpos_fold_smem(int R) { return (size_t)(2 * R + 1) * 8; }
+static __global__ void __launch_bounds__(kRelposFoldThreads)
 relpos_fold(float *dtable, const float *part, const int32_t *bucket, const RelposShape p) {
     pdl_begin();
-    extern __shared__ float dist[];  // [2R + 1]
+    extern __shared__ float dist[];  // [2R + 1], then the bucket ids
+    __shared__ float sums[4][256];
     const int W = 2 * p.R + 1;
+    int32_t *ids = reinterpret_cast<int32_t *>(dist + W);
     const int64_t h = blockIdx.x;
     const bool any = p.rows_per_head > 0;
     const int64_t first = any ? h * p.rows_per_head / p.per : 0;
     const int64_t last = any ? ((h + 1) * p.rows_per_head - 1) / p.per : -1;
-    for (int d = threadIdx.x; d < W; d += 256) {
+    const int tx = threadIdx.x & 255, ty = threadIdx.x >> 8;
+    for (int d = threadIdx.x; d < W; d += kRelposFoldThreads) ids[d] = __ldg(bucket + d);
+    for (int d0 = 0; d0 < W; d0 += 256) {
+        const int d = d0 + tx;
         float v = 0.f;
-#pragma unroll 8
-        for (int64_t k = first; k <= last; ++k) v += __ldcg(part + (k + h) * W + d);
-        dist[d] = v;
+        if (d < W) {
+#pragma unroll 10
+            for (int64_t k = first + ty; k <= last; k += 4)
+                v += __ldcg(part + (k + h) * W + d);
+        }
+        sums[ty][tx] = v;
+        __syncthreads();
+        if (ty == 0 && d < W) dist[d] = (v + sums[1][tx]) + (sums[2][tx] + sums[3][tx]);
+        __syncthreads();
     }
-    __syncthreads();
     const int lane = threadIdx.x & 31;
-    const int64_t k0 = (int64_t)blockIdx.y * kRelposFoldBuckets;
-    for (int64_t k = k0 + (threadIdx.x >> 5); k < min(k0 + kRelposFoldBuckets, p.num_buckets);
-         k += 8) {
-        float v = 0.f;
-        for (int d = lane; d < W; d += 32)
-            if (__ldg(bucket + d) == k) v += dist[d];
+    const int64_t k = (int64_t)blockIdx.y * kRelposFoldBuckets + (threadIdx.x >> 5);
+    if (k >= p.num_buckets) return;
+    float v = 0.f;
+    for (int d = lane; d < W; d += 32)
+        if (ids[d] == k) v += dist[d];
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-        if (lane == 0) dtable[k * p.H + h] = v;
-    }
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    if (lane == 0) dtable[k * p.H + h] = v;
 }
 
 }  // namespace lsr

@@ -188,8 +188,8 @@ cudaError_t launch_relpos_bw(T *dinp, float *dtable, const T *dout, const T *y, 
         if (e != cudaSuccess) return e;
     }  // else rows_per_head is 0 too and the gradient becomes zero
     const dim3 grid((unsigned)p.H, (unsigned)ceil_div(p.num_buckets, kRelposFoldBuckets));
-    return launch_pdl(relpos_fold, grid, dim3(256), relpos_sums_bytes(p.R), st, dtable,
-                      (const float *)part, bucket, p);
+    return launch_pdl(relpos_fold, grid, dim3(kRelposFoldThreads), relpos_fold_smem(p.R), st,
+                      dtable, (const float *)part, bucket, p);
 }
 
 #define LSR_RELPOS_FW_INSTANTIATE(T)                                                        \
