@@ -488,8 +488,9 @@ ls_status ls_softmax_bw_relpos(void *dinp, float *dtable, const void *dout, cons
                                int causal, float scale, void *workspace, size_t workspace_bytes,
                                ls_dtype dt, void *stream);
 
-/* Largest head size of the per-head norm. */
+/* Largest head size and most query or key heads of the per-head norm. */
 #define LS_MAX_HEAD_DIM ((int64_t)1024)
+#define LS_MAX_HEADS ((int64_t)1 << 29)
 
 /*
  * RMSNorm of every query head and every key head, and the rotation by the
@@ -518,8 +519,8 @@ ls_status ls_softmax_bw_relpos(void *dinp, float *dtable, const void *dout, cons
  * Hq or Hk may be 0 (its pointers are then ignored).
  * Errors: LS_ERR_INVALID_ARG for a NULL pointer that is needed, negative
  * sizes, D < 1, rot odd or outside [0, D], a stride below heads * D, eps < 0
- * or not finite; LS_ERR_UNSUPPORTED for an unknown dtype or D beyond
- * LS_MAX_HEAD_DIM; LS_ERR_MISALIGNED as everywhere.
+ * or not finite; LS_ERR_UNSUPPORTED for an unknown dtype or sizes beyond the
+ * limits above; LS_ERR_MISALIGNED as everywhere.
  */
 ls_status ls_qk_norm_rope_fw(void *q_out, void *k_out, float *q_rstd, float *k_rstd,
                              const void *q, const void *k, const void *gamma_q,

@@ -99,6 +99,8 @@ def test_qk_rejections(abi):
         assert call(abi, max_pos=0) == bad
         assert call(abi, qs=63) == bad and call(abi, ks=31) == bad
         assert call(abi, tokens=1 << 60) == un
+        assert call(abi, Hq=(1 << 29) + 1, qs=1 << 40) == un
+        assert call(abi, Hk=(1 << 29) + 1, ks=1 << 40) == un
         assert call(abi, tokens=1 << 40, qs=1 << 40) == un
     assert _qk(abi, eps=-1.0) == bad and _qk(abi, eps=math.nan) == bad
     assert _qk(abi, q_out=None) == bad and _qk(abi, qos=63) == bad and _qk(abi, kos=31) == bad

@@ -694,7 +694,7 @@ static ls_status qk_check(int64_t tokens, int64_t Hq, int64_t Hk, int64_t D, int
                           const int32_t *positions) {
     if (tokens < 0 || Hq < 0 || Hk < 0 || D < 1 || rot < 0 || rot > D || rot % 2 != 0)
         return LS_ERR_INVALID_ARG;
-    if (D > LS_MAX_HEAD_DIM || Hq > INT32_MAX || Hk > INT32_MAX) return LS_ERR_UNSUPPORTED;
+    if (D > LS_MAX_HEAD_DIM || Hq > LS_MAX_HEADS || Hk > LS_MAX_HEADS) return LS_ERR_UNSUPPORTED;
     if (tokens > 0 && (Hq + Hk + 1) * D > INT64_MAX / tokens) return LS_ERR_UNSUPPORTED;
     if (rot > 0 && tokens > 0 && Hq + Hk > 0) {
         if (!cos || !sin || !positions || max_pos < 1) return LS_ERR_INVALID_ARG;
@@ -773,7 +773,7 @@ ls_status ls_qk_norm_rope_fw(void *q_out, void *k_out, float *q_rstd, float *k_r
 }
 
 size_t ls_qk_norm_rope_bw_workspace_size(int64_t tokens, int64_t Hq, int64_t Hk, int64_t D) {
-    if (tokens <= 0 || Hq < 0 || Hk < 0 || Hq > INT32_MAX || Hk > INT32_MAX || D <= 0 ||
+    if (tokens <= 0 || Hq < 0 || Hk < 0 || Hq > LS_MAX_HEADS || Hk > LS_MAX_HEADS || D <= 0 ||
         D > LS_MAX_HEAD_DIM)
         return 0;
     return (size_t)lsr::qk_bw_parts(tokens, Hq, Hk) * (size_t)D * sizeof(float);

@@ -10,20 +10,22 @@
 
 namespace lsr {
 
-// Blocks of the backward, a constant (not the device's SM count), so that the
-// order of the gamma gradient's sums depends only on the problem.
+// Most blocks of the backward.
 constexpr int64_t kQkBwBlocks = 4 * 152;
 
-// Blocks of the query and key sides, in proportion to their rows, each side
-// with at most one block per row.
-inline void qk_bw_split(int64_t tokens, int64_t Hq, int64_t Hk, int64_t &nq, int64_t &nk) {
-    const int64_t heads = Hq + Hk;
-    nq = heads ? kQkBwBlocks * Hq / heads : 0;
-    nk = heads ? kQkBwBlocks - nq : 0;
-    if (Hq > 0 && nq < 1) nq = 1;
-    if (Hk > 0 && nk < 1) nk = 1;
-    if (nq > tokens * Hq) nq = tokens * Hq;
-    if (nk > tokens * Hk) nk = tokens * Hk;
+// Blocks of the query and key sides of the backward: `blocks` (a constant, not
+// the device's SM count, so that the order of the gamma gradient's sums depends
+// only on the problem) in proportion to the sides' work, each side with at most
+// one block per eight tokens.
+inline void qk_bw_split(int64_t tokens, int64_t blocks, int64_t wq, int64_t wk, int64_t &nq,
+                        int64_t &nk) {
+    nq = blocks * wq / (wq + wk);
+    if (wq > 0 && nq < 1) nq = 1;
+    if (wk > 0 && nq > blocks - 1) nq = blocks - 1;
+    nk = wk > 0 ? blocks - nq : 0;
+    const int64_t most = ceil_div(tokens, 8);
+    if (nq > most) nq = most;
+    if (nk > most) nk = most;
 }
 
 // Whether a side's heads are whole vectors of V elements at their alignment.
@@ -84,6 +86,18 @@ bool qk_pick(const QkSide<T> &q, const QkSide<T> &k, const QkRope &r, F f) {
     return false;
 }
 
+template <typename T, int NS>
+cudaError_t launch_qk_fw_slots(const QkSide<T> &q, const QkSide<T> &k, const QkRope &r,
+                               cudaStream_t st) {
+    // (heads as the groups of the vector kernel, one per warp at a time)
+    const int64_t heads = q.heads + k.heads, slots = (int64_t)device_sm_count() * 16;
+    int64_t per_item = r.tokens > 0 ? r.tokens * heads / slots : 1;
+    per_item = per_item < 1 ? 1 : (per_item > heads ? heads : per_item);
+    const int64_t items = r.tokens * ceil_div(heads, per_item);
+    return launch_persistent<qk_fw_slots<T, NS>>(256, 0, ceil_div(items, 8), st, q, k, r,
+                                                 (int)per_item);
+}
+
 template <typename T>
 cudaError_t launch_qk_fw(QkSide<T> q, QkSide<T> k, QkRope r, cudaStream_t st) {
     cudaError_t e = cudaSuccess;
@@ -93,29 +107,19 @@ cudaError_t launch_qk_fw(QkSide<T> q, QkSide<T> k, QkRope r, cudaStream_t st) {
                               : launch_qk_fw_vec<T, V, L, false>(q, k, r, st);
         }))
         return e;
-    const int64_t rows = r.tokens * (q.heads + k.heads);
-    return launch_persistent<qk_fw_loop<T>>(256, 0, ceil_div(rows, 8), st, q, k, r);
-}
-
-// Blocks of the vector kernel: two on each SM, in proportion to the sides'
-// groups of heads, each side with at most one block per eight tokens.
-inline void qk_bw_vec_split(int64_t tokens, int64_t gq, int64_t gk, int64_t &nq, int64_t &nk) {
-    constexpr int64_t blocks = 2 * 152;
-    static_assert(blocks <= kQkBwBlocks, "the workspace holds kQkBwBlocks parts");
-    nq = blocks * gq / (gq + gk);
-    if (gq > 0 && nq < 1) nq = 1;
-    if (gk > 0 && nq > blocks - 1) nq = blocks - 1;
-    nk = gk > 0 ? blocks - nq : 0;
-    const int64_t most = ceil_div(tokens, 8);
-    if (nq > most) nq = most;
-    if (nk > most) nk = most;
+#define X(NS_) \
+    if (r.D <= 64 * NS_) return launch_qk_fw_slots<T, NS_>(q, k, r, st);
+    X(1) X(2) X(4) X(8) X(16)
+#undef X
+    return cudaErrorInvalidValue;  // not reachable: D <= kQkMaxHeadDim
 }
 
 template <typename T, int V, int LPR, bool INTER>
 cudaError_t launch_qk_bw_vec(const QkSide<T> &q, const QkSide<T> &k, const QkRope &r, float *part,
                              int64_t &nq, int64_t &nk, cudaStream_t st) {
     constexpr int RPW = 32 / LPR;
-    qk_bw_vec_split(r.tokens, ceil_div(q.heads, RPW), ceil_div(k.heads, RPW), nq, nk);
+    // two blocks on each SM; a side's work goes by its groups of heads
+    qk_bw_split(r.tokens, 2 * 152, ceil_div(q.heads, RPW), ceil_div(k.heads, RPW), nq, nk);
     ensure_dynamic_smem<qk_bw_vec<T, V, LPR, INTER>>(qk_bw_smem<T, V>());
     return launch_pdl(qk_bw_vec<T, V, LPR, INTER>, dim3((unsigned)(nq + nk)), dim3(256),
                       qk_bw_smem<T, V>(), st, q, k, r, part, (int)nq);
@@ -131,9 +135,14 @@ cudaError_t launch_qk_bw_rows(const QkSide<T> &q, const QkSide<T> &k, const QkRo
                               : launch_qk_bw_vec<T, V, L, false>(q, k, r, part, nq, nk, st);
         }))
         return e;
-    qk_bw_split(r.tokens, q.heads, k.heads, nq, nk);
-    return launch_pdl(qk_bw_loop<T>, dim3((unsigned)(nq + nk)), dim3(256), (size_t)8 * r.D * 4, st,
-                      q, k, r, part, (int)nq);
+    qk_bw_split(r.tokens, kQkBwBlocks, q.heads, k.heads, nq, nk);
+#define X(NS_)                                                                          \
+    if (r.D <= 64 * NS_)                                                                \
+        return launch_pdl(qk_bw_slots<T, NS_>, dim3((unsigned)(nq + nk)), dim3(256),    \
+                          (size_t)8 * r.D * 4, st, q, k, r, part, (int)nq);
+    X(1) X(2) X(4) X(8) X(16)
+#undef X
+    return cudaErrorInvalidValue;  // not reachable: D <= kQkMaxHeadDim
 }
 
 template <typename T>

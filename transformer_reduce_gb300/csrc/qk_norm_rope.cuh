@@ -21,141 +21,187 @@
 
 namespace lsr {
 
-// Cosine and sine of pair p at one token's position; NaN for a position
-// outside the table (there is no device-side trap).
-__device__ __forceinline__ float2 qk_angle(const QkRope &r, int64_t pos, int p) {
-    if (pos < 0 || pos >= r.max_pos) return f2(__int_as_float(0x7fc00000));
-    const int64_t at = pos * (r.rot / 2) + p;
-    return make_float2(__ldg(r.cos + at), __ldg(r.sin + at));
-}
-
-// The two features of slot u of a row: the rotation's pairs first, then the
-// unrotated features two by two (b == D: the last of an odd count, alone).
-__device__ __forceinline__ void qk_slot(const QkRope &r, int u, int &a, int &b) {
-    const int half = r.rot / 2;
-    if (u < half) {
-        a = r.interleaved ? 2 * u : u;
-        b = r.interleaved ? 2 * u + 1 : u + half;
-    } else {
-        a = 2 * u;  // rot + 2 (u - half)
-        b = a + 1;
-    }
-}
-
 // ----------------------------------------------------------------------------
-// Any head size and alignment: one warp per head, a lane owns the slots lane,
-// lane + 32, ... and both features of each, so calls may be in place.
+// Any head size and alignment.  One warp per head; its features go in slots of
+// two: the rotation's pairs first, then the unrotated features two by two (the
+// last of an odd count alone).  A lane owns the slots lane + 32 i, i < NS, and
+// both features of each, so calls may be in place.  A warp takes a token, loads
+// its angles once and goes through the heads, the next one's features loading
+// while it works on the current one.
 // ----------------------------------------------------------------------------
-template <typename T>
-__global__ void __launch_bounds__(256)
-qk_fw_loop(const QkSide<T> qs, const QkSide<T> ks, const QkRope r) {
-    pdl_begin();
-    using Tr = Traits<T>;
-    const int lane = threadIdx.x & 31;
-    const int64_t heads = qs.heads + ks.heads;
-    const int64_t rows = r.tokens * heads;
-    const int slots = (r.D + 1) / 2;
-    for (int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); row < rows;
-         row += (int64_t)gridDim.x * 8) {
-        const int64_t tok = row / heads;
-        int64_t h = row - tok * heads;
-        const bool isq = h < qs.heads;
-        const QkSide<T> &sd = isq ? qs : ks;
-        if (!isq) h -= qs.heads;
-        const T *x = sd.x + tok * sd.x_stride + h * r.D;
-        T *o = sd.out + tok * sd.out_stride + h * r.D;
-        float ss = 0.f;
-        for (int j = lane; j < r.D; j += 32) {
-            const float v = Tr::load1(x + j);
-            ss = fmaf(v, v, ss);
+template <int NS>
+struct QkSlots {
+    int a[NS], b[NS];      // the features; -1: there is none
+    float2 cs[NS];         // cosine and sine, (1, 0) where nothing is rotated
+    __device__ __forceinline__ QkSlots(const QkRope &r, int lane) {
+        const int half = r.rot / 2;
+#pragma unroll
+        for (int i = 0; i < NS; ++i) {
+            const int u = lane + 32 * i;
+            const bool far = !r.interleaved && u < half;
+            a[i] = far ? u : 2 * u;
+            b[i] = far ? u + half : 2 * u + 1;
+            if (a[i] >= r.D) a[i] = -1;
+            if (b[i] >= r.D) b[i] = -1;
+            cs[i] = make_float2(1.f, 0.f);
         }
-        ss = group_reduce<32, OpSum>(ss, nullptr);
-        const float rstd = 1.f / sqrtf(ss / (float)r.D + r.eps);
-        if (lane == 0 && sd.rstd_out) sd.rstd_out[tok * sd.heads + h] = rstd;
-        const int64_t pos = r.rot ? __ldg(r.positions + tok) : 0;
-        for (int u = lane; u < slots; u += 32) {
-            int a, b;
-            qk_slot(r, u, a, b);
-            const bool two = b < r.D;
-            float na = Tr::load1(x + a) * rstd * Tr::load1_cached(sd.gamma + a);
-            float nb = two ? Tr::load1(x + b) * rstd * Tr::load1_cached(sd.gamma + b) : 0.f;
-            if (u < r.rot / 2) {
-                const float2 cs = qk_angle(r, pos, u);
-                const float ya = na * cs.x - nb * cs.y;
-                nb = nb * cs.x + na * cs.y;
-                na = ya;
+    }
+    // The angles of a position; NaN outside the table (there is no device-side
+    // trap).
+    __device__ __forceinline__ void angles(const QkRope &r, int lane, int64_t tok) {
+        const int half = r.rot / 2;
+        if (half == 0) return;
+        const int64_t pos = __ldg(r.positions + tok);
+        const bool in = pos >= 0 && pos < r.max_pos;
+#pragma unroll
+        for (int i = 0; i < NS; ++i) {
+            const int u = lane + 32 * i;
+            if (u < half)
+                cs[i] = in ? make_float2(__ldg(r.cos + pos * half + u),
+                                         __ldg(r.sin + pos * half + u))
+                           : f2(__int_as_float(0x7fc00000));
+        }
+    }
+    template <typename T>
+    __device__ __forceinline__ void load(const T *p, float2 (&v)[NS]) const {
+#pragma unroll
+        for (int i = 0; i < NS; ++i) {
+            v[i].x = a[i] >= 0 ? Traits<T>::load1(p + a[i]) : 0.f;
+            v[i].y = b[i] >= 0 ? Traits<T>::load1(p + b[i]) : 0.f;
+        }
+    }
+    template <typename T>
+    __device__ __forceinline__ void gamma(const T *p, float2 (&v)[NS]) const {
+#pragma unroll
+        for (int i = 0; i < NS; ++i) {
+            v[i].x = a[i] >= 0 ? Traits<T>::load1_cached(p + a[i]) : 0.f;
+            v[i].y = b[i] >= 0 ? Traits<T>::load1_cached(p + b[i]) : 0.f;
+        }
+    }
+    template <typename T>
+    __device__ __forceinline__ void store(T *p, const float2 (&v)[NS]) const {
+#pragma unroll
+        for (int i = 0; i < NS; ++i) {
+            if (a[i] >= 0) Traits<T>::store1(p + a[i], v[i].x);
+            if (b[i] >= 0) Traits<T>::store1(p + b[i], v[i].y);
+        }
+    }
+    // (x, y) turned by slot i's angle, back by the opposite one.
+    __device__ __forceinline__ bool turns(const QkRope &r, int lane, int i) const {
+        return lane + 32 * i < r.rot / 2;
+    }
+};
+
+template <typename T, int NS>
+__global__ void __launch_bounds__(256)
+qk_fw_slots(const QkSide<T> qs, const QkSide<T> ks, const QkRope r, int per_item) {
+    pdl_begin();
+    const int lane = threadIdx.x & 31;
+    const int Hq = (int)qs.heads, heads = Hq + (int)ks.heads;
+    const int per_token = (heads + per_item - 1) / per_item;
+    const int64_t items = r.tokens * per_token;
+    const float invD = 1.f / (float)r.D;
+    QkSlots<NS> sl(r, lane);
+    for (int64_t item = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); item < items;
+         item += (int64_t)gridDim.x * 8) {
+        const int64_t tok = item / per_token;
+        const int f0 = (int)(item - tok * per_token) * per_item, f1 = min(f0 + per_item, heads);
+        auto row = [&](int f) {
+            return f < Hq ? qs.x + tok * qs.x_stride + (int64_t)f * r.D
+                          : ks.x + tok * ks.x_stride + (int64_t)(f - Hq) * r.D;
+        };
+        float2 next[NS], g[NS];
+        sl.load(row(f0), next);
+        sl.angles(r, lane, tok);
+        for (int f = f0; f < f1; ++f) {
+            const bool isq = f < Hq;
+            const int h = isq ? f : f - Hq;
+            if (f == f0 || f == Hq) sl.gamma(isq ? qs.gamma : ks.gamma, g);
+            float2 v[NS];
+            float2 ss = f2(0.f);
+#pragma unroll
+            for (int i = 0; i < NS; ++i) {
+                v[i] = next[i];
+                ss = fma2(v[i], v[i], ss);
             }
-            Tr::store1(o + a, na);
-            if (two) Tr::store1(o + b, nb);
+            if (f + 1 < f1) sl.load(row(f + 1), next);
+            const float sum = group_reduce<32, OpSum>(ss.x + ss.y, nullptr);
+            const float rstd = rsqrtf(fmaf(sum, invD, r.eps));
+#pragma unroll
+            for (int i = 0; i < NS; ++i) {
+                v[i] = mul2(mul2(v[i], f2(rstd)), g[i]);
+                if (sl.turns(r, lane, i)) {
+                    const float2 n = v[i], cs = sl.cs[i];
+                    v[i] = make_float2(fmaf(n.x, cs.x, -(n.y * cs.y)), fmaf(n.y, cs.x, n.x * cs.y));
+                }
+            }
+            sl.store(isq ? qs.out + tok * qs.out_stride + (int64_t)h * r.D
+                         : ks.out + tok * ks.out_stride + (int64_t)h * r.D,
+                     v);
+            float *rstd_out = isq ? qs.rstd_out : ks.rstd_out;
+            if (lane == 0 && rstd_out) rstd_out[tok * (isq ? qs.heads : ks.heads) + h] = rstd;
         }
     }
 }
 
 // Backward: block b < q_blocks works on query heads, the others on key heads,
-// each on a contiguous run of its side's rows, with the run's gamma gradient
-// in shared memory (one array per warp: a lane's features are its own).
-template <typename T>
+// with the gamma gradients of the lane's features in registers; the block's
+// warps are added in shared memory at the end.
+template <typename T, int NS>
 __global__ void __launch_bounds__(256)
-qk_bw_loop(const QkSide<T> qs, const QkSide<T> ks, const QkRope r, float *part, int q_blocks) {
+qk_bw_slots(const QkSide<T> qs, const QkSide<T> ks, const QkRope r, float *part, int q_blocks) {
     pdl_begin();
-    using Tr = Traits<T>;
     extern __shared__ float acc[];  // [8][D]
-    const int lane = threadIdx.x & 31;
-    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const bool isq = (int)blockIdx.x < q_blocks;
     const QkSide<T> &sd = isq ? qs : ks;
     const int64_t nblk = isq ? q_blocks : (int)gridDim.x - q_blocks;
     const int64_t blk = isq ? blockIdx.x : (int)blockIdx.x - q_blocks;
-    const int64_t rows = r.tokens * sd.heads;
-    const int64_t per = (rows + nblk - 1) / nblk;
-    const int64_t beg = blk * per, end = min(beg + per, rows);
-    const int slots = (r.D + 1) / 2;
-    float *mine = acc + warp * r.D;
-    for (int j = lane; j < r.D; j += 32) mine[j] = 0.f;
-    __syncwarp();
-    for (int64_t row = beg + warp; row < end; row += 8) {
-        const int64_t tok = row / sd.heads, h = row - tok * sd.heads;
-        const T *x = sd.x + tok * sd.x_stride + h * r.D;
-        const T *dy = sd.dout + tok * sd.dout_stride + h * r.D;
-        T *dx = sd.out + tok * sd.out_stride + h * r.D;
-        const float rstd = __ldg(sd.rstd + row);
-        const int64_t pos = r.rot ? __ldg(r.positions + tok) : 0;
-        // dn and xhat of one slot
-        auto slot = [&](int u, int a, int b, float &da, float &db, float &xa, float &xb) {
-            const bool two = b < r.D;
-            da = Tr::load1(dy + a);
-            db = two ? Tr::load1(dy + b) : 0.f;
-            xa = Tr::load1(x + a) * rstd;
-            xb = two ? Tr::load1(x + b) * rstd : 0.f;
-            if (u < r.rot / 2) {
-                const float2 cs = qk_angle(r, pos, u);
-                const float na = da * cs.x + db * cs.y;
-                db = db * cs.x - da * cs.y;
-                da = na;
+    const float invD = 1.f / (float)r.D;
+    QkSlots<NS> sl(r, lane);
+    float2 g[NS], dg[NS];
+    sl.gamma(sd.gamma, g);
+#pragma unroll
+    for (int i = 0; i < NS; ++i) dg[i] = f2(0.f);
+    for (int64_t tok = blk * 8 + warp; tok < r.tokens; tok += nblk * 8) {
+        const T *xt = sd.x + tok * sd.x_stride, *yt = sd.dout + tok * sd.dout_stride;
+        float2 nx[NS], ny[NS];
+        sl.load(xt, nx);
+        sl.load(yt, ny);
+        float nr = __ldg(sd.rstd + tok * sd.heads);
+        sl.angles(r, lane, tok);
+        for (int64_t h = 0; h < sd.heads; ++h) {
+            float2 x[NS], d[NS];
+            const float rstd = nr;
+            float2 t = f2(0.f);
+#pragma unroll
+            for (int i = 0; i < NS; ++i) {
+                x[i] = mul2(nx[i], f2(rstd));  // xhat
+                d[i] = ny[i];
+                if (sl.turns(r, lane, i)) {  // dn
+                    const float2 y = ny[i], cs = sl.cs[i];
+                    d[i] = make_float2(fmaf(y.x, cs.x, y.y * cs.y), fmaf(y.y, cs.x, -(y.x * cs.y)));
+                }
+                const float2 p = mul2(d[i], x[i]);
+                dg[i] = add2(dg[i], p);
+                t = fma2(p, g[i], t);
             }
-        };
-        float s = 0.f;
-        for (int u = lane; u < slots; u += 32) {
-            int a, b;
-            float da, db, xa, xb;
-            qk_slot(r, u, a, b);
-            slot(u, a, b, da, db, xa, xb);
-            s = fmaf(da * Tr::load1_cached(sd.gamma + a), xa, s);
-            if (b < r.D) s = fmaf(db * Tr::load1_cached(sd.gamma + b), xb, s);
-        }
-        s = group_reduce<32, OpSum>(s, nullptr) / (float)r.D;
-        for (int u = lane; u < slots; u += 32) {
-            int a, b;
-            float da, db, xa, xb;
-            qk_slot(r, u, a, b);
-            slot(u, a, b, da, db, xa, xb);
-            mine[a] = fmaf(da, xa, mine[a]);
-            Tr::store1(dx + a, rstd * (da * Tr::load1_cached(sd.gamma + a) - xa * s));
-            if (b < r.D) {
-                mine[b] = fmaf(db, xb, mine[b]);
-                Tr::store1(dx + b, rstd * (db * Tr::load1_cached(sd.gamma + b) - xb * s));
+            if (h + 1 < sd.heads) {
+                sl.load(xt + (h + 1) * r.D, nx);
+                sl.load(yt + (h + 1) * r.D, ny);
+                nr = __ldg(sd.rstd + tok * sd.heads + h + 1);
             }
+            const float mean = group_reduce<32, OpSum>(t.x + t.y, nullptr) * invD;
+#pragma unroll
+            for (int i = 0; i < NS; ++i)
+                d[i] = mul2(f2(rstd), fma2(x[i], f2(-mean), mul2(d[i], g[i])));
+            sl.store(sd.out + tok * sd.out_stride + h * r.D, d);
         }
+    }
+#pragma unroll
+    for (int i = 0; i < NS; ++i) {
+        if (sl.a[i] >= 0) acc[warp * r.D + sl.a[i]] = dg[i].x;
+        if (sl.b[i] >= 0) acc[warp * r.D + sl.b[i]] = dg[i].y;
     }
     __syncthreads();
     for (int j = threadIdx.x; j < r.D; j += 256) {
