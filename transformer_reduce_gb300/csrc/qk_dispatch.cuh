@@ -65,7 +65,10 @@ cudaError_t launch_qk_fw_vec(const QkSide<T> &q, const QkSide<T> &k, const QkRop
 }
 
 // Calls f(V, LPR) as integral constants for the widest vectors that the call's
-// sizes and addresses allow; false if none do.
+// sizes and addresses allow; false if none do.  Forward / backward of 8192
+// tokens of 16 + 16 heads, bf16, against one warp per head (qk_fw_slots): 84
+// features in 8-byte vectors 29 / 41 us, 72 / 92; 36 features in 4-byte vectors
+// 23 / 33, 56 / 61; 100 features in 4-byte vectors (32 lanes) 44 / 98, 72 / 95.
 template <typename T, typename F>
 bool qk_pick(const QkSide<T> &q, const QkSide<T> &k, const QkRope &r, F f) {
     constexpr int W = Traits<T>::kVec;  // 16 bytes
