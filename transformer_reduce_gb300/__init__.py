@@ -719,18 +719,27 @@ def _list_device(tensors):
     return _dev(*tensors).index  # says what is wrong
 
 
+def _each(method, tensors):
+    """``t.method()`` of every tensor of a list, as a list."""
+    try:
+        return list(map(getattr(_torch().Tensor, method), tensors))
+    except TypeError:  # something that only looks like a tensor
+        return [getattr(t, method)() for t in tensors]
+
+
 def _grad_lists(grads):
-    """(tensors, device index, pointers, element counts, and dtype codes) of a
-    list of dense tensors, the last as a host array."""
+    """(tensors, device index, pointers, element counts, dtypes, and dtype codes
+    as a host array) of a list of dense tensors."""
     grads = list(grads)
     if not grads:
         raise ValueError("an empty list has no device: give at least one gradient")
     index = _list_device(grads)
+    dtypes = list(map(_DTYPE, grads))
     try:
-        codes = array.array("i", map(_DTYPE_CODES.__getitem__, map(_DTYPE, grads)))
+        codes = array.array("i", map(_DTYPE_CODES.__getitem__, dtypes))
     except KeyError:  # the first call, or an unsupported dtype
         codes = array.array("i", map(ls_dtype, grads))
-    return grads, index, [t.data_ptr() for t in grads], [t.numel() for t in grads], codes
+    return grads, index, _each("data_ptr", grads), _each("numel", grads), dtypes, codes
 
 
 def _at(a) -> int:
@@ -760,7 +769,7 @@ def _norm_outputs(grads, index, workspace, norm):
 def grad_norm(grads, workspace=None, norm=None):
     """Global norm sqrt(sum g^2) over a list of gradients (fp32, fp16 and bf16
     may be mixed), fp32 [1] on their device."""
-    grads, index, ptrs, sizes, codes = _grad_lists(grads)
+    grads, index, ptrs, sizes, _, codes = _grad_lists(grads)
     workspace, norm = _norm_outputs(grads, index, workspace, norm)
     ptrs, sizes = array.array("Q", ptrs), array.array("q", sizes)
     _launch("ls_grad_norm", index, _ptr(norm), _at(ptrs), _at(sizes), _at(codes), len(grads),
@@ -773,20 +782,19 @@ def grad_clip(grads, max_norm: float, out=None, eps: float = 1e-6, workspace=Non
     being ``grad_norm(grads)``; returns (out, norm).  ``out`` None clips in
     place; otherwise it is a list of tensors with the gradients' element counts
     and dtypes.  No tensor may be in ``out`` twice."""
-    grads, index, ptrs, sizes, codes = _grad_lists(grads)
+    grads, index, ptrs, sizes, dtypes, codes = _grad_lists(grads)
     if out is None:
         out, optrs = grads, ptrs
     else:
         out = list(out)
         if len(out) != len(grads):
             raise ValueError(f"out must hold {len(grads)} tensors, got {len(out)}")
-        if [t.numel() for t in out] != sizes or \
-                list(map(_DTYPE, out)) != list(map(_DTYPE, grads)):
+        if _each("numel", out) != sizes or list(map(_DTYPE, out)) != dtypes:
             for i, (o, g) in enumerate(zip(out, grads)):
                 _want(f"out[{i}]", o, g.shape, g.dtype)
         if _list_device(out) != index:
             raise ValueError(f"out must be on {grads[0].device}")
-        optrs = [t.data_ptr() for t in out]
+        optrs = _each("data_ptr", out)
     if len(set(optrs)) < len(out):
         held = [p for p, n in zip(optrs, sizes) if n]
         if len(set(held)) < len(held):
