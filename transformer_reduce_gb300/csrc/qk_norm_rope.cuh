@@ -27,7 +27,8 @@ namespace lsr {
 // last of an odd count alone).  A lane owns the slots lane + 32 i, i < NS, and
 // both features of each, so calls may be in place.  A warp takes a token, loads
 // its angles once and goes through the heads, the next one's features loading
-// while it works on the current one.
+// while it works on the current one.  Bound by its 2-byte accesses:
+// [8192,(16,16),101] bf16 forward 72 us, backward 94 us (1.5 and 1.7 TB/s).
 // ----------------------------------------------------------------------------
 template <int NS>
 struct QkSlots {
@@ -86,7 +87,7 @@ struct QkSlots {
             if (b[i] >= 0) Traits<T>::store1(p + b[i], v[i].y);
         }
     }
-    // (x, y) turned by slot i's angle, back by the opposite one.
+    // Whether slot i is rotated.
     __device__ __forceinline__ bool turns(const QkRope &r, int lane, int i) const {
         return lane + 32 * i < r.rot / 2;
     }
@@ -416,6 +417,10 @@ constexpr int kQkStages = 3;  // the current group and two on their way
 template <typename T, int V>
 constexpr size_t qk_bw_smem() { return (size_t)kQkStages * 256 * (4 * sizeof(QkRaw<T, V>) + 4); }
 
+// Measured on a GB300, [16384,(16,16),64] bf16, packed: forward 26.6 us (5.1
+// TB/s), backward with its fold 35.3 us (5.8 TB/s); memory latency with two
+// blocks per SM (three with 80 registers spill and measured 32 us).
+//
 // A group is the 32 / LPR heads of one side that a warp takes at once; an item
 // is up to `per_item` groups of one token (all of them, unless that would
 // leave too few items for the GPU).  ngq, ngk: groups of the two sides.
