@@ -19,9 +19,9 @@
 // of the list, which the norm's pass read last and L2 still holds.  The cut
 // depends only on the list, so the norm is bitwise reproducible.
 //
-// Bound by memory: 144 tensors of 151 M bf16 elements, norm 48.5 us (6.2 TB/s)
-// and scaling 95.8 us (6.3 TB/s), 153 us together; short lists by the two
-// launches (12 tensors of 0.8 M: 7.1 us).
+// Bound by memory: 144 tensors of 151 M bf16 elements, norm 48.7 us (6.2 TB/s),
+// norm and scaling 152.8 us (5.9 TB/s); short lists by the two launches (12
+// tensors of 0.8 M: 7.2 us).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>

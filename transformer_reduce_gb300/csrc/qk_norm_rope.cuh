@@ -27,8 +27,9 @@ namespace lsr {
 // last of an odd count alone).  A lane owns the slots lane + 32 i, i < NS, and
 // both features of each, so calls may be in place.  A warp takes a token, loads
 // its angles once and goes through the heads, the next one's features loading
-// while it works on the current one.  Bound by its 2-byte accesses:
-// [8192,(16,16),101] bf16 forward 72 us, backward 94 us (1.5 and 1.7 TB/s).
+// while it works on the current one.  Bound by the latency
+// of its loads (one head ahead; issue 56 and 34 % of the slots, the load pipe
+// 20 %): [8192,(16,16),101] bf16 forward 72 us, backward 94 us (1.5 and 1.7 TB/s).
 // ----------------------------------------------------------------------------
 template <int NS>
 struct QkSlots {
@@ -419,7 +420,7 @@ constexpr size_t qk_bw_smem() { return (size_t)kQkStages * 256 * (4 * sizeof(QkR
 
 // Measured on a GB300, [16384,(16,16),64] bf16, packed: forward 26.6 us (5.1
 // TB/s), backward with its fold 35.3 us (5.8 TB/s); memory latency with two
-// blocks per SM (three with 80 registers spill and measured 32 us).
+// blocks per SM (three, at 80 registers, measured 31.3 us forward).
 //
 // A group is the 32 / LPR heads of one side that a warp takes at once; an item
 // is up to `per_item` groups of one token (all of them, unless that would

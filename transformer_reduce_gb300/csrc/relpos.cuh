@@ -80,9 +80,9 @@ __device__ __forceinline__ void group_natural_merge(float &m, float &s, float *s
 // ----------------------------------------------------------------------------
 // Forward, any length and alignment: TPR threads per row (a warp, or the whole
 // block for long rows), scalar accesses, an online pass and a second pass that
-// reads the row again and writes it.  Bound by its scalar accesses
-// ([32,16,512,512] bf16: 611 us here, 87 in the kernel below, which takes all
-// but the longest rows).
+// reads the row again and writes it.  Bound by issue (69 % of the slots, one
+// element per instruction): [32,16,512,512] bf16 611 us here, 87 in the kernel
+// below, which takes all but the longest rows and tensors at different offsets.
 // ----------------------------------------------------------------------------
 template <typename T, int TPR>
 __global__ void __launch_bounds__(256)
@@ -149,7 +149,7 @@ relpos_fw_loop(T *out, const T *inp, const T *mask, const T *table, const int32_
 
 // ----------------------------------------------------------------------------
 // Backward, any length and alignment, as the looped forward ([32,16,512,512]
-// bf16: 849 us here, 134 in the kernel below).
+// bf16: 832 us here, 134 in the kernel below).
 // ----------------------------------------------------------------------------
 template <typename T, int TPR>
 __global__ void __launch_bounds__(256)
@@ -499,7 +499,7 @@ __device__ __forceinline__ void relpos_mask(const T *mrow, int j0, int lo, int h
 }
 
 // Measured on a GB300: [32,16,512,512] bf16 with padding 87.4 us, 5.4 TB/s of the
-// bytes it cannot do without (the plain softmax of this shape: 84.2 us), bound
+// bytes it cannot do without (the plain softmax of these inputs: 91.6 us), bound
 // by issue (71 % of the slots; 80 registers, three blocks per SM);
 // [4,8,333,777] fp32 with a mask added element by element 21.0 us (2.8 TB/s).
 // Before rows were staged ahead and packed two to a warp: 146 us.
@@ -740,8 +740,8 @@ __host__ __device__ constexpr size_t relpos_bw_smem(int n, int band_stride) {
 // Measured on a GB300 with the fold below: [32,16,512,512] bf16 with padding
 // 134.3 us (5.0 TB/s), [8,12,777,777] fp16 causal 73.6 us (3.2 TB/s).  Bound by
 // issue at four warps per scheduler (128 registers: y and dout of a row are
-// held as floats; reading them twice from shared memory instead, 80 registers
-// and three blocks per SM measured slower).
+// held as floats; reading them twice from shared memory instead measured 140
+// against then 138.6 us, one stage and three blocks per SM at 80 registers 155).
 // blockDim.x: relpos_block<TPR>() threads, or fewer (whole warps and row
 // groups) where the arrays would not fit.
 template <typename T, int TPR, int CPT, bool AL, bool MASKED>
@@ -1000,9 +1000,9 @@ relpos_bw_vec(T *dinp, float *part, const T *dout, const T *y, const T *mask_or_
 // dtable[k, h] for one head h = blockIdx.x and the buckets of blockIdx.y: the
 // segment sums of each distance (four threads per distance, every fourth
 // segment each, so that a long chain of loads does not set the time), then
-// each bucket's distances, one warp per bucket.  All in a fixed order.  Bound by
-// the latency of its loads: 38 segments of 257 sums for 16 heads about 4 us less
-// with four threads per distance than with one.
+// each bucket's distances, one warp per bucket.  All in a fixed order.  Four
+// threads share a distance, because the loads of one wait for each other: the
+// backward of [32,16,512,512] bf16 took 138.8 us with one, 134.3 with four.
 constexpr int kRelposFoldBuckets = 32;
 constexpr int kRelposFoldThreads = 1024;
 constexpr size_t relpos_fold_smem(int R) { return (size_t)(2 * R + 1) * 8; }
