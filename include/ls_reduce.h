@@ -432,7 +432,9 @@ ls_status ls_cross_entropy_bw(void *dlogits, const void *logits, const int32_t *
  * lies in the query's future (j > i + Tk - Tq); invisible keys are written as
  * 0 and their scores never matter, NaN or not.  A row without a visible key,
  * or whose every z is -inf, is written as zeros.  A single decoding step is
- * Tq = 1.
+ * Tq = 1.  z is formed in FP32 (scaled score and bias in one rounding, then
+ * the mask) and the weights are e^(z - max z) at any magnitude: a row that
+ * sees only keys hidden by a finite mask is the softmax of those z.
  *
  *   out    [B,H,Tq,Tk] dt, device, written.  May equal `inp` (in place).
  *   inp    [B,H,Tq,Tk] dt, device, read.

@@ -635,11 +635,14 @@ relpos_fw_vec(T *out, const T *inp, const T *mask_or_null, const T *table, const
                 for (int h2 = 0; h2 < H2; ++h2) m = fmax3(m, v[k][h2].x, v[k][h2].y);
             }
             m = relpos_reduce<TPR, BLOCK, OpMax>(m, red_max, grp);
-            // e^(z - m) as one fused multiply-add where m * log2 e is finite;
-            // else (a row of the type's lowest values, an infinite or missing
-            // maximum) the difference is taken first
+            // e^(z - m) as one fused multiply-add.  The rounding of m * log2 e
+            // multiplies the whole row by one number, which the quotient loses:
+            // at most 2^(1/16) for |m| < 2^20, but from 2^31 on it can leave
+            // the range of ex2.  Rows of larger maxima (only keys hidden by a
+            // finite mask are left) and infinite or missing ones take the
+            // difference first.
             float2 nmL = f2(-m * kLog2e);
-            if (!(fabsf(m) < 1e30f)) {
+            if (!(fabsf(m) < 0x1p20f)) {
                 const float2 nm = f2(m == -INFINITY ? 0.f : -m);
 #pragma unroll
                 for (int k = 0; k < CPT; ++k)
