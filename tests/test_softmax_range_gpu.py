@@ -1,6 +1,8 @@
 """GPU parity of the softmax with a relative position bias where a row's largest
-score is far from zero: rows that see only keys hidden by a finite mask, large
-scores."""
+score is far from zero (rows that see only keys hidden by a finite mask, large
+scores), and for every kind of mask, within a bound that stays tight there."""
+import math
+
 import pytest
 import torch
 
@@ -11,6 +13,7 @@ pytestmark = pytest.mark.gpu
 
 DEV = "cuda:0"
 DT = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}
+INF = math.inf
 # finite masks that programs hide keys with, and the ones around 2^20 and 2^31
 FILLS = [-1e4, -2.0 ** 20, -1.5 * 2.0 ** 20, -1e8, -1e9, -2.0 ** 31, -2e9, -3e9, -2.0 ** 32 + 1, -5e9,
          -1e10, -1e12, -1e15, -1e20, -1e29, -1e30, -1e36, 1e10, 1e20]
@@ -98,3 +101,32 @@ def test_rows_of_large_scores(lib, dt, power):
             x = (whole.double() * scale).to(dtype)
             _check(lib, x, table, buckets, None, False, 1.0, f"{Tk}")
             _check(lib, -x.abs() - x.abs().max(), table, buckets, None, True, 1.0, f"{Tk} negative")
+
+def _mask(kind, B, Tk, dtype, seed):
+    if kind == "none":
+        return None
+    g = torch.Generator().manual_seed(seed)
+    low = torch.finfo(dtype).min
+    n = torch.randint(1, Tk + 1, (B,), generator=g)
+    n[0], n[1] = 0, Tk
+    m = torch.zeros(B, Tk)
+    for b in range(B):
+        m[b, int(n[b]):] = low if kind in ("lowest", "mixed") else -INF
+    if kind in ("holes", "mixed"):
+        m = torch.where(torch.rand(B, Tk, generator=g) < 0.3, torch.tensor(-INF), m)
+    if kind == "mixed":
+        m = (m + S.grid(torch.randn(B, Tk, generator=g), 2.0 ** -4)).clamp(min=low) + \
+            torch.where(m.isneginf(), m, torch.zeros(()))
+    return m.to(dtype).to(DEV)
+
+
+@pytest.mark.parametrize("dt", list(DT))
+@pytest.mark.parametrize("kind", ["none", "pad", "holes", "lowest", "mixed"])
+@pytest.mark.parametrize("shape", [(3, 2, 40, 40), (3, 5, 17, 264), (3, 3, 77, 203), (3, 2, 1, 1001),
+                                   (3, 2, 3, 2049)])
+def test_masks_within_a_bound_that_binds(lib, dt, kind, shape):
+    x, table, buckets = _inputs(lib, shape, DT[dt], seed=7)
+    mask = _mask(kind, shape[0], shape[3], DT[dt], 11)
+    for causal in (False, True):
+        for scale in (0.5, 1.0):
+            _check(lib, x, table, buckets, mask, causal, scale, f"{kind} causal {causal}")
