@@ -612,11 +612,13 @@ ls_status ls_grad_norm(float *norm, const void *const *grads, const int64_t *siz
  * an infinite one makes finite elements 0 and infinite ones NaN.
  *
  *   out     HOST array of `count` device pointers, written, each of its
- *           gradient's size and dtype; may equal grads entry by entry.  No
- *           other overlap between entries is allowed.
+ *           gradient's size and dtype; may equal grads entry by entry.  Any
+ *           other overlap, of two outputs or of an output and a gradient, is
+ *           refused.  (Gradients may overlap one another where they are only
+ *           read.)
  *   max_norm  finite and > 0.   eps  finite and >= 0.
  * Other arguments and errors as for ls_grad_norm; LS_ERR_INVALID_ARG for a
- * bad max_norm or eps.
+ * bad max_norm or eps and for overlapping outputs.
  */
 ls_status ls_grad_clip(float *norm, void *const *out, const void *const *grads,
                        const int64_t *sizes, const int32_t *dtypes, int64_t count, float max_norm,

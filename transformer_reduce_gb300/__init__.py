@@ -11,6 +11,7 @@ if the library is missing or a call fails, they raise.
 from __future__ import annotations
 
 import array
+import bisect
 import operator
 
 from . import _lib as _lib_module
@@ -777,11 +778,27 @@ def grad_norm(grads, workspace=None, norm=None):
     return norm
 
 
+def _overlap(out, grads, nbytes):
+    """Which output (a pointer; None: none) overlaps another output, or a
+    gradient that is not its own in place."""
+    spans = sorted((p, p + n, i) for i, (p, n) in enumerate(zip(out, nbytes)) if n)
+    for (_, end, i), (beg, _, j) in zip(spans, spans[1:]):
+        if beg < end:
+            return f"out[{max(i, j)}] overlaps out[{min(i, j)}]"
+    starts = [s[0] for s in spans]
+    for j, (p, n) in enumerate(zip(grads, nbytes)):
+        k = bisect.bisect_left(starts, p + n) - 1  # the last output that begins before its end
+        if n and out[j] != p and k >= 0 and spans[k][1] > p:
+            return f"out[{spans[k][2]}] overlaps grads[{j}]"
+    return None
+
+
 def grad_clip(grads, max_norm: float, out=None, eps: float = 1e-6, workspace=None, norm=None):
     """Multiplies a list of gradients by min(1, max_norm / (norm + eps)), norm
     being ``grad_norm(grads)``; returns (out, norm).  ``out`` None clips in
     place; otherwise it is a list of tensors with the gradients' element counts
-    and dtypes.  No tensor may be in ``out`` twice."""
+    and dtypes, any of which may be its own gradient.  Outputs that overlap one
+    another or other entries' gradients are refused."""
     grads, index, ptrs, sizes, dtypes, codes = _grad_lists(grads)
     if out is None:
         out, optrs = grads, ptrs
@@ -803,6 +820,13 @@ def grad_clip(grads, max_norm: float, out=None, eps: float = 1e-6, workspace=Non
     same = optrs is ptrs
     ptrs, sizes = array.array("Q", ptrs), array.array("q", sizes)
     optrs = ptrs if same else array.array("Q", optrs)
-    _launch("ls_grad_clip", index, _ptr(norm), _at(optrs), _at(ptrs), _at(sizes), _at(codes),
-            len(grads), float(max_norm), float(eps), _ptr(workspace), workspace.numel() * 4)
+    try:
+        _launch("ls_grad_clip", index, _ptr(norm), _at(optrs), _at(ptrs), _at(sizes), _at(codes),
+                len(grads), float(max_norm), float(eps), _ptr(workspace), workspace.numel() * 4)
+    except LsError as e:
+        why = e.status == LS_ERR_INVALID_ARG and \
+            _overlap(optrs, ptrs, [n * g.element_size() for n, g in zip(sizes, grads)])
+        if why:
+            raise ValueError(why) from None
+        raise
     return out, norm

@@ -7,6 +7,7 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <atomic>
 #include <cmath>
 
@@ -859,6 +860,45 @@ static ls_status grad_check(const float *norm, void *const *out, bool clip,
     return LS_OK;
 }
 
+// Whether an output overlaps another output, or a gradient that is not its own
+// in place.  (A list's outputs are taken kBlock at a time and sorted; the
+// spans of a block that do not overlap are in order by their ends too, so the
+// last one that begins before an address range ends decides.)
+static bool grad_overlaps(void *const *out, const void *const *grads, const int64_t *sizes,
+                          const int32_t *dtypes, int64_t count) {
+    struct Span {
+        uintptr_t beg, end;
+    };
+    auto span = [&](const void *p, int64_t i) {
+        const uintptr_t a = reinterpret_cast<uintptr_t>(p);
+        return Span{a, a + (uintptr_t)sizes[i] * elem_size((ls_dtype)dtypes[i])};
+    };
+    constexpr int64_t kBlock = 512;
+    Span held[kBlock];
+    for (int64_t i0 = 0; i0 < count; i0 += kBlock) {
+        const int64_t i1 = std::min(count, i0 + kBlock);
+        int n = 0;
+        for (int64_t i = i0; i < i1; ++i)
+            if (sizes[i] > 0) held[n++] = span(out[i], i);
+        if (n == 0) continue;
+        std::sort(held, held + n, [](const Span &a, const Span &b) { return a.beg < b.beg; });
+        for (int k = 1; k < n; ++k)
+            if (held[k].beg < held[k - 1].end) return true;
+        auto meets = [&](const Span &s) {
+            if (s.end <= held[0].beg || s.beg >= held[n - 1].end) return false;
+            const Span *past = std::partition_point(
+                held, held + n, [&](const Span &a) { return a.beg < s.end; });
+            return past[-1].end > s.beg;
+        };
+        for (int64_t j = 0; j < count; ++j) {
+            if (sizes[j] == 0) continue;
+            if (out[j] != grads[j] && meets(span(grads[j], j))) return true;
+            if (j >= i1 && meets(span(out[j], j))) return true;
+        }
+    }
+    return false;
+}
+
 size_t ls_grad_norm_workspace_size(int64_t count) {
     return (size_t)lsr::grad_parts(count) * sizeof(double);
 }
@@ -882,6 +922,7 @@ ls_status ls_grad_clip(float *norm, void *const *out, const void *const *grads,
     const ls_status s = grad_check(norm, out, true, grads, sizes, dtypes, count, workspace,
                                    workspace_bytes);
     if (s != LS_OK) return s;
+    if (grad_overlaps(out, grads, sizes, dtypes, count)) return LS_ERR_INVALID_ARG;
     return from_cuda(lsr::launch_grad_clip(norm, out, grads, sizes, dtypes, count, max_norm, eps,
                                            static_cast<double *>(workspace),
                                            static_cast<cudaStream_t>(stream)));
