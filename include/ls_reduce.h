@@ -549,7 +549,7 @@ size_t ls_qk_norm_rope_bw_workspace_size(int64_t tokens, int64_t Hq, int64_t Hk,
  *   dq, dk        [tokens,heads,D] dt, device, written.  May equal dq_out and
  *                 dk_out (same strides).
  *   dgamma_q, dgamma_k  [D] float32, device, written (overwritten; zeros when
- *                 tokens == 0).
+ *                 tokens == 0; ignored, not written, for a side of 0 heads).
  *   dq_out, dk_out  gradients of the forward's outputs, dt, device, read.
  *   q, k, gamma_*, cos, sin, positions  as given to the forward.
  *   q_rstd, k_rstd  as saved by the forward.

@@ -679,14 +679,12 @@ def qk_norm_rope_bw(dq_out, dk_out, q, k, gamma_q, gamma_k, q_rstd, k_rstd, cos=
         dk = k.new_empty((tokens, Hk, D))
     else:
         dks = _like_heads("dk", dk, k)
-    # a side without heads has no gradient to sum: its gamma gradient is zero
-    make = q.new_empty if Hq and Hk else q.new_zeros
     if dgamma_q is None:
-        dgamma_q = make(D, dtype=f32)
+        dgamma_q = q.new_empty(D, dtype=f32)
     else:
         _want("dgamma_q", dgamma_q, (D,), f32)
     if dgamma_k is None:
-        dgamma_k = make(D, dtype=f32)
+        dgamma_k = q.new_empty(D, dtype=f32)
     else:
         _want("dgamma_k", dgamma_k, (D,), f32)
     dev = _one_device((q, k, dq_out, dk_out, dq, dk),
@@ -697,6 +695,11 @@ def qk_norm_rope_bw(dq_out, dk_out, q, k, gamma_q, gamma_k, q_rstd, k_rstd, cos=
             gamma_q.data_ptr(), gamma_k.data_ptr(), q_rstd.data_ptr(), k_rstd.data_ptr(),
             _ptr(cos), _ptr(sin), _ptr(positions), tokens, Hq, Hk, D, rot, max_pos, dqs, dks,
             dqos, dkos, qs, ks, 1 if interleaved else 0, workspace.data_ptr(), 4 * n, ls_dtype(q))
+    # a side without heads has no gradient to sum, and the library leaves its pointers alone
+    if not Hq:
+        dgamma_q.zero_()
+    if not Hk:
+        dgamma_k.zero_()
     return dq, dk, dgamma_q, dgamma_k
 
 
