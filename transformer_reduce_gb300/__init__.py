@@ -709,7 +709,7 @@ def qk_norm_rope_bw(dq_out, dk_out, q, k, gamma_q, gamma_k, q_rstd, k_rstd, cos=
 _DTYPE = operator.attrgetter("dtype")
 
 
-def _list_device(tensors):
+def _list_device(name, tensors):
     """The index of the one CUDA device of a list's dense tensors."""
     Tensor = _torch().Tensor
     try:
@@ -718,8 +718,10 @@ def _list_device(tensors):
             index = devices.pop()
             if index >= 0:
                 return index
-    except TypeError:
-        pass  # something that only looks like a tensor
+    except TypeError:  # something that only looks like a tensor, or none
+        for i, t in enumerate(tensors):
+            if not hasattr(t, "data_ptr"):
+                raise TypeError(f"{name}[{i}] is no tensor but {t!r}") from None
     return _dev(*tensors).index  # says what is wrong
 
 
@@ -737,7 +739,7 @@ def _grad_lists(grads):
     grads = list(grads)
     if not grads:
         raise ValueError("an empty list has no device: give at least one gradient")
-    index = _list_device(grads)
+    index = _list_device("grads", grads)
     dtypes = list(map(_DTYPE, grads))
     try:
         codes = array.array("i", map(_DTYPE_CODES.__getitem__, dtypes))
@@ -809,10 +811,11 @@ def grad_clip(grads, max_norm: float, out=None, eps: float = 1e-6, workspace=Non
         out = list(out)
         if len(out) != len(grads):
             raise ValueError(f"out must hold {len(grads)} tensors, got {len(out)}")
+        out_index = _list_device("out", out)
         if _each("numel", out) != sizes or list(map(_DTYPE, out)) != dtypes:
             for i, (o, g) in enumerate(zip(out, grads)):
                 _want(f"out[{i}]", o, g.shape, g.dtype)
-        if _list_device(out) != index:
+        if out_index != index:
             raise ValueError(f"out must be on {grads[0].device}")
         optrs = _each("data_ptr", out)
     if len(set(optrs)) < len(out):
