@@ -68,15 +68,23 @@ cudaError_t launch_qk_fw_vec(const QkSide<T> &q, const QkSide<T> &k, const QkRop
 // sizes and addresses allow; false if none do.  Forward / backward of 8192
 // tokens of 16 + 16 heads, bf16, against one warp per head (qk_fw_slots): 84
 // features in 8-byte vectors 29 / 41 us, 72 / 92; 36 features in 4-byte vectors
-// 23 / 33, 56 / 61; 100 features in 4-byte vectors (32 lanes) 44 / 98, 72 / 95.
-template <typename T, typename F>
+// 23 / 33, 56 / 61.
+// Vectors of two elements on 32 lanes (66 to 128 features) are for the forward
+// alone.  The same call in vectors / by one warp per head, forward and
+// backward: bf16 66 features 43 / 71 and 98 / 87 us, 100 features 44 / 72 and
+// 99 / 92, 126 features 44 / 73 and 99 / 98; fp32 66 features 44 / 66 and 103 /
+// 84, 100 features 49 / 68 and 112 / 91, 126 features 56 / 72 and 113 / 97.
+// (Only 128 features of bf16 4 bytes off a boundary lose by it: 96 / 98.)
+template <typename T, bool BACK, typename F>
 bool qk_pick(const QkSide<T> &q, const QkSide<T> &k, const QkRope &r, F f) {
     constexpr int W = Traits<T>::kVec;  // 16 bytes
     int lanes = qk_lanes_vec(q, k, r, W, 2);
-#define X(V_, L_)                                                                \
-    if (lanes == L_) {                                                           \
-        f(std::integral_constant<int, V_>(), std::integral_constant<int, L_>()); \
-        return true;                                                             \
+#define X(V_, L_)                                                                    \
+    if constexpr (!(BACK && (V_) == 2 && L_ == 32)) {                                \
+        if (lanes == L_) {                                                           \
+            f(std::integral_constant<int, V_>(), std::integral_constant<int, L_>()); \
+            return true;                                                             \
+        }                                                                            \
     }
     X(W, 2) X(W, 4) X(W, 8) X(W, 16) X(W, 32)
     lanes = qk_lanes_vec(q, k, r, W / 2, 8);  // 8 bytes
@@ -104,7 +112,7 @@ cudaError_t launch_qk_fw_slots(const QkSide<T> &q, const QkSide<T> &k, const QkR
 template <typename T>
 cudaError_t launch_qk_fw(QkSide<T> q, QkSide<T> k, QkRope r, cudaStream_t st) {
     cudaError_t e = cudaSuccess;
-    if (qk_pick(q, k, r, [&](auto v, auto lanes) {
+    if (qk_pick<T, false>(q, k, r, [&](auto v, auto lanes) {
             constexpr int V = decltype(v)::value, L = decltype(lanes)::value;
             e = r.interleaved ? launch_qk_fw_vec<T, V, L, true>(q, k, r, st)
                               : launch_qk_fw_vec<T, V, L, false>(q, k, r, st);
@@ -132,7 +140,7 @@ template <typename T>
 cudaError_t launch_qk_bw_rows(const QkSide<T> &q, const QkSide<T> &k, const QkRope &r, float *part,
                               int64_t &nq, int64_t &nk, cudaStream_t st) {
     cudaError_t e = cudaSuccess;
-    if (qk_pick(q, k, r, [&](auto v, auto lanes) {
+    if (qk_pick<T, true>(q, k, r, [&](auto v, auto lanes) {
             constexpr int V = decltype(v)::value, L = decltype(lanes)::value;
             e = r.interleaved ? launch_qk_bw_vec<T, V, L, true>(q, k, r, part, nq, nk, st)
                               : launch_qk_bw_vec<T, V, L, false>(q, k, r, part, nq, nk, st);
