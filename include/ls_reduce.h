@@ -74,9 +74,12 @@ typedef enum ls_status {
  *
  *   out   [B,H,Tq,Tk] dt, device, written.  May equal `inp` (in place).
  *   inp   [B,H,Tq,Tk] dt, device, read.  Scores are expected to be finite.
- *   mask  [B,Tk] dt additive mask (0 = keep, -inf = padded key), device,
+ *   mask  [B,Tk] dt additive mask (0 = keep, -inf = padded key; any finite
+ *         bias is added, and a row that sees only keys hidden by one, -1e10
+ *         or the type's lowest value, is the softmax of its z), device,
  *         read; NULL means no mask.  Shared by all heads and queries of a
- *         batch entry.  Keys whose mask is -inf are not read from `inp`.
+ *         batch entry.  Keys whose mask is -inf are not read from `inp` where
+ *         a batch entry's visible keys are contiguous, and never matter.
  *   causal  nonzero: mask future keys.  Requires Tq <= Tk; the Tq queries are
  *           the last Tq positions of the key sequence (bottom-right
  *           alignment), so query i sees keys j <= i + (Tk - Tq); with

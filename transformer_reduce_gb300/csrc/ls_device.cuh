@@ -337,9 +337,9 @@ __device__ __forceinline__ void group_sum2_of(float &a, float &b, float *smem, i
     }
 }
 
-// Online (max, sum-of-exp2) pair, merged across a row group; used by the
-// looped path for rows longer than the register-resident buckets.  The pair
-// (m, s) stands for s * 2^m; m = -inf means "no finite element yet".
+// Online (max, sum-of-exp2) pair, merged across a row group; used by the cross
+// entropy.  The pair (m, s) stands for s * 2^m; m = -inf means "no finite
+// element yet".
 __device__ __forceinline__ void ms_merge(float &m, float &s, float m2, float s2) {
     float mn = fmaxf(m, m2);
     if (mn == -INFINITY)
@@ -394,6 +394,41 @@ __device__ __forceinline__ float fast_rcp(float x) {
     float y;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+
+// Online pair (m, s) standing for s * e^m, merged across a row group.
+// Natural units: a row whose every key carries the lowest value of the
+// storage type still has a finite maximum, which log2 units would overflow.
+__device__ __forceinline__ void natural_merge(float &m, float &s, float m2, float s2) {
+    const float mn = fmaxf(m, m2);
+    if (mn == -INFINITY) {
+        s += s2;  // empty, or NaN sums of rows without a comparable key
+        return;
+    }
+    s = (m == -INFINITY ? s : s * fast_exp2((m - mn) * kLog2e)) +
+        (m2 == -INFINITY ? s2 : s2 * fast_exp2((m2 - mn) * kLog2e));
+    m = mn;
+}
+template <int TPR>
+__device__ __forceinline__ void group_natural_merge(float &m, float &s, float *smem) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        const float m2 = __shfl_xor_sync(0xffffffffu, m, o);
+        const float s2 = __shfl_xor_sync(0xffffffffu, s, o);
+        natural_merge(m, s, m2, s2);
+    }
+    if constexpr (TPR > 32) {
+        const int warp = threadIdx.x >> 5;
+        if ((threadIdx.x & 31) == 0) {
+            smem[warp] = m;
+            smem[32 + warp] = s;
+        }
+        __syncthreads();
+        m = smem[0];
+        s = smem[32];
+        for (int w = 1; w < TPR / 32; ++w) natural_merge(m, s, smem[w], smem[32 + w]);
+        __syncthreads();
+    }
 }
 
 }  // namespace lsr

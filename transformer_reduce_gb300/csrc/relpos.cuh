@@ -42,41 +42,6 @@ __device__ __forceinline__ float relpos_bias(const T *table, const int32_t *buck
     return id >= 0 && id < p.num_buckets ? Traits<T>::load1_cached(table + id * p.H + h) : 0.f;
 }
 
-// Online pair (m, s) standing for s * e^m, merged across a row group.
-// Natural units: a row whose every key carries the lowest value of the
-// storage type still has a finite maximum, which log2 units would overflow.
-__device__ __forceinline__ void natural_merge(float &m, float &s, float m2, float s2) {
-    const float mn = fmaxf(m, m2);
-    if (mn == -INFINITY) {
-        s += s2;  // empty, or NaN sums of rows without a comparable key
-        return;
-    }
-    s = (m == -INFINITY ? s : s * fast_exp2((m - mn) * kLog2e)) +
-        (m2 == -INFINITY ? s2 : s2 * fast_exp2((m2 - mn) * kLog2e));
-    m = mn;
-}
-template <int TPR>
-__device__ __forceinline__ void group_natural_merge(float &m, float &s, float *smem) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        const float m2 = __shfl_xor_sync(0xffffffffu, m, o);
-        const float s2 = __shfl_xor_sync(0xffffffffu, s, o);
-        natural_merge(m, s, m2, s2);
-    }
-    if constexpr (TPR > 32) {
-        const int warp = threadIdx.x >> 5;
-        if ((threadIdx.x & 31) == 0) {
-            smem[warp] = m;
-            smem[32 + warp] = s;
-        }
-        __syncthreads();
-        m = smem[0];
-        s = smem[32];
-        for (int w = 1; w < TPR / 32; ++w) natural_merge(m, s, smem[w], smem[32 + w]);
-        __syncthreads();
-    }
-}
-
 // ----------------------------------------------------------------------------
 // Forward, any length and alignment: TPR threads per row (a warp, or the whole
 // block for long rows), scalar accesses, an online pass and a second pass that

@@ -243,8 +243,24 @@ softmax_fw_vec(T *out, const T *inp, const T *mask, int64_t rows,
         // e = 2^(v * mul - m * log2e); window rows of the scaled softmax hold
         // x, whose maximum times scale (> 0) is the maximum of scale * x
         if (SCALED && !gen) m *= scale;
-        const float mL = m == -INFINITY ? 0.f : m * kLog2e;  // a row with no visible key sums to 0
-        const float2 mul = f2(SCALED && !gen ? scale * kLog2e : kLog2e);
+        float mL = m == -INFINITY ? 0.f : m * kLog2e;  // a row with no visible key sums to 0
+        float2 mul = f2(SCALED && !gen ? scale * kLog2e : kLog2e);
+        // The rounding of m * log2 e multiplies the whole row by one number,
+        // which the quotient loses while it is small: 2^(1/16) at most for
+        // |m| < 2^20.  Rows of larger maxima (only keys hidden by a finite
+        // mask are left) take the difference first.
+        if (!(fabsf(m) < 0x1p20f) && m != -INFINITY) {
+            const float2 by = f2(SCALED && !gen ? scale : 1.f);
+#pragma unroll
+            for (int kk = 0; kk < CPT; ++kk) {
+                const int j0 = (kk * TPR + lane) * V;
+                if (j0 < hi && j0 + V > lo)
+#pragma unroll
+                    for (int h = 0; h < H2; ++h) v[kk][h] = add2(mul2(v[kk][h], by), f2(-m));
+            }
+            mL = 0.f;
+            mul = f2(kLog2e);
+        }
         float2 sum2 = f2(0.f);
 #pragma unroll
         for (int kk = 0; kk < CPT; ++kk) {
@@ -354,7 +370,9 @@ softmax_bw_vec(T *dinp, const T *dout, const T *y, int64_t rows, int Tk) {
 
 // ----------------------------------------------------------------------------
 // Looped forward for long, ragged or unaligned rows: scalar accesses, pass 1
-// keeps an online (max, sum of exp2) per thread, pass 2 re-reads and writes.
+// keeps an online (max, sum of exponentials) per thread, pass 2 re-reads and
+// writes.  The maximum is subtracted before the product with log2 e, so that
+// rows of any finite values are a softmax.
 // ----------------------------------------------------------------------------
 template <typename T, int TPR>
 __global__ void __launch_bounds__(TPR <= 32 ? 256 : TPR)
@@ -382,15 +400,15 @@ softmax_fw_loop(T *out, const T *inp, const T *mask, int64_t rows,
         for (int64_t j = lane; j < jend; j += TPR) {
             const float mv = mrow ? Tr::load1_cached(mrow + j) : 0.f;
             if (mv == -INFINITY) continue;
-            const float z = fmaf(Tr::load1(xrow + j), scale, mv) * kLog2e;
+            const float z = fmaf(Tr::load1(xrow + j), scale, mv);
             if (z > m) {  // new running max: rescale what was summed so far
-                s = (m == -INFINITY ? 0.f : s * exp2f(m - z)) + 1.f;
+                s = (m == -INFINITY ? 0.f : s * fast_exp2((m - z) * kLog2e)) + 1.f;
                 m = z;
-            } else {
-                s += exp2f(z - m);
+            } else if (z != -INFINITY) {
+                s += fast_exp2((z - m) * kLog2e);
             }
         }
-        group_ms_merge<TPR>(m, s, red);
+        group_natural_merge<TPR>(m, s, red);
         const float inv = (m == -INFINITY || !(s > 0.f)) ? 0.f : 1.f / s;
         if (m == -INFINITY) m = 0.f;
 
@@ -401,7 +419,7 @@ softmax_fw_loop(T *out, const T *inp, const T *mask, int64_t rows,
                 if (j < jend) {
                     const float mv = mrow ? Tr::load1_cached(mrow + j) : 0.f;
                     if (mv != -INFINITY)
-                        yv = exp2f(fmaf(Tr::load1(xrow + j), scale, mv) * kLog2e - m) * inv;
+                        yv = fast_exp2((fmaf(Tr::load1(xrow + j), scale, mv) - m) * kLog2e) * inv;
                 }
                 Tr::store1(orow + j, yv);
             }
