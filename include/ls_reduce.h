@@ -473,13 +473,16 @@ size_t ls_softmax_bw_relpos_workspace_size(int64_t H, int64_t max_distance);
  *     dtable[k,h] = sum over every b, i and visible j with
  *                   bucket[r + R] == k of dz[b,h,i,j]
  * dz enters the table's sum in FP32, before dinp is rounded.  Invisible keys
- * are neither read from dout / out_fw nor summed.  The sums are taken in an
- * order that depends only on the arguments: bitwise reproducible.
+ * are not summed, and what dout / out_fw hold there never matters; 16-byte
+ * chunks without a visible key are not read where a batch entry's visible keys
+ * are contiguous.  The sums are taken in an order that depends only on the
+ * sizes, the dtype and the pointers' offsets within 16 bytes: the same call is
+ * bitwise reproducible.
  *
  *   dinp    [B,H,Tq,Tk] dt, device, written.  May equal `dout`.
  *   dtable  [num_buckets,H] float32, device, written (overwritten; zeros when
  *           there is no score).
- *   dout, out_fw  [B,H,Tq,Tk] dt, device, read on visible keys only.
+ *   dout, out_fw  [B,H,Tq,Tk] dt, device, read (see above).
  *   mask, bucket, causal, scale  as given to the forward.
  *   workspace  device scratch of at least
  *           ls_softmax_bw_relpos_workspace_size(H, max_distance) bytes,
@@ -547,7 +550,9 @@ size_t ls_qk_norm_rope_bw_workspace_size(int64_t tokens, int64_t Hq, int64_t Hk,
  * back by the position's angles, xhat = x * rstd and g = gamma * dn, per row:
  *     dx_j     = rstd * (g_j - xhat_j * sum_k(g_k xhat_k) / D)
  *     dgamma_j = sum over every token and head of the side of dn_j * xhat_j
- * The gamma sums are taken in an order that depends only on the sizes.
+ * The gamma sums are taken in an order that depends only on the sizes, the
+ * dtype, the strides and the pointers' alignment (which choose the width of the
+ * accesses): the same call is bitwise reproducible.
  *
  *   dq, dk        [tokens,heads,D] dt, device, written.  May equal dq_out and
  *                 dk_out (same strides).
@@ -588,7 +593,8 @@ size_t ls_grad_norm_workspace_size(int64_t count);
  *     norm = sqrt(sum over all tensors of the sum of g^2)
  * Squares are summed in FP32 within 8 vectors of a thread (in FP64 where they
  * would over- or underflow) and in FP64 beyond, in an order that depends only
- * on the list: bitwise reproducible.  inf or NaN elements give inf or NaN.
+ * on the list's sizes and dtypes and its pointers' offsets within 16 bytes: the
+ * same call is bitwise reproducible.  inf or NaN elements give inf or NaN.
  *
  *   norm    [1] float32, device, written (0 for an empty list).
  *   grads, sizes, dtypes  HOST arrays of `count` entries, read before the

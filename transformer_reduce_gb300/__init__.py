@@ -486,8 +486,8 @@ def softmax_relpos_workspace(H: int, max_distance: int, device):
 def softmax_bw_relpos(dout, out_fw, buckets, num_buckets: int, mask=None, causal: bool = False,
                       scale=None, workspace=None, dinp=None, dtable=None):
     """Gradients of ``softmax_fw_relpos``: (dscores, dtable), dtable fp32
-    [num_buckets, H] in a fixed summation order.  Reads only visible keys;
-    ``dinp`` may be ``dout``."""
+    [num_buckets, H] in a fixed summation order.  What ``dout`` and ``out_fw``
+    hold at invisible keys never matters; ``dinp`` may be ``dout``."""
     f32 = _torch().float32
     if dout.dim() != 4:
         raise ValueError("dout must be [B, H, Tq, Tk]")
@@ -638,8 +638,8 @@ def qk_norm_rope_fw(q, k, gamma_q, gamma_k, cos=None, sin=None, positions=None,
                       (gamma_q, gamma_k, cos, sin, positions, q_rstd, k_rstd))
     _launch("ls_qk_norm_rope_fw", dev, q_out.data_ptr(), k_out.data_ptr(), q_rstd.data_ptr(),
             k_rstd.data_ptr(), q.data_ptr(), k.data_ptr(), gamma_q.data_ptr(),
-            gamma_k.data_ptr(), _ptr(cos), _ptr(sin), _ptr(positions), tokens, Hq, Hk, D, rot, max_pos, qos, kos, qs, ks, 1 if interleaved else 0,
-            float(eps), ls_dtype(q))
+            gamma_k.data_ptr(), _ptr(cos), _ptr(sin), _ptr(positions), tokens, Hq, Hk, D, rot,
+            max_pos, qos, kos, qs, ks, 1 if interleaved else 0, float(eps), ls_dtype(q))
     return q_out, k_out, q_rstd, k_rstd
 
 
@@ -773,8 +773,8 @@ def _norm_outputs(grads, index, workspace, norm):
 
 
 def grad_norm(grads, workspace=None, norm=None):
-    """Global norm sqrt(sum g^2) over a list of gradients (fp32, fp16 and bf16
-    may be mixed), fp32 [1] on their device."""
+    """Global norm sqrt(sum g^2) over a list of contiguous gradients (fp32, fp16
+    and bf16 may be mixed), fp32 [1] on their device."""
     grads, index, ptrs, sizes, _, codes = _grad_lists(grads)
     workspace, norm = _norm_outputs(grads, index, workspace, norm)
     ptrs, sizes = array.array("Q", ptrs), array.array("q", sizes)

@@ -24,7 +24,8 @@
 // share an entry, are summed in registers.  Each (block, segment) writes its
 // 2R + 1 sums to the workspace; a second kernel adds a head's segments in
 // order and then the distances of each bucket in order.  No atomics: the
-// result depends only on the problem, never on scheduling.
+// result depends only on the problem (and on the tensors' offsets within 16
+// bytes, which choose the kernel), never on scheduling.
 #pragma once
 
 #include "launch.h"
@@ -470,6 +471,9 @@ __device__ __forceinline__ void relpos_mask(const T *mrow, int j0, int lo, int h
 // Before rows were staged ahead and packed two to a warp: 146 us.
 // MASKED: there is a mask (without one its registers and branches are gone: the
 // backward of [8,12,777,777] fp16, causal, 85 -> 76 us).
+// At the 80 registers of three blocks, 17 of the 92 instantiations of a 16-bit
+// type spill 4 to 68 bytes (those with a mask and four chunks, rows of odd
+// lengths most); none of fp32 do.
 template <typename T, int TPR, int CPT, bool AL, bool MASKED>
 __global__ void __launch_bounds__(relpos_block<TPR>(), (relpos_fw_min_blocks<TPR, CPT>()))
 relpos_fw_vec(T *out, const T *inp, const T *mask_or_null, const T *table, const int32_t *bucket,
@@ -710,6 +714,11 @@ __host__ __device__ constexpr size_t relpos_bw_smem(int n, int band_stride) {
 // issue at four warps per scheduler (128 registers: y and dout of a row are
 // held as floats; reading them twice from shared memory instead measured 140
 // against then 138.6 us, one stage and three blocks per SM at 80 registers 155).
+// The cut into one run of rows per block is uneven under causal and padding: of
+// the second case's 301 blocks the heaviest has 1.68 times the mean of visible
+// keys and 1.34 times that of bytes, the heaviest pair of blocks of an SM 1.21
+// and 1.11 times.  13 of the 76 instantiations of a 16-bit type spill 4 to 36
+// bytes.
 // blockDim.x: relpos_block<TPR>() threads, or fewer (whole warps and row
 // groups) where the arrays would not fit.
 template <typename T, int TPR, int CPT, bool AL, bool MASKED>
