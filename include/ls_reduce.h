@@ -54,7 +54,8 @@ typedef enum ls_dtype {
 
 typedef enum ls_status {
     LS_OK = 0,
-    LS_ERR_INVALID_ARG = 1,  /* NULL pointer, negative size, inconsistent shape */
+    LS_ERR_INVALID_ARG = 1,  /* NULL pointer, negative size, inconsistent shape,
+                                overlapping outputs */
     LS_ERR_UNSUPPORTED = 2,  /* unknown dtype, or a size beyond the limits below */
     LS_ERR_MISALIGNED = 3,   /* pointer not aligned to its element size */
     LS_ERR_WORKSPACE = 4,    /* workspace missing or smaller than required */

@@ -113,7 +113,7 @@ extern "C" {
 const char *ls_status_string(ls_status s) {
     switch (s) {
         case LS_OK: return "LS_OK";
-        case LS_ERR_INVALID_ARG: return "LS_ERR_INVALID_ARG: null pointer, negative size or inconsistent shape";
+        case LS_ERR_INVALID_ARG: return "LS_ERR_INVALID_ARG: null pointer, negative size, inconsistent shape or overlapping outputs";
         case LS_ERR_UNSUPPORTED: return "LS_ERR_UNSUPPORTED: unknown dtype or size beyond the library limits";
         case LS_ERR_MISALIGNED: return "LS_ERR_MISALIGNED: pointer not aligned to its element size";
         case LS_ERR_WORKSPACE: return "LS_ERR_WORKSPACE: workspace missing, too small or not 16-byte aligned";
