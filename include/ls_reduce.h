@@ -514,7 +514,9 @@ ls_status ls_softmax_bw_relpos(void *dinp, float *dtable, const void *dout, cons
  * The normed value is not rounded before the rotation.
  *
  *   q_out, k_out  [tokens,Hq,D], [tokens,Hk,D] dt, device, written.  May equal
- *                 q and k (in place, same strides).
+ *                 q and k (in place, same strides).  Any other overlap with
+ *                 each other or with q and k is refused, also both in place
+ *                 where q and k share memory.
  *   q_rstd, k_rstd  [tokens,Hq], [tokens,Hk] float32, device, written (saved
  *                 for the backward); NULL: not written.
  *   q, k          [tokens,Hq,D], [tokens,Hk,D] dt, device, read.
@@ -528,7 +530,7 @@ ls_status ls_softmax_bw_relpos(void *dinp, float *dtable, const void *dout, cons
  * Hq or Hk may be 0 (its pointers are then ignored).
  * Errors: LS_ERR_INVALID_ARG for a NULL pointer that is needed, negative
  * sizes, D < 1, rot odd or outside [0, D], a stride below heads * D, eps < 0
- * or not finite; LS_ERR_UNSUPPORTED for an unknown dtype or sizes beyond the
+ * or not finite, overlapping outputs; LS_ERR_UNSUPPORTED for an unknown dtype or sizes beyond the
  * limits above; LS_ERR_MISALIGNED as everywhere.
  */
 ls_status ls_qk_norm_rope_fw(void *q_out, void *k_out, float *q_rstd, float *k_rstd,
@@ -556,7 +558,8 @@ size_t ls_qk_norm_rope_bw_workspace_size(int64_t tokens, int64_t Hq, int64_t Hk,
  * accesses): the same call is bitwise reproducible.
  *
  *   dq, dk        [tokens,heads,D] dt, device, written.  May equal dq_out and
- *                 dk_out (same strides).
+ *                 dk_out (same strides); other overlaps are refused, as in the
+ *                 forward.
  *   dgamma_q, dgamma_k  [D] float32, device, written (overwritten; zeros when
  *                 tokens == 0; ignored, not written, for a side of 0 heads).
  *   dq_out, dk_out  gradients of the forward's outputs, dt, device, read.

@@ -613,7 +613,7 @@ def qk_norm_rope_fw(q, k, gamma_q, gamma_k, cos=None, sin=None, positions=None,
     rot features; pairs are (p, p + rot / 2), or neighbours when
     ``interleaved``.  Returns (q_out, k_out, q_rstd, k_rstd), the statistics
     fp32.  Tokens may be strided (slices of a packed projection); the outputs
-    may be the inputs (in place, same strides)."""
+    may be the inputs (in place, same strides) where q and k do not overlap."""
     f32 = _torch().float32
     tokens, Hq, Hk, D, qs, ks = _both_heads(q, k, gamma_q, gamma_k)
     rot, max_pos = _rotation(cos, sin, positions, tokens, D)

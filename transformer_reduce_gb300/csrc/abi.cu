@@ -715,6 +715,34 @@ static ls_status qk_tensor(const void *p, int64_t tokens, int64_t heads, int64_t
     return aligned(p, es) ? LS_OK : LS_ERR_MISALIGNED;
 }
 
+// A tensor of `tokens` rows of `row` bytes, `stride` bytes apart.
+struct QkSpan {
+    uintptr_t at;
+    int64_t row, stride;
+};
+static QkSpan qk_span(const void *p, int64_t heads, int64_t D, int64_t stride, size_t es) {
+    return QkSpan{reinterpret_cast<uintptr_t>(p), heads * D * (int64_t)es, stride * (int64_t)es};
+}
+
+// Whether two of them share a byte.  (Of tensors with different strides whose
+// ranges meet, only those that begin within a row of each other are found.)
+static bool qk_meet(const QkSpan &a, const QkSpan &b, int64_t tokens) {
+    if (a.row == 0 || b.row == 0) return false;
+    const int64_t d = (int64_t)(b.at - a.at), last = tokens - 1;
+    if (tokens == 1 || a.stride != b.stride) return d < a.row && -d < b.row;
+    // row j of b begins (j - i) * stride + d bytes past row i of a
+    int64_t k = d / a.stride, rest = d % a.stride;
+    if (rest < 0) {
+        rest += a.stride;
+        --k;
+    }
+    return (rest < a.row && k >= -last && k <= last) ||
+           (a.stride - rest < b.row && k + 1 >= -last && k + 1 <= last);
+}
+static bool qk_same(const QkSpan &a, const QkSpan &b, int64_t tokens) {
+    return a.at == b.at && (tokens == 1 || a.stride == b.stride);
+}
+
 static lsr::QkRope qk_rope(const float *cos, const float *sin, const int32_t *positions,
                            int64_t tokens, int64_t max_pos, int64_t D, int64_t rot,
                            int interleaved, float eps) {
@@ -753,6 +781,16 @@ ls_status ls_qk_norm_rope_fw(void *q_out, void *k_out, float *q_rstd, float *k_r
     if ((gamma_q && !aligned(gamma_q, es)) || (gamma_k && !aligned(gamma_k, es)) ||
         (q_rstd && !aligned(q_rstd, 4)) || (k_rstd && !aligned(k_rstd, 4)))
         return LS_ERR_MISALIGNED;
+    // each side reads and writes on its own: no output may touch the other
+    // side's tensors, nor its own input other than in place
+    const QkSpan so[2] = {qk_span(q_out, Hq, D, q_out_stride, es),
+                          qk_span(k_out, Hk, D, k_out_stride, es)};
+    const QkSpan si[2] = {qk_span(q, Hq, D, q_stride, es), qk_span(k, Hk, D, k_stride, es)};
+    if (qk_meet(so[0], so[1], tokens)) return LS_ERR_INVALID_ARG;
+    for (int i = 0; i < 2; ++i)
+        if (qk_meet(so[i], si[1 - i], tokens) ||
+            (!qk_same(so[i], si[i], tokens) && qk_meet(so[i], si[i], tokens)))
+            return LS_ERR_INVALID_ARG;
     const lsr::QkRope r =
         qk_rope(cos, sin, positions, tokens, max_pos, D, rot, interleaved, eps);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -811,6 +849,18 @@ ls_status ls_qk_norm_rope_bw(void *dq, void *dk, float *dgamma_q, float *dgamma_
     const size_t need = ls_qk_norm_rope_bw_workspace_size(tokens, Hq, Hk, D);
     if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 16)))
         return LS_ERR_WORKSPACE;
+    if (tokens > 0) {  // as in the forward
+        const QkSpan so[2] = {qk_span(dq, Hq, D, dq_stride, es), qk_span(dk, Hk, D, dk_stride, es)};
+        const QkSpan sd[2] = {qk_span(dq_out, Hq, D, dq_out_stride, es),
+                              qk_span(dk_out, Hk, D, dk_out_stride, es)};
+        const QkSpan si[2] = {qk_span(q, Hq, D, q_stride, es), qk_span(k, Hk, D, k_stride, es)};
+        if (qk_meet(so[0], so[1], tokens)) return LS_ERR_INVALID_ARG;
+        for (int i = 0; i < 2; ++i)
+            if (qk_meet(so[i], sd[1 - i], tokens) || qk_meet(so[i], si[1 - i], tokens) ||
+                (!qk_same(so[i], sd[i], tokens) && qk_meet(so[i], sd[i], tokens)) ||
+                (!qk_same(so[i], si[i], tokens) && qk_meet(so[i], si[i], tokens)))
+                return LS_ERR_INVALID_ARG;
+    }
     const lsr::QkRope r =
         qk_rope(cos, sin, positions, tokens, max_pos, D, rot, interleaved, 0.f);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
