@@ -637,6 +637,79 @@ ls_status ls_grad_clip(float *norm, void *const *out, const void *const *grads,
                        const int64_t *sizes, const int32_t *dtypes, int64_t count, float max_norm,
                        float eps, void *workspace, size_t workspace_bytes, void *stream);
 
+/* Limits of the cross entropy from hidden states. */
+#define LS_MAX_LINEAR_ROWS ((int64_t)1 << 26)
+#define LS_MAX_LINEAR_HIDDEN ((int64_t)1 << 16)
+#define LS_MAX_LINEAR_VOCAB ((int64_t)1 << 28)
+
+/*
+ * Bytes of device workspace the cross entropy from hidden states needs.  The
+ * forward's holds a copy of the rows that count and 8 bytes per row and 256
+ * vocabulary entries; the backward's also a piece of the vocabulary's logit
+ * gradients (about 512 MiB, or 4096 entries per row if that is more).  Both
+ * hold a copy of w for fp32 and where hidden is no multiple of 8.  0 for sizes
+ * that are refused and, forward, without rows.  Host-only; launches nothing.
+ */
+size_t ls_linear_cross_entropy_fw_workspace_size(int64_t rows, int64_t hidden, int64_t vocab,
+                                                 ls_dtype dt);
+size_t ls_linear_cross_entropy_bw_workspace_size(int64_t rows, int64_t hidden, int64_t vocab,
+                                                 ls_dtype dt);
+
+/*
+ * Softmax cross entropy taken from hidden states and the vocabulary matrix,
+ * forward: ls_cross_entropy_fw of the logits z = x w^T, which are never stored.
+ * For each row r with target class t = target[r]:
+ *     lse_r  = log sum_v exp(z_rv),   loss_r = lse_r - z_rt
+ * The logits are FP32 sums of exact products of the stored values (fp32: of
+ * products good to about 2^-23) and are not rounded.  Ignored rows (negative
+ * target): loss = lse = 0; target >= vocab: NaN; neither row of x is read.
+ *
+ *   loss, lse  [rows] float32, device, written.
+ *   x          [rows, hidden] dt, device, read.
+ *   w          [vocab, hidden] dt, device, read.  16-byte aligned where its
+ *              rows are 16-bit types of a multiple of 8 elements.
+ *   target     [rows] int32, device, read.
+ *   workspace  device scratch of at least
+ *              ls_linear_cross_entropy_fw_workspace_size(...) bytes, 16-byte
+ *              aligned, contents ignored.  Calls that overlap on the GPU must
+ *              not share it.
+ * Errors: LS_ERR_INVALID_ARG for rows < 0, hidden or vocab < 1, a NULL pointer
+ * when rows > 0, outputs or a workspace that overlap each other or an input;
+ * LS_ERR_UNSUPPORTED for an unknown dtype, sizes beyond the limits above or
+ * more than 2^38 elements in x and w; LS_ERR_MISALIGNED, LS_ERR_WORKSPACE,
+ * LS_ERR_CUDA as everywhere.  rows == 0 launches nothing.
+ */
+ls_status ls_linear_cross_entropy_fw(float *loss, float *lse, const void *x, const void *w,
+                                     const int32_t *target, int64_t rows, int64_t hidden,
+                                     int64_t vocab, void *workspace, size_t workspace_bytes,
+                                     ls_dtype dt, void *stream);
+
+/*
+ * Softmax cross entropy from hidden states, backward: the gradients of
+ * sum_r loss_r * dloss_r, from the lse saved by the forward.
+ *     q_rv = dloss_r * ( exp(z_rv - lse_r) - [v == t_r] ),  0 in ignored rows
+ *     dx   = q w,     dw = q^T x
+ * q is made and used by pieces of the vocabulary.  For 16-bit types each q is
+ * rounded once to the storage type (fp16: after a scaling by a power of two
+ * that keeps small weights normal), since the tensor cores multiply operands
+ * of one type; sums are FP32.  Ignored rows get dx = 0 and add nothing to dw,
+ * whatever x, lse and dloss hold there.  A target >= vocab makes its row of dx
+ * and all of dw NaN.  The sums' order depends only on the sizes, the dtype and
+ * the targets' signs: the same call is bitwise reproducible.
+ *
+ *   dx         [rows, hidden] dt, device, written.
+ *   dw         [vocab, hidden] dt, device, written (overwritten; zeros when no
+ *              row counts); NULL: not computed.
+ *   x, w, target  as given to the forward.
+ *   lse, dloss [rows] float32, device, read.
+ *   workspace  as for the forward, ls_linear_cross_entropy_bw_workspace_size.
+ * Errors as for the forward.
+ */
+ls_status ls_linear_cross_entropy_bw(void *dx, void *dw, const void *x, const void *w,
+                                     const int32_t *target, const float *lse, const float *dloss,
+                                     int64_t rows, int64_t hidden, int64_t vocab, void *workspace,
+                                     size_t workspace_bytes, ls_dtype dt, void *stream);
+
 /* Static, human-readable name of a status code (never NULL). */
 const char *ls_status_string(ls_status s);
 

@@ -26,6 +26,8 @@ from ._lib import (LS_BF16, LS_ERR_CUDA, ls_cross_entropy_bw, ls_cross_entropy_f
 from ._lib import (ls_grad_clip, ls_grad_norm, ls_grad_norm_workspace_size, ls_qk_norm_rope_bw,
                    ls_qk_norm_rope_bw_workspace_size, ls_qk_norm_rope_fw, ls_softmax_bw_relpos,
                    ls_softmax_bw_relpos_workspace_size, ls_softmax_fw_relpos)
+from ._lib import (ls_linear_cross_entropy_bw, ls_linear_cross_entropy_bw_workspace_size,
+                   ls_linear_cross_entropy_fw, ls_linear_cross_entropy_fw_workspace_size)
 
 __all__ = [
     "softmax_fw", "softmax_bw", "softmax_bw_masked", "layernorm_fw", "layernorm_bw_dinp",
@@ -42,6 +44,9 @@ __all__ = [
     "ls_softmax_fw_relpos", "ls_softmax_bw_relpos", "ls_softmax_bw_relpos_workspace_size",
     "ls_qk_norm_rope_fw", "ls_qk_norm_rope_bw", "ls_qk_norm_rope_bw_workspace_size",
     "ls_grad_norm", "ls_grad_clip", "ls_grad_norm_workspace_size",
+    "linear_cross_entropy_fw", "linear_cross_entropy_bw", "linear_cross_entropy_workspace",
+    "ls_linear_cross_entropy_fw", "ls_linear_cross_entropy_bw",
+    "ls_linear_cross_entropy_fw_workspace_size", "ls_linear_cross_entropy_bw_workspace_size",
 ]
 
 
@@ -836,3 +841,88 @@ def grad_clip(grads, max_norm: float, out=None, eps: float = 1e-6, workspace=Non
             raise ValueError(why) from None
         raise
     return out, norm
+
+
+# ----------------------------------------------------------------------------
+# cross entropy from hidden states
+# ----------------------------------------------------------------------------
+def _linear(hidden, weight, target):
+    """(rows, hidden size, vocab) of the cross entropy from hidden states."""
+    if hidden.dim() != 2 or weight.dim() != 2:
+        raise ValueError("hidden must be [rows, hidden size] and weight [vocab, hidden size]")
+    (rows, D), V = hidden.shape, weight.shape[0]
+    _want("weight", weight, (V, D), hidden.dtype)
+    _want("target", target, (rows,), _torch().int32)
+    return rows, D, V
+
+
+def linear_cross_entropy_workspace(rows: int, hidden: int, vocab: int, dtype, device,
+                                   backward: bool = False):
+    """A workspace tensor of the size ls_linear_cross_entropy_fw (or, with
+    ``backward``, _bw) needs for hidden states of ``dtype``."""
+    torch = _torch()
+    size = ls_linear_cross_entropy_bw_workspace_size if backward else \
+        ls_linear_cross_entropy_fw_workspace_size
+    n = size(rows, hidden, vocab, ls_dtype(torch.empty(0, dtype=dtype)))
+    return torch.empty(max(n, 16) // 4, device=device, dtype=torch.float32)
+
+
+def linear_cross_entropy_fw(hidden, weight, target, workspace=None, loss=None, lse=None):
+    """Per-row softmax cross entropy of the logits hidden @ weight.T (hidden
+    [rows, D], weight [vocab, D]), which are not stored, against int32 target
+    [rows] (negative = ignored row); returns (loss, lse), fp32."""
+    f32 = _torch().float32
+    rows, D, V = _linear(hidden, weight, target)
+    code = ls_dtype(hidden)
+    if workspace is None:
+        n = max(ls_linear_cross_entropy_fw_workspace_size(rows, D, V, code), 16) // 4
+        workspace = hidden.new_empty(n, dtype=f32)
+    else:
+        _workspace("workspace", workspace)
+        n = workspace.numel()
+    if loss is None:
+        loss = hidden.new_empty(rows, dtype=f32)
+    else:
+        _want("loss", loss, (rows,), f32)
+    if lse is None:
+        lse = hidden.new_empty(rows, dtype=f32)
+    else:
+        _want("lse", lse, (rows,), f32)
+    dev = _same_device(hidden, weight, target, workspace, loss, lse)
+    _launch("ls_linear_cross_entropy_fw", dev, loss.data_ptr(), lse.data_ptr(), hidden.data_ptr(),
+            weight.data_ptr(), target.data_ptr(), rows, D, V, workspace.data_ptr(), 4 * n, code)
+    return loss, lse
+
+
+def linear_cross_entropy_bw(hidden, weight, target, lse, dloss, weight_grad: bool = True,
+                            workspace=None, dhidden=None, dweight=None):
+    """Gradients of ``linear_cross_entropy_fw`` from its inputs, its lse and the
+    upstream gradient of each row's loss: (dhidden, dweight) in the inputs'
+    dtype, dweight None without ``weight_grad`` (a frozen vocabulary)."""
+    torch = _torch()
+    f32 = torch.float32
+    rows, D, V = _linear(hidden, weight, target)
+    _stats(rows, hidden, lse=lse, dloss=dloss)
+    code = ls_dtype(hidden)
+    if workspace is None:
+        n = max(ls_linear_cross_entropy_bw_workspace_size(rows, D, V, code), 16) // 4
+        workspace = hidden.new_empty(n, dtype=f32)
+    else:
+        _workspace("workspace", workspace)
+        n = workspace.numel()
+    if dhidden is None:
+        dhidden = torch.empty_like(hidden)
+    else:
+        _want("dhidden", dhidden, hidden.shape, hidden.dtype)
+    if not weight_grad:
+        if dweight is not None:
+            raise ValueError("dweight is not computed without weight_grad")
+    elif dweight is None:
+        dweight = torch.empty_like(weight)
+    else:
+        _want("dweight", dweight, weight.shape, weight.dtype)
+    dev = _same_device(hidden, weight, target, lse, dloss, workspace, dhidden, dweight)
+    _launch("ls_linear_cross_entropy_bw", dev, dhidden.data_ptr(), _ptr(dweight),
+            hidden.data_ptr(), weight.data_ptr(), target.data_ptr(), lse.data_ptr(),
+            dloss.data_ptr(), rows, D, V, workspace.data_ptr(), 4 * n, code)
+    return dhidden, dweight

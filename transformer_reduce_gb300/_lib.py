@@ -54,6 +54,10 @@ SIGNATURES = {
     "ls_grad_norm_workspace_size": ([_I64], _SZ),
     "ls_grad_norm": ([_VP] * 4 + [_I64, _VP, _SZ, _VP], _INT),
     "ls_grad_clip": ([_VP] * 5 + [_I64, _F32, _F32, _VP, _SZ, _VP], _INT),
+    "ls_linear_cross_entropy_fw_workspace_size": ([_I64, _I64, _I64, _INT], _SZ),
+    "ls_linear_cross_entropy_bw_workspace_size": ([_I64, _I64, _I64, _INT], _SZ),
+    "ls_linear_cross_entropy_fw": ([_VP] * 5 + [_I64] * 3 + [_VP, _SZ, _INT, _VP], _INT),
+    "ls_linear_cross_entropy_bw": ([_VP] * 7 + [_I64] * 3 + [_VP, _SZ, _INT, _VP], _INT),
     "ls_status_string": ([_INT], ctypes.c_char_p),
 }
 
@@ -231,3 +235,24 @@ def ls_grad_clip(norm, out, grads, sizes, dtypes, count, max_norm, eps, workspac
     """As ls_grad_norm; ``out`` is a host array of void pointers too."""
     return load().ls_grad_clip(norm, out, grads, sizes, dtypes, count, max_norm, eps, workspace,
                                workspace_bytes, stream)
+
+
+def ls_linear_cross_entropy_fw_workspace_size(rows, hidden, vocab, dt) -> int:
+    return load().ls_linear_cross_entropy_fw_workspace_size(rows, hidden, vocab, dt)
+
+
+def ls_linear_cross_entropy_bw_workspace_size(rows, hidden, vocab, dt) -> int:
+    return load().ls_linear_cross_entropy_bw_workspace_size(rows, hidden, vocab, dt)
+
+
+def ls_linear_cross_entropy_fw(loss, lse, x, w, target, rows, hidden, vocab, workspace,
+                               workspace_bytes, dt, stream=0) -> int:
+    return load().ls_linear_cross_entropy_fw(loss, lse, x, w, target, rows, hidden, vocab,
+                                             workspace, workspace_bytes, dt, stream)
+
+
+def ls_linear_cross_entropy_bw(dx, dw, x, w, target, lse, dloss, rows, hidden, vocab, workspace,
+                               workspace_bytes, dt, stream=0) -> int:
+    """``dw`` None: the gradient of w is not computed."""
+    return load().ls_linear_cross_entropy_bw(dx, dw, x, w, target, lse, dloss, rows, hidden, vocab,
+                                             workspace, workspace_bytes, dt, stream)

@@ -978,4 +978,132 @@ ls_status ls_grad_clip(float *norm, void *const *out, const void *const *grads,
                                            static_cast<cudaStream_t>(stream)));
 }
 
+// ----------------------------------------------------------------------------
+// cross entropy from hidden states
+// ----------------------------------------------------------------------------
+// Bytes [at, at + n) of a tensor.
+struct Span {
+    uintptr_t at;
+    uint64_t n;
+};
+static Span span_of(const void *p, int64_t elements, size_t es) {
+    return Span{reinterpret_cast<uintptr_t>(p), p ? (uint64_t)elements * es : 0};
+}
+static bool spans_meet(const Span &a, const Span &b) {
+    return a.n > 0 && b.n > 0 && a.at < b.at + b.n && b.at < a.at + a.n;
+}
+// Whether an output shares memory with another output or an input.
+static bool outputs_overlap(std::initializer_list<Span> outs, std::initializer_list<Span> ins) {
+    for (auto o = outs.begin(); o != outs.end(); ++o) {
+        for (auto q = o + 1; q != outs.end(); ++q)
+            if (spans_meet(*o, *q)) return true;
+        for (const Span &i : ins)
+            if (spans_meet(*o, i)) return true;
+    }
+    return false;
+}
+
+static ls_status linear_ce_sizes(int64_t rows, int64_t hidden, int64_t vocab) {
+    if (rows < 0 || hidden < 1 || vocab < 1) return LS_ERR_INVALID_ARG;
+    if (rows > LS_MAX_LINEAR_ROWS || hidden > LS_MAX_LINEAR_HIDDEN || vocab > LS_MAX_LINEAR_VOCAB ||
+        (rows + vocab) * hidden > ((int64_t)1 << 38))
+        return LS_ERR_UNSUPPORTED;
+    return LS_OK;
+}
+
+static size_t linear_ce_size(bool backward, int64_t rows, int64_t hidden, int64_t vocab,
+                             ls_dtype dt) {
+    const size_t es = elem_size(dt);
+    if (es == 0 || linear_ce_sizes(rows, hidden, vocab) != LS_OK) return 0;
+    return lsr::linear_ce_workspace(backward, rows, hidden, vocab, es);
+}
+
+size_t ls_linear_cross_entropy_fw_workspace_size(int64_t rows, int64_t hidden, int64_t vocab,
+                                                 ls_dtype dt) {
+    return rows == 0 ? 0 : linear_ce_size(false, rows, hidden, vocab, dt);
+}
+
+size_t ls_linear_cross_entropy_bw_workspace_size(int64_t rows, int64_t hidden, int64_t vocab,
+                                                 ls_dtype dt) {
+    return linear_ce_size(true, rows, hidden, vocab, dt);
+}
+
+// What both directions want of x, w and the targets.
+static ls_status linear_ce_check(const void *x, const void *w, const int32_t *target, int64_t rows,
+                                 int64_t hidden, size_t es) {
+    if (!w || (rows > 0 && (!x || !target))) return LS_ERR_INVALID_ARG;
+    // 16-bit rows of whole 16 bytes are read where they lie
+    const size_t wa = es == 2 && hidden % 8 == 0 ? 16 : es;
+    if (!aligned(x, es) || !aligned(w, wa) || !aligned(target, 4)) return LS_ERR_MISALIGNED;
+    return LS_OK;
+}
+
+ls_status ls_linear_cross_entropy_fw(float *loss, float *lse, const void *x, const void *w,
+                                     const int32_t *target, int64_t rows, int64_t hidden,
+                                     int64_t vocab, void *workspace, size_t workspace_bytes,
+                                     ls_dtype dt, void *stream) {
+    const size_t es = elem_size(dt);
+    if (es == 0) return LS_ERR_UNSUPPORTED;
+    ls_status s = linear_ce_sizes(rows, hidden, vocab);
+    if (s != LS_OK) return s;
+    if (rows == 0) return LS_OK;
+    if (!loss || !lse) return LS_ERR_INVALID_ARG;
+    if ((s = linear_ce_check(x, w, target, rows, hidden, es)) != LS_OK) return s;
+    if (!aligned(loss, 4) || !aligned(lse, 4)) return LS_ERR_MISALIGNED;
+    const size_t need = ls_linear_cross_entropy_fw_workspace_size(rows, hidden, vocab, dt);
+    if (!workspace || workspace_bytes < need || !aligned(workspace, 16)) return LS_ERR_WORKSPACE;
+    if (outputs_overlap({span_of(loss, rows, 4), span_of(lse, rows, 4), span_of(workspace, need, 1)},
+                        {span_of(x, rows * hidden, es), span_of(w, vocab * hidden, es),
+                         span_of(target, rows, 4)}))
+        return LS_ERR_INVALID_ARG;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    auto launch = [&](auto zero) {
+        using T = decltype(zero);
+        return from_cuda(lsr::launch_linear_ce_fw<T>(loss, lse, static_cast<const T *>(x),
+                                                     static_cast<const T *>(w), target, rows,
+                                                     hidden, vocab, workspace, st));
+    };
+    switch (dt) {
+        case LS_F32: return launch(float());
+        case LS_F16: return launch(__half());
+        case LS_BF16: return launch(__nv_bfloat16());
+    }
+    return LS_ERR_UNSUPPORTED;
+}
+
+ls_status ls_linear_cross_entropy_bw(void *dx, void *dw, const void *x, const void *w,
+                                     const int32_t *target, const float *lse, const float *dloss,
+                                     int64_t rows, int64_t hidden, int64_t vocab, void *workspace,
+                                     size_t workspace_bytes, ls_dtype dt, void *stream) {
+    const size_t es = elem_size(dt);
+    if (es == 0) return LS_ERR_UNSUPPORTED;
+    ls_status s = linear_ce_sizes(rows, hidden, vocab);
+    if (s != LS_OK) return s;
+    if (rows > 0 && (!dx || !lse || !dloss)) return LS_ERR_INVALID_ARG;
+    if (rows == 0 && !dw) return LS_OK;
+    if ((s = linear_ce_check(x, w, target, rows, hidden, es)) != LS_OK) return s;
+    if (!aligned(dx, es) || !aligned(dw, es) || !aligned(lse, 4) || !aligned(dloss, 4))
+        return LS_ERR_MISALIGNED;
+    const size_t need = ls_linear_cross_entropy_bw_workspace_size(rows, hidden, vocab, dt);
+    if (!workspace || workspace_bytes < need || !aligned(workspace, 16)) return LS_ERR_WORKSPACE;
+    if (outputs_overlap({span_of(dx, rows * hidden, es), span_of(dw, vocab * hidden, es),
+                         span_of(workspace, need, 1)},
+                        {span_of(x, rows * hidden, es), span_of(w, vocab * hidden, es),
+                         span_of(target, rows, 4), span_of(lse, rows, 4), span_of(dloss, rows, 4)}))
+        return LS_ERR_INVALID_ARG;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    auto launch = [&](auto zero) {
+        using T = decltype(zero);
+        return from_cuda(lsr::launch_linear_ce_bw<T>(
+            static_cast<T *>(dx), static_cast<T *>(dw), static_cast<const T *>(x),
+            static_cast<const T *>(w), target, lse, dloss, rows, hidden, vocab, workspace, st));
+    };
+    switch (dt) {
+        case LS_F32: return launch(float());
+        case LS_F16: return launch(__half());
+        case LS_BF16: return launch(__nv_bfloat16());
+    }
+    return LS_ERR_UNSUPPORTED;
+}
+
 }  // extern "C"

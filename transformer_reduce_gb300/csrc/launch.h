@@ -140,4 +140,16 @@ cudaError_t launch_grad_clip(float *norm, void *const *out, const void *const *g
                              const int64_t *sizes, const int32_t *dts, int64_t count,
                              float max_norm, float eps, double *part, cudaStream_t st);
 
+// Softmax cross entropy from hidden states x [rows, D] and a vocabulary matrix
+// w [V, D] (es: bytes of an element), and its gradients (dw may be NULL).
+size_t linear_ce_workspace(bool backward, int64_t rows, int64_t D, int64_t V, size_t es);
+template <typename T>
+cudaError_t launch_linear_ce_fw(float *loss, float *lse, const T *x, const T *w,
+                                const int32_t *target, int64_t rows, int64_t D, int64_t V,
+                                void *workspace, cudaStream_t st);
+template <typename T>
+cudaError_t launch_linear_ce_bw(T *dx, T *dw, const T *x, const T *w, const int32_t *target,
+                                const float *lse, const float *dloss, int64_t rows, int64_t D,
+                                int64_t V, void *workspace, cudaStream_t st);
+
 }  // namespace lsr

@@ -1,0 +1,731 @@
+// linear_ce.cuh -- softmax cross entropy taken from hidden states x [rows, D]
+// and a vocabulary matrix W [V, D] without keeping the logits z = x W^T, and its
+// gradients (sm_103a, fifth-generation tensor cores).
+//
+//     lse_r  = log sum_v exp(z_rv),   loss_r = lse_r - z_r,t(r)
+//     q_rv   = dloss_r (exp(z_rv - lse_r) - [v == t(r)])
+//     dx     = q W,   dW = q^T x
+//
+// Three matrix products of 2 rows D V operations bound all of it (the backward
+// needs the logits again, so it makes three, the forward one).
+//
+//  * The rows that count (target >= 0) are first gathered into a dense copy of x
+//    in their order, so that ignored rows cost nothing and what they hold, NaN
+//    or not, touches nothing.
+//  * One persistent kernel makes every product: one warp loads tiles of 128 (M)
+//    and 256 (N) rows of 64 elements with TMA, one thread issues tcgen05.mma on
+//    them, four warps read the FP32 accumulators from tensor memory, which holds
+//    two tiles so that the next product runs meanwhile.
+//  * Forward: the four warps reduce a tile of logits to each row's largest
+//    logit and sum of exponentials; a second kernel joins a row's tiles in order.
+//  * Backward, by pieces of the vocabulary: the logits of a piece become q,
+//    rounded to the operands' 16-bit type, in the workspace; q W is added to dx
+//    in FP32 over the pieces, q^T x is the piece's rows of dW.
+//  * fp32 operands are three bf16 planes each (8 + 8 + 8 bits of the 24); six
+//    products of planes, smallest first, leave out terms below 2^-24.  The
+//    tensor cores cut the accumulator off where a step of 16 is added, so that
+//    a long sum drifts; after every 256 elements of fp32 operands the sum so far
+//    is therefore added up, rounding to nearest, in a second accumulator.
+//
+// Every sum has one order, given by the sizes: the results are reproducible.
+#pragma once
+
+#include <type_traits>
+
+#include "launch.h"
+#include "tensor_core.cuh"
+
+namespace lsr {
+
+constexpr int kLceM = 128, kLceN = 256, kLceK = 64;  // tile, and elements of a step along K
+constexpr int kLceStages = 4;
+constexpr int kLceBox = 64 * kLceK * 2;  // bytes of one 64 x 64 TMA box
+constexpr int kLceStage = (kLceM + kLceN) / 64 * kLceBox;
+constexpr int kLceThreads = 192;  // loader, issuer, four warps on the accumulators
+constexpr size_t kLceSmem = (size_t)kLceStages * kLceStage + 1024;
+// fp32: steps of kLceK whose products are summed before they join the tile's sum
+// ([1001,333] by [10007,333], largest error of dx over the largest dx: 1.9e-5
+// without the cut).
+constexpr int kLceCut = 4;
+constexpr int kLceChunk = 1024;  // rows counted together
+constexpr int kLcePackRows = 32;
+
+// What the kernels of one call share.
+struct LceArgs {
+    int64_t rows, D, V;     // as given
+    int64_t row_cap;        // rows of the dense copy, a multiple of kLceM
+    int64_t v0, vc;         // the piece: vocabulary entries [v0, v0 + vc)
+    int64_t q_pitch;        // elements of a row of q
+    int planes;             // 1, or 3 for fp32
+    int bf16;               // operand type of the products
+    int first, last;        // of the pieces
+    int with_dw;
+    // in the workspace
+    const int *count;       // rows that count
+    const int *row_of;      // [row_cap] their index
+    const int *target;      // [row_cap]
+    const float *row_lse2;  // [row_cap] lse * log2 e
+    const float *row_up;    // [row_cap] dloss times the scale of q
+    const float *unscale;   // 1 / the scale of q
+    float *row_hit;         // [row_cap] the target's logit
+    float2 *part;           // [tiles of V][row_cap] (largest logit * log2 e, sum)
+    void *q;                // [planes][row_cap][q_pitch]
+    float *dx_sum;          // [row_cap][D] over the pieces so far
+    void *dx, *dw;          // outputs
+};
+
+// The planes of a product, smallest terms first.
+__device__ __forceinline__ int2 lce_planes(int planes, int s) {
+    if (planes == 1) return make_int2(0, 0);
+    constexpr int kA[6] = {2, 0, 1, 1, 0, 0}, kB[6] = {0, 2, 1, 0, 1, 0};
+    return make_int2(kA[s], kB[s]);
+}
+
+// x in planes of the operand type: the value itself, or its three bf16 parts.
+template <typename T>
+struct LceSplit {
+    using O = T;
+    static constexpr int kPlanes = 1;
+    __device__ __forceinline__ static void put(O *p, int64_t, T v) { *p = v; }
+};
+template <>
+struct LceSplit<float> {
+    using O = __nv_bfloat16;
+    static constexpr int kPlanes = 3;
+    __device__ __forceinline__ static void parts(float v, O (&o)[3]) {
+        o[0] = __float2bfloat16_rn(v);
+        const float a = __bfloat162float(o[0]);
+        // what is left of a finite value; an infinite one would leave NaN
+        const float r = fabsf(a) < INFINITY ? v - a : 0.f;
+        o[1] = __float2bfloat16_rn(r);
+        o[2] = __float2bfloat16_rn(r - __bfloat162float(o[1]));
+    }
+    __device__ __forceinline__ static void put(O *p, int64_t plane, float v) {
+        O o[3];
+        parts(v, o);
+        p[0] = o[0];
+        p[plane] = o[1];
+        p[2 * plane] = o[2];
+    }
+};
+
+// ----------------------------------------------------------------------------
+// Rows that count.
+// ----------------------------------------------------------------------------
+struct LcePack {
+    int64_t rows, D, V, row_cap, pitch;  // pitch: elements of a row of the copy
+    int backward;
+    const int32_t *target;
+    const float *lse, *dloss;
+    int *chunk_count;     // [chunks]
+    float *chunk_up;      // [chunks] largest |dloss|
+    int *count, *row_of, *row_target;
+    float *row_lse2, *row_up, *unscale;
+    float *loss, *lse_out;  // forward: of the rows that do not count
+};
+
+// A row counts when it has a class.  (The backward keeps those beyond the
+// vocabulary too: their gradients are NaN.)
+__device__ __forceinline__ bool lce_counts(const LcePack &p, int32_t t) {
+    return t >= 0 && (p.backward || t < p.V);
+}
+
+static __global__ void __launch_bounds__(256) lce_count(const LcePack p) {
+    pdl_begin();
+    __shared__ int n_s[8];
+    __shared__ float up_s[8];
+    int n = 0;
+    float up = 0.f;
+    bool odd = false;  // a gradient that is not finite
+    for (int i = threadIdx.x; i < kLceChunk; i += 256) {
+        const int64_t r = (int64_t)blockIdx.x * kLceChunk + i;
+        if (r < p.rows && lce_counts(p, __ldg(p.target + r))) {
+            ++n;
+            if (p.backward) {
+                const float g = fabsf(__ldg(p.dloss + r));
+                odd |= !(g < INFINITY);
+                up = fmaxf(up, g);
+            }
+        }
+    }
+    if (odd) up = INFINITY;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        n += __shfl_xor_sync(0xffffffffu, n, o);
+        up = fmaxf(up, __shfl_xor_sync(0xffffffffu, up, o));
+    }
+    if ((threadIdx.x & 31) == 0) {
+        n_s[threadIdx.x >> 5] = n;
+        up_s[threadIdx.x >> 5] = up;
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        for (int w = 1; w < 8; ++w) {
+            n += n_s[w];
+            up = fmaxf(up, up_s[w]);
+        }
+        p.chunk_count[blockIdx.x] = n;
+        p.chunk_up[blockIdx.x] = up;
+    }
+}
+
+// Copies kLcePackRows rows of x to their places; the last block also clears
+// the rows up to the next tile.  T: type of x.  dx: of a backward, where the
+// rows that do not count become 0.
+template <typename T>
+__global__ void __launch_bounds__(256)
+lce_pack_rows(typename LceSplit<T>::O *out, const T *x, T *dx, const LcePack p) {
+    pdl_begin();
+    using O = typename LceSplit<T>::O;
+    __shared__ int before_s[8], all_s[8];
+    __shared__ float up_s[8];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int64_t row0 = (int64_t)blockIdx.x * kLcePackRows;
+    const int64_t chunk = row0 / kLceChunk;
+    const int64_t chunks = (p.rows + kLceChunk - 1) / kLceChunk;
+    int before = 0, all = 0;
+    float up = 0.f;
+    for (int64_t c = tid; c < chunks; c += 256) {
+        const int n = p.chunk_count[c];
+        all += n;
+        if (c < chunk) before += n;
+        up = fmaxf(up, p.chunk_up[c]);
+    }
+    for (int64_t r = chunk * kLceChunk + tid; r < row0; r += 256)
+        before += lce_counts(p, __ldg(p.target + r));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        before += __shfl_xor_sync(0xffffffffu, before, o);
+        all += __shfl_xor_sync(0xffffffffu, all, o);
+        up = fmaxf(up, __shfl_xor_sync(0xffffffffu, up, o));
+    }
+    if (lane == 0) {
+        before_s[warp] = before;
+        all_s[warp] = all;
+        up_s[warp] = up;
+    }
+    __syncthreads();
+    before = all = 0;
+    up = 0.f;
+    for (int w = 0; w < 8; ++w) {
+        before += before_s[w];
+        all += all_s[w];
+        up = fmaxf(up, up_s[w]);
+    }
+    // q in fp16 is scaled by a power of two so that the largest |dloss| is in
+    // [2^13, 2^14): a weight of 2^-27 is then still a normal number
+    float scale = 1.f;
+    if (sizeof(T) == 2 && std::is_same<T, __half>::value && p.backward && up > 0.f &&
+        up < INFINITY) {
+        const int e = min(max(ilogbf(up), -110), 110);
+        scale = exp2f((float)(13 - e));
+    }
+    if (blockIdx.x == 0 && tid == 0) {
+        *p.count = all;
+        if (p.backward) *p.unscale = 1.f / scale;
+    }
+    const int64_t plane = p.row_cap * p.pitch;
+    // the block's rows: a ballot of the targets gives every row its place
+    const int64_t mine = row0 + lane;
+    const int32_t t_lane = mine < p.rows ? __ldg(p.target + mine) : -1;
+    const uint32_t live = __ballot_sync(0xffffffffu, mine < p.rows && lce_counts(p, t_lane));
+    for (int i = warp; i < kLcePackRows; i += 8) {
+        const int64_t r = row0 + i;
+        if (r >= p.rows) break;
+        const int32_t t = __shfl_sync(0xffffffffu, t_lane, i);
+        const T *xr = x + r * p.D;
+        if (!((live >> i) & 1u)) {
+            if (p.backward) {
+                for (int64_t d = lane; d < p.D; d += 32) dx[r * p.D + d] = T(0.f);
+            } else if (lane == 0) {
+                const float v = t < 0 ? 0.f : __int_as_float(0x7fc00000);
+                p.loss[r] = v;
+                p.lse_out[r] = v;
+            }
+            continue;
+        }
+        const int64_t at = before + __popc(live & ((1u << i) - 1u));
+        O *o = out + at * p.pitch;
+        if (lane == 0) {
+            p.row_of[at] = (int)r;
+            p.row_target[at] = t;
+            if (p.backward) {
+                const bool in = t < p.V;
+                p.row_lse2[at] = in ? __ldg(p.lse + r) * kLog2e : __int_as_float(0x7fc00000);
+                p.row_up[at] = __ldg(p.dloss + r) * scale;
+            }
+        }
+        constexpr int V = Traits<T>::kVec;
+        if (sizeof(T) == 2 && p.D % V == 0 && reinterpret_cast<uintptr_t>(x) % 16 == 0) {
+            for (int64_t c = lane; c < p.D / V; c += 32)
+                reinterpret_cast<uint4 *>(o)[c] = ld_cached16(xr + c * V);
+        } else {
+            for (int64_t d = lane; d < p.D; d += 32) LceSplit<T>::put(o + d, plane, xr[d]);
+        }
+        for (int64_t d = p.D + lane; d < p.pitch; d += 32)
+            LceSplit<T>::put(o + d, plane, T(0.f));
+    }
+    if (blockIdx.x == gridDim.x - 1) {
+        const int64_t end = ((int64_t)all + kLceM - 1) / kLceM * kLceM;
+        for (int64_t r = all + warp; r < end; r += 8) {
+            for (int64_t d = lane; d < p.pitch; d += 32)
+                LceSplit<T>::put(out + r * p.pitch + d, plane, T(0.f));
+        }
+    }
+}
+
+// W in planes with rows of `pitch` elements (fp32, and rows that TMA cannot
+// address).
+template <typename T>
+__global__ void __launch_bounds__(256)
+lce_pack_weight(typename LceSplit<T>::O *out, const T *w, int64_t V, int64_t D, int64_t pitch) {
+    pdl_begin();
+    const int64_t n = V * pitch;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
+        const int64_t v = i / pitch, d = i - v * pitch;
+        LceSplit<T>::put(out + i, n, d < D ? w[v * D + d] : T(0.f));
+    }
+}
+
+// ----------------------------------------------------------------------------
+// The products.
+// ----------------------------------------------------------------------------
+enum { kLceStats = 0, kLceQ = 1, kLceGrads = 2 };
+
+// A tile of a launch.
+struct LceTile {
+    int job;      // kLceGrads: 0 dx, 1 dW
+    int64_t m, n; // tile indexes
+    int64_t nk;   // steps along K (of each product of planes)
+};
+
+template <int EPI>
+__device__ __forceinline__ int64_t lce_tiles(const LceArgs &g, int64_t count) {
+    const int64_t mt = (count + kLceM - 1) / kLceM;
+    if (EPI != kLceGrads) return mt * ((g.vc + kLceN - 1) / kLceN);
+    const int64_t nt = (g.D + kLceN - 1) / kLceN;
+    return (mt + (g.with_dw ? (g.vc + kLceM - 1) / kLceM : 0)) * nt;
+}
+// Products of logits: M fastest, so that the tiles in flight share the rows of
+// W (x stays in L2).  Gradients: N fastest, they share the rows of q.
+template <int EPI>
+__device__ __forceinline__ LceTile lce_tile(const LceArgs &g, int64_t count, int64_t i) {
+    LceTile t;
+    const int64_t mt = (count + kLceM - 1) / kLceM;
+    t.job = 0;
+    if (EPI != kLceGrads) {
+        t.n = i / mt;
+        t.m = i - t.n * mt;
+        t.nk = (g.D + kLceK - 1) / kLceK;
+        return t;
+    }
+    const int64_t nt = (g.D + kLceN - 1) / kLceN;
+    t.m = i / nt;
+    t.n = i - t.m * nt;
+    t.nk = (g.vc + kLceK - 1) / kLceK;
+    if (t.m >= mt) {
+        t.job = 1;
+        t.m -= mt;
+        t.nk = (count + kLceK - 1) / kLceK;
+    }
+    return t;
+}
+
+template <typename T>
+__device__ __forceinline__ T lce_round(float v);
+template <>
+__device__ __forceinline__ float lce_round<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ __half lce_round<__half>(float v) { return __float2half_rn(v); }
+template <>
+__device__ __forceinline__ __nv_bfloat16 lce_round<__nv_bfloat16>(float v) {
+    return __float2bfloat16_rn(v);
+}
+
+// 32 values to consecutive elements, the first n of them.
+template <typename T>
+__device__ __forceinline__ void lce_store32(T *p, const float (&f)[32], int n) {
+    constexpr int V = Traits<T>::kVec;
+    if (n >= 32 && reinterpret_cast<uintptr_t>(p) % 16 == 0) {
+#pragma unroll
+        for (int c = 0; c < 32; c += V) {
+            float e[V];
+#pragma unroll
+            for (int i = 0; i < V; ++i) e[i] = f[c + i];
+            *reinterpret_cast<uint4 *>(p + c) = Traits<T>::pack(e);
+        }
+    } else {
+#pragma unroll
+        for (int c = 0; c < 32; ++c)
+            if (c < n) p[c] = lce_round<T>(f[c]);
+    }
+}
+
+// T: storage type of the call.  Maps: a0, b0 of the only product or of dx; a1,
+// b1 of dW.
+template <int EPI, typename T>
+__global__ void __launch_bounds__(kLceThreads, 1)
+lce_product(const __grid_constant__ CUtensorMap a0, const __grid_constant__ CUtensorMap b0,
+            const __grid_constant__ CUtensorMap a1, const __grid_constant__ CUtensorMap b1,
+            const LceArgs g) {
+    pdl_begin();
+    extern __shared__ __align__(1024) uint8_t lce_smem[];
+    __shared__ __align__(8) uint64_t bars[2 * kLceStages + 5];
+    __shared__ uint32_t tmem_at;
+    __shared__ int abort_s;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t base = (smem_addr(lce_smem) + 1023u) & ~1023u;
+    const uint32_t bar0 = smem_addr(bars);
+    auto full = [&](int s) { return bar0 + 8u * s; };
+    auto empty = [&](int s) { return bar0 + 8u * (kLceStages + s); };
+    auto acc_full = [&](int b) { return bar0 + 8u * (2 * kLceStages + b); };
+    auto acc_empty = [&](int b) { return bar0 + 8u * (2 * kLceStages + 2 + b); };
+    const uint32_t drained = bar0 + 8u * (2 * kLceStages + 4);
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kLceStages; ++s) {
+            mbar_init(full(s), 1);
+            mbar_init(empty(s), 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(acc_full(b), 1);
+            mbar_init(acc_empty(b), 4);
+        }
+        mbar_init(drained, 1);
+        mbar_init_fence();
+        abort_s = 0;
+    }
+    if (warp == 1) tmem_alloc(smem_addr(&tmem_at), 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_at;
+    volatile int *abort = &abort_s;
+    const int64_t count = *g.count;
+    const int64_t tiles = lce_tiles<EPI>(g, count);
+    constexpr bool kCut = sizeof(T) == 4;  // planes, and sums cut in parts
+    constexpr int kBufs = kCut ? 1 : 2;    // accumulators in turn; kCut: the second holds the sum
+    constexpr int kSegs = kCut ? 6 : 1;
+    auto part_of = [](int64_t left) { return kCut && left > kLceCut ? (int64_t)kLceCut : left; };
+
+    if (warp == 0) {
+        // ---- loader ----
+        if (lane == 0) {
+            tma_prefetch_map(&a0);
+            tma_prefetch_map(&b0);
+            int s = 0;
+            uint32_t phase = 0;
+            int64_t issued = 0;
+            bool ok = true;
+            for (int64_t i = blockIdx.x; i < tiles && ok; i += gridDim.x) {
+                const LceTile t = lce_tile<EPI>(g, count, i);
+                const CUtensorMap *ma = t.job ? &a1 : &a0, *mb = t.job ? &b1 : &b0;
+                const bool a_mn = t.job == 1, b_mn = EPI == kLceGrads;
+                const int m0 = (int)(t.m * kLceM), n0 = (int)(t.n * kLceN);
+                for (int64_t kp = 0; kp < t.nk && ok; kp += kLceCut) {
+                    const int64_t len = part_of(t.nk - kp);
+                    for (int64_t j = 0; j < len * kSegs; ++j) {
+                        const int seg = (int)(j / len);
+                        const int2 pl = lce_planes(kCut ? 3 : 1, seg);
+                        ok = mbar_wait(empty(s), phase ^ 1u, abort);
+                        if (!ok) break;
+                        mbar_expect(full(s), kLceStage);
+                        const uint32_t at = base + s * kLceStage;
+                        const int k0 = (int)(kp + j - seg * len) * kLceK;
+#pragma unroll
+                        for (int b = 0; b < kLceM / 64; ++b)
+                            tma_load_3d(at + b * kLceBox, ma, full(s), a_mn ? m0 + 64 * b : k0,
+                                        a_mn ? k0 : m0 + 64 * b, pl.x);
+#pragma unroll
+                        for (int b = 0; b < kLceN / 64; ++b)
+                            tma_load_3d(at + (kLceM / 64 + b) * kLceBox, mb, full(s),
+                                        b_mn ? n0 + 64 * b : k0, b_mn ? k0 : n0 + 64 * b, pl.y);
+                        ++issued;
+                        if (++s == kLceStages) {
+                            s = 0;
+                            phase ^= 1u;
+                        }
+                    }
+                    if (!kCut) break;
+                }
+            }
+            // no copy may be in flight when the block ends: the last ones' barriers
+            for (int64_t j = issued > kLceStages ? issued - kLceStages : 0; j < issued; ++j)
+                mbar_wait(full((int)(j % kLceStages)), (uint32_t)((j / kLceStages) & 1), nullptr);
+        }
+    } else if (warp == 1) {
+        // ---- issuer ----
+        if (lane == 0) {
+            int s = 0, buf = 0;
+            uint32_t phase = 0, acc_phase = 0;
+            bool ok = true;
+            for (int64_t i = blockIdx.x; i < tiles && ok; i += gridDim.x) {
+                const LceTile t = lce_tile<EPI>(g, count, i);
+                if (t.nk == 0) continue;
+                const bool a_mn = t.job == 1, b_mn = EPI == kLceGrads;
+                const uint32_t idesc = tc_idesc(g.bf16 != 0, a_mn, b_mn, kLceM, kLceN);
+                for (int64_t kp = 0; kp < t.nk && ok; kp += kLceCut) {
+                    const int64_t len = part_of(t.nk - kp) * kSegs;
+                    ok = mbar_wait(acc_empty(buf), acc_phase ^ 1u, abort);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t d = tmem + buf * kLceN;
+                    for (int64_t k = 0; k < len; ++k) {
+                        ok = mbar_wait(full(s), phase, abort);
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint32_t at = base + s * kLceStage;
+                        const uint64_t da = tc_desc(at, kLceBox);
+                        const uint64_t db = tc_desc(at + kLceM / 64 * kLceBox, kLceBox);
+                        // 16 elements further along K: 32 bytes of a row, or 16 rows
+                        const uint64_t sa = a_mn ? 16 * 128 / 16 : 32 / 16;
+                        const uint64_t sb = b_mn ? 16 * 128 / 16 : 32 / 16;
+#pragma unroll
+                        for (int kk = 0; kk < kLceK / 16; ++kk)
+                            tc_mma(d, da + kk * sa, db + kk * sb, idesc, k > 0 || kk > 0);
+                        tc_commit(empty(s));
+                        if (++s == kLceStages) {
+                            s = 0;
+                            phase ^= 1u;
+                        }
+                    }
+                    if (!ok) break;
+                    tc_commit(acc_full(buf));
+                    if (++buf == kBufs) {
+                        buf = 0;
+                        acc_phase ^= 1u;
+                    }
+                    if (!kCut) break;
+                }
+            }
+            tc_commit(drained);
+            mbar_wait(drained, 0, nullptr);
+        }
+    } else {
+        // ---- accumulators ----
+        const int quarter = warp & 3;
+        const int row_in = 32 * quarter + lane;
+        int buf = 0;
+        uint32_t acc_phase = 0;
+        bool ok = true;
+        for (int64_t i = blockIdx.x; i < tiles; i += gridDim.x) {
+            const LceTile t = lce_tile<EPI>(g, count, i);
+            const bool some = t.nk > 0;
+            const uint32_t mine = tmem + ((uint32_t)(32 * quarter) << 16);
+            auto arrived = [&]() {  // the whole warp agrees on whether the product came
+                if (some && ok)
+                    ok = __all_sync(0xffffffffu, mbar_wait(acc_full(buf), acc_phase, abort));
+                tc_fence_after();
+            };
+            auto release = [&]() {
+                if (!some) return;
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(acc_empty(buf));
+                if (++buf == kBufs) {
+                    buf = 0;
+                    acc_phase ^= 1u;
+                }
+            };
+            // fp32: all parts of the sum but the last
+            bool more = false;
+            if constexpr (kCut) {
+                for (int64_t left = t.nk - kLceCut; left > 0; left -= kLceCut) {
+                    arrived();
+                    if (ok) {
+#pragma unroll 1
+                        for (int c = 0; c < kLceN / 32; ++c) {
+                            float f[32];
+                            tmem_load32(f, mine + 32 * c);
+                            if (more) {
+                                float sum[32];
+                                tmem_load32(sum, mine + kLceN + 32 * c);
+#pragma unroll
+                                for (int e = 0; e < 32; ++e) f[e] += sum[e];
+                            }
+                            tmem_store32(mine + kLceN + 32 * c, f);
+                        }
+                    }
+                    more = true;
+                    release();
+                }
+            }
+            arrived();
+            const uint32_t src = mine + buf * kLceN;
+            const int64_t row = t.m * kLceM + row_in;
+            // columns [32 c, 32 c + 32) of the tile; NaN if the product did not come
+            auto load = [&](int c, float(&f)[32]) {
+                if (some && ok) {
+                    tmem_load32(f, src + 32 * c);
+                    if (kCut && more) {
+                        float sum[32];
+                        tmem_load32(sum, mine + kLceN + 32 * c);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) f[e] += sum[e];
+                    }
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) f[e] = ok ? 0.f : __int_as_float(0x7fc00000);
+                }
+            };
+            if constexpr (EPI == kLceStats) {
+                const int64_t n0 = g.v0 + t.n * kLceN;
+                const int width = (int)min((int64_t)kLceN, g.V - n0);
+                const int hit = row < count ? g.target[row] - (int)n0 : -1;
+                float m = -INFINITY, sum = 0.f;
+#pragma unroll 1
+                for (int c = 0; c < kLceN / 32; ++c) {
+                    float f[32];
+                    load(c, f);
+                    if (32 * c >= width) continue;
+                    if (32 * c + 32 > width) {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            if (32 * c + e >= width) f[e] = -INFINITY;
+                    }
+                    if ((unsigned)(hit - 32 * c) < 32u) {
+                        float v = 0.f;
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            if (hit - 32 * c == e) v = f[e];
+                        g.row_hit[row] = v;
+                    }
+                    float top = f[0];
+#pragma unroll
+                    for (int e = 1; e < 31; e += 2) top = fmax3(top, f[e], f[e + 1]);
+                    top = fmaxf(top, f[31]);
+                    const float m2 = fmaxf(m, top * kLog2e);
+                    const float use = m2 == -INFINITY ? 0.f : m2;
+                    float2 s2 = f2(0.f);
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2) {
+                        float2 z = fma2(make_float2(f[e], f[e + 1]), f2(kLog2e), f2(-use));
+                        z.x = fast_exp2(z.x);
+                        z.y = fast_exp2(z.y);
+                        s2 = add2(s2, z);
+                    }
+                    sum = (m == -INFINITY ? sum : sum * fast_exp2(m - use)) + (s2.x + s2.y);
+                    m = m2;
+                }
+                if (row < count) g.part[t.n * g.row_cap + row] = make_float2(m, sum);
+            } else if constexpr (EPI == kLceQ) {
+                using O = typename LceSplit<T>::O;
+                const int64_t n0 = t.n * kLceN;  // within the piece
+                const int width = (int)min((int64_t)kLceN, g.V - g.v0 - n0);
+                const bool live = row < count;
+                const float l2 = live ? g.row_lse2[row] : 0.f;
+                const float up = live ? g.row_up[row] : 0.f;
+                const int hit = live ? g.target[row] - (int)(g.v0 + n0) : -1;
+                O *q = static_cast<O *>(g.q) + row * g.q_pitch + n0;
+                const int64_t plane = g.row_cap * g.q_pitch;
+#pragma unroll 1
+                for (int c = 0; c < kLceN / 32; ++c) {
+                    float f[32];
+                    load(c, f);
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2) {
+                        float2 z = fma2(make_float2(f[e], f[e + 1]), f2(kLog2e), f2(-l2));
+                        f[e] = fast_exp2(z.x);
+                        f[e + 1] = fast_exp2(z.y);
+                    }
+                    if ((unsigned)(hit - 32 * c) < 32u) {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            if (hit - 32 * c == e) f[e] -= 1.f;
+                    }
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        f[e] = live && 32 * c + e < width ? f[e] * up : 0.f;
+                    if constexpr (LceSplit<T>::kPlanes == 1) {
+                        lce_store32<O>(q + 32 * c, f, 32);
+                    } else {
+                        float h1[32], h2[32];
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) {
+                            O o[3];
+                            LceSplit<float>::parts(f[e], o);
+                            f[e] = __bfloat162float(o[0]);
+                            h1[e] = __bfloat162float(o[1]);
+                            h2[e] = __bfloat162float(o[2]);
+                        }
+                        lce_store32<O>(q + 32 * c, f, 32);
+                        lce_store32<O>(q + plane + 32 * c, h1, 32);
+                        lce_store32<O>(q + 2 * plane + 32 * c, h2, 32);
+                    }
+                }
+            } else {
+                const float un = *g.unscale;
+                const int64_t n0 = t.n * kLceN;
+                const int width = (int)min((int64_t)kLceN, g.D - n0);
+                const bool live = t.job ? row < g.vc : row < count;
+                T *out = nullptr;
+                if (live)
+                    out = t.job ? static_cast<T *>(g.dw) + (g.v0 + row) * g.D + n0
+                                : static_cast<T *>(g.dx) + (int64_t)g.row_of[row] * g.D + n0;
+                float *sums = g.dx_sum + row * g.D + n0;
+#pragma unroll 1
+                for (int c = 0; c < kLceN / 32; ++c) {
+                    float f[32];
+                    load(c, f);
+                    const int n = width - 32 * c;
+                    if (n <= 0 || !live) continue;
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) f[e] *= un;
+                    if (t.job) {
+                        lce_store32<T>(out + 32 * c, f, n);
+                        continue;
+                    }
+                    if (!g.first) {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            if (e < n) f[e] += sums[32 * c + e];
+                    }
+                    if (g.last)
+                        lce_store32<T>(out + 32 * c, f, n);
+                    else
+                        lce_store32<float>(sums + 32 * c, f, n);
+                }
+            }
+            release();
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_free(tmem, 512);
+    }
+}
+
+// lse and loss of the rows that count, from the tiles' (largest, sum), eight
+// threads per row: each joins every eighth tile, the first joins the eight.
+static __global__ void __launch_bounds__(256)
+lce_join(float *loss, float *lse, const LceArgs g, int64_t tiles) {
+    pdl_begin();
+    __shared__ float m_s[8][32], s_s[8][32];
+    const int r_in = threadIdx.x & 31, part = threadIdx.x >> 5;
+    const int64_t count = *g.count;
+    for (int64_t r0 = (int64_t)blockIdx.x * 32; r0 < count; r0 += (int64_t)gridDim.x * 32) {
+        const int64_t row = r0 + r_in;
+        float m = -INFINITY, s = 0.f;
+        if (row < count) {
+#pragma unroll 4
+            for (int64_t t = part; t < tiles; t += 8) {
+                const float2 v = __ldcg(g.part + t * g.row_cap + row);
+                ms_merge(m, s, v.x, v.y);
+            }
+        }
+        m_s[part][r_in] = m;
+        s_s[part][r_in] = s;
+        __syncthreads();
+        if (part == 0 && row < count) {
+            for (int k = 1; k < 8; ++k) ms_merge(m, s, m_s[k][r_in], s_s[k][r_in]);
+            const float l = (m + log2f(s)) * 0.6931471805599453f;
+            const int64_t at = g.row_of[row];
+            lse[at] = l;
+            loss[at] = l - g.row_hit[row];
+        }
+        __syncthreads();
+    }
+}
+
+}  // namespace lsr
