@@ -637,6 +637,84 @@ ls_status ls_grad_clip(float *norm, void *const *out, const void *const *grads,
                        const int64_t *sizes, const int32_t *dtypes, int64_t count, float max_norm,
                        float eps, void *workspace, size_t workspace_bytes, void *stream);
 
+/*
+ * Difference of two attention softmax maps with a learned weight, forward (the
+ * attention map of a differential attention layer).  Head h of batch entry b
+ * has two maps of scores over the same keys; the Tq queries are the last Tq of
+ * the Tk key positions:
+ *     z_aj = scale * x_a[b,h,i,j] + mask[b,j]      (a = 1, 2)
+ *     p_a  = softmax over the visible j of z_a
+ *     out[b,h,i,j] = p_1j - lam_h * p_2j
+ * Visible and invisible keys as for ls_softmax_fw_relpos: invisible ones are
+ * written as 0 and their scores never matter, NaN or not; a map without a
+ * visible key, or whose every z is -inf, is 0.  NaN or +inf among a map's
+ * visible scores make the row's visible outputs NaN.
+ *
+ *   out    [B,H,Tq,Tk] dt, dense, device, written.  May equal x1 where that is
+ *          dense (in place).
+ *   stats  [B,H,Tq,4] float32, 16-byte aligned, device, written: of each map
+ *          the largest z (0 if there is none) and 1 / sum_j exp(z_j - largest)
+ *          (0 if nothing is visible), saved for the backward; NULL: not
+ *          written.
+ *   x1, x2 [B,H,Tq,Tk] dt, device, read, with dense [Tq,Tk] and strides of
+ *          x*_batch and x*_head elements (>= 0) between batch entries and
+ *          heads: both may be slices of one tensor [B,2H,Tq,Tk], by halves or
+ *          by neighbouring heads.  A stride over a single entry is ignored.
+ *   lam    [lam_count] float32, device, read: one weight per head (lam_count
+ *          == H) or one for all heads (lam_count == 1).
+ *   mask, causal, scale  as for ls_softmax_fw_relpos; mask may be NULL.
+ * Errors: LS_ERR_INVALID_ARG for NULL out / x1 / x2 / lam with a non-empty
+ * problem, negative sizes or strides, lam_count other than 1 and H, causal with
+ * Tq > Tk, scale not finite or <= 0, outputs that overlap each other or an
+ * input (except in place); LS_ERR_UNSUPPORTED for an unknown dtype, Tq or Tk
+ * beyond LS_MAX_ROW_LENGTH, H beyond LS_MAX_HEADS, B beyond 2^30 or more than
+ * 2^44 rows; LS_ERR_MISALIGNED as everywhere.
+ */
+ls_status ls_softmax_fw_diff(void *out, float *stats, const void *x1, const void *x2,
+                             const float *lam, const void *mask, int64_t B, int64_t H, int64_t Tq,
+                             int64_t Tk, int64_t x1_batch, int64_t x1_head, int64_t x2_batch,
+                             int64_t x2_head, int64_t lam_count, int causal, float scale,
+                             ls_dtype dt, void *stream);
+
+/*
+ * Bytes of device workspace ls_softmax_bw_diff needs: 4 per row.  0 without
+ * rows and for sizes that it refuses.  Host-only; launches nothing.
+ */
+size_t ls_softmax_bw_diff_workspace_size(int64_t B, int64_t H, int64_t Tq);
+
+/*
+ * Difference of two attention softmax maps, backward.  The weights p_a are made
+ * again from the scores and the saved statistics.  On visible keys, with
+ * D_a = sum over visible k of p_ak dout_k:
+ *     dx_1j  =  scale * p_1j * (dout_j - D_1)
+ *     dx_2j  = -scale * lam_h * p_2j * (dout_j - D_2)       (0 on invisible keys)
+ *     dlam_h = -sum over b, i of D_2     (lam_count == 1: over h too)
+ * Invisible keys are not summed, and what dout and the scores hold there never
+ * matters.  The sums' order depends only on the sizes, the strides, the dtype
+ * and the pointers' offsets within 16 bytes: the same call is bitwise
+ * reproducible.
+ *
+ *   dx1, dx2  as x1 and x2, written, with strides of their own; no two heads
+ *           may share memory.  dx1 may equal x1 and dx2 x2 (same strides).
+ *   dlam    [lam_count] float32, device, written (overwritten; zeros when there
+ *           is no score).
+ *   dout    [B,H,Tq,Tk] dt, dense, device, read on visible keys.
+ *   x1, x2, lam, mask, causal, scale  as given to the forward.
+ *   stats   as written by the forward.
+ *   workspace  device scratch of at least
+ *           ls_softmax_bw_diff_workspace_size(B, H, Tq) bytes, 16-byte aligned,
+ *           contents ignored.  May be NULL when there is no score.  Calls that
+ *           overlap on the GPU must not share it.
+ * Errors as for ls_softmax_fw_diff, plus LS_ERR_WORKSPACE.
+ */
+ls_status ls_softmax_bw_diff(void *dx1, void *dx2, float *dlam, const void *dout, const void *x1,
+                             const void *x2, const float *lam, const float *stats,
+                             const void *mask, int64_t B, int64_t H, int64_t Tq, int64_t Tk,
+                             int64_t dx1_batch, int64_t dx1_head, int64_t dx2_batch,
+                             int64_t dx2_head, int64_t x1_batch, int64_t x1_head, int64_t x2_batch,
+                             int64_t x2_head, int64_t lam_count, int causal, float scale,
+                             void *workspace, size_t workspace_bytes, ls_dtype dt, void *stream);
+
 /* Limits of the cross entropy from hidden states. */
 #define LS_MAX_LINEAR_ROWS ((int64_t)1 << 26)
 #define LS_MAX_LINEAR_HIDDEN ((int64_t)1 << 16)

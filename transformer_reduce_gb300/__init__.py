@@ -27,7 +27,8 @@ from ._lib import (ls_grad_clip, ls_grad_norm, ls_grad_norm_workspace_size, ls_q
                    ls_qk_norm_rope_bw_workspace_size, ls_qk_norm_rope_fw, ls_softmax_bw_relpos,
                    ls_softmax_bw_relpos_workspace_size, ls_softmax_fw_relpos)
 from ._lib import (ls_linear_cross_entropy_bw, ls_linear_cross_entropy_bw_workspace_size,
-                   ls_linear_cross_entropy_fw, ls_linear_cross_entropy_fw_workspace_size)
+                   ls_linear_cross_entropy_fw, ls_linear_cross_entropy_fw_workspace_size,
+                   ls_softmax_bw_diff, ls_softmax_bw_diff_workspace_size, ls_softmax_fw_diff)
 
 __all__ = [
     "softmax_fw", "softmax_bw", "softmax_bw_masked", "layernorm_fw", "layernorm_bw_dinp",
@@ -44,6 +45,8 @@ __all__ = [
     "ls_softmax_fw_relpos", "ls_softmax_bw_relpos", "ls_softmax_bw_relpos_workspace_size",
     "ls_qk_norm_rope_fw", "ls_qk_norm_rope_bw", "ls_qk_norm_rope_bw_workspace_size",
     "ls_grad_norm", "ls_grad_clip", "ls_grad_norm_workspace_size",
+    "softmax_fw_diff", "softmax_bw_diff", "softmax_diff_workspace",
+    "ls_softmax_fw_diff", "ls_softmax_bw_diff", "ls_softmax_bw_diff_workspace_size",
     "linear_cross_entropy_fw", "linear_cross_entropy_bw", "linear_cross_entropy_workspace",
     "ls_linear_cross_entropy_fw", "ls_linear_cross_entropy_bw",
     "ls_linear_cross_entropy_fw_workspace_size", "ls_linear_cross_entropy_bw_workspace_size",
@@ -841,6 +844,112 @@ def grad_clip(grads, max_norm: float, out=None, eps: float = 1e-6, workspace=Non
             raise ValueError(why) from None
         raise
     return out, norm
+
+
+# ----------------------------------------------------------------------------
+# difference of two softmax maps
+# ----------------------------------------------------------------------------
+def _map_strides(name, t, shape, dtype):
+    """Batch and head strides of a [B, H, Tq, Tk] tensor whose [Tq, Tk] are dense
+    (a slice of a tensor's heads is)."""
+    if t.shape != shape or t.dtype != dtype:
+        _want(name, t, shape, dtype)
+    sb, sh, sq, sk = t.stride()
+    B, H, Tq, Tk = shape
+    if (Tk > 1 and sk != 1) or (Tq > 1 and sq != Tk):
+        raise ValueError(f"{name} must have dense rows and columns in every head")
+    return sb, sh
+
+
+def _diff(scores1, scores2, lam, mask):
+    """(shape, dtype, strides of both maps) of a difference of softmax maps."""
+    if scores1.dim() != 4:
+        raise ValueError("scores1 must be [B, H, Tq, Tk]")
+    shape, dtype = scores1.shape, scores1.dtype
+    B, H, _, Tk = shape
+    strides = _map_strides("scores1", scores1, shape, dtype) + \
+        _map_strides("scores2", scores2, shape, dtype)
+    if lam.shape != (1,):
+        _want("lam", lam, (H,), _torch().float32)
+    elif lam.dtype != _torch().float32:
+        _want("lam", lam, (1,), _torch().float32)
+    if mask is not None and (mask.dtype != dtype or mask.shape != (B, Tk)):
+        _want("mask", mask, (B, Tk), dtype)
+    return shape, dtype, strides
+
+
+def softmax_fw_diff(scores1, scores2, lam, mask=None, causal: bool = False, scale=None, out=None,
+                    stats=None):
+    """softmax(scale * scores1 + mask) - lam * softmax(scale * scores2 + mask) over
+    the last axis of two maps [B,H,Tq,Tk], which may be slices of one tensor's
+    heads; ``lam`` fp32 [H] or [1] (one weight for all heads), ``mask`` additive
+    [B,Tk], future keys masked when ``causal``.  Returns (out, stats), stats fp32
+    [B,H,Tq,4] saved for the backward.  ``out`` may be a dense ``scores1``."""
+    f32 = _torch().float32
+    shape, dtype, strides = _diff(scores1, scores2, lam, mask)
+    B, H, Tq, Tk = shape
+    if out is None:
+        out = scores1.new_empty(shape)
+    else:
+        _want("out", out, shape, dtype)
+    if stats is None:
+        stats = scores1.new_empty((B, H, Tq, 4), dtype=f32)
+    else:
+        _want("stats", stats, (B, H, Tq, 4), f32)
+    dev = _one_device((scores1, scores2), (lam, mask, out, stats))
+    _launch("ls_softmax_fw_diff", dev, out.data_ptr(), stats.data_ptr(), scores1.data_ptr(),
+            scores2.data_ptr(), lam.data_ptr(), _ptr(mask), B, H, Tq, Tk, *strides, lam.numel(),
+            1 if causal else 0, 1.0 if scale is None else float(scale), ls_dtype(scores1))
+    return out, stats
+
+
+def softmax_diff_workspace(B: int, H: int, Tq: int, device):
+    """A workspace tensor of the size ls_softmax_bw_diff needs."""
+    n = ls_softmax_bw_diff_workspace_size(B, H, Tq)
+    return _torch().empty(max(n, 16) // 4, device=device, dtype=_torch().float32)
+
+
+def softmax_bw_diff(dout, scores1, scores2, lam, stats, mask=None, causal: bool = False,
+                    scale=None, workspace=None, dscores1=None, dscores2=None, dlam=None):
+    """Gradients of ``softmax_fw_diff`` from that of its output, its inputs and its
+    statistics: (dscores1, dscores2, dlam), dlam fp32 of lam's shape in a fixed
+    summation order.  What ``dout`` and the scores hold at invisible keys never
+    matters.  ``dscores1`` may be ``scores1`` and ``dscores2`` ``scores2``, and
+    both may be slices of one tensor's heads."""
+    f32 = _torch().float32
+    shape, dtype, strides = _diff(scores1, scores2, lam, mask)
+    B, H, Tq, Tk = shape
+    if dout.shape != shape or dout.dtype != dtype:
+        _want("dout", dout, shape, dtype)
+    if stats.shape != (B, H, Tq, 4) or stats.dtype != f32:
+        _want("stats", stats, (B, H, Tq, 4), f32)
+    if workspace is None:
+        n = max(ls_softmax_bw_diff_workspace_size(B, H, Tq), 16) // 4
+        workspace = dout.new_empty(n, dtype=f32)
+    else:
+        _workspace("workspace", workspace)
+        n = workspace.numel()
+    dense = (H * Tq * Tk, Tq * Tk)
+    if dscores1 is None:
+        dscores1, d1 = dout.new_empty(shape), dense
+    else:
+        d1 = _map_strides("dscores1", dscores1, shape, dtype)
+    if dscores2 is None:
+        dscores2, d2 = dout.new_empty(shape), dense
+    else:
+        d2 = _map_strides("dscores2", dscores2, shape, dtype)
+    if dlam is None:
+        dlam = lam.new_empty(lam.shape)
+    else:
+        _want("dlam", dlam, lam.shape, f32)
+    dev = _one_device((scores1, scores2, dscores1, dscores2),
+                      (dout, lam, stats, mask, workspace, dlam))
+    _launch("ls_softmax_bw_diff", dev, dscores1.data_ptr(), dscores2.data_ptr(), dlam.data_ptr(),
+            dout.data_ptr(), scores1.data_ptr(), scores2.data_ptr(), lam.data_ptr(),
+            stats.data_ptr(), _ptr(mask), B, H, Tq, Tk, *d1, *d2, *strides, lam.numel(),
+            1 if causal else 0, 1.0 if scale is None else float(scale), workspace.data_ptr(),
+            4 * n, ls_dtype(dout))
+    return dscores1, dscores2, dlam
 
 
 # ----------------------------------------------------------------------------

@@ -58,6 +58,9 @@ SIGNATURES = {
     "ls_linear_cross_entropy_bw_workspace_size": ([_I64, _I64, _I64, _INT], _SZ),
     "ls_linear_cross_entropy_fw": ([_VP] * 5 + [_I64] * 3 + [_VP, _SZ, _INT, _VP], _INT),
     "ls_linear_cross_entropy_bw": ([_VP] * 7 + [_I64] * 3 + [_VP, _SZ, _INT, _VP], _INT),
+    "ls_softmax_fw_diff": ([_VP] * 6 + [_I64] * 9 + [_INT, _F32, _INT, _VP], _INT),
+    "ls_softmax_bw_diff_workspace_size": ([_I64] * 3, _SZ),
+    "ls_softmax_bw_diff": ([_VP] * 9 + [_I64] * 13 + [_INT, _F32, _VP, _SZ, _INT, _VP], _INT),
     "ls_status_string": ([_INT], ctypes.c_char_p),
 }
 
@@ -256,3 +259,23 @@ def ls_linear_cross_entropy_bw(dx, dw, x, w, target, lse, dloss, rows, hidden, v
     """``dw`` None: the gradient of w is not computed."""
     return load().ls_linear_cross_entropy_bw(dx, dw, x, w, target, lse, dloss, rows, hidden, vocab,
                                              workspace, workspace_bytes, dt, stream)
+
+
+def ls_softmax_fw_diff(out, stats, x1, x2, lam, mask, B, H, Tq, Tk, x1_batch, x1_head, x2_batch,
+                       x2_head, lam_count, causal, scale, dt, stream=0) -> int:
+    return load().ls_softmax_fw_diff(out, stats, x1, x2, lam, mask, B, H, Tq, Tk, x1_batch,
+                                     x1_head, x2_batch, x2_head, lam_count, int(bool(causal)),
+                                     scale, dt, stream)
+
+
+def ls_softmax_bw_diff_workspace_size(B, H, Tq) -> int:
+    return load().ls_softmax_bw_diff_workspace_size(B, H, Tq)
+
+
+def ls_softmax_bw_diff(dx1, dx2, dlam, dout, x1, x2, lam, stats, mask, B, H, Tq, Tk, dx1_batch,
+                       dx1_head, dx2_batch, dx2_head, x1_batch, x1_head, x2_batch, x2_head,
+                       lam_count, causal, scale, workspace, workspace_bytes, dt, stream=0) -> int:
+    return load().ls_softmax_bw_diff(dx1, dx2, dlam, dout, x1, x2, lam, stats, mask, B, H, Tq, Tk,
+                                     dx1_batch, dx1_head, dx2_batch, dx2_head, x1_batch, x1_head,
+                                     x2_batch, x2_head, lam_count, int(bool(causal)), scale,
+                                     workspace, workspace_bytes, dt, stream)

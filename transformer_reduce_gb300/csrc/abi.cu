@@ -106,6 +106,15 @@ lsr::QkSide<T> qk_side(void *out, const void *x, const void *dout, const void *g
     return s;
 }
 
+// A tensor of heads with its typed pointer.
+template <typename T>
+lsr::DiffRows<T> diff_rows(void *p, int64_t B, int64_t H, int64_t len, int64_t batch,
+                                  int64_t head) {
+    // (the stride of a single entry does not matter, and may be anything)
+    const int64_t sb = B > 1 ? batch : H * len, sh = H > 1 ? head : len;
+    return lsr::DiffRows<T>{static_cast<T *>(p), sb, sh, (B - 1) * sb + (H - 1) * sh + len};
+}
+
 }  // namespace
 
 extern "C" {
@@ -1097,6 +1106,218 @@ ls_status ls_linear_cross_entropy_bw(void *dx, void *dw, const void *x, const vo
         return from_cuda(lsr::launch_linear_ce_bw<T>(
             static_cast<T *>(dx), static_cast<T *>(dw), static_cast<const T *>(x),
             static_cast<const T *>(w), target, lse, dloss, rows, hidden, vocab, workspace, st));
+    };
+    switch (dt) {
+        case LS_F32: return launch(float());
+        case LS_F16: return launch(__half());
+        case LS_BF16: return launch(__nv_bfloat16());
+    }
+    return LS_ERR_UNSUPPORTED;
+}
+
+// ----------------------------------------------------------------------------
+// difference of two softmax maps
+// ----------------------------------------------------------------------------
+// B batch entries of H heads of `len` dense elements each.
+struct HeadSpan {
+    uintptr_t at;
+    int64_t len, batch, head;  // bytes
+};
+// Whether a tensor may be written: no two of its heads share memory.
+static bool heads_apart(int64_t B, int64_t H, int64_t len, int64_t batch, int64_t head) {
+    if (batch < 0 || head < 0) return false;
+    const bool outer = (H == 1 || head >= len) && (B == 1 || batch >= (H - 1) * head + len);
+    const bool inner = (B == 1 || batch >= len) && (H == 1 || head >= (B - 1) * batch + len);
+    return outer || inner;
+}
+// Whether two tensors share a byte.  (Of tensors with different strides:
+// whether their ranges meet.)
+static bool heads_meet(const HeadSpan &a, const HeadSpan &b, int64_t B, int64_t H) {
+    const int64_t sb = B > 1 ? a.batch : 0, sh = H > 1 ? a.head : 0;
+    const int64_t tb = B > 1 ? b.batch : 0, th = H > 1 ? b.head : 0;
+    const uintptr_t a_end = a.at + (uintptr_t)((B - 1) * sb + (H - 1) * sh + a.len);
+    const uintptr_t b_end = b.at + (uintptr_t)((B - 1) * tb + (H - 1) * th + b.len);
+    if (a.len == 0 || b.len == 0 || a_end <= b.at || b_end <= a.at) return false;
+    if (sb != tb || sh != th) return true;
+    // -len_b < d + x * sb + y * sh < len_a for some |x| < B, |y| < H: for every step of
+    // the shorter axis, the nearest step of the other
+    const int64_t d = (int64_t)(b.at - a.at);
+    const int64_t n = B < H ? B : H, m = B < H ? H : B;
+    const int64_t sn = B < H ? sb : sh, sm = B < H ? sh : sb;
+    for (int64_t y = 1 - n; y < n; ++y) {
+        const int64_t v = d + y * sn;
+        int64_t x = sm > 0 ? -v / sm : 0;
+        for (int64_t k = x - 1; k <= x + 1; ++k) {
+            const int64_t c = k < 1 - m ? 1 - m : (k > m - 1 ? m - 1 : k);
+            const int64_t gap = v + c * sm;
+            if (gap < a.len && -gap < b.len) return true;
+        }
+    }
+    return false;
+}
+static bool heads_same(const HeadSpan &a, const HeadSpan &b, int64_t B, int64_t H) {
+    return a.at == b.at && (B == 1 || a.batch == b.batch) && (H == 1 || a.head == b.head);
+}
+
+// Sizes of both directions.
+static ls_status diff_check(int64_t B, int64_t H, int64_t Tq, int64_t Tk, int64_t lam_count,
+                            int causal, float scale) {
+    if (B < 0 || H < 0 || Tq < 0 || Tk < 0) return LS_ERR_INVALID_ARG;
+    if (causal && Tq > Tk) return LS_ERR_INVALID_ARG;
+    if (!std::isfinite(scale) || !(scale > 0.f)) return LS_ERR_INVALID_ARG;
+    if (lam_count != 1 && lam_count != H) return LS_ERR_INVALID_ARG;
+    const int64_t most = (int64_t)1 << 30;
+    if (B > most || H > LS_MAX_HEADS || Tq > LS_MAX_ROW_LENGTH || Tk > LS_MAX_ROW_LENGTH)
+        return LS_ERR_UNSUPPORTED;
+    if (B > 0 && H > 0 && Tq > 0 && Tk > 0 &&
+        (B * H > ((int64_t)1 << 44) / Tq || B * H * Tq > ((int64_t)1 << 58) / Tk))
+        return LS_ERR_UNSUPPORTED;
+    return LS_OK;
+}
+// A tensor of heads: [B, H, Tq, Tk] with strides of elements.
+static ls_status diff_tensor(const void *p, int64_t B, int64_t H, int64_t len, int64_t batch,
+                             int64_t head, size_t es) {
+    if (!p || batch < 0 || head < 0) return LS_ERR_INVALID_ARG;
+    const int64_t most = (int64_t)1 << 58;
+    if ((B > 1 && batch > most / B) || (H > 1 && head > most / H)) return LS_ERR_UNSUPPORTED;
+    (void)len;
+    return aligned(p, es) ? LS_OK : LS_ERR_MISALIGNED;
+}
+static HeadSpan head_span(const void *p, int64_t len, int64_t batch, int64_t head, size_t es) {
+    return HeadSpan{reinterpret_cast<uintptr_t>(p), len * (int64_t)es, batch * (int64_t)es,
+                    head * (int64_t)es};
+}
+// A tensor that lies in one piece.
+static HeadSpan flat_span(const void *p, int64_t elements, size_t es) {
+    return HeadSpan{reinterpret_cast<uintptr_t>(p), p ? elements * (int64_t)es : 0, 0, 0};
+}
+static lsr::DiffShape diff_shape(int64_t B, int64_t H, int64_t Tq, int64_t Tk, int64_t lam_count,
+                                 int causal, float scale) {
+    lsr::DiffShape p = {};
+    p.rows = B * H * Tq;
+    p.H = H;
+    p.Tq = Tq;
+    p.Tk = Tk;
+    p.qoff = Tk - Tq;
+    p.lam_step = lam_count == 1 ? 0 : 1;
+    p.causal = causal ? 1 : 0;
+    p.scale = scale;
+    return p;
+}
+
+ls_status ls_softmax_fw_diff(void *out, float *stats, const void *x1, const void *x2,
+                             const float *lam, const void *mask, int64_t B, int64_t H, int64_t Tq,
+                             int64_t Tk, int64_t x1_batch, int64_t x1_head, int64_t x2_batch,
+                             int64_t x2_head, int64_t lam_count, int causal, float scale,
+                             ls_dtype dt, void *stream) {
+    const size_t es = elem_size(dt);
+    if (es == 0) return LS_ERR_UNSUPPORTED;
+    ls_status s = diff_check(B, H, Tq, Tk, lam_count, causal, scale);
+    if (s != LS_OK) return s;
+    const int64_t len = Tq * Tk;
+    if (B == 0 || H == 0 || len == 0) return LS_OK;
+    if (!out || !lam) return LS_ERR_INVALID_ARG;
+    if ((s = diff_tensor(x1, B, H, len, x1_batch, x1_head, es)) != LS_OK ||
+        (s = diff_tensor(x2, B, H, len, x2_batch, x2_head, es)) != LS_OK)
+        return s;
+    if (!aligned(out, es) || !aligned(mask, es) || !aligned(lam, 4) || !aligned(stats, 16))
+        return LS_ERR_MISALIGNED;
+    const HeadSpan so = head_span(out, len, H * len, len, es);
+    const HeadSpan i1 = head_span(x1, len, x1_batch, x1_head, es);
+    const HeadSpan i2 = head_span(x2, len, x2_batch, x2_head, es);
+    if ((heads_meet(so, i1, B, H) && !heads_same(so, i1, B, H)) || heads_meet(so, i2, B, H))
+        return LS_ERR_INVALID_ARG;
+    if (outputs_overlap({span_of(out, B * H * len, es), span_of(stats, 4 * B * H * Tq, 4)},
+                        {span_of(lam, lam_count, 4), span_of(mask, B * Tk, es)}))
+        return LS_ERR_INVALID_ARG;
+    const HeadSpan ss = flat_span(stats, 4 * B * H * Tq, 4);
+    if (stats && (heads_meet(ss, i1, B, H) || heads_meet(ss, i2, B, H))) return LS_ERR_INVALID_ARG;
+    const lsr::DiffShape p = diff_shape(B, H, Tq, Tk, lam_count, causal, scale);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    auto launch = [&](auto zero) {
+        using T = decltype(zero);
+        return from_cuda(lsr::launch_diff_fw<T>(
+            static_cast<T *>(out), reinterpret_cast<float4 *>(stats),
+            diff_rows<const T>(const_cast<void *>(x1), B, H, len, x1_batch, x1_head),
+            diff_rows<const T>(const_cast<void *>(x2), B, H, len, x2_batch, x2_head), lam,
+            static_cast<const T *>(mask), p, st));
+    };
+    switch (dt) {
+        case LS_F32: return launch(float());
+        case LS_F16: return launch(__half());
+        case LS_BF16: return launch(__nv_bfloat16());
+    }
+    return LS_ERR_UNSUPPORTED;
+}
+
+size_t ls_softmax_bw_diff_workspace_size(int64_t B, int64_t H, int64_t Tq) {
+    if (B <= 0 || H <= 0 || Tq <= 0 || diff_check(B, H, Tq, 1, H, 0, 1.f) != LS_OK) return 0;
+    return (size_t)(B * H * Tq) * sizeof(float);
+}
+
+ls_status ls_softmax_bw_diff(void *dx1, void *dx2, float *dlam, const void *dout, const void *x1,
+                             const void *x2, const float *lam, const float *stats,
+                             const void *mask, int64_t B, int64_t H, int64_t Tq, int64_t Tk,
+                             int64_t dx1_batch, int64_t dx1_head, int64_t dx2_batch,
+                             int64_t dx2_head, int64_t x1_batch, int64_t x1_head, int64_t x2_batch,
+                             int64_t x2_head, int64_t lam_count, int causal, float scale,
+                             void *workspace, size_t workspace_bytes, ls_dtype dt, void *stream) {
+    const size_t es = elem_size(dt);
+    if (es == 0) return LS_ERR_UNSUPPORTED;
+    ls_status s = diff_check(B, H, Tq, Tk, lam_count, causal, scale);
+    if (s != LS_OK) return s;
+    if (lam_count == 0) return LS_OK;
+    if (!dlam) return LS_ERR_INVALID_ARG;
+    if (!aligned(dlam, 4)) return LS_ERR_MISALIGNED;
+    const int64_t len = Tq * Tk;
+    const lsr::DiffShape p = diff_shape(B, H, Tq, Tk, lam_count, causal, scale);
+    if (p.rows > 0 && Tk > 0) {
+        if (!dout || !lam || !stats) return LS_ERR_INVALID_ARG;
+        if ((s = diff_tensor(dx1, B, H, len, dx1_batch, dx1_head, es)) != LS_OK ||
+            (s = diff_tensor(dx2, B, H, len, dx2_batch, dx2_head, es)) != LS_OK ||
+            (s = diff_tensor(x1, B, H, len, x1_batch, x1_head, es)) != LS_OK ||
+            (s = diff_tensor(x2, B, H, len, x2_batch, x2_head, es)) != LS_OK)
+            return s;
+        if (!heads_apart(B, H, len, dx1_batch, dx1_head) ||
+            !heads_apart(B, H, len, dx2_batch, dx2_head))
+            return LS_ERR_INVALID_ARG;
+        if (!aligned(dout, es) || !aligned(mask, es) || !aligned(lam, 4) || !aligned(stats, 16))
+            return LS_ERR_MISALIGNED;
+        const size_t need = ls_softmax_bw_diff_workspace_size(B, H, Tq);
+        if (!workspace || workspace_bytes < need || !aligned(workspace, 16))
+            return LS_ERR_WORKSPACE;
+        const HeadSpan o1 = head_span(dx1, len, dx1_batch, dx1_head, es);
+        const HeadSpan o2 = head_span(dx2, len, dx2_batch, dx2_head, es);
+        const HeadSpan i1 = head_span(x1, len, x1_batch, x1_head, es);
+        const HeadSpan i2 = head_span(x2, len, x2_batch, x2_head, es);
+        const HeadSpan g = head_span(dout, len, H * len, len, es);
+        const HeadSpan flat[] = {flat_span(stats, 4 * p.rows, 4), flat_span(workspace, p.rows, 4),
+                                 flat_span(mask, B * Tk, es), flat_span(lam, lam_count, 4),
+                                 flat_span(dlam, lam_count, 4)};
+        if (heads_meet(o1, o2, B, H)) return LS_ERR_INVALID_ARG;
+        if (outputs_overlap({span_of(dlam, lam_count, 4), span_of(workspace, p.rows, 4)},
+                            {span_of(dout, p.rows * Tk, es), span_of(stats, 4 * p.rows, 4),
+                             span_of(mask, B * Tk, es), span_of(lam, lam_count, 4)}))
+            return LS_ERR_INVALID_ARG;
+        for (const HeadSpan *o : {&o1, &o2}) {
+            const HeadSpan &own = o == &o1 ? i1 : i2, &other = o == &o1 ? i2 : i1;
+            if ((heads_meet(*o, own, B, H) && !heads_same(*o, own, B, H)) ||
+                heads_meet(*o, other, B, H) || heads_meet(*o, g, B, H))
+                return LS_ERR_INVALID_ARG;
+            for (const HeadSpan &f : flat)
+                if (heads_meet(*o, f, B, H)) return LS_ERR_INVALID_ARG;
+        }
+    }
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    auto launch = [&](auto zero) {
+        using T = decltype(zero);
+        return from_cuda(lsr::launch_diff_bw<T>(
+            diff_rows<T>(dx1, B, H, len, dx1_batch, dx1_head),
+            diff_rows<T>(dx2, B, H, len, dx2_batch, dx2_head), dlam, static_cast<const T *>(dout),
+            diff_rows<const T>(const_cast<void *>(x1), B, H, len, x1_batch, x1_head),
+            diff_rows<const T>(const_cast<void *>(x2), B, H, len, x2_batch, x2_head), lam,
+            reinterpret_cast<const float4 *>(stats), static_cast<const T *>(mask), p,
+            static_cast<float *>(workspace), st));
     };
     switch (dt) {
         case LS_F32: return launch(float());

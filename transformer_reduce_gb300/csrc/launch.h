@@ -140,6 +140,35 @@ cudaError_t launch_grad_clip(float *norm, void *const *out, const void *const *g
                              const int64_t *sizes, const int32_t *dts, int64_t count,
                              float max_norm, float eps, double *part, cudaStream_t st);
 
+// Difference of two attention softmax maps with a learned weight.
+struct DiffShape {
+    int64_t rows;  // B * H * Tq, in the order (b, h, i)
+    int64_t per;   // rows of a block's run
+    int64_t H, Tq, Tk, qoff;
+    int lam_step;  // 1: a weight per head, 0: one for all
+    int causal;
+    float scale;
+};
+// Where a tensor's rows lie: element offset b * batch + h * head + i * Tk.
+template <typename T>
+struct DiffRows {
+    T *p;
+    int64_t batch, head;
+    int64_t extent;  // elements from the first to past the last
+    __device__ __forceinline__ int64_t at(int64_t b, int64_t h, int64_t i, int64_t Tk) const {
+        return b * batch + h * head + i * Tk;
+    }
+};
+template <typename T>
+cudaError_t launch_diff_fw(T *out, float4 *stats, DiffRows<const T> x1, DiffRows<const T> x2,
+                           const float *lam, const T *mask, DiffShape p, cudaStream_t st);
+// row_dot: workspace of a float per row.
+template <typename T>
+cudaError_t launch_diff_bw(DiffRows<T> dx1, DiffRows<T> dx2, float *dlam, const T *dout,
+                           DiffRows<const T> x1, DiffRows<const T> x2, const float *lam,
+                           const float4 *stats, const T *mask, DiffShape p, float *row_dot,
+                           cudaStream_t st);
+
 // Softmax cross entropy from hidden states x [rows, D] and a vocabulary matrix
 // w [V, D] (es: bytes of an element), and its gradients (dw may be NULL).
 size_t linear_ce_workspace(bool backward, int64_t rows, int64_t D, int64_t V, size_t es);
