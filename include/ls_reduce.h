@@ -715,6 +715,91 @@ ls_status ls_softmax_bw_diff(void *dx1, void *dx2, float *dlam, const void *dout
                              int64_t x2_head, int64_t lam_count, int causal, float scale,
                              void *workspace, size_t workspace_bytes, ls_dtype dt, void *stream);
 
+/* Widest row of the norms around a block. */
+#define LS_MAX_BLOCK_HIDDEN ((int64_t)16384)
+
+/*
+ * Norms after and before a block of a Transformer layer, with the block's gate
+ * and the scaled residual stream, forward.  x is the block's output, r the
+ * residual stream it is added to; N is LayerNorm (layer != 0) or RMSNorm:
+ *     n = N(x; gamma_post, beta_post)          or x without gamma_post
+ *     h = residual_scale * r + gate * n        (gate 1 without gate)
+ *     y = N(h; gamma_pre, beta_pre)            only with gamma_pre
+ *   LayerNorm: N(v)_j = (v_j - mean) * rstd * gamma_j + beta_j
+ *   RMSNorm:   N(v)_j = v_j * rstd * gamma_j
+ * rstd = 1 / sqrt(variance (mean square for RMSNorm) + eps).  h enters its norm
+ * in FP32, before it is rounded.
+ *
+ *   h      [rows, hidden] dt, device, written: the new residual stream.
+ *   y      [rows, hidden] dt, device, written: the next block's input; ignored
+ *          without gamma_pre.  h and y may each be x or r itself.
+ *   stats  [4, rows] float32, device, written: mean and rstd of x, mean and
+ *          rstd of h (mean 0 for RMSNorm; 0 and 1 for a norm that is not taken).
+ *   x, r   [rows, hidden] dt, device, read.
+ *   gate   [gates, hidden] dt, device, read, or NULL: rows [k * rows / gates,
+ *          (k + 1) * rows / gates) share gate k, so one gate is a learned vector,
+ *          one per sequence a conditioned one, `rows` of them one per token.
+ *   gamma_post, beta_post, gamma_pre, beta_pre  [hidden] dt, device, read, or
+ *          NULL; a beta wants LayerNorm and its gamma.
+ * Errors: LS_ERR_INVALID_ARG for negative rows, hidden < 1, NULL h / stats / x
+ * / r or (with gamma_pre) y when rows > 0, gates < 1 or no divisor of rows, a
+ * beta without LayerNorm or gamma, eps < 0 or not finite, residual_scale not
+ * finite, overlapping outputs; LS_ERR_UNSUPPORTED for an unknown dtype, hidden
+ * beyond LS_MAX_BLOCK_HIDDEN or more than 2^40 rows; LS_ERR_MISALIGNED as
+ * everywhere.
+ */
+ls_status ls_block_norm_fw(void *h, void *y, float *stats, const void *x, const void *r,
+                           const void *gate, const void *gamma_post, const void *beta_post,
+                           const void *gamma_pre, const void *beta_pre, int64_t rows,
+                           int64_t hidden, int64_t gates, float residual_scale, float eps,
+                           int layer, ls_dtype dt, void *stream);
+
+/*
+ * Bytes of device workspace ls_block_norm_bw needs (gates: 0 without a gate).
+ * 0 without rows and for sizes that it refuses.  Host-only; launches nothing.
+ */
+size_t ls_block_norm_bw_workspace_size(int64_t rows, int64_t hidden, int64_t gates, int layer,
+                                       ls_dtype dt);
+
+/*
+ * Norms around a block, backward.  With up = dh + (input gradient of the second
+ * norm for dy), xhat and hhat the normed rows before gamma:
+ *     dr = residual_scale * up
+ *     dx = input gradient of the first norm for gate * up   (gate * up without it)
+ *     dgate_k     = sum over the gate's rows of up * n
+ *     dgamma_post = sum of gate * up * xhat,   dbeta_post = sum of gate * up
+ *     dgamma_pre  = sum of dy * hhat,          dbeta_pre  = sum of dy
+ * The sums are taken in FP32 in an order that depends only on the sizes and the
+ * dtype: the same call is bitwise reproducible.
+ *
+ *   dx, dr  [rows, hidden] dt, device, written.  dx may be dy, dh, x or h
+ *          itself, dr dy, dh or h.
+ *   dgate  [gates, hidden] float32, device, written; ignored without gate.
+ *   dgamma_post, dgamma_pre  [hidden] float32, device, written; ignored without
+ *          the gamma.  dbeta_post, dbeta_pre  [hidden] float32, device, written,
+ *          or NULL; want LayerNorm and the gamma.  All sums are zeros when rows
+ *          == 0.
+ *   dy     [rows, hidden] dt, device, read with gamma_pre: gradient of y.
+ *   dh     [rows, hidden] dt, device, read: gradient of h from its other uses;
+ *          NULL (with gamma_pre): none.
+ *   x      as given to the forward; read with gamma_post or gate.
+ *   h, stats  as written by the forward (h read with gamma_pre).
+ *   gate, gamma_post, beta_post, gamma_pre  as given to the forward.
+ *   workspace  device scratch of at least ls_block_norm_bw_workspace_size(...)
+ *          bytes, 16-byte aligned, contents ignored; may be NULL when that is 0.
+ *          Calls that overlap on the GPU must not share it.
+ * Errors as for the forward (dy and h missing with gamma_pre, dh missing
+ * without it, x missing with gamma_post or gate, a missing gradient of a given
+ * parameter), plus LS_ERR_WORKSPACE.
+ */
+ls_status ls_block_norm_bw(void *dx, void *dr, float *dgate, float *dgamma_post, float *dbeta_post,
+                           float *dgamma_pre, float *dbeta_pre, const void *dy, const void *dh,
+                           const void *x, const void *h, const float *stats, const void *gate,
+                           const void *gamma_post, const void *beta_post, const void *gamma_pre,
+                           int64_t rows, int64_t hidden, int64_t gates, float residual_scale,
+                           int layer, void *workspace, size_t workspace_bytes, ls_dtype dt,
+                           void *stream);
+
 /* Limits of the cross entropy from hidden states. */
 #define LS_MAX_LINEAR_ROWS ((int64_t)1 << 26)
 #define LS_MAX_LINEAR_HIDDEN ((int64_t)1 << 16)

@@ -28,7 +28,8 @@ from ._lib import (ls_grad_clip, ls_grad_norm, ls_grad_norm_workspace_size, ls_q
                    ls_softmax_bw_relpos_workspace_size, ls_softmax_fw_relpos)
 from ._lib import (ls_linear_cross_entropy_bw, ls_linear_cross_entropy_bw_workspace_size,
                    ls_linear_cross_entropy_fw, ls_linear_cross_entropy_fw_workspace_size,
-                   ls_softmax_bw_diff, ls_softmax_bw_diff_workspace_size, ls_softmax_fw_diff)
+                   ls_softmax_bw_diff, ls_softmax_bw_diff_workspace_size, ls_softmax_fw_diff,
+                   ls_block_norm_bw, ls_block_norm_bw_workspace_size, ls_block_norm_fw)
 
 __all__ = [
     "softmax_fw", "softmax_bw", "softmax_bw_masked", "layernorm_fw", "layernorm_bw_dinp",
@@ -47,6 +48,8 @@ __all__ = [
     "ls_grad_norm", "ls_grad_clip", "ls_grad_norm_workspace_size",
     "softmax_fw_diff", "softmax_bw_diff", "softmax_diff_workspace",
     "ls_softmax_fw_diff", "ls_softmax_bw_diff", "ls_softmax_bw_diff_workspace_size",
+    "block_norm_fw", "block_norm_bw", "block_norm_workspace",
+    "ls_block_norm_fw", "ls_block_norm_bw", "ls_block_norm_bw_workspace_size",
     "linear_cross_entropy_fw", "linear_cross_entropy_bw", "linear_cross_entropy_workspace",
     "ls_linear_cross_entropy_fw", "ls_linear_cross_entropy_bw",
     "ls_linear_cross_entropy_fw_workspace_size", "ls_linear_cross_entropy_bw_workspace_size",
@@ -950,6 +953,133 @@ def softmax_bw_diff(dout, scores1, scores2, lam, stats, mask=None, causal: bool 
             1 if causal else 0, 1.0 if scale is None else float(scale), workspace.data_ptr(),
             4 * n, ls_dtype(dout))
     return dscores1, dscores2, dlam
+
+
+# ----------------------------------------------------------------------------
+# norms around a block
+# ----------------------------------------------------------------------------
+_NORM_KINDS = {"rms": 0, "layer": 1}
+
+
+def _block(x, kind, gate, **vectors):
+    """(rows, hidden, gates, layer) of the norms around a block."""
+    rows, hidden = _rows_hidden(x)
+    layer = _NORM_KINDS.get(kind)
+    if layer is None:
+        raise ValueError(f"kind must be 'rms' or 'layer', got {kind!r}")
+    want = (hidden,)
+    for name, t in vectors.items():
+        if t is None:
+            continue
+        if t.shape != want or t.dtype != x.dtype:
+            _want(name, t, want, x.dtype)
+        if name[:4] == "beta" and (not layer or vectors.get("gamma" + name[4:]) is None):
+            raise ValueError(f"{name} wants kind='layer' and gamma{name[4:]}")
+    gates = 0
+    if gate is not None:
+        if gate.dim() != 2 or gate.shape[0] < 1 or rows % gate.shape[0]:
+            raise ValueError(f"gate must be [gates, {hidden}] with gates a divisor of {rows} rows")
+        gates = gate.shape[0]
+        if gate.shape[1] != hidden or gate.dtype != x.dtype:
+            _want("gate", gate, (gates, hidden), x.dtype)
+    return rows, hidden, gates, layer
+
+
+def block_norm_fw(x, residual, gamma_pre=None, beta_pre=None, gamma_post=None, beta_post=None,
+                  gate=None, residual_scale: float = 1.0, kind: str = "rms", eps: float = 1e-6,
+                  h=None, y=None, stats=None):
+    """The norms after and before a block with its gate and residual scale, for a
+    block's output x and the residual stream (both [rows, hidden]):
+        h = residual_scale * residual + gate * N(x; gamma_post, beta_post)
+        y = N(h; gamma_pre, beta_pre)
+    with N RMSNorm (``kind`` "rms") or LayerNorm ("layer").  Without gamma_post
+    x enters as it is, without gamma_pre there is no y.  ``gate`` is [gates,
+    hidden]: equal runs of rows share one each.  Returns (h, y, stats), stats
+    fp32 [4, rows] saved for the backward.  ``h`` and ``y`` may be x or the
+    residual stream (in place)."""
+    f32 = _torch().float32
+    rows, hidden, gates, layer = _block(x, kind, gate, gamma_pre=gamma_pre, beta_pre=beta_pre,
+                                        gamma_post=gamma_post, beta_post=beta_post)
+    shape, dtype = x.shape, x.dtype
+    if residual.shape != shape or residual.dtype != dtype:
+        _want("residual", residual, shape, dtype)
+    if h is None:
+        h = x.new_empty(shape)
+    else:
+        _want("h", h, shape, dtype)
+    if gamma_pre is None:
+        if y is not None:
+            raise ValueError("y is not computed without gamma_pre")
+    elif y is None:
+        y = x.new_empty(shape)
+    else:
+        _want("y", y, shape, dtype)
+    if stats is None:
+        stats = x.new_empty((4, rows), dtype=f32)
+    else:
+        _want("stats", stats, (4, rows), f32)
+    dev = _same_device(x, residual, gamma_pre, beta_pre, gamma_post, beta_post, gate, h, y, stats)
+    _launch("ls_block_norm_fw", dev, h.data_ptr(), _ptr(y), stats.data_ptr(), x.data_ptr(),
+            residual.data_ptr(), _ptr(gate), _ptr(gamma_post), _ptr(beta_post), _ptr(gamma_pre),
+            _ptr(beta_pre), rows, hidden, gates, float(residual_scale), float(eps), layer,
+            ls_dtype(x))
+    return h, y, stats
+
+
+def block_norm_workspace(rows: int, hidden: int, gates: int, kind: str, dtype, device):
+    """A workspace tensor of the size ls_block_norm_bw needs (``gates`` 0 without
+    a gate)."""
+    torch = _torch()
+    n = ls_block_norm_bw_workspace_size(rows, hidden, gates, _NORM_KINDS[kind],
+                                        ls_dtype(torch.empty(0, dtype=dtype)))
+    return torch.empty(max(n, 16) // 4, device=device, dtype=torch.float32)
+
+
+def block_norm_bw(dy, dh, x, h, stats, gamma_pre=None, gamma_post=None, beta_post=None, gate=None,
+                  residual_scale: float = 1.0, kind: str = "rms", workspace=None, dx=None, dr=None):
+    """Gradients of ``block_norm_fw`` from those of y (``dy``) and of h's other
+    uses (``dh``, None: there are none), the forward's x and its h and stats:
+    (dx, dresidual, dgamma_pre, dbeta_pre, dgamma_post, dbeta_post, dgate), those
+    of the parameters fp32 in a fixed summation order and None where there is no
+    such parameter (the betas' are given for "layer").  ``dx`` may be dy, dh, x
+    or h, ``dr`` dy, dh or h (in place)."""
+    f32 = _torch().float32
+    rows, hidden, gates, layer = _block(x, kind, gate, gamma_pre=gamma_pre, gamma_post=gamma_post,
+                                        beta_post=beta_post)
+    shape, dtype = x.shape, x.dtype
+    if gamma_pre is None:
+        if dy is not None:
+            raise ValueError("there is no y, and no dy, without gamma_pre")
+        if dh is None:
+            raise ValueError("dh is needed without gamma_pre")
+    elif dy is None or h is None:
+        raise ValueError("dy and h are needed with gamma_pre")
+    for name, t in (("dy", dy), ("dh", dh), ("h", h), ("dx", dx), ("dr", dr)):
+        if t is not None and (t.shape != shape or t.dtype != dtype):
+            _want(name, t, shape, dtype)
+    if stats.shape != (4, rows) or stats.dtype != f32:
+        _want("stats", stats, (4, rows), f32)
+    code = ls_dtype(x)
+    if workspace is None:
+        n = max(ls_block_norm_bw_workspace_size(rows, hidden, gates, layer, code), 16) // 4
+        workspace = x.new_empty(n, dtype=f32)
+    else:
+        _workspace("workspace", workspace)
+        n = workspace.numel()
+    dx = x.new_empty(shape) if dx is None else dx
+    dr = x.new_empty(shape) if dr is None else dr
+    dgp = x.new_empty(hidden, dtype=f32) if gamma_post is not None else None
+    dbp = x.new_empty(hidden, dtype=f32) if gamma_post is not None and layer else None
+    dg = x.new_empty(hidden, dtype=f32) if gamma_pre is not None else None
+    db = x.new_empty(hidden, dtype=f32) if gamma_pre is not None and layer else None
+    dgate = x.new_empty((gates, hidden), dtype=f32) if gates else None
+    dev = _same_device(dy, dh, x, h, stats, gamma_pre, gamma_post, beta_post, gate, workspace, dx,
+                       dr)
+    _launch("ls_block_norm_bw", dev, dx.data_ptr(), dr.data_ptr(), _ptr(dgate), _ptr(dgp),
+            _ptr(dbp), _ptr(dg), _ptr(db), _ptr(dy), _ptr(dh), x.data_ptr(), _ptr(h),
+            stats.data_ptr(), _ptr(gate), _ptr(gamma_post), _ptr(beta_post), _ptr(gamma_pre), rows,
+            hidden, gates, float(residual_scale), layer, workspace.data_ptr(), 4 * n, code)
+    return dx, dr, dg, db, dgp, dbp, dgate
 
 
 # ----------------------------------------------------------------------------

@@ -61,6 +61,9 @@ SIGNATURES = {
     "ls_softmax_fw_diff": ([_VP] * 6 + [_I64] * 9 + [_INT, _F32, _INT, _VP], _INT),
     "ls_softmax_bw_diff_workspace_size": ([_I64] * 3, _SZ),
     "ls_softmax_bw_diff": ([_VP] * 9 + [_I64] * 13 + [_INT, _F32, _VP, _SZ, _INT, _VP], _INT),
+    "ls_block_norm_fw": ([_VP] * 10 + [_I64] * 3 + [_F32, _F32, _INT, _INT, _VP], _INT),
+    "ls_block_norm_bw_workspace_size": ([_I64] * 3 + [_INT, _INT], _SZ),
+    "ls_block_norm_bw": ([_VP] * 16 + [_I64] * 3 + [_F32, _INT, _VP, _SZ, _INT, _VP], _INT),
     "ls_status_string": ([_INT], ctypes.c_char_p),
 }
 
@@ -279,3 +282,23 @@ def ls_softmax_bw_diff(dx1, dx2, dlam, dout, x1, x2, lam, stats, mask, B, H, Tq,
                                      dx1_batch, dx1_head, dx2_batch, dx2_head, x1_batch, x1_head,
                                      x2_batch, x2_head, lam_count, int(bool(causal)), scale,
                                      workspace, workspace_bytes, dt, stream)
+
+
+def ls_block_norm_fw(h, y, stats, x, r, gate, gamma_post, beta_post, gamma_pre, beta_pre, rows,
+                     hidden, gates, residual_scale, eps, layer, dt, stream=0) -> int:
+    return load().ls_block_norm_fw(h, y, stats, x, r, gate, gamma_post, beta_post, gamma_pre,
+                                   beta_pre, rows, hidden, gates, residual_scale, eps,
+                                   int(bool(layer)), dt, stream)
+
+
+def ls_block_norm_bw_workspace_size(rows, hidden, gates, layer, dt) -> int:
+    return load().ls_block_norm_bw_workspace_size(rows, hidden, gates, int(bool(layer)), dt)
+
+
+def ls_block_norm_bw(dx, dr, dgate, dgamma_post, dbeta_post, dgamma_pre, dbeta_pre, dy, dh, x, h,
+                     stats, gate, gamma_post, beta_post, gamma_pre, rows, hidden, gates,
+                     residual_scale, layer, workspace, workspace_bytes, dt, stream=0) -> int:
+    return load().ls_block_norm_bw(dx, dr, dgate, dgamma_post, dbeta_post, dgamma_pre, dbeta_pre,
+                                   dy, dh, x, h, stats, gate, gamma_post, beta_post, gamma_pre,
+                                   rows, hidden, gates, residual_scale, int(bool(layer)),
+                                   workspace, workspace_bytes, dt, stream)

@@ -27,7 +27,9 @@ LIB_PATH = os.path.join(PKG, LIB_NAME)
 SOURCES = ["abi.cu", "kernels_f32.cu", "kernels_f16.cu", "kernels_bf16.cu", "noalloc.cu",
            "cross_entropy.cu", "linear_ce.cu",
            "diff_fw_f32.cu", "diff_fw_f16.cu", "diff_fw_bf16.cu", "diff_bw_f32.cu", "diff_bw_f16.cu",
-           "diff_bw_bf16.cu", "relpos_fw_f32.cu", "relpos_fw_f16.cu",
+           "diff_bw_bf16.cu", "block_norm_fw_f32.cu", "block_norm_fw_f16.cu",
+           "block_norm_fw_bf16.cu", "block_norm_bw_f32.cu", "block_norm_bw_f16.cu",
+           "block_norm_bw_bf16.cu", "relpos_fw_f32.cu", "relpos_fw_f16.cu",
            "relpos_fw_bf16.cu", "relpos_bw_f32.cu", "relpos_bw_f16.cu", "relpos_bw_bf16.cu",
            "qk_norm_rope_f32.cu", "qk_norm_rope_f16.cu", "qk_norm_rope_bf16.cu", "grad_clip.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

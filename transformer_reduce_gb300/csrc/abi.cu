@@ -1327,4 +1327,185 @@ ls_status ls_softmax_bw_diff(void *dx1, void *dx2, float *dlam, const void *dout
     return LS_ERR_UNSUPPORTED;
 }
 
+// ----------------------------------------------------------------------------
+// norms around a block
+// ----------------------------------------------------------------------------
+static ls_status block_norm_check(int64_t rows, int64_t hidden, int64_t gates, bool has_gate,
+                                  float residual_scale) {
+    if (rows < 0 || hidden < 1 || !std::isfinite(residual_scale)) return LS_ERR_INVALID_ARG;
+    if (has_gate && (gates < 1 || rows % gates != 0)) return LS_ERR_INVALID_ARG;
+    if (hidden > LS_MAX_BLOCK_HIDDEN || rows > ((int64_t)1 << 40)) return LS_ERR_UNSUPPORTED;
+    return LS_OK;
+}
+
+ls_status ls_block_norm_fw(void *h, void *y, float *stats, const void *x, const void *r,
+                           const void *gate, const void *gamma_post, const void *beta_post,
+                           const void *gamma_pre, const void *beta_pre, int64_t rows,
+                           int64_t hidden, int64_t gates, float residual_scale, float eps,
+                           int layer, ls_dtype dt, void *stream) {
+    const size_t es = elem_size(dt);
+    if (es == 0) return LS_ERR_UNSUPPORTED;
+    const ls_status s = block_norm_check(rows, hidden, gates, gate != nullptr, residual_scale);
+    if (s != LS_OK) return s;
+    if (!(eps >= 0.f) || !std::isfinite(eps)) return LS_ERR_INVALID_ARG;
+    if ((beta_post && (!layer || !gamma_post)) || (beta_pre && (!layer || !gamma_pre)))
+        return LS_ERR_INVALID_ARG;
+    if (rows == 0) return LS_OK;
+    if (!h || !stats || !x || !r || (gamma_pre && !y)) return LS_ERR_INVALID_ARG;
+    for (const void *p : {(const void *)h, (const void *)y, x, r, gate, gamma_post, beta_post,
+                          gamma_pre, beta_pre})
+        if (!aligned(p, es)) return LS_ERR_MISALIGNED;
+    if (!aligned(stats, 4)) return LS_ERR_MISALIGNED;
+    const int64_t n = rows * hidden;
+    if (!gamma_pre) y = nullptr;  // not written
+    // h and y may be x or r itself; nothing else may meet them
+    const Span small[] = {span_of(gate, gate ? gates * hidden : 0, es),
+                          span_of(gamma_post, hidden, es), span_of(beta_post, hidden, es),
+                          span_of(gamma_pre, hidden, es), span_of(beta_pre, hidden, es)};
+    const Span outs[] = {span_of(h, n, es), span_of(y, n, es), span_of(stats, 4 * rows, 4)};
+    const Span rows_in[] = {span_of(x, n, es), span_of(r, n, es)};
+    for (int i = 0; i < 3; ++i) {
+        for (int j = i + 1; j < 3; ++j)
+            if (spans_meet(outs[i], outs[j])) return LS_ERR_INVALID_ARG;
+        for (const Span &q : small)
+            if (spans_meet(outs[i], q)) return LS_ERR_INVALID_ARG;
+        for (const Span &q : rows_in)
+            if (spans_meet(outs[i], q) && (i == 2 || outs[i].at != q.at)) return LS_ERR_INVALID_ARG;
+    }
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    auto launch = [&](auto zero) {
+        using T = decltype(zero);
+        lsr::BlockNorm<T> a = {};
+        a.rows = rows;
+        a.hidden = hidden;
+        a.gate_rows = gate ? rows / gates : rows;
+        a.residual_scale = residual_scale;
+        a.eps = eps;
+        a.layer = layer ? 1 : 0;
+        a.x = static_cast<const T *>(x);
+        a.r = static_cast<const T *>(r);
+        a.gate = static_cast<const T *>(gate);
+        a.gamma_post = static_cast<const T *>(gamma_post);
+        a.beta_post = static_cast<const T *>(beta_post);
+        a.gamma_pre = static_cast<const T *>(gamma_pre);
+        a.beta_pre = static_cast<const T *>(beta_pre);
+        a.stats = stats;
+        a.h = static_cast<T *>(h);
+        a.y = static_cast<T *>(y);
+        return from_cuda(lsr::launch_block_norm_fw<T>(a, st));
+    };
+    switch (dt) {
+        case LS_F32: return launch(float());
+        case LS_F16: return launch(__half());
+        case LS_BF16: return launch(__nv_bfloat16());
+    }
+    return LS_ERR_UNSUPPORTED;
+}
+
+size_t ls_block_norm_bw_workspace_size(int64_t rows, int64_t hidden, int64_t gates, int layer,
+                                       ls_dtype dt) {
+    if (rows <= 0 || gates < 0 || block_norm_check(rows, hidden, gates, gates > 0, 1.f) != LS_OK)
+        return 0;
+    switch (dt) {
+        case LS_F32: return lsr::block_norm_workspace<float>(rows, hidden, gates, layer != 0);
+        case LS_F16: return lsr::block_norm_workspace<__half>(rows, hidden, gates, layer != 0);
+        case LS_BF16:
+            return lsr::block_norm_workspace<__nv_bfloat16>(rows, hidden, gates, layer != 0);
+    }
+    return 0;
+}
+
+ls_status ls_block_norm_bw(void *dx, void *dr, float *dgate, float *dgamma_post, float *dbeta_post,
+                           float *dgamma_pre, float *dbeta_pre, const void *dy, const void *dh,
+                           const void *x, const void *h, const float *stats, const void *gate,
+                           const void *gamma_post, const void *beta_post, const void *gamma_pre,
+                           int64_t rows, int64_t hidden, int64_t gates, float residual_scale,
+                           int layer, void *workspace, size_t workspace_bytes, ls_dtype dt,
+                           void *stream) {
+    const size_t es = elem_size(dt);
+    if (es == 0) return LS_ERR_UNSUPPORTED;
+    const ls_status s = block_norm_check(rows, hidden, gates, gate != nullptr, residual_scale);
+    if (s != LS_OK) return s;
+    if (!gate) gates = 0;
+    const bool post = gamma_post != nullptr, pre = gamma_pre != nullptr;
+    if ((beta_post && (!layer || !post)) || (dbeta_post && (!layer || !post)) ||
+        (dbeta_pre && (!layer || !pre)))
+        return LS_ERR_INVALID_ARG;
+    if ((post && !dgamma_post) || (pre && !dgamma_pre) || (gate && !dgate))
+        return LS_ERR_INVALID_ARG;
+    if (!post) dgamma_post = nullptr;
+    if (!pre) dgamma_pre = nullptr;
+    if (!gate) dgate = nullptr;
+    if (rows > 0 && (!dx || !dr || !stats || (pre && (!dy || !h)) || (!pre && !dh) ||
+                     ((post || gate) && !x)))
+        return LS_ERR_INVALID_ARG;
+    if (!pre) dy = h = nullptr;  // not read
+    if (!post && !gate) x = nullptr;
+    for (const void *p : {(const void *)dx, (const void *)dr, dy, dh, x, h, gate, gamma_post,
+                          beta_post, gamma_pre})
+        if (!aligned(p, es)) return LS_ERR_MISALIGNED;
+    for (const float *p : {(const float *)dgate, (const float *)dgamma_post,
+                           (const float *)dbeta_post, (const float *)dgamma_pre,
+                           (const float *)dbeta_pre, stats})
+        if (!aligned(p, 4)) return LS_ERR_MISALIGNED;
+    const size_t need = ls_block_norm_bw_workspace_size(rows, hidden, gates, layer, dt);
+    if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 16)))
+        return LS_ERR_WORKSPACE;
+    const int64_t n = rows * hidden;
+    // dx may be dy, dh, x or h itself and dr dy, dh or h; nothing else may meet
+    // them or the sums
+    const Span outs[] = {span_of(dx, n, es), span_of(dr, n, es),
+                         span_of(dgate, gates * hidden, 4), span_of(dgamma_post, hidden, 4),
+                         span_of(dbeta_post, hidden, 4), span_of(dgamma_pre, hidden, 4),
+                         span_of(dbeta_pre, hidden, 4), span_of(workspace, need, 1)};
+    const Span small[] = {span_of(gate, gates * hidden, es), span_of(gamma_post, hidden, es),
+                          span_of(beta_post, hidden, es), span_of(gamma_pre, hidden, es),
+                          span_of(stats, 4 * rows, 4)};
+    const Span rows_in[] = {span_of(x, n, es), span_of(dy, n, es), span_of(dh, n, es),
+                            span_of(h, n, es)};
+    for (int i = 0; i < 8; ++i) {
+        for (int j = i + 1; j < 8; ++j)
+            if (spans_meet(outs[i], outs[j])) return LS_ERR_INVALID_ARG;
+        for (const Span &q : small)
+            if (spans_meet(outs[i], q)) return LS_ERR_INVALID_ARG;
+        for (int j = 0; j < 4; ++j)
+            if (spans_meet(outs[i], rows_in[j]) &&
+                (i > 1 || (i == 1 && j == 0) || outs[i].at != rows_in[j].at))
+                return LS_ERR_INVALID_ARG;
+    }
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    auto launch = [&](auto zero) {
+        using T = decltype(zero);
+        lsr::BlockNorm<T> a = {};
+        a.rows = rows;
+        a.hidden = hidden;
+        a.gate_rows = gate ? rows / gates : rows;
+        a.residual_scale = residual_scale;
+        a.layer = layer ? 1 : 0;
+        a.x = static_cast<const T *>(x);
+        a.gate = static_cast<const T *>(gate);
+        a.gamma_post = static_cast<const T *>(gamma_post);
+        a.beta_post = static_cast<const T *>(beta_post);
+        a.gamma_pre = static_cast<const T *>(gamma_pre);
+        a.dy = static_cast<const T *>(dy);
+        a.dh = static_cast<const T *>(dh);
+        a.h_in = static_cast<const T *>(h);
+        a.stats_in = stats;
+        a.dx = static_cast<T *>(dx);
+        a.dr = static_cast<T *>(dr);
+        a.dgate = dgate;
+        a.dgamma_post = dgamma_post;
+        a.dbeta_post = dbeta_post;
+        a.dgamma_pre = dgamma_pre;
+        a.dbeta_pre = dbeta_pre;
+        return from_cuda(lsr::launch_block_norm_bw<T>(a, static_cast<float *>(workspace), st));
+    };
+    switch (dt) {
+        case LS_F32: return launch(float());
+        case LS_F16: return launch(__half());
+        case LS_BF16: return launch(__nv_bfloat16());
+    }
+    return LS_ERR_UNSUPPORTED;
+}
+
 }  // extern "C"

@@ -169,6 +169,30 @@ cudaError_t launch_diff_bw(DiffRows<T> dx1, DiffRows<T> dx2, float *dlam, const 
                            const float4 *stats, const T *mask, DiffShape p, float *row_dot,
                            cudaStream_t st);
 
+// Norms after and before a block with its gate and residual scale.
+template <typename T>
+struct BlockNorm {
+    int64_t rows, hidden, gate_rows;  // gate_rows: rows that share a gate
+    float residual_scale, eps;
+    int layer;  // LayerNorm, else RMSNorm
+    const T *x, *r, *gate, *gamma_post, *beta_post, *gamma_pre, *beta_pre;
+    float *stats;  // [4][rows]: mean and rstd after, mean and rstd before the next block
+    T *h, *y;      // forward
+    // backward
+    const T *dy, *dh, *h_in;
+    const float *stats_in;
+    T *dx, *dr;
+    float *dgate, *dgamma_post, *dbeta_post, *dgamma_pre, *dbeta_pre;
+};
+constexpr int kBlockNormMaxHidden = 16384;
+template <typename T>
+cudaError_t launch_block_norm_fw(const BlockNorm<T> &a, cudaStream_t st);
+template <typename T>
+cudaError_t launch_block_norm_bw(const BlockNorm<T> &a, float *part, cudaStream_t st);
+// Bytes of the backward's workspace (gates: 0 without a gate).
+template <typename T>
+size_t block_norm_workspace(int64_t rows, int64_t hidden, int64_t gates, bool layer);
+
 // Softmax cross entropy from hidden states x [rows, D] and a vocabulary matrix
 // w [V, D] (es: bytes of an element), and its gradients (dw may be NULL).
 size_t linear_ce_workspace(bool backward, int64_t rows, int64_t D, int64_t V, size_t es);
