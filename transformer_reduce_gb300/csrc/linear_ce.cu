@@ -13,10 +13,13 @@ namespace lsr {
 // 4096 entries that is a tenth of its products' time).
 constexpr int64_t kLceQBytes = (int64_t)512 << 20;
 constexpr int64_t kLceMinPiece = 4096;
+// Fewest steps of K of a cut of dx, and most cuts.
+constexpr int64_t kLceMinCut = 16;
+constexpr int64_t kLceMaxCuts = 32;
 
 // Where everything lies in the workspace.
 struct LceLayout {
-    int64_t row_cap, chunks, pitch, w_pitch, vc, pieces, q_pitch;
+    int64_t row_cap, chunks, pitch, w_pitch, vc, pieces, q_pitch, splits, split_k;
     int planes;
     bool pack_w;
     size_t chunk_count, chunk_up, single, row_of, row_target, row_lse2, row_up, row_hit, x, w, part,
@@ -44,6 +47,17 @@ static LceLayout lce_layout(bool backward, int64_t rows, int64_t D, int64_t V, s
             l.pieces = ceil_div(V, l.vc);
         }
         l.q_pitch = round_up(l.vc, kLceN);
+        // dx is cut along the vocabulary where its few tiles would be longer than
+        // half of a pair's share of the gradients' work
+        const int64_t nt = ceil_div(D, kLceN), mt = l.row_cap / kLceM;
+        const int64_t nk = ceil_div(l.vc, kLceK), dw = ceil_div(l.vc, kLceM) * nt;
+        const int64_t work = mt * nt * nk + dw * (l.row_cap / kLceK);
+        int64_t k = work / kLceSms;
+        if (k < kLceMinCut) k = kLceMinCut;
+        if (k < ceil_div(nk, kLceMaxCuts)) k = ceil_div(nk, kLceMaxCuts);
+        l.splits = k < nk ? ceil_div(nk, k) : 1;
+        l.split_k = ceil_div(nk, l.splits);
+        l.splits = ceil_div(nk, l.split_k);
     }
     size_t at = 0;
     auto take = [&](int64_t bytes) {
@@ -62,10 +76,10 @@ static LceLayout lce_layout(bool backward, int64_t rows, int64_t D, int64_t V, s
         l.row_lse2 = take(l.row_cap * 4);
         l.row_up = take(l.row_cap * 4);
         l.q = take(l.planes * l.row_cap * l.q_pitch * 2);
-        if (l.pieces > 1) l.dx_sum = take(l.row_cap * D * 4);
+        if (l.pieces > 1 || l.splits > 1) l.dx_sum = take(l.splits * l.row_cap * D * 4);
     } else {
         l.row_hit = take(l.row_cap * 4);
-        l.part = take(ceil_div(V, kLceN) * l.row_cap * 8);
+        l.part = take(2 * ceil_div(V, kLceN) * l.row_cap * 8);
     }
     l.total = at;
     return l;
@@ -111,12 +125,12 @@ cudaError_t lce_launch(const CUtensorMap &a0, const CUtensorMap &b0, const CUten
     ensure_dynamic_smem<K>(kLceSmem);
     const int64_t mt = ceil_div(g.rows, kLceM), nt = ceil_div(g.D, kLceN);
     const int64_t tiles = EPI == kLceGrads
-                              ? (mt + (g.with_dw ? ceil_div(g.vc, kLceM) : 0)) * nt
+                              ? (mt * g.splits + (g.with_dw ? ceil_div(g.vc, kLceM) : 0)) * nt
                               : mt * ceil_div(g.vc, kLceN);
     if (tiles == 0) return cudaSuccess;
-    const int64_t sms = device_sm_count();
-    return launch_pdl(K, dim3((unsigned)(tiles < sms ? tiles : sms)), dim3(kLceThreads), kLceSmem,
-                      st, a0, b0, a1, b1, g);
+    const int64_t pairs = device_sm_count() / 2;
+    return launch_pdl(K, dim3((unsigned)(2 * (tiles < pairs ? tiles : pairs))), dim3(kLceThreads),
+                      kLceSmem, st, a0, b0, a1, b1, g);
 }
 
 // Packs the rows that count and, where needed, W; fills what both directions
@@ -205,7 +219,7 @@ cudaError_t launch_linear_ce_fw(float *loss, float *lse, const T *x, const T *w,
     if (e != cudaSuccess) return e;
     const int64_t blocks = ceil_div(rows, 32), most = (int64_t)device_sm_count() * 8;
     return launch_pdl(lce_join, dim3((unsigned)(blocks < most ? blocks : most)), dim3(256), 0, st,
-                      loss, lse, g, ceil_div(V, kLceN));
+                      loss, lse, g, 2 * ceil_div(V, kLceN));
 }
 
 template <typename T>
@@ -224,6 +238,8 @@ cudaError_t launch_linear_ce_bw(T *dx, T *dw, const T *x, const T *w, const int3
     g.dx = dx;
     g.dw = dw;
     g.with_dw = dw != nullptr;
+    g.splits = l.splits;
+    g.split_k = l.split_k;
     CUtensorMap mx, mw, mq;
     e = lce_map(&mx, ws + l.x, g.bf16, l.pitch, l.row_cap, l.planes, l.pitch, l.row_cap * l.pitch);
     if (e == cudaSuccess)
@@ -238,9 +254,14 @@ cudaError_t launch_linear_ce_bw(T *dx, T *dw, const T *x, const T *w, const int3
         e = lce_map(&mw, static_cast<const uint8_t *>(wp) + g.v0 * l.w_pitch * 2, g.bf16, l.w_pitch,
                     V - g.v0, l.planes, l.w_pitch, V * l.w_pitch);
         if (e == cudaSuccess) e = lce_launch<kLceQ, T>(mx, mw, mx, mw, g, st);
+        const int64_t nk = ceil_div(g.vc, kLceK);  // (the last piece may be shorter)
+        g.split_k = ceil_div(nk, l.splits);
         if (e == cudaSuccess) e = lce_launch<kLceGrads, T>(mq, mw, mq, mx, g, st);
     }
-    return e;
+    if (e != cudaSuccess || l.splits == 1 || rows == 0) return e;
+    const int64_t blocks = ceil_div(rows * D, 256), most = (int64_t)device_sm_count() * 8;
+    return launch_pdl(lce_join_dx<T>, dim3((unsigned)(blocks < most ? blocks : most)), dim3(256), 0,
+                      st, g);
 }
 
 #define LSR_LCE_INSTANTIATE(T)                                                                  \

@@ -12,12 +12,17 @@
 //  * The rows that count (target >= 0) are first gathered into a dense copy of x
 //    in their order, so that ignored rows cost nothing and what they hold, NaN
 //    or not, touches nothing.
-//  * One persistent kernel makes every product: one warp loads tiles of 128 (M)
-//    and 256 (N) rows of 64 elements with TMA, one thread issues tcgen05.mma on
-//    them, four warps read the FP32 accumulators from tensor memory, which holds
-//    two tiles so that the next product runs meanwhile.
-//  * Forward: the four warps reduce a tile of logits to each row's largest
-//    logit and sum of exponentials; a second kernel joins a row's tiles in order.
+//  * One persistent kernel makes every product, in pairs of blocks on tiles of
+//    256 by 256: in either block one warp loads 128 rows of A and of B, 64
+//    elements wide, with TMA, one thread of the pair issues tcgen05.mma on both
+//    blocks' operands, and eight warps read the block's 128 rows of FP32
+//    accumulators from tensor memory, which holds two tiles so that the next
+//    product runs meanwhile.  (A block alone on 128 by 256 reads all of B itself:
+//    shared memory then takes as long as the tensor cores, and [8192,1024] bf16
+//    by 50257 took 595 us forward.)
+//  * Forward: the eight warps reduce a tile of logits to each row's largest
+//    logit and sum of exponentials, per 128 columns; a second kernel joins a
+//    row's parts in order.
 //  * Backward, by pieces of the vocabulary: the logits of a piece become q,
 //    rounded to the operands' 16-bit type, in the workspace; q W is added to dx
 //    in FP32 over the pieces, q^T x is the piece's rows of dW.
@@ -37,12 +42,14 @@
 
 namespace lsr {
 
-constexpr int kLceM = 128, kLceN = 256, kLceK = 64;  // tile, and elements of a step along K
-constexpr int kLceStages = 4;
+constexpr int kLceM = 256, kLceN = 256, kLceK = 64;  // tile, and elements of a step along K
+constexpr int kLceHalf = 128;  // rows of A, rows of B and rows of the accumulator in a block
+constexpr int kLceStages = 6;
 constexpr int kLceBox = 64 * kLceK * 2;  // bytes of one 64 x 64 TMA box
-constexpr int kLceStage = (kLceM + kLceN) / 64 * kLceBox;
-constexpr int kLceThreads = 192;  // loader, issuer, four warps on the accumulators
+constexpr int kLceStage = 2 * kLceHalf / 64 * kLceBox;
+constexpr int kLceThreads = 320;  // loader, issuer, eight warps on the accumulators
 constexpr size_t kLceSmem = (size_t)kLceStages * kLceStage + 1024;
+constexpr int kLceSms = 152;  // what the cuts are made for
 // fp32: steps of kLceK whose products are summed before they join the tile's sum
 // ([1001,333] by [10007,333], largest error of dx over the largest dx: 1.9e-5
 // without the cut).
@@ -60,6 +67,7 @@ struct LceArgs {
     int bf16;               // operand type of the products
     int first, last;        // of the pieces
     int with_dw;
+    int64_t splits, split_k;  // cuts of the sum over a piece in dx, and steps of K of each
     // in the workspace
     const int *count;       // rows that count
     const int *row_of;      // [row_cap] their index
@@ -68,9 +76,9 @@ struct LceArgs {
     const float *row_up;    // [row_cap] dloss times the scale of q
     const float *unscale;   // 1 / the scale of q
     float *row_hit;         // [row_cap] the target's logit
-    float2 *part;           // [tiles of V][row_cap] (largest logit * log2 e, sum)
+    float2 *part;           // [half tiles of V][row_cap] (largest logit * log2 e, sum)
     void *q;                // [planes][row_cap][q_pitch]
-    float *dx_sum;          // [row_cap][D] over the pieces so far
+    float *dx_sum;          // [splits][row_cap][D] over the pieces so far
     void *dx, *dw;          // outputs
 };
 
@@ -294,42 +302,82 @@ enum { kLceStats = 0, kLceQ = 1, kLceGrads = 2 };
 
 // A tile of a launch.
 struct LceTile {
-    int job;      // kLceGrads: 0 dx, 1 dW
-    int64_t m, n; // tile indexes
-    int64_t nk;   // steps along K (of each product of planes)
+    int job;        // kLceGrads: 0 dx, 1 dW
+    int64_t m, n;   // tile indexes
+    int64_t k0, nk; // first step along K and steps (of each product of planes)
+    int64_t split;  // dx: which cut of K
 };
 
+// The tiles of one pair of blocks, in order.  Products of logits: pair c takes
+// tiles c, c + pairs, ..., M fastest, so that the tiles in flight share the rows
+// of W (x stays in L2).  Gradients: first the dx tiles the same way, N fastest
+// (they share the rows of q); a dx tile is several dW tiles long, and pairs with
+// one more of them take the fewer dW tiles, so that all end together.
 template <int EPI>
-__device__ __forceinline__ int64_t lce_tiles(const LceArgs &g, int64_t count) {
-    const int64_t mt = (count + kLceM - 1) / kLceM;
-    if (EPI != kLceGrads) return mt * ((g.vc + kLceN - 1) / kLceN);
-    const int64_t nt = (g.D + kLceN - 1) / kLceN;
-    return (mt + (g.with_dw ? (g.vc + kLceM - 1) / kLceM : 0)) * nt;
-}
-// Products of logits: M fastest, so that the tiles in flight share the rows of
-// W (x stays in L2).  Gradients: N fastest, they share the rows of q.
-template <int EPI>
-__device__ __forceinline__ LceTile lce_tile(const LceArgs &g, int64_t count, int64_t i) {
-    LceTile t;
-    const int64_t mt = (count + kLceM - 1) / kLceM;
-    t.job = 0;
-    if (EPI != kLceGrads) {
-        t.n = i / mt;
-        t.m = i - t.n * mt;
-        t.nk = (g.D + kLceK - 1) / kLceK;
+struct LceWalk {
+    int64_t mt, nt, pair, pairs, dx_tiles, dw_tiles, dx_mine, dw_mine, dw_first, dw_step, nk_m, nk_v;
+    __device__ __forceinline__ LceWalk(const LceArgs &g, int64_t count) {
+        pair = blockIdx.x >> 1;
+        pairs = gridDim.x >> 1;
+        mt = (count + kLceM - 1) / kLceM;
+        if (EPI != kLceGrads) {
+            nt = (g.vc + kLceN - 1) / kLceN;
+            nk_v = (g.D + kLceK - 1) / kLceK;
+            dx_tiles = mt * nt;
+            dw_mine = 0;
+        } else {
+            nt = (g.D + kLceN - 1) / kLceN;
+            nk_v = (g.vc + kLceK - 1) / kLceK;
+            nk_m = (count + kLceK - 1) / kLceK;
+            dx_tiles = mt * nt * g.splits;
+            dw_tiles = g.with_dw ? (g.vc + kLceM - 1) / kLceM * nt : 0;
+        }
+        const int64_t most = dx_tiles / pairs, longer = dx_tiles - most * pairs;
+        dx_mine = most + (pair < longer ? 1 : 0);
+        if (EPI == kLceGrads) {
+            const int64_t lx = g.split_k, lw = nk_m < 1 ? 1 : nk_m;
+            // dW tiles of a pair with one more dx tile
+            int64_t fewer =
+                ((dx_tiles * lx + dw_tiles * lw) / pairs - (most + 1) * lx + lw / 2) / lw;
+            fewer = min(max(fewer, (int64_t)0), dw_tiles / pairs);
+            if (pair < longer) {
+                dw_first = pair;
+                dw_step = longer;
+                dw_mine = fewer;
+            } else {
+                dw_first = longer * fewer + pair - longer;
+                dw_step = pairs - longer;
+                dw_mine = dw_first < dw_tiles ? (dw_tiles - dw_first + dw_step - 1) / dw_step : 0;
+            }
+        }
+    }
+    __device__ __forceinline__ int64_t tiles() const { return dx_mine + dw_mine; }
+    __device__ __forceinline__ LceTile at(const LceArgs &g, int64_t i) const {
+        LceTile t;
+        t.job = 0;
+        t.k0 = t.split = 0;
+        if (EPI != kLceGrads) {
+            const int64_t u = pair + i * pairs;
+            t.n = u / mt;
+            t.m = u - t.n * mt;
+            t.nk = nk_v;
+        } else if (i < dx_mine) {
+            const int64_t u = pair + i * pairs, mn = u / nt;
+            t.n = u - mn * nt;
+            t.split = mn / mt;
+            t.m = mn - t.split * mt;
+            t.k0 = t.split * g.split_k;
+            t.nk = max(min(g.split_k, nk_v - t.k0), (int64_t)0);
+        } else {
+            const int64_t u = dw_first + (i - dx_mine) * dw_step;
+            t.job = 1;
+            t.m = u / nt;
+            t.n = u - t.m * nt;
+            t.nk = nk_m;
+        }
         return t;
     }
-    const int64_t nt = (g.D + kLceN - 1) / kLceN;
-    t.m = i / nt;
-    t.n = i - t.m * nt;
-    t.nk = (g.vc + kLceK - 1) / kLceK;
-    if (t.m >= mt) {
-        t.job = 1;
-        t.m -= mt;
-        t.nk = (count + kLceK - 1) / kLceK;
-    }
-    return t;
-}
+};
 
 template <typename T>
 __device__ __forceinline__ T lce_round(float v);
@@ -364,7 +412,7 @@ __device__ __forceinline__ void lce_store32(T *p, const float (&f)[32], int n) {
 // T: storage type of the call.  Maps: a0, b0 of the only product or of dx; a1,
 // b1 of dW.
 template <int EPI, typename T>
-__global__ void __launch_bounds__(kLceThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLceThreads, 1)
 lce_product(const __grid_constant__ CUtensorMap a0, const __grid_constant__ CUtensorMap b0,
             const __grid_constant__ CUtensorMap a1, const __grid_constant__ CUtensorMap b1,
             const LceArgs g) {
@@ -374,11 +422,14 @@ lce_product(const __grid_constant__ CUtensorMap a0, const __grid_constant__ CUte
     __shared__ uint32_t tmem_at;
     __shared__ int abort_s;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = (int)cluster_rank();
     const uint32_t base = (smem_addr(lce_smem) + 1023u) & ~1023u;
     const uint32_t bar0 = smem_addr(bars);
+    // operands of both blocks have arrived (the first block's counts)
     auto full = [&](int s) { return bar0 + 8u * s; };
     auto empty = [&](int s) { return bar0 + 8u * (kLceStages + s); };
     auto acc_full = [&](int b) { return bar0 + 8u * (2 * kLceStages + b); };
+    // both blocks' accumulators have been read (the first block's counts)
     auto acc_empty = [&](int b) { return bar0 + 8u * (2 * kLceStages + 2 + b); };
     const uint32_t drained = bar0 + 8u * (2 * kLceStages + 4);
     if (threadIdx.x == 0) {
@@ -388,7 +439,7 @@ lce_product(const __grid_constant__ CUtensorMap a0, const __grid_constant__ CUte
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(acc_full(b), 1);
-            mbar_init(acc_empty(b), 4);
+            mbar_init(acc_empty(b), 16);
         }
         mbar_init(drained, 1);
         mbar_init_fence();
@@ -397,11 +448,13 @@ lce_product(const __grid_constant__ CUtensorMap a0, const __grid_constant__ CUte
     if (warp == 1) tmem_alloc(smem_addr(&tmem_at), 512);
     tc_fence_before();
     __syncthreads();
+    cluster_sync();
     tc_fence_after();
     const uint32_t tmem = tmem_at;
     volatile int *abort = &abort_s;
     const int64_t count = *g.count;
-    const int64_t tiles = lce_tiles<EPI>(g, count);
+    const LceWalk<EPI> walk(g, count);
+    const int64_t tiles = walk.tiles();
     constexpr bool kCut = sizeof(T) == 4;  // planes, and sums cut in parts
     constexpr int kBufs = kCut ? 1 : 2;    // accumulators in turn; kCut: the second holds the sum
     constexpr int kSegs = kCut ? 6 : 1;
@@ -416,11 +469,12 @@ lce_product(const __grid_constant__ CUtensorMap a0, const __grid_constant__ CUte
             uint32_t phase = 0;
             int64_t issued = 0;
             bool ok = true;
-            for (int64_t i = blockIdx.x; i < tiles && ok; i += gridDim.x) {
-                const LceTile t = lce_tile<EPI>(g, count, i);
+            for (int64_t i = 0; i < tiles && ok; ++i) {
+                const LceTile t = walk.at(g, i);
                 const CUtensorMap *ma = t.job ? &a1 : &a0, *mb = t.job ? &b1 : &b0;
                 const bool a_mn = t.job == 1, b_mn = EPI == kLceGrads;
-                const int m0 = (int)(t.m * kLceM), n0 = (int)(t.n * kLceN);
+                const int m0 = (int)(t.m * kLceM) + rank * kLceHalf;
+                const int n0 = (int)(t.n * kLceN) + rank * kLceHalf;
                 for (int64_t kp = 0; kp < t.nk && ok; kp += kLceCut) {
                     const int64_t len = part_of(t.nk - kp);
                     for (int64_t j = 0; j < len * kSegs; ++j) {
@@ -428,16 +482,17 @@ lce_product(const __grid_constant__ CUtensorMap a0, const __grid_constant__ CUte
                         const int2 pl = lce_planes(kCut ? 3 : 1, seg);
                         ok = mbar_wait(empty(s), phase ^ 1u, abort);
                         if (!ok) break;
-                        mbar_expect(full(s), kLceStage);
+                        if (rank == 0) mbar_expect(full(s), 2 * kLceStage);
                         const uint32_t at = base + s * kLceStage;
-                        const int k0 = (int)(kp + j - seg * len) * kLceK;
+                        const uint32_t here = cluster_addr(full(s), 0);
+                        const int k0 = (int)(t.k0 + kp + j - seg * len) * kLceK;
 #pragma unroll
-                        for (int b = 0; b < kLceM / 64; ++b)
-                            tma_load_3d(at + b * kLceBox, ma, full(s), a_mn ? m0 + 64 * b : k0,
+                        for (int b = 0; b < kLceHalf / 64; ++b)
+                            tma_load_3d(at + b * kLceBox, ma, here, a_mn ? m0 + 64 * b : k0,
                                         a_mn ? k0 : m0 + 64 * b, pl.x);
 #pragma unroll
-                        for (int b = 0; b < kLceN / 64; ++b)
-                            tma_load_3d(at + (kLceM / 64 + b) * kLceBox, mb, full(s),
+                        for (int b = 0; b < kLceHalf / 64; ++b)
+                            tma_load_3d(at + (kLceHalf / 64 + b) * kLceBox, mb, here,
                                         b_mn ? n0 + 64 * b : k0, b_mn ? k0 : n0 + 64 * b, pl.y);
                         ++issued;
                         if (++s == kLceStages) {
@@ -448,18 +503,24 @@ lce_product(const __grid_constant__ CUtensorMap a0, const __grid_constant__ CUte
                     if (!kCut) break;
                 }
             }
-            // no copy may be in flight when the block ends: the last ones' barriers
-            for (int64_t j = issued > kLceStages ? issued - kLceStages : 0; j < issued; ++j)
-                mbar_wait(full((int)(j % kLceStages)), (uint32_t)((j / kLceStages) & 1), nullptr);
+            // no copy may be in flight when the block ends: the last ones have been
+            // multiplied, or, after a wait that ran out, have arrived
+            for (int64_t j = issued > kLceStages ? issued - kLceStages : 0; j < issued; ++j) {
+                const uint32_t p = (uint32_t)((j / kLceStages) & 1);
+                if (ok || rank != 0)
+                    mbar_wait(empty((int)(j % kLceStages)), p, nullptr);
+                else
+                    mbar_wait(full((int)(j % kLceStages)), p, nullptr);
+            }
         }
     } else if (warp == 1) {
-        // ---- issuer ----
-        if (lane == 0) {
+        // ---- issuer, in the first block ----
+        if (lane == 0 && rank == 0) {
             int s = 0, buf = 0;
             uint32_t phase = 0, acc_phase = 0;
             bool ok = true;
-            for (int64_t i = blockIdx.x; i < tiles && ok; i += gridDim.x) {
-                const LceTile t = lce_tile<EPI>(g, count, i);
+            for (int64_t i = 0; i < tiles && ok; ++i) {
+                const LceTile t = walk.at(g, i);
                 if (t.nk == 0) continue;
                 const bool a_mn = t.job == 1, b_mn = EPI == kLceGrads;
                 const uint32_t idesc = tc_idesc(g.bf16 != 0, a_mn, b_mn, kLceM, kLceN);
@@ -475,7 +536,7 @@ lce_product(const __grid_constant__ CUtensorMap a0, const __grid_constant__ CUte
                         tc_fence_after();
                         const uint32_t at = base + s * kLceStage;
                         const uint64_t da = tc_desc(at, kLceBox);
-                        const uint64_t db = tc_desc(at + kLceM / 64 * kLceBox, kLceBox);
+                        const uint64_t db = tc_desc(at + kLceHalf / 64 * kLceBox, kLceBox);
                         // 16 elements further along K: 32 bytes of a row, or 16 rows
                         const uint64_t sa = a_mn ? 16 * 128 / 16 : 32 / 16;
                         const uint64_t sb = b_mn ? 16 * 128 / 16 : 32 / 16;
@@ -497,20 +558,24 @@ lce_product(const __grid_constant__ CUtensorMap a0, const __grid_constant__ CUte
                     if (!kCut) break;
                 }
             }
-            tc_commit(drained);
+            tc_commit_own(drained);
             mbar_wait(drained, 0, nullptr);
         }
     } else {
         // ---- accumulators ----
+        // a warp reads the 32 rows that its number allows, and half of the columns
         const int quarter = warp & 3;
-        const int row_in = 32 * quarter + lane;
+        const int half = (warp - 2) >> 2;
+        const int row_in = rank * kLceHalf + 32 * quarter + lane;
+        constexpr int kChunks = kLceN / 2 / 32;  // of 32 columns
         int buf = 0;
         uint32_t acc_phase = 0;
         bool ok = true;
-        for (int64_t i = blockIdx.x; i < tiles; i += gridDim.x) {
-            const LceTile t = lce_tile<EPI>(g, count, i);
+        for (int64_t i = 0; i < tiles; ++i) {
+            const LceTile t = walk.at(g, i);
             const bool some = t.nk > 0;
-            const uint32_t mine = tmem + ((uint32_t)(32 * quarter) << 16);
+            const uint32_t mine =
+                tmem + ((uint32_t)(32 * quarter) << 16) + half * (kLceN / 2);
             auto arrived = [&]() {  // the whole warp agrees on whether the product came
                 if (some && ok)
                     ok = __all_sync(0xffffffffu, mbar_wait(acc_full(buf), acc_phase, abort));
@@ -520,7 +585,7 @@ lce_product(const __grid_constant__ CUtensorMap a0, const __grid_constant__ CUte
                 if (!some) return;
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(acc_empty(buf));
+                if (lane == 0) mbar_arrive_cluster(cluster_addr(acc_empty(buf), 0));
                 if (++buf == kBufs) {
                     buf = 0;
                     acc_phase ^= 1u;
@@ -533,7 +598,7 @@ lce_product(const __grid_constant__ CUtensorMap a0, const __grid_constant__ CUte
                     arrived();
                     if (ok) {
 #pragma unroll 1
-                        for (int c = 0; c < kLceN / 32; ++c) {
+                        for (int c = 0; c < kChunks; ++c) {
                             float f[32];
                             tmem_load32(f, mine + 32 * c);
                             if (more) {
@@ -552,7 +617,7 @@ lce_product(const __grid_constant__ CUtensorMap a0, const __grid_constant__ CUte
             arrived();
             const uint32_t src = mine + buf * kLceN;
             const int64_t row = t.m * kLceM + row_in;
-            // columns [32 c, 32 c + 32) of the tile; NaN if the product did not come
+            // columns [32 c, 32 c + 32) of the half; NaN if the product did not come
             auto load = [&](int c, float(&f)[32]) {
                 if (some && ok) {
                     tmem_load32(f, src + 32 * c);
@@ -568,12 +633,12 @@ lce_product(const __grid_constant__ CUtensorMap a0, const __grid_constant__ CUte
                 }
             };
             if constexpr (EPI == kLceStats) {
-                const int64_t n0 = g.v0 + t.n * kLceN;
-                const int width = (int)min((int64_t)kLceN, g.V - n0);
+                const int64_t n0 = t.n * kLceN + half * (kLceN / 2);
+                const int width = (int)min((int64_t)(kLceN / 2), g.V - n0);
                 const int hit = row < count ? g.target[row] - (int)n0 : -1;
                 float m = -INFINITY, sum = 0.f;
 #pragma unroll 1
-                for (int c = 0; c < kLceN / 32; ++c) {
+                for (int c = 0; c < kChunks; ++c) {
                     float f[32];
                     load(c, f);
                     if (32 * c >= width) continue;
@@ -606,11 +671,11 @@ lce_product(const __grid_constant__ CUtensorMap a0, const __grid_constant__ CUte
                     sum = (m == -INFINITY ? sum : sum * fast_exp2(m - use)) + (s2.x + s2.y);
                     m = m2;
                 }
-                if (row < count) g.part[t.n * g.row_cap + row] = make_float2(m, sum);
+                if (row < count) g.part[(2 * t.n + half) * g.row_cap + row] = make_float2(m, sum);
             } else if constexpr (EPI == kLceQ) {
                 using O = typename LceSplit<T>::O;
-                const int64_t n0 = t.n * kLceN;  // within the piece
-                const int width = (int)min((int64_t)kLceN, g.V - g.v0 - n0);
+                const int64_t n0 = t.n * kLceN + half * (kLceN / 2);  // within the piece
+                const int width = (int)min((int64_t)(kLceN / 2), g.V - g.v0 - n0);
                 const bool live = row < count;
                 const float l2 = live ? g.row_lse2[row] : 0.f;
                 const float up = live ? g.row_up[row] : 0.f;
@@ -618,7 +683,7 @@ lce_product(const __grid_constant__ CUtensorMap a0, const __grid_constant__ CUte
                 O *q = static_cast<O *>(g.q) + row * g.q_pitch + n0;
                 const int64_t plane = g.row_cap * g.q_pitch;
 #pragma unroll 1
-                for (int c = 0; c < kLceN / 32; ++c) {
+                for (int c = 0; c < kChunks; ++c) {
                     float f[32];
                     load(c, f);
 #pragma unroll
@@ -654,16 +719,16 @@ lce_product(const __grid_constant__ CUtensorMap a0, const __grid_constant__ CUte
                 }
             } else {
                 const float un = *g.unscale;
-                const int64_t n0 = t.n * kLceN;
-                const int width = (int)min((int64_t)kLceN, g.D - n0);
+                const int64_t n0 = t.n * kLceN + half * (kLceN / 2);
+                const int width = (int)min((int64_t)(kLceN / 2), g.D - n0);
                 const bool live = t.job ? row < g.vc : row < count;
                 T *out = nullptr;
                 if (live)
                     out = t.job ? static_cast<T *>(g.dw) + (g.v0 + row) * g.D + n0
                                 : static_cast<T *>(g.dx) + (int64_t)g.row_of[row] * g.D + n0;
-                float *sums = g.dx_sum + row * g.D + n0;
+                float *sums = g.dx_sum + (t.split * g.row_cap + row) * g.D + n0;
 #pragma unroll 1
-                for (int c = 0; c < kLceN / 32; ++c) {
+                for (int c = 0; c < kChunks; ++c) {
                     float f[32];
                     load(c, f);
                     const int n = width - 32 * c;
@@ -679,7 +744,7 @@ lce_product(const __grid_constant__ CUtensorMap a0, const __grid_constant__ CUte
                         for (int e = 0; e < 32; ++e)
                             if (e < n) f[e] += sums[32 * c + e];
                     }
-                    if (g.last)
+                    if (g.last && g.splits == 1)
                         lce_store32<T>(out + 32 * c, f, n);
                     else
                         lce_store32<float>(sums + 32 * c, f, n);
@@ -688,11 +753,27 @@ lce_product(const __grid_constant__ CUtensorMap a0, const __grid_constant__ CUte
             release();
         }
     }
+    // (neither block ends while the other may still reach into it)
     tc_fence_before();
     __syncthreads();
+    cluster_sync();
     if (warp == 1) {
         tc_fence_after();
         tmem_free(tmem, 512);
+    }
+}
+
+// dx of the rows that count, where the sum over the vocabulary was cut.
+template <typename T>
+__global__ void __launch_bounds__(256) lce_join_dx(const LceArgs g) {
+    pdl_begin();
+    const int64_t n = (int64_t)*g.count * g.D, step = g.row_cap * g.D;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
+        float v = __ldcg(g.dx_sum + i);
+#pragma unroll 4
+        for (int64_t s = 1; s < g.splits; ++s) v += __ldcg(g.dx_sum + s * step + i);
+        const int64_t r = i / g.D;
+        static_cast<T *>(g.dx)[g.row_of[r] * g.D + (i - r * g.D)] = lce_round<T>(v);
     }
 }
 
