@@ -32,7 +32,7 @@ static LceLayout lce_layout(bool backward, int64_t rows, int64_t D, int64_t V, s
     LceLayout l = {};
     l.planes = es == 4 ? 3 : 1;
     l.row_cap = round_up(rows < 1 ? 1 : rows, kLceM);
-    l.chunks = ceil_div(rows, kLceChunk);
+    l.chunks = rows > kLceCountRows ? ceil_div(rows, kLceChunk) : 0;
     l.pitch = round_up(D, 8);  // TMA wants rows of whole 16 bytes
     l.pack_w = es == 4 || D % 8 != 0;
     l.w_pitch = l.pitch;
@@ -90,8 +90,9 @@ size_t linear_ce_workspace(bool backward, int64_t rows, int64_t D, int64_t V, si
 }
 
 // Map of [planes][rows][cols] 16-bit elements, rows `pitch` apart, in boxes of
-// 64 x 64; elements beyond the rows or columns read as 0.
-static cudaError_t lce_map(CUtensorMap *map, const void *base, bool bf16, int64_t cols,
+// 64 columns by 128 rows for an operand that lies along K in memory, by 64 for
+// others; elements beyond the rows or columns read as 0.
+static cudaError_t lce_map(CUtensorMap *map, bool along_k, const void *base, bool bf16, int64_t cols,
                            int64_t rows, int64_t planes, int64_t pitch, int64_t plane) {
     using Encode = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
                                 const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
@@ -109,7 +110,7 @@ static cudaError_t lce_map(CUtensorMap *map, const void *base, bool bf16, int64_
     }
     const cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)planes};
     const cuuint64_t strides[2] = {(cuuint64_t)pitch * 2, (cuuint64_t)plane * 2};
-    const cuuint32_t box[3] = {64, 64, 1}, step[3] = {1, 1, 1};
+    const cuuint32_t box[3] = {64, along_k ? 128u : 64u, 1}, step[3] = {1, 1, 1};
     const CUresult r = reinterpret_cast<Encode>(fn)(
         map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
         const_cast<void *>(base), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
@@ -151,7 +152,7 @@ cudaError_t lce_prepare(LceArgs *g, const void **w_at, const LceLayout &l, bool 
     p.target = target;
     p.lse = lse;
     p.dloss = dloss;
-    p.chunk_count = reinterpret_cast<int *>(ws + l.chunk_count);
+    p.chunk_count = l.chunks > 0 ? reinterpret_cast<int *>(ws + l.chunk_count) : nullptr;
     p.chunk_up = reinterpret_cast<float *>(ws + l.chunk_up);
     p.count = reinterpret_cast<int *>(ws + l.single);
     p.unscale = reinterpret_cast<float *>(ws + l.single + 4);
@@ -172,7 +173,7 @@ cudaError_t lce_prepare(LceArgs *g, const void **w_at, const LceLayout &l, bool 
     *w_at = w;
     if (l.pack_w) {
         *w_at = ws + l.w;
-        const int64_t blocks = ceil_div(V * l.w_pitch, 256);
+        const int64_t blocks = ceil_div(V, 8);
         const int64_t most = (int64_t)device_sm_count() * 8;
         e = launch_pdl(lce_pack_weight<T>, dim3((unsigned)(blocks < most ? blocks : most)),
                        dim3(256), 0, st, reinterpret_cast<O *>(ws + l.w), w, V, D, l.w_pitch);
@@ -210,16 +211,17 @@ cudaError_t launch_linear_ce_fw(float *loss, float *lse, const T *x, const T *w,
     g.row_hit = reinterpret_cast<float *>(ws + l.row_hit);
     g.part = reinterpret_cast<float2 *>(ws + l.part);
     CUtensorMap mx, mw;
-    e = lce_map(&mx, ws + l.x, g.bf16, l.pitch, l.row_cap, l.planes, l.pitch, l.row_cap * l.pitch);
+    e = lce_map(&mx, true, ws + l.x, g.bf16, l.pitch, l.row_cap, l.planes, l.pitch,
+                l.row_cap * l.pitch);
     if (e == cudaSuccess)
-        e = lce_map(&mw, wp, g.bf16, l.w_pitch, V, l.planes, l.w_pitch, V * l.w_pitch);
+        e = lce_map(&mw, true, wp, g.bf16, l.w_pitch, V, l.planes, l.w_pitch, V * l.w_pitch);
     // (both 16-bit types share the kernel)
     using S = typename std::conditional<sizeof(T) == 4, float, __half>::type;
     if (e == cudaSuccess) e = lce_launch<kLceStats, S>(mx, mw, mx, mw, g, st);
     if (e != cudaSuccess) return e;
     const int64_t blocks = ceil_div(rows, 32), most = (int64_t)device_sm_count() * 8;
-    return launch_pdl(lce_join, dim3((unsigned)(blocks < most ? blocks : most)), dim3(256), 0, st,
-                      loss, lse, g, 2 * ceil_div(V, kLceN));
+    return launch_pdl(lce_join, dim3((unsigned)(blocks < most ? blocks : most)),
+                      dim3(32 * kLceJoin), 0, st, loss, lse, g, 2 * ceil_div(V, kLceN));
 }
 
 template <typename T>
@@ -240,23 +242,31 @@ cudaError_t launch_linear_ce_bw(T *dx, T *dw, const T *x, const T *w, const int3
     g.with_dw = dw != nullptr;
     g.splits = l.splits;
     g.split_k = l.split_k;
-    CUtensorMap mx, mw, mq;
-    e = lce_map(&mx, ws + l.x, g.bf16, l.pitch, l.row_cap, l.planes, l.pitch, l.row_cap * l.pitch);
-    if (e == cudaSuccess)
-        e = lce_map(&mq, ws + l.q, g.bf16, l.q_pitch, l.row_cap, l.planes, l.q_pitch,
-                    l.row_cap * l.q_pitch);
+    CUtensorMap x_k, x_n, w_k, w_n, q_k, q_n;  // along K, and not
+    const int64_t x_plane = l.row_cap * l.pitch, q_plane = l.row_cap * l.q_pitch;
+    for (const bool k : {true, false}) {
+        if (e == cudaSuccess)
+            e = lce_map(k ? &x_k : &x_n, k, ws + l.x, g.bf16, l.pitch, l.row_cap, l.planes, l.pitch,
+                        x_plane);
+        if (e == cudaSuccess)
+            e = lce_map(k ? &q_k : &q_n, k, ws + l.q, g.bf16, l.q_pitch, l.row_cap, l.planes,
+                        l.q_pitch, q_plane);
+    }
     for (int64_t i = 0; i < l.pieces && e == cudaSuccess; ++i) {
         g.v0 = i * l.vc;
         g.vc = V - g.v0 < l.vc ? V - g.v0 : l.vc;
         g.first = i == 0;
         g.last = i == l.pieces - 1;
         // rows of W from the piece on
-        e = lce_map(&mw, static_cast<const uint8_t *>(wp) + g.v0 * l.w_pitch * 2, g.bf16, l.w_pitch,
-                    V - g.v0, l.planes, l.w_pitch, V * l.w_pitch);
-        if (e == cudaSuccess) e = lce_launch<kLceQ, T>(mx, mw, mx, mw, g, st);
+        for (const bool k : {true, false})
+            if (e == cudaSuccess)
+                e = lce_map(k ? &w_k : &w_n, k,
+                            static_cast<const uint8_t *>(wp) + g.v0 * l.w_pitch * 2, g.bf16,
+                            l.w_pitch, V - g.v0, l.planes, l.w_pitch, V * l.w_pitch);
+        if (e == cudaSuccess) e = lce_launch<kLceQ, T>(x_k, w_k, x_k, w_k, g, st);
         const int64_t nk = ceil_div(g.vc, kLceK);  // (the last piece may be shorter)
         g.split_k = ceil_div(nk, l.splits);
-        if (e == cudaSuccess) e = lce_launch<kLceGrads, T>(mq, mw, mq, mx, g, st);
+        if (e == cudaSuccess) e = lce_launch<kLceGrads, T>(q_k, w_n, q_n, x_n, g, st);
     }
     if (e != cudaSuccess || l.splits == 1 || rows == 0) return e;
     const int64_t blocks = ceil_div(rows * D, 256), most = (int64_t)device_sm_count() * 8;

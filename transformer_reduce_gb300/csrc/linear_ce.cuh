@@ -55,7 +55,11 @@ constexpr int kLceSms = 152;  // what the cuts are made for
 // without the cut).
 constexpr int kLceCut = 4;
 constexpr int kLceChunk = 1024;  // rows counted together
-constexpr int kLcePackRows = 32;
+constexpr int kLcePackRows = 8;  // one per warp
+// Rows up to which every block of the packing counts all targets itself,
+// without a launch before it (at 8192 rows that took 35 us in the backward
+// instead of 5 and 10).
+constexpr int64_t kLceCountRows = 2048;
 
 // What the kernels of one call share.
 struct LceArgs {
@@ -73,8 +77,8 @@ struct LceArgs {
     const int *row_of;      // [row_cap] their index
     const int *target;      // [row_cap]
     const float *row_lse2;  // [row_cap] lse * log2 e
-    const float *row_up;    // [row_cap] dloss times the scale of q
-    const float *unscale;   // 1 / the scale of q
+    const float *row_up;    // [row_cap] dloss / unscale
+    const float *unscale;   // what q is to be multiplied with
     float *row_hit;         // [row_cap] the target's logit
     float2 *part;           // [half tiles of V][row_cap] (largest logit * log2 e, sum)
     void *q;                // [planes][row_cap][q_pitch]
@@ -82,11 +86,10 @@ struct LceArgs {
     void *dx, *dw;          // outputs
 };
 
-// The planes of a product, smallest terms first.
-__device__ __forceinline__ int2 lce_planes(int planes, int s) {
-    if (planes == 1) return make_int2(0, 0);
-    constexpr int kA[6] = {2, 0, 1, 1, 0, 0}, kB[6] = {0, 2, 1, 0, 1, 0};
-    return make_int2(kA[s], kB[s]);
+// The planes of the s-th product of two fp32 operands, smallest terms first: of
+// A 2, 0, 1, 1, 0, 0 and of B 0, 2, 1, 0, 1, 0.
+__device__ __forceinline__ int2 lce_planes(int s) {
+    return make_int2((0x001102 >> (4 * s)) & 3, (0x010120 >> (4 * s)) & 3);
 }
 
 // x in planes of the operand type: the value itself, or its three bf16 parts.
@@ -125,7 +128,7 @@ struct LcePack {
     int backward;
     const int32_t *target;
     const float *lse, *dloss;
-    int *chunk_count;     // [chunks]
+    int *chunk_count;     // [chunks], NULL: up to kLceCountRows rows
     float *chunk_up;      // [chunks] largest |dloss|
     int *count, *row_of, *row_target;
     float *row_lse2, *row_up, *unscale;
@@ -193,14 +196,27 @@ lce_pack_rows(typename LceSplit<T>::O *out, const T *x, T *dx, const LcePack p) 
     const int64_t chunks = (p.rows + kLceChunk - 1) / kLceChunk;
     int before = 0, all = 0;
     float up = 0.f;
-    for (int64_t c = tid; c < chunks; c += 256) {
-        const int n = p.chunk_count[c];
-        all += n;
-        if (c < chunk) before += n;
-        up = fmaxf(up, p.chunk_up[c]);
+    if (p.chunk_count) {
+        for (int64_t c = tid; c < chunks; c += 256) {
+            const int n = p.chunk_count[c];
+            all += n;
+            if (c < chunk) before += n;
+            up = fmaxf(up, p.chunk_up[c]);
+        }
+        for (int64_t r = chunk * kLceChunk + tid; r < row0; r += 256)
+            before += lce_counts(p, __ldg(p.target + r));
+    } else {
+#pragma unroll 4
+        for (int r = tid; r < (int)p.rows; r += 256) {
+            const bool counts = lce_counts(p, __ldg(p.target + r));
+            all += counts;
+            before += counts && r < row0;
+            if (p.backward) {
+                const float g = counts ? fabsf(__ldg(p.dloss + r)) : 0.f;
+                up = g < INFINITY ? fmaxf(up, g) : INFINITY;  // (of NaN too)
+            }
+        }
     }
-    for (int64_t r = chunk * kLceChunk + tid; r < row0; r += 256)
-        before += lce_counts(p, __ldg(p.target + r));
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
         before += __shfl_xor_sync(0xffffffffu, before, o);
@@ -220,26 +236,25 @@ lce_pack_rows(typename LceSplit<T>::O *out, const T *x, T *dx, const LcePack p) 
         all += all_s[w];
         up = fmaxf(up, up_s[w]);
     }
-    // q in fp16 is scaled by a power of two so that the largest |dloss| is in
-    // [2^13, 2^14): a weight of 2^-27 is then still a normal number
-    float scale = 1.f;
-    if (sizeof(T) == 2 && std::is_same<T, __half>::value && p.backward && up > 0.f &&
-        up < INFINITY) {
-        const int e = min(max(ilogbf(up), -110), 110);
-        scale = exp2f((float)(13 - e));
-    }
+    // q is made of dloss over the largest |dloss|: equal gradients, as of a mean
+    // loss, then put no rounding of their own on all of q.  For fp16 that is
+    // scaled by 2^14: a weight of 2^-28 is still a normal number.
+    const bool scaled = p.backward && up > 0.f && up < INFINITY;
+    const float top = scaled ? up : 1.f;
+    const float scale = scaled && std::is_same<T, __half>::value ? 0x1p14f : 1.f;
     if (blockIdx.x == 0 && tid == 0) {
         *p.count = all;
-        if (p.backward) *p.unscale = 1.f / scale;
+        if (p.backward) *p.unscale = top / scale;
     }
     const int64_t plane = p.row_cap * p.pitch;
     // the block's rows: a ballot of the targets gives every row its place
     const int64_t mine = row0 + lane;
-    const int32_t t_lane = mine < p.rows ? __ldg(p.target + mine) : -1;
-    const uint32_t live = __ballot_sync(0xffffffffu, mine < p.rows && lce_counts(p, t_lane));
-    for (int i = warp; i < kLcePackRows; i += 8) {
-        const int64_t r = row0 + i;
-        if (r >= p.rows) break;
+    const bool there = lane < kLcePackRows && mine < p.rows;
+    const int32_t t_lane = there ? __ldg(p.target + mine) : -1;
+    const uint32_t live = __ballot_sync(0xffffffffu, there && lce_counts(p, t_lane));
+    const int i = warp;
+    const int64_t r = row0 + i;
+    if (r < p.rows) {
         const int32_t t = __shfl_sync(0xffffffffu, t_lane, i);
         const T *xr = x + r * p.D;
         if (!((live >> i) & 1u)) {
@@ -250,28 +265,31 @@ lce_pack_rows(typename LceSplit<T>::O *out, const T *x, T *dx, const LcePack p) 
                 p.loss[r] = v;
                 p.lse_out[r] = v;
             }
-            continue;
-        }
-        const int64_t at = before + __popc(live & ((1u << i) - 1u));
-        O *o = out + at * p.pitch;
-        if (lane == 0) {
-            p.row_of[at] = (int)r;
-            p.row_target[at] = t;
-            if (p.backward) {
-                const bool in = t < p.V;
-                p.row_lse2[at] = in ? __ldg(p.lse + r) * kLog2e : __int_as_float(0x7fc00000);
-                p.row_up[at] = __ldg(p.dloss + r) * scale;
-            }
-        }
-        constexpr int V = Traits<T>::kVec;
-        if (sizeof(T) == 2 && p.D % V == 0 && reinterpret_cast<uintptr_t>(x) % 16 == 0) {
-            for (int64_t c = lane; c < p.D / V; c += 32)
-                reinterpret_cast<uint4 *>(o)[c] = ld_cached16(xr + c * V);
         } else {
-            for (int64_t d = lane; d < p.D; d += 32) LceSplit<T>::put(o + d, plane, xr[d]);
+            const int64_t at = before + __popc(live & ((1u << i) - 1u));
+            O *o = out + at * p.pitch;
+            if (lane == 0) {
+                p.row_of[at] = (int)r;
+                p.row_target[at] = t;
+                if (p.backward) {
+                    const bool in = t < p.V;
+                    p.row_lse2[at] = in ? __ldg(p.lse + r) * kLog2e : __int_as_float(0x7fc00000);
+                    p.row_up[at] = __ldg(p.dloss + r) / top * scale;
+                }
+            }
+            constexpr int V = Traits<T>::kVec;
+            if (sizeof(T) == 2 && p.D % V == 0 && reinterpret_cast<uintptr_t>(x) % 16 == 0) {
+#pragma unroll 4
+                for (int64_t c = lane; c < p.D / V; c += 32)
+                    reinterpret_cast<uint4 *>(o)[c] = ld_cached16(xr + c * V);
+            } else {
+#pragma unroll 8
+                for (int64_t d = lane; d < p.D; d += 32)
+                    LceSplit<T>::put(o + d, plane, __ldg(xr + d));
+            }
+            for (int64_t d = p.D + lane; d < p.pitch; d += 32)
+                LceSplit<T>::put(o + d, plane, T(0.f));
         }
-        for (int64_t d = p.D + lane; d < p.pitch; d += 32)
-            LceSplit<T>::put(o + d, plane, T(0.f));
     }
     if (blockIdx.x == gridDim.x - 1) {
         const int64_t end = ((int64_t)all + kLceM - 1) / kLceM * kLceM;
@@ -289,9 +307,13 @@ __global__ void __launch_bounds__(256)
 lce_pack_weight(typename LceSplit<T>::O *out, const T *w, int64_t V, int64_t D, int64_t pitch) {
     pdl_begin();
     const int64_t n = V * pitch;
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
-        const int64_t v = i / pitch, d = i - v * pitch;
-        LceSplit<T>::put(out + i, n, d < D ? w[v * D + d] : T(0.f));
+    const int lane = threadIdx.x & 31;
+    for (int64_t v = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); v < V; v += (int64_t)gridDim.x * 8) {
+#pragma unroll 8
+        for (int64_t d = lane; d < D; d += 32)
+            LceSplit<T>::put(out + v * pitch + d, n, __ldg(w + v * D + d));
+        for (int64_t d = D + lane; d < pitch; d += 32)
+            LceSplit<T>::put(out + v * pitch + d, n, T(0.f));
     }
 }
 
@@ -316,6 +338,7 @@ struct LceTile {
 template <int EPI>
 struct LceWalk {
     int64_t mt, nt, pair, pairs, dx_tiles, dw_tiles, dx_mine, dw_mine, dw_first, dw_step, nk_m, nk_v;
+    int64_t i, fast, slow, fast_n, step_f, step_s;  // the next tile, and from it to the one after
     __device__ __forceinline__ LceWalk(const LceArgs &g, int64_t count) {
         pair = blockIdx.x >> 1;
         pairs = gridDim.x >> 1;
@@ -352,28 +375,58 @@ struct LceWalk {
         }
     }
     __device__ __forceinline__ int64_t tiles() const { return dx_mine + dw_mine; }
-    __device__ __forceinline__ LceTile at(const LceArgs &g, int64_t i) const {
+    // Divides once per run of tiles, not per tile: the loader's tiles are as short
+    // as 16 steps, and four divisions in each cost it a third of its time.
+    __device__ __forceinline__ void start(int64_t first, int64_t step, int64_t n) {
+        fast_n = n < 1 ? 1 : n;
+        slow = first / fast_n;
+        fast = first - slow * fast_n;
+        step_s = step / fast_n;
+        step_f = step - step_s * fast_n;
+    }
+    __device__ __forceinline__ void begin() {
+        i = 0;
+        if (EPI != kLceGrads)
+            start(pair, pairs, mt);
+        else if (dx_mine > 0)
+            start(pair, pairs, nt);
+        else
+            start(dw_first, dw_step, nt);
+    }
+    __device__ __forceinline__ LceTile next(const LceArgs &g) {
         LceTile t;
         t.job = 0;
         t.k0 = t.split = 0;
         if (EPI != kLceGrads) {
-            const int64_t u = pair + i * pairs;
-            t.n = u / mt;
-            t.m = u - t.n * mt;
+            t.n = slow;
+            t.m = fast;
             t.nk = nk_v;
         } else if (i < dx_mine) {
-            const int64_t u = pair + i * pairs, mn = u / nt;
-            t.n = u - mn * nt;
-            t.split = mn / mt;
-            t.m = mn - t.split * mt;
+            t.n = fast;
+            t.split = 0;
+            t.m = slow;
+            while (t.m >= mt) {  // (at most kLceMaxCuts times)
+                t.m -= mt;
+                ++t.split;
+            }
             t.k0 = t.split * g.split_k;
             t.nk = max(min(g.split_k, nk_v - t.k0), (int64_t)0);
         } else {
-            const int64_t u = dw_first + (i - dx_mine) * dw_step;
             t.job = 1;
-            t.m = u / nt;
-            t.n = u - t.m * nt;
+            t.m = slow;
+            t.n = fast;
             t.nk = nk_m;
+        }
+        ++i;
+        if (EPI == kLceGrads && i == dx_mine) {
+            start(dw_first, dw_step, nt);
+        } else {
+            fast += step_f;
+            slow += step_s;
+            if (fast >= fast_n) {
+                fast -= fast_n;
+                ++slow;
+            }
         }
         return t;
     }
@@ -390,11 +443,28 @@ __device__ __forceinline__ __nv_bfloat16 lce_round<__nv_bfloat16>(float v) {
     return __float2bfloat16_rn(v);
 }
 
-// 32 values to consecutive elements, the first n of them.
+// 32 values to consecutive elements, the first n of them: whole 32-byte sectors
+// where they are aligned (a lane's row lies far from the next lane's, and halves
+// of a sector cost as much as all of it).
 template <typename T>
 __device__ __forceinline__ void lce_store32(T *p, const float (&f)[32], int n) {
     constexpr int V = Traits<T>::kVec;
-    if (n >= 32 && reinterpret_cast<uintptr_t>(p) % 16 == 0) {
+    if (n >= 32 && reinterpret_cast<uintptr_t>(p) % 32 == 0) {
+#pragma unroll
+        for (int c = 0; c < 32; c += 2 * V) {
+            float e0[V], e1[V];
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                e0[i] = f[c + i];
+                e1[i] = f[c + V + i];
+            }
+            const uint4 a = Traits<T>::pack(e0), b = Traits<T>::pack(e1);
+            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p + c),
+                         "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z),
+                         "r"(b.w)
+                         : "memory");
+        }
+    } else if (n >= 32 && reinterpret_cast<uintptr_t>(p) % 16 == 0) {
 #pragma unroll
         for (int c = 0; c < 32; c += V) {
             float e[V];
@@ -410,7 +480,8 @@ __device__ __forceinline__ void lce_store32(T *p, const float (&f)[32], int n) {
 }
 
 // T: storage type of the call.  Maps: a0, b0 of the only product or of dx; a1,
-// b1 of dW.
+// b1 of dW; in boxes of 64 by 128 rows where the operand lies along K, else of
+// 64 by 64.
 template <int EPI, typename T>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLceThreads, 1)
 lce_product(const __grid_constant__ CUtensorMap a0, const __grid_constant__ CUtensorMap b0,
@@ -453,7 +524,8 @@ lce_product(const __grid_constant__ CUtensorMap a0, const __grid_constant__ CUte
     const uint32_t tmem = tmem_at;
     volatile int *abort = &abort_s;
     const int64_t count = *g.count;
-    const LceWalk<EPI> walk(g, count);
+    LceWalk<EPI> walk(g, count);
+    walk.begin();
     const int64_t tiles = walk.tiles();
     constexpr bool kCut = sizeof(T) == 4;  // planes, and sums cut in parts
     constexpr int kBufs = kCut ? 1 : 2;    // accumulators in turn; kCut: the second holds the sum
@@ -465,36 +537,46 @@ lce_product(const __grid_constant__ CUtensorMap a0, const __grid_constant__ CUte
         if (lane == 0) {
             tma_prefetch_map(&a0);
             tma_prefetch_map(&b0);
+            const uint32_t first = cluster_addr(bar0, 0) - bar0;  // to the first block's barriers
             int s = 0;
             uint32_t phase = 0;
             int64_t issued = 0;
             bool ok = true;
             for (int64_t i = 0; i < tiles && ok; ++i) {
-                const LceTile t = walk.at(g, i);
+                const LceTile t = walk.next(g);
                 const CUtensorMap *ma = t.job ? &a1 : &a0, *mb = t.job ? &b1 : &b0;
                 const bool a_mn = t.job == 1, b_mn = EPI == kLceGrads;
                 const int m0 = (int)(t.m * kLceM) + rank * kLceHalf;
                 const int n0 = (int)(t.n * kLceN) + rank * kLceHalf;
                 for (int64_t kp = 0; kp < t.nk && ok; kp += kLceCut) {
-                    const int64_t len = part_of(t.nk - kp);
-                    for (int64_t j = 0; j < len * kSegs; ++j) {
-                        const int seg = (int)(j / len);
-                        const int2 pl = lce_planes(kCut ? 3 : 1, seg);
+                    const int len = (int)part_of(t.nk - kp);
+                    for (int j = 0, seg = 0, k0 = (int)(t.k0 + kp) * kLceK; seg < kSegs;) {
+                        const int2 pl = kCut ? lce_planes(seg) : make_int2(0, 0);
                         ok = mbar_wait(empty(s), phase ^ 1u, abort);
                         if (!ok) break;
                         if (rank == 0) mbar_expect(full(s), 2 * kLceStage);
                         const uint32_t at = base + s * kLceStage;
-                        const uint32_t here = cluster_addr(full(s), 0);
-                        const int k0 = (int)(t.k0 + kp + j - seg * len) * kLceK;
-#pragma unroll
-                        for (int b = 0; b < kLceHalf / 64; ++b)
-                            tma_load_3d(at + b * kLceBox, ma, here, a_mn ? m0 + 64 * b : k0,
-                                        a_mn ? k0 : m0 + 64 * b, pl.x);
-#pragma unroll
-                        for (int b = 0; b < kLceHalf / 64; ++b)
-                            tma_load_3d(at + (kLceHalf / 64 + b) * kLceBox, mb, here,
-                                        b_mn ? n0 + 64 * b : k0, b_mn ? k0 : n0 + 64 * b, pl.y);
+                        const uint32_t here = full(s) + first;
+                        // along K: 128 rows at once; along M or N: 64 and 64 columns
+                        if (a_mn) {
+                            tma_load_3d(at, ma, here, m0, k0, pl.x);
+                            tma_load_3d(at + kLceBox, ma, here, m0 + 64, k0, pl.x);
+                        } else {
+                            tma_load_3d(at, ma, here, k0, m0, pl.x);
+                        }
+                        if (b_mn) {
+                            tma_load_3d(at + 2 * kLceBox, mb, here, n0, k0, pl.y);
+                            tma_load_3d(at + 3 * kLceBox, mb, here, n0 + 64, k0, pl.y);
+                        } else {
+                            tma_load_3d(at + 2 * kLceBox, mb, here, k0, n0, pl.y);
+                        }
                         ++issued;
+                        k0 += kLceK;
+                        if (++j == len) {  // the next product of planes
+                            j = 0;
+                            ++seg;
+                            k0 = (int)(t.k0 + kp) * kLceK;
+                        }
                         if (++s == kLceStages) {
                             s = 0;
                             phase ^= 1u;
@@ -520,23 +602,23 @@ lce_product(const __grid_constant__ CUtensorMap a0, const __grid_constant__ CUte
             uint32_t phase = 0, acc_phase = 0;
             bool ok = true;
             for (int64_t i = 0; i < tiles && ok; ++i) {
-                const LceTile t = walk.at(g, i);
+                const LceTile t = walk.next(g);
                 if (t.nk == 0) continue;
                 const bool a_mn = t.job == 1, b_mn = EPI == kLceGrads;
                 const uint32_t idesc = tc_idesc(g.bf16 != 0, a_mn, b_mn, kLceM, kLceN);
                 for (int64_t kp = 0; kp < t.nk && ok; kp += kLceCut) {
-                    const int64_t len = part_of(t.nk - kp) * kSegs;
+                    const int len = (int)part_of(t.nk - kp) * kSegs;
                     ok = mbar_wait(acc_empty(buf), acc_phase ^ 1u, abort);
                     if (!ok) break;
                     tc_fence_after();
                     const uint32_t d = tmem + buf * kLceN;
-                    for (int64_t k = 0; k < len; ++k) {
+                    for (int k = 0; k < len; ++k) {
                         ok = mbar_wait(full(s), phase, abort);
                         if (!ok) break;
                         tc_fence_after();
                         const uint32_t at = base + s * kLceStage;
                         const uint64_t da = tc_desc(at, kLceBox);
-                        const uint64_t db = tc_desc(at + kLceHalf / 64 * kLceBox, kLceBox);
+                        const uint64_t db = tc_desc(at + 2 * kLceBox, kLceBox);
                         // 16 elements further along K: 32 bytes of a row, or 16 rows
                         const uint64_t sa = a_mn ? 16 * 128 / 16 : 32 / 16;
                         const uint64_t sb = b_mn ? 16 * 128 / 16 : 32 / 16;
@@ -567,12 +649,11 @@ lce_product(const __grid_constant__ CUtensorMap a0, const __grid_constant__ CUte
         const int quarter = warp & 3;
         const int half = (warp - 2) >> 2;
         const int row_in = rank * kLceHalf + 32 * quarter + lane;
-        constexpr int kChunks = kLceN / 2 / 32;  // of 32 columns
         int buf = 0;
         uint32_t acc_phase = 0;
         bool ok = true;
         for (int64_t i = 0; i < tiles; ++i) {
-            const LceTile t = walk.at(g, i);
+            const LceTile t = walk.next(g);
             const bool some = t.nk > 0;
             const uint32_t mine =
                 tmem + ((uint32_t)(32 * quarter) << 16) + half * (kLceN / 2);
@@ -598,12 +679,13 @@ lce_product(const __grid_constant__ CUtensorMap a0, const __grid_constant__ CUte
                     arrived();
                     if (ok) {
 #pragma unroll 1
-                        for (int c = 0; c < kChunks; ++c) {
-                            float f[32];
-                            tmem_load32(f, mine + 32 * c);
+                        for (int c = 0; c < kLceN / 2 / 32; ++c) {
+                            float f[32], sum[32];
+                            tmem_load32(f, 0, mine + 32 * c);
+                            if (more) tmem_load32(sum, 0, mine + kLceN + 32 * c);
+                            tmem_wait(f);
                             if (more) {
-                                float sum[32];
-                                tmem_load32(sum, mine + kLceN + 32 * c);
+                                tmem_wait(sum);
 #pragma unroll
                                 for (int e = 0; e < 32; ++e) f[e] += sum[e];
                             }
@@ -617,140 +699,152 @@ lce_product(const __grid_constant__ CUtensorMap a0, const __grid_constant__ CUte
             arrived();
             const uint32_t src = mine + buf * kLceN;
             const int64_t row = t.m * kLceM + row_in;
-            // columns [32 c, 32 c + 32) of the half; NaN if the product did not come
-            auto load = [&](int c, float(&f)[32]) {
-                if (some && ok) {
-                    tmem_load32(f, src + 32 * c);
-                    if (kCut && more) {
+            // the row's half of the tile; NaN if the product did not come.  The
+            // accumulator is free once it is read.
+            constexpr int kCols = kLceN / 2;
+            float f[kCols];
+            if (some && ok) {
+#pragma unroll
+                for (int c = 0; c < kCols; c += 32) tmem_load32(f, c, src + c);
+                tmem_wait(f);
+                if (kCut && more) {
+#pragma unroll
+                    for (int c = 0; c < kCols; c += 32) {
                         float sum[32];
-                        tmem_load32(sum, mine + kLceN + 32 * c);
+                        tmem_load32(sum, 0, mine + kLceN + c);
+                        tmem_wait(sum);
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) f[e] += sum[e];
+                        for (int e = 0; e < 32; ++e) f[c + e] += sum[e];
                     }
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) f[e] = ok ? 0.f : __int_as_float(0x7fc00000);
                 }
-            };
+            } else {
+#pragma unroll
+                for (int e = 0; e < kCols; ++e) f[e] = ok ? 0.f : __int_as_float(0x7fc00000);
+            }
+            release();
             if constexpr (EPI == kLceStats) {
-                const int64_t n0 = t.n * kLceN + half * (kLceN / 2);
-                const int width = (int)min((int64_t)(kLceN / 2), g.V - n0);
+                const int64_t n0 = t.n * kLceN + half * kCols;
+                const int width = (int)min((int64_t)kCols, g.V - n0);
                 const int hit = row < count ? g.target[row] - (int)n0 : -1;
-                float m = -INFINITY, sum = 0.f;
-#pragma unroll 1
-                for (int c = 0; c < kChunks; ++c) {
-                    float f[32];
-                    load(c, f);
-                    if (32 * c >= width) continue;
-                    if (32 * c + 32 > width) {
+                if (width < kCols) {
 #pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            if (32 * c + e >= width) f[e] = -INFINITY;
-                    }
-                    if ((unsigned)(hit - 32 * c) < 32u) {
-                        float v = 0.f;
-#pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            if (hit - 32 * c == e) v = f[e];
-                        g.row_hit[row] = v;
-                    }
-                    float top = f[0];
-#pragma unroll
-                    for (int e = 1; e < 31; e += 2) top = fmax3(top, f[e], f[e + 1]);
-                    top = fmaxf(top, f[31]);
-                    const float m2 = fmaxf(m, top * kLog2e);
-                    const float use = m2 == -INFINITY ? 0.f : m2;
-                    float2 s2 = f2(0.f);
-#pragma unroll
-                    for (int e = 0; e < 32; e += 2) {
-                        float2 z = fma2(make_float2(f[e], f[e + 1]), f2(kLog2e), f2(-use));
-                        z.x = fast_exp2(z.x);
-                        z.y = fast_exp2(z.y);
-                        s2 = add2(s2, z);
-                    }
-                    sum = (m == -INFINITY ? sum : sum * fast_exp2(m - use)) + (s2.x + s2.y);
-                    m = m2;
+                    for (int e = 0; e < kCols; ++e)
+                        if (e >= width) f[e] = -INFINITY;
                 }
+                if ((unsigned)hit < (unsigned)kCols) {
+                    float v = 0.f;
+#pragma unroll
+                    for (int e = 0; e < kCols; ++e)
+                        if (hit == e) v = f[e];
+                    g.row_hit[row] = v;
+                }
+                // four chains each
+                float top[4];
+                float2 s2[4];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    top[c] = fmaxf(f[2 * c], f[2 * c + 1]);
+                    s2[c] = f2(0.f);
+                }
+#pragma unroll
+                for (int e = 8; e < kCols; e += 8)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        top[c] = fmax3(top[c], f[e + 2 * c], f[e + 2 * c + 1]);
+                const float m = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * kLog2e;
+                const float use = m == -INFINITY ? 0.f : m;
+#pragma unroll
+                for (int e = 0; e < kCols; e += 2) {
+                    float2 z = fma2(make_float2(f[e], f[e + 1]), f2(kLog2e), f2(-use));
+                    z.x = fast_exp2(z.x);
+                    z.y = fast_exp2(z.y);
+                    s2[e / 2 % 4] = add2(s2[e / 2 % 4], z);
+                }
+                const float2 t2 = add2(add2(s2[0], s2[1]), add2(s2[2], s2[3]));
+                const float sum = t2.x + t2.y;
                 if (row < count) g.part[(2 * t.n + half) * g.row_cap + row] = make_float2(m, sum);
             } else if constexpr (EPI == kLceQ) {
                 using O = typename LceSplit<T>::O;
-                const int64_t n0 = t.n * kLceN + half * (kLceN / 2);  // within the piece
-                const int width = (int)min((int64_t)(kLceN / 2), g.V - g.v0 - n0);
+                const int64_t n0 = t.n * kLceN + half * kCols;  // within the piece
+                const int width = (int)min((int64_t)kCols, g.V - g.v0 - n0);
                 const bool live = row < count;
                 const float l2 = live ? g.row_lse2[row] : 0.f;
                 const float up = live ? g.row_up[row] : 0.f;
                 const int hit = live ? g.target[row] - (int)(g.v0 + n0) : -1;
                 O *q = static_cast<O *>(g.q) + row * g.q_pitch + n0;
                 const int64_t plane = g.row_cap * g.q_pitch;
-#pragma unroll 1
-                for (int c = 0; c < kChunks; ++c) {
-                    float f[32];
-                    load(c, f);
 #pragma unroll
-                    for (int e = 0; e < 32; e += 2) {
-                        float2 z = fma2(make_float2(f[e], f[e + 1]), f2(kLog2e), f2(-l2));
-                        f[e] = fast_exp2(z.x);
-                        f[e + 1] = fast_exp2(z.y);
-                    }
-                    if ((unsigned)(hit - 32 * c) < 32u) {
+                for (int e = 0; e < kCols; e += 2) {
+                    const float2 z = fma2(make_float2(f[e], f[e + 1]), f2(kLog2e), f2(-l2));
+                    f[e] = fast_exp2(z.x);
+                    f[e + 1] = fast_exp2(z.y);
+                }
+                if ((unsigned)hit < (unsigned)kCols) {
 #pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            if (hit - 32 * c == e) f[e] -= 1.f;
-                    }
+                    for (int e = 0; e < kCols; ++e)
+                        if (hit == e) f[e] -= 1.f;
+                }
 #pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        f[e] = live && 32 * c + e < width ? f[e] * up : 0.f;
+                for (int e = 0; e < kCols; ++e) f[e] *= up;
+                if (!live || width < kCols) {
+#pragma unroll
+                    for (int e = 0; e < kCols; ++e)
+                        if (!live || e >= width) f[e] = 0.f;
+                }
+#pragma unroll
+                for (int c = 0; c < kCols; c += 32) {
+                    float p0[32];
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) p0[e] = f[c + e];
                     if constexpr (LceSplit<T>::kPlanes == 1) {
-                        lce_store32<O>(q + 32 * c, f, 32);
+                        lce_store32<O>(q + c, p0, 32);
                     } else {
-                        float h1[32], h2[32];
+                        float p1[32], p2[32];
 #pragma unroll
                         for (int e = 0; e < 32; ++e) {
                             O o[3];
-                            LceSplit<float>::parts(f[e], o);
-                            f[e] = __bfloat162float(o[0]);
-                            h1[e] = __bfloat162float(o[1]);
-                            h2[e] = __bfloat162float(o[2]);
+                            LceSplit<float>::parts(p0[e], o);
+                            p0[e] = __bfloat162float(o[0]);
+                            p1[e] = __bfloat162float(o[1]);
+                            p2[e] = __bfloat162float(o[2]);
                         }
-                        lce_store32<O>(q + 32 * c, f, 32);
-                        lce_store32<O>(q + plane + 32 * c, h1, 32);
-                        lce_store32<O>(q + 2 * plane + 32 * c, h2, 32);
+                        lce_store32<O>(q + c, p0, 32);
+                        lce_store32<O>(q + plane + c, p1, 32);
+                        lce_store32<O>(q + 2 * plane + c, p2, 32);
                     }
                 }
             } else {
                 const float un = *g.unscale;
-                const int64_t n0 = t.n * kLceN + half * (kLceN / 2);
-                const int width = (int)min((int64_t)(kLceN / 2), g.D - n0);
+                const int64_t n0 = t.n * kLceN + half * kCols;
+                const int width = (int)min((int64_t)kCols, g.D - n0);
                 const bool live = t.job ? row < g.vc : row < count;
                 T *out = nullptr;
                 if (live)
                     out = t.job ? static_cast<T *>(g.dw) + (g.v0 + row) * g.D + n0
                                 : static_cast<T *>(g.dx) + (int64_t)g.row_of[row] * g.D + n0;
                 float *sums = g.dx_sum + (t.split * g.row_cap + row) * g.D + n0;
-#pragma unroll 1
-                for (int c = 0; c < kChunks; ++c) {
-                    float f[32];
-                    load(c, f);
-                    const int n = width - 32 * c;
-                    if (n <= 0 || !live) continue;
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) f[e] *= un;
+                for (int c = 0; c < kCols; c += 32) {
+                    const int n = width - c;
+                    if (n <= 0 || !live) continue;
+                    float v[32];
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) v[e] = f[c + e] * un;
                     if (t.job) {
-                        lce_store32<T>(out + 32 * c, f, n);
+                        lce_store32<T>(out + c, v, n);
                         continue;
                     }
                     if (!g.first) {
 #pragma unroll
                         for (int e = 0; e < 32; ++e)
-                            if (e < n) f[e] += sums[32 * c + e];
+                            if (e < n) v[e] += sums[c + e];
                     }
                     if (g.last && g.splits == 1)
-                        lce_store32<T>(out + 32 * c, f, n);
+                        lce_store32<T>(out + c, v, n);
                     else
-                        lce_store32<float>(sums + 32 * c, f, n);
+                        lce_store32<float>(sums + c, v, n);
                 }
             }
-            release();
         }
     }
     // (neither block ends while the other may still reach into it)
@@ -777,33 +871,60 @@ __global__ void __launch_bounds__(256) lce_join_dx(const LceArgs g) {
     }
 }
 
-// lse and loss of the rows that count, from the tiles' (largest, sum), eight
-// threads per row: each joins every eighth tile, the first joins the eight.
-static __global__ void __launch_bounds__(256)
-lce_join(float *loss, float *lse, const LceArgs g, int64_t tiles) {
+// lse and loss of the rows that count, from the parts' (largest, sum): 32 rows
+// per block, each by 32 threads that take every 32nd part, eight at a time; the
+// threads' pairs are joined in order.
+constexpr int kLceJoin = 32;
+static __global__ void __launch_bounds__(32 * kLceJoin)
+lce_join(float *loss, float *lse, const LceArgs g, int64_t parts) {
     pdl_begin();
-    __shared__ float m_s[8][32], s_s[8][32];
+    __shared__ float m_s[kLceJoin][33], s_s[kLceJoin][33];
     const int r_in = threadIdx.x & 31, part = threadIdx.x >> 5;
     const int64_t count = *g.count;
     for (int64_t r0 = (int64_t)blockIdx.x * 32; r0 < count; r0 += (int64_t)gridDim.x * 32) {
         const int64_t row = r0 + r_in;
         float m = -INFINITY, s = 0.f;
         if (row < count) {
-#pragma unroll 4
-            for (int64_t t = part; t < tiles; t += 8) {
-                const float2 v = __ldcg(g.part + t * g.row_cap + row);
-                ms_merge(m, s, v.x, v.y);
+            for (int64_t t = part; t < parts; t += 8 * kLceJoin) {
+                float2 v[8];
+#pragma unroll
+                for (int u = 0; u < 8; ++u) {
+                    const int64_t k = t + (int64_t)u * kLceJoin;
+                    v[u] = k < parts ? __ldcg(g.part + k * g.row_cap + row)
+                                     : make_float2(-INFINITY, 0.f);
+                }
+                float top = m;
+#pragma unroll
+                for (int u = 0; u < 8; ++u) top = fmaxf(top, v[u].x);
+                const float use = top == -INFINITY ? 0.f : top;
+                s = m == -INFINITY ? s : s * exp2f(m - use);
+#pragma unroll
+                for (int u = 0; u < 8; ++u)
+                    s += v[u].x == -INFINITY ? v[u].y : v[u].y * exp2f(v[u].x - use);
+                m = top;
             }
         }
         m_s[part][r_in] = m;
         s_s[part][r_in] = s;
         __syncthreads();
-        if (part == 0 && row < count) {
-            for (int k = 1; k < 8; ++k) ms_merge(m, s, m_s[k][r_in], s_s[k][r_in]);
-            const float l = (m + log2f(s)) * 0.6931471805599453f;
-            const int64_t at = g.row_of[row];
-            lse[at] = l;
-            loss[at] = l - g.row_hit[row];
+        // warp w joins row w
+        const int64_t mine = r0 + part;
+        if (mine < count) {
+            float mm = m_s[r_in][part], ss = s_s[r_in][part];
+            float top = mm;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1)
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            const float use = top == -INFINITY ? 0.f : top;
+            ss = mm == -INFINITY ? ss : ss * exp2f(mm - use);
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+            if (r_in == 0) {
+                const float l = (top + log2f(ss)) * 0.6931471805599453f;
+                const int64_t at = g.row_of[mine];
+                lse[at] = l;
+                loss[at] = l - g.row_hit[mine];
+            }
         }
         __syncthreads();
     }

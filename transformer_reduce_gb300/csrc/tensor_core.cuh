@@ -30,8 +30,7 @@ __device__ __forceinline__ void mbar_expect(uint32_t bar, uint32_t bytes) {
 }
 // Arrives on a barrier of any block of the cluster (an address of mapa).
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar)
-                 : "memory");
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 // The address of this block's shared memory `addr` in block `rank` of the cluster.
 __device__ __forceinline__ uint32_t cluster_addr(uint32_t addr, uint32_t rank) {
@@ -51,7 +50,7 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
     uint32_t ok;
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
         "selp.u32 %0, 1, 0, p;\n\t}"
         : "=r"(ok)
         : "r"(bar), "r"(parity)
@@ -159,25 +158,45 @@ __device__ __forceinline__ uint64_t tc_desc(uint32_t addr, uint32_t lead) {
     return (uint64_t)((addr & 0x3ffffu) >> 4) | ((uint64_t)(lead >> 4) << 16) |
            ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
 }
-// 32 columns of the warp's 32 lanes (lane i of warp w: row 32 (w % 4) + i).
-__device__ __forceinline__ void tmem_load32(float (&f)[32], uint32_t addr) {
-    uint32_t r[32];
+// 32 columns of the warp's 32 lanes (lane i of warp w: row 32 (w % 4) + i) into
+// f[at ...], on their way until tmem_wait.
+template <int N>
+__device__ __forceinline__ void tmem_load32(float (&f)[N], int at, uint32_t addr) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
         "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n\t"
-        "tcgen05.wait::ld.sync.aligned;"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-          "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
-          "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
-          "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        :
+          "=f"(f[at + 0]), "=f"(f[at + 1]), "=f"(f[at + 2]), "=f"(f[at + 3]),
+          "=f"(f[at + 4]), "=f"(f[at + 5]), "=f"(f[at + 6]), "=f"(f[at + 7]),
+          "=f"(f[at + 8]), "=f"(f[at + 9]), "=f"(f[at + 10]), "=f"(f[at + 11]),
+          "=f"(f[at + 12]), "=f"(f[at + 13]), "=f"(f[at + 14]), "=f"(f[at + 15]),
+          "=f"(f[at + 16]), "=f"(f[at + 17]), "=f"(f[at + 18]), "=f"(f[at + 19]),
+          "=f"(f[at + 20]), "=f"(f[at + 21]), "=f"(f[at + 22]), "=f"(f[at + 23]),
+          "=f"(f[at + 24]), "=f"(f[at + 25]), "=f"(f[at + 26]), "=f"(f[at + 27]),
+          "=f"(f[at + 28]), "=f"(f[at + 29]), "=f"(f[at + 30]), "=f"(f[at + 31])
         : "r"(addr)
         : "memory");
-#pragma unroll
-    for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(r[i]);
 }
-
+// Waits for the loads into f; what reads it comes after.
+template <int N>
+__device__ __forceinline__ void tmem_wait(float (&f)[N]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int at = 0; at < N; at += 32)
+        asm volatile(""
+                     :
+          "+f"(f[at + 0]), "+f"(f[at + 1]), "+f"(f[at + 2]), "+f"(f[at + 3]),
+          "+f"(f[at + 4]), "+f"(f[at + 5]), "+f"(f[at + 6]), "+f"(f[at + 7]),
+          "+f"(f[at + 8]), "+f"(f[at + 9]), "+f"(f[at + 10]), "+f"(f[at + 11]),
+          "+f"(f[at + 12]), "+f"(f[at + 13]), "+f"(f[at + 14]), "+f"(f[at + 15]),
+          "+f"(f[at + 16]), "+f"(f[at + 17]), "+f"(f[at + 18]), "+f"(f[at + 19]),
+          "+f"(f[at + 20]), "+f"(f[at + 21]), "+f"(f[at + 22]), "+f"(f[at + 23]),
+          "+f"(f[at + 24]), "+f"(f[at + 25]), "+f"(f[at + 26]), "+f"(f[at + 27]),
+          "+f"(f[at + 28]), "+f"(f[at + 29]), "+f"(f[at + 30]), "+f"(f[at + 31])
+                     :
+                     : "memory");
+}
 // The same 32 columns written back.
 __device__ __forceinline__ void tmem_store32(uint32_t addr, const float (&f)[32]) {
     asm volatile(
