@@ -1378,6 +1378,7 @@ ls_status ls_block_norm_fw(void *h, void *y, float *stats, const void *x, const 
         lsr::BlockNorm<T> a = {};
         a.rows = rows;
         a.hidden = hidden;
+        a.gates = gates;
         a.gate_rows = gate ? rows / gates : rows;
         a.residual_scale = residual_scale;
         a.eps = eps;
@@ -1479,6 +1480,7 @@ ls_status ls_block_norm_bw(void *dx, void *dr, float *dgate, float *dgamma_post,
         lsr::BlockNorm<T> a = {};
         a.rows = rows;
         a.hidden = hidden;
+        a.gates = gates;
         a.gate_rows = gate ? rows / gates : rows;
         a.residual_scale = residual_scale;
         a.layer = layer ? 1 : 0;

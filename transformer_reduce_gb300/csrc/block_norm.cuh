@@ -82,56 +82,72 @@ __device__ __forceinline__ uint4 bn_load(const T *row, int c, int hidden, bool s
         f[e] = c + e < hidden ? Traits<T>::load1_cached(row + c + e) : 0.f;
     return Traits<T>::pack(f);
 }
+// The same as pairs, of a vector that every row reads.
 template <typename T, bool AL>
-__device__ __forceinline__ void bn_store(T *row, int c, int hidden, const float (&f)[Traits<T>::kVec]) {
-    constexpr int V = Traits<T>::kVec;
-    if (AL) {
-        st_stream16(row + c, Traits<T>::pack(f));
-    } else {
-#pragma unroll
-        for (int e = 0; e < V; ++e)
-            if (c + e < hidden) Traits<T>::store1(row + c + e, f[e]);
-    }
+__device__ __forceinline__ void bn_pairs(const T *row, int c, int hidden,
+                                         float2 (&f)[Traits<T>::kVec / 2]) {
+    unpack2<T>(bn_load<T, AL>(row, c, hidden, false), f);
 }
 template <typename T, bool AL>
-__device__ __forceinline__ void bn_floats(const T *row, int c, int hidden, float (&f)[Traits<T>::kVec]) {
-    Traits<T>::unpack(bn_load<T, AL>(row, c, hidden, false), f);
+__device__ __forceinline__ void bn_store(T *row, int c, int hidden,
+                                         const float2 (&f)[Traits<T>::kVec / 2]) {
+    constexpr int H2 = Traits<T>::kVec / 2;
+    if (AL) {
+        st_stream16(row + c, pack2<T>(f));
+    } else {
+#pragma unroll
+        for (int e = 0; e < H2; ++e) {
+            if (c + 2 * e < hidden) Traits<T>::store1(row + c + 2 * e, f[e].x);
+            if (c + 2 * e + 1 < hidden) Traits<T>::store1(row + c + 2 * e + 1, f[e].y);
+        }
+    }
 }
 
 // Mean and rstd of a row in registers: the mean first, then the squares of the
 // differences, so that a large mean costs no digits.  RMSNorm has mean 0.
-template <typename T, int TPR, int CPT, bool LAYER, typename Red>
-__device__ __forceinline__ void bn_stats(const float (&v)[CPT][Traits<T>::kVec], int lane, int hidden,
-                                         float eps, Red &red, float &mean, float &rstd) {
-    constexpr int V = Traits<T>::kVec;
+template <typename T, int TPR, int CPT, bool AL, bool LAYER, typename Red>
+__device__ __forceinline__ void bn_stats(const float2 (&v)[CPT][Traits<T>::kVec / 2], int lane,
+                                         int hidden, float eps, Red &red, float &mean,
+                                         float &rstd) {
+    constexpr int V = Traits<T>::kVec, H2 = V / 2;
     const float inv = 1.f / (float)hidden;
     mean = 0.f;
     if constexpr (LAYER) {
-        float s = 0.f;
+        float2 s = f2(0.f);
 #pragma unroll
         for (int k = 0; k < CPT; ++k)
 #pragma unroll
-            for (int e = 0; e < V; ++e) s += v[k][e];  // (columns past the row are 0)
-        mean = red.sum(s) * inv;
+            for (int e = 0; e < H2; ++e) s = add2(s, v[k][e]);  // (columns past the row are 0)
+        mean = red.sum(s.x + s.y) * inv;
     }
-    float q = 0.f;
+    float2 q = f2(0.f);
 #pragma unroll
     for (int k = 0; k < CPT; ++k) {
         const int c = (k * TPR + lane) * V;
+        if (LAYER && c >= hidden) continue;
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-            const float d = v[k][e] - mean;
-            if (!LAYER || c + e < hidden) q = fmaf(d, d, q);
+        for (int e = 0; e < H2; ++e) {
+            float2 d = LAYER ? add2(v[k][e], f2(-mean)) : v[k][e];
+            if (LAYER && !AL) {
+                if (c + 2 * e >= hidden) d.x = 0.f;
+                if (c + 2 * e + 1 >= hidden) d.y = 0.f;
+            }
+            q = fma2(d, d, q);
         }
     }
-    rstd = 1.f / sqrtf(red.sum(q) * inv + eps);
+    rstd = 1.f / sqrtf(red.sum(q.x + q.y) * inv + eps);
 }
 
+// Resident blocks per SM asked of ptxas.
+template <int TPR, int CPT>
+constexpr int bn_fw_min_blocks() { return TPR > 512 ? 1 : (CPT <= 2 ? 768 : 512) / bn_block<TPR>(); }
+
+// The next row is on its way (in registers) while the current one is normed.
 template <typename T, int TPR, int CPT, bool AL, bool LAYER>
-__global__ void __launch_bounds__(bn_block<TPR>())
+__global__ void __launch_bounds__(bn_block<TPR>(), (bn_fw_min_blocks<TPR, CPT>()))
 bn_fw(const BlockNorm<T> a, int64_t per) {
     pdl_begin();
-    constexpr int V = Traits<T>::kVec;
+    constexpr int V = Traits<T>::kVec, H2 = V / 2;
     constexpr int BLOCK = bn_block<TPR>(), G = BLOCK / TPR;
     __shared__ float red_s[4 * BLOCK / 32];
     const int lane = threadIdx.x % TPR, grp = threadIdx.x / TPR;
@@ -141,63 +157,78 @@ bn_fw(const BlockNorm<T> a, int64_t per) {
     const int64_t end = min(beg + per, a.rows);
     int64_t gate_at = a.gate && beg < end ? beg / a.gate_rows : 0;
     int64_t gate_left = a.gate && beg < end ? (gate_at + 1) * a.gate_rows - beg : 0;
-    for (int64_t row = beg; row < end; ++row) {
-        const int64_t at = row * a.hidden;
-        float v[CPT][V], res[CPT][V];
+    uint4 xr[CPT], rr[CPT];
+    auto fetch = [&](int64_t row) {
 #pragma unroll
         for (int k = 0; k < CPT; ++k) {
             const int c = (k * TPR + lane) * V;
-            uint4 xr = make_uint4(0u, 0u, 0u, 0u), rr = xr;
-            if (c < hidden) {
-                xr = bn_load<T, AL>(a.x + at, c, hidden, true);
-                rr = bn_load<T, AL>(a.r + at, c, hidden, true);
+            xr[k] = rr[k] = make_uint4(0u, 0u, 0u, 0u);
+            if (c < hidden && row < end) {
+                xr[k] = bn_load<T, AL>(a.x + row * a.hidden, c, hidden, true);
+                rr[k] = bn_load<T, AL>(a.r + row * a.hidden, c, hidden, true);
             }
-            Traits<T>::unpack(xr, v[k]);
-            Traits<T>::unpack(rr, res[k]);
         }
+    };
+    fetch(beg);
+    for (int64_t row = beg; row < end; ++row) {
+        const int64_t at = row * a.hidden;
+        float2 v[CPT][H2];
+        uint4 res[CPT];
+#pragma unroll
+        for (int k = 0; k < CPT; ++k) {
+            unpack2<T>(xr[k], v[k]);
+            res[k] = rr[k];
+        }
+        fetch(row + 1);
         float mean1 = 0.f, rstd1 = 1.f, mean2 = 0.f, rstd2 = 1.f;
         if (a.gamma_post)
-            bn_stats<T, TPR, CPT, LAYER>(v, lane, hidden, a.eps, red, mean1, rstd1);
+            bn_stats<T, TPR, CPT, AL, LAYER>(v, lane, hidden, a.eps, red, mean1, rstd1);
         const T *gate = a.gate ? a.gate + gate_at * a.hidden : nullptr;
 #pragma unroll
         for (int k = 0; k < CPT; ++k) {
             const int c = (k * TPR + lane) * V;
             if (c >= hidden) continue;
-            float f[V];
+            float2 f[H2];
             if (a.gamma_post) {
-                bn_floats<T, AL>(a.gamma_post, c, hidden, f);
+                bn_pairs<T, AL>(a.gamma_post, c, hidden, f);
 #pragma unroll
-                for (int e = 0; e < V; ++e) v[k][e] = (v[k][e] - mean1) * rstd1 * f[e];
+                for (int e = 0; e < H2; ++e) {
+                    if (LAYER) v[k][e] = add2(v[k][e], f2(-mean1));
+                    v[k][e] = mul2(mul2(v[k][e], f2(rstd1)), f[e]);
+                }
                 if (LAYER && a.beta_post) {
-                    bn_floats<T, AL>(a.beta_post, c, hidden, f);
+                    bn_pairs<T, AL>(a.beta_post, c, hidden, f);
 #pragma unroll
-                    for (int e = 0; e < V; ++e) v[k][e] += f[e];
+                    for (int e = 0; e < H2; ++e) v[k][e] = add2(v[k][e], f[e]);
                 }
             }
             if (gate) {
-                bn_floats<T, AL>(gate, c, hidden, f);
+                bn_pairs<T, AL>(gate, c, hidden, f);
 #pragma unroll
-                for (int e = 0; e < V; ++e) v[k][e] *= f[e];
+                for (int e = 0; e < H2; ++e) v[k][e] = mul2(v[k][e], f[e]);
             }
+            unpack2<T>(res[k], f);
 #pragma unroll
-            for (int e = 0; e < V; ++e)
-                v[k][e] = AL || c + e < hidden ? fmaf(a.residual_scale, res[k][e], v[k][e]) : 0.f;
+            for (int e = 0; e < H2; ++e) v[k][e] = fma2(f2(a.residual_scale), f[e], v[k][e]);
             bn_store<T, AL>(a.h + at, c, hidden, v[k]);
         }
         if (a.gamma_pre) {
-            bn_stats<T, TPR, CPT, LAYER>(v, lane, hidden, a.eps, red, mean2, rstd2);
+            bn_stats<T, TPR, CPT, AL, LAYER>(v, lane, hidden, a.eps, red, mean2, rstd2);
 #pragma unroll
             for (int k = 0; k < CPT; ++k) {
                 const int c = (k * TPR + lane) * V;
                 if (c >= hidden) continue;
-                float f[V];
-                bn_floats<T, AL>(a.gamma_pre, c, hidden, f);
+                float2 f[H2];
+                bn_pairs<T, AL>(a.gamma_pre, c, hidden, f);
 #pragma unroll
-                for (int e = 0; e < V; ++e) v[k][e] = (v[k][e] - mean2) * rstd2 * f[e];
+                for (int e = 0; e < H2; ++e) {
+                    if (LAYER) v[k][e] = add2(v[k][e], f2(-mean2));
+                    v[k][e] = mul2(mul2(v[k][e], f2(rstd2)), f[e]);
+                }
                 if (LAYER && a.beta_pre) {
-                    bn_floats<T, AL>(a.beta_pre, c, hidden, f);
+                    bn_pairs<T, AL>(a.beta_pre, c, hidden, f);
 #pragma unroll
-                    for (int e = 0; e < V; ++e) v[k][e] += f[e];
+                    for (int e = 0; e < H2; ++e) v[k][e] = add2(v[k][e], f[e]);
                 }
                 bn_store<T, AL>(a.y + at, c, hidden, v[k]);
             }
@@ -221,6 +252,7 @@ struct BnCut {
     int64_t parts;    // runs of one gate's rows, or 0: a run holds whole gates' rows
     int64_t workers;
     int64_t blocks;
+    int single;       // no gate or one: its sums follow from the totals of A and B
 };
 
 // ----------------------------------------------------------------------------
@@ -235,14 +267,36 @@ constexpr size_t bn_bw_smem(int vec) {
     // at the end a float per column and worker
     const size_t stage = bn_staged<TPR, CPT, AL>() ? (size_t)2 * 4 * CPT * bn_block<TPR>() * 16 : 0;
     const size_t sums = bn_block<TPR>() == TPR ? 0 : (size_t)bn_block<TPR>() * CPT * vec * 4;
-    return stage > sums ? stage : sums;
+    return stage < sums ? sums : stage;
 }
 
+// FP32 sums of a chunk's columns.
+template <bool AL, int H2>
+__device__ __forceinline__ void bn_sums(float *row, int c, int hidden, const float2 (&v)[H2]) {
+    if (AL) {
+#pragma unroll
+        for (int e = 0; e < H2; e += 2)
+            *reinterpret_cast<float4 *>(row + c + 2 * e) =
+                make_float4(v[e].x, v[e].y, v[e + 1].x, v[e + 1].y);
+    } else {
+#pragma unroll
+        for (int e = 0; e < H2; ++e) {
+            if (c + 2 * e < hidden) row[c + 2 * e] = v[e].x;
+            if (c + 2 * e + 1 < hidden) row[c + 2 * e + 1] = v[e].y;
+        }
+    }
+}
+
+// Threads of an SM that ptxas is asked to leave registers for.
+template <int CPT, bool MULTI>
+constexpr int bn_bw_threads() { return CPT == 1 && !MULTI ? 768 : 512; }
+
 template <typename T, int TPR, int CPT, bool AL, bool LAYER, bool MULTI>
-__global__ void __launch_bounds__(bn_block<TPR>(), bn_block<TPR>() <= 512 ? 512 / bn_block<TPR>() : 1)
+__global__ void __launch_bounds__(bn_block<TPR>(),
+                                  TPR > 512 ? 1 : bn_bw_threads<CPT, MULTI>() / bn_block<TPR>())
 bn_bw(const BlockNorm<T> a, const BnCut cut, float *part, float *gate_part) {
     pdl_begin();
-    constexpr int V = Traits<T>::kVec;
+    constexpr int V = Traits<T>::kVec, H2 = V / 2;
     constexpr int BLOCK = bn_block<TPR>(), G = BLOCK / TPR;
     constexpr bool kStaged = bn_staged<TPR, CPT, AL>();
     extern __shared__ __align__(128) uint4 dsmem[];  // [2][4][CPT][BLOCK], a thread's own slots
@@ -284,112 +338,115 @@ bn_bw(const BlockNorm<T> a, const BnCut cut, float *part, float *gate_part) {
         }
         if (kStaged) cp_async_commit();
     };
-    auto fetch = [&](int which, const T *row, int s, int k, int c, float (&f)[V]) {
+    auto fetch = [&](int which, const T *row, int s, int k, int c, float2 (&f)[H2]) {
         if (kStaged)
-            Traits<T>::unpack(stage[((s * 4 + which) * CPT + k) * BLOCK], f);
+            unpack2<T>(stage[((s * 4 + which) * CPT + k) * BLOCK], f);
         else
-            bn_floats<T, AL>(row, c, hidden, f);
+            bn_pairs<T, AL>(row, c, hidden, f);
     };
-    float g2[CPT][V], b2[CPT][V], sa[CPT][V], sb[CPT][V], gp[CPT][V], bp[CPT][V];
+    float2 g2[CPT][H2], b2[CPT][H2], sa[CPT][H2], sb[CPT][H2], gp[CPT][H2], bp[CPT][H2];
 #pragma unroll
     for (int k = 0; k < CPT; ++k)
 #pragma unroll
-        for (int e = 0; e < V; ++e)
-            g2[k][e] = b2[k][e] = sa[k][e] = sb[k][e] = gp[k][e] = bp[k][e] = 0.f;
+        for (int e = 0; e < H2; ++e)
+            g2[k][e] = b2[k][e] = sa[k][e] = sb[k][e] = gp[k][e] = bp[k][e] = f2(0.f);
 
     issue(beg, 0);
     int turn = 0;
     for (int64_t row = beg; row < end; ++row, turn ^= 1) {
-        issue(row + 1, turn ^ 1);
-        if (kStaged) cp_async_wait<1>();  // this thread's copies of the row have landed
         const int64_t at = row * a.hidden;
         const float mean1 = LAYER ? __ldg(a.stats_in + row) : 0.f;
         const float rstd1 = __ldg(a.stats_in + a.rows + row);
         const float mean2 = LAYER ? __ldg(a.stats_in + 2 * a.rows + row) : 0.f;
         const float rstd2 = __ldg(a.stats_in + 3 * a.rows + row);
-        float up[CPT][V];
-        // the norm before the next block
+        issue(row + 1, turn ^ 1);
+        if (kStaged) cp_async_wait<1>();  // this thread's copies of the row have landed
+        // (v - mean) * rstd in one multiply-add
+        auto hat_of = [&](float2 v, float mean, float rstd) {
+            return LAYER ? mul2(add2(v, f2(-mean)), f2(rstd)) : mul2(v, f2(rstd));
+        };
+        float2 up[CPT][H2], hat[CPT][H2];
+        // the norm before the next block: up holds dy * gamma
         float s1 = 0.f, s2 = 0.f;
         if (pre) {
+            float2 p1 = f2(0.f), p2 = f2(0.f);
 #pragma unroll
             for (int k = 0; k < CPT; ++k) {
                 const int c = (k * TPR + lane) * V;
                 if (c >= hidden) continue;
-                float dy[V], hv[V], gm[V];
+                float2 dy[H2], gm[H2];
                 fetch(0, a.dy + at, turn, k, c, dy);
-                fetch(1, a.h_in + at, turn, k, c, hv);
-                bn_floats<T, AL>(a.gamma_pre, c, hidden, gm);
+                fetch(1, a.h_in + at, turn, k, c, hat[k]);
+                bn_pairs<T, AL>(a.gamma_pre, c, hidden, gm);
 #pragma unroll
-                for (int e = 0; e < V; ++e) {
-                    const float hat = (hv[e] - mean2) * rstd2, g = dy[e] * gm[e];
-                    if (LAYER) s1 += g;
-                    s2 = fmaf(g, hat, s2);
-                    g2[k][e] = fmaf(dy[e], hat, g2[k][e]);
-                    if (LAYER) b2[k][e] += dy[e];
+                for (int e = 0; e < H2; ++e) {
+                    hat[k][e] = hat_of(hat[k][e], mean2, rstd2);
+                    up[k][e] = mul2(dy[e], gm[e]);
+                    if (LAYER) p1 = add2(p1, up[k][e]);
+                    p2 = fma2(up[k][e], hat[k][e], p2);
+                    g2[k][e] = fma2(dy[e], hat[k][e], g2[k][e]);
+                    if (LAYER) b2[k][e] = add2(b2[k][e], dy[e]);
                 }
             }
+            s1 = p1.x + p1.y;
+            s2 = p2.x + p2.y;
             red.sum2(s1, s2);
             s1 *= inv;
             s2 *= inv;
         }
         const T *gate = a.gate ? a.gate + gate_at * a.hidden : nullptr;
-        float t1 = 0.f, t2 = 0.f;
+        float2 q1 = f2(0.f), q2 = f2(0.f);
 #pragma unroll
         for (int k = 0; k < CPT; ++k) {
             const int c = (k * TPR + lane) * V;
             if (c >= hidden) continue;
-            float f[V];
+            float2 f[H2];
             if (a.dh) {
-                fetch(2, a.dh + at, turn, k, c, up[k]);
+                fetch(2, a.dh + at, turn, k, c, f);
             } else {
 #pragma unroll
-                for (int e = 0; e < V; ++e) up[k][e] = 0.f;
+                for (int e = 0; e < H2; ++e) f[e] = f2(0.f);
             }
-            if (pre) {
-                float dy[V], hv[V];
-                fetch(0, a.dy + at, turn, k, c, dy);
-                fetch(1, a.h_in + at, turn, k, c, hv);
-                bn_floats<T, AL>(a.gamma_pre, c, hidden, f);
 #pragma unroll
-                for (int e = 0; e < V; ++e) {
-                    const float hat = (hv[e] - mean2) * rstd2;
-                    up[k][e] = fmaf(rstd2, fmaf(-hat, s2, fmaf(dy[e], f[e], -s1)), up[k][e]);
+            for (int e = 0; e < H2; ++e) {
+                if (pre) {
+                    float2 g = LAYER ? add2(up[k][e], f2(-s1)) : up[k][e];
+                    g = fma2(hat[k][e], f2(-s2), g);
+                    up[k][e] = fma2(f2(rstd2), g, f[e]);
+                } else {
+                    up[k][e] = f[e];
                 }
+                f[e] = mul2(f2(a.residual_scale), up[k][e]);
             }
-            if (!AL) {  // (columns past the row)
-#pragma unroll
-                for (int e = 0; e < V; ++e)
-                    if (c + e >= hidden) up[k][e] = 0.f;
-            }
-#pragma unroll
-            for (int e = 0; e < V; ++e) f[e] = a.residual_scale * up[k][e];
-            float xv[V], gm[V];
             if (need_x) {
-                fetch(3, a.x + at, turn, k, c, xv);
+                fetch(3, a.x + at, turn, k, c, hat[k]);
 #pragma unroll
-                for (int e = 0; e < V; ++e) {
-                    xv[e] = post ? (xv[e] - mean1) * rstd1 : xv[e];
-                    sa[k][e] = fmaf(up[k][e], xv[e], sa[k][e]);
-                    if (LAYER) sb[k][e] += up[k][e];
+                for (int e = 0; e < H2; ++e) {
+                    if (post) hat[k][e] = hat_of(hat[k][e], mean1, rstd1);
+                    sa[k][e] = fma2(up[k][e], hat[k][e], sa[k][e]);
+                    if (LAYER) sb[k][e] = add2(sb[k][e], up[k][e]);
                 }
             }
             bn_store<T, AL>(a.dr + at, c, hidden, f);
             if (gate) {
-                bn_floats<T, AL>(gate, c, hidden, gm);
+                bn_pairs<T, AL>(gate, c, hidden, f);
 #pragma unroll
-                for (int e = 0; e < V; ++e) up[k][e] *= gm[e];
+                for (int e = 0; e < H2; ++e) up[k][e] = mul2(up[k][e], f[e]);
             }
             if (post) {
-                bn_floats<T, AL>(a.gamma_post, c, hidden, gm);
+                bn_pairs<T, AL>(a.gamma_post, c, hidden, f);
 #pragma unroll
-                for (int e = 0; e < V; ++e) {
-                    up[k][e] *= gm[e];
-                    if (LAYER) t1 += up[k][e];
-                    t2 = fmaf(up[k][e], xv[e], t2);
+                for (int e = 0; e < H2; ++e) {
+                    up[k][e] = mul2(up[k][e], f[e]);
+                    if (LAYER) q1 = add2(q1, up[k][e]);
+                    q2 = fma2(up[k][e], hat[k][e], q2);
                 }
             }
         }
+        float t1 = 0.f, t2 = 0.f;
         if (post) {
+            t1 = q1.x + q1.y;
+            t2 = q2.x + q2.y;
             red.sum2(t1, t2);
             t1 *= inv;
             t2 *= inv;
@@ -399,12 +456,10 @@ bn_bw(const BlockNorm<T> a, const BnCut cut, float *part, float *gate_part) {
             const int c = (k * TPR + lane) * V;
             if (c >= hidden) continue;
             if (post) {
-                float xv[V];
-                fetch(3, a.x + at, turn, k, c, xv);
 #pragma unroll
-                for (int e = 0; e < V; ++e) {
-                    const float hat = (xv[e] - mean1) * rstd1;
-                    up[k][e] = rstd1 * fmaf(-hat, t2, up[k][e] - t1);
+                for (int e = 0; e < H2; ++e) {
+                    const float2 g = LAYER ? add2(up[k][e], f2(-t1)) : up[k][e];
+                    up[k][e] = mul2(f2(rstd1), fma2(hat[k][e], f2(-t2), g));
                 }
             }
             bn_store<T, AL>(a.dx + at, c, hidden, up[k]);
@@ -414,19 +469,26 @@ bn_bw(const BlockNorm<T> a, const BnCut cut, float *part, float *gate_part) {
             for (int k = 0; k < CPT; ++k) {
                 const int c = (k * TPR + lane) * V;
                 if (c >= hidden) continue;
-                float gm[V], gam[V], bet[V];
-                bn_floats<T, AL>(gate, c, hidden, gm);
-                if (post) bn_floats<T, AL>(a.gamma_post, c, hidden, gam);
-                if (LAYER && a.beta_post) bn_floats<T, AL>(a.beta_post, c, hidden, bet);
+                float2 f[H2];
+                bn_pairs<T, AL>(gate, c, hidden, f);
 #pragma unroll
-                for (int e = 0; e < V; ++e) {
-                    gp[k][e] = fmaf(gm[e], sa[k][e], gp[k][e]);
-                    if (LAYER) bp[k][e] = fmaf(gm[e], sb[k][e], bp[k][e]);
-                    float d = post ? gam[e] * sa[k][e] : sa[k][e];
-                    if (LAYER && a.beta_post) d = fmaf(bet[e], sb[k][e], d);
-                    if (AL || c + e < hidden) a.dgate[gate_at * a.hidden + c + e] = d;
-                    sa[k][e] = sb[k][e] = 0.f;
+                for (int e = 0; e < H2; ++e) {
+                    gp[k][e] = fma2(f[e], sa[k][e], gp[k][e]);
+                    if (LAYER) bp[k][e] = fma2(f[e], sb[k][e], bp[k][e]);
                 }
+                if (post) {
+                    bn_pairs<T, AL>(a.gamma_post, c, hidden, f);
+#pragma unroll
+                    for (int e = 0; e < H2; ++e) sa[k][e] = mul2(f[e], sa[k][e]);
+                }
+                if (LAYER && a.beta_post) {
+                    bn_pairs<T, AL>(a.beta_post, c, hidden, f);
+#pragma unroll
+                    for (int e = 0; e < H2; ++e) sa[k][e] = fma2(f[e], sb[k][e], sa[k][e]);
+                }
+                bn_sums<AL>(a.dgate + gate_at * a.hidden, c, hidden, sa[k]);
+#pragma unroll
+                for (int e = 0; e < H2; ++e) sa[k][e] = sb[k][e] = f2(0.f);
             }
             ++gate_at;
             gate_left = a.gate_rows;
@@ -434,29 +496,38 @@ bn_bw(const BlockNorm<T> a, const BnCut cut, float *part, float *gate_part) {
     }
     if (kStaged) cp_async_wait<0>();  // (only empty groups are left)
     if (!MULTI) {
-        // one gate (or none): its part of the gate's sums, and gate A, gate B
-        const T *gate = a.gate && worker < cut.workers ? a.gate + gate_at * a.hidden : nullptr;
+        // rows under one gate: its part of the gate's sums, and gate A, gate B
+        const bool own = a.gate && !cut.single && worker < cut.workers;
 #pragma unroll
         for (int k = 0; k < CPT; ++k) {
             const int c = (k * TPR + lane) * V;
             if (c >= hidden) continue;
-            float gm[V], gam[V], bet[V];
-            if (gate) bn_floats<T, AL>(gate, c, hidden, gm);
-            if (gate && post) bn_floats<T, AL>(a.gamma_post, c, hidden, gam);
-            if (LAYER && a.beta_post) bn_floats<T, AL>(a.beta_post, c, hidden, bet);
 #pragma unroll
-            for (int e = 0; e < V; ++e) {
-                gp[k][e] = gate ? gm[e] * sa[k][e] : sa[k][e];
-                bp[k][e] = gate ? gm[e] * sb[k][e] : sb[k][e];
-                if (gate && (AL || c + e < hidden)) {
-                    float d = post ? gam[e] * sa[k][e] : sa[k][e];
-                    if (LAYER && post && a.beta_post) d = fmaf(bet[e], sb[k][e], d);
-                    if (cut.parts == 1)
-                        a.dgate[gate_at * a.hidden + c + e] = d;
-                    else
-                        gate_part[worker * a.hidden + c + e] = d;
-                }
+            for (int e = 0; e < H2; ++e) {
+                gp[k][e] = sa[k][e];
+                bp[k][e] = sb[k][e];
             }
+            if (!own) continue;
+            float2 f[H2];
+            bn_pairs<T, AL>(a.gate + gate_at * a.hidden, c, hidden, f);
+#pragma unroll
+            for (int e = 0; e < H2; ++e) {
+                gp[k][e] = mul2(f[e], gp[k][e]);
+                if (LAYER) bp[k][e] = mul2(f[e], bp[k][e]);
+            }
+            if (post) {
+                bn_pairs<T, AL>(a.gamma_post, c, hidden, f);
+#pragma unroll
+                for (int e = 0; e < H2; ++e) sa[k][e] = mul2(f[e], sa[k][e]);
+            }
+            if (LAYER && a.beta_post) {
+                bn_pairs<T, AL>(a.beta_post, c, hidden, f);
+#pragma unroll
+                for (int e = 0; e < H2; ++e) sa[k][e] = fma2(f[e], sb[k][e], sa[k][e]);
+            }
+            bn_sums<AL>(cut.parts == 1 ? a.dgate + gate_at * a.hidden
+                                       : gate_part + worker * a.hidden,
+                        c, hidden, sa[k]);
         }
     }
     // the block's sums: dgamma_pre, dgamma_post, dbeta_pre, dbeta_post
@@ -469,13 +540,13 @@ bn_bw(const BlockNorm<T> a, const BnCut cut, float *part, float *gate_part) {
 #pragma unroll
         for (int k = 0; k < CPT; ++k) {
             const int c = (k * TPR + lane) * V;
+            const float2(&v)[H2] = s == 0 ? g2[k] : s == 1 ? gp[k] : s == 2 ? b2[k] : bp[k];
+            if (G > 1) {
 #pragma unroll
-            for (int e = 0; e < V; ++e) {
-                const float v = s == 0 ? g2[k][e] : s == 1 ? gp[k][e] : s == 2 ? b2[k][e] : bp[k][e];
-                if (G > 1)
-                    sums[grp * TPR * CPT * V + c + e] = v;
-                else if (c + e < hidden)
-                    out[c + e] = v;
+                for (int e = 0; e < H2; ++e)
+                    *reinterpret_cast<float2 *>(&sums[grp * TPR * CPT * V + c + 2 * e]) = v[e];
+            } else if (c < hidden) {
+                bn_sums<AL>(out, c, hidden, v);
             }
         }
         if (G > 1) {
@@ -489,47 +560,102 @@ bn_bw(const BlockNorm<T> a, const BnCut cut, float *part, float *gate_part) {
     }
 }
 
-// Column sums of the blocks' (or workers') parts: 32 columns of one vector per
-// block, every eighth part per slice, then the slices in order.
+// Column sums of the blocks' (or workers') parts: C neighbouring columns per
+// lane of one vector, every 16th part per warp, then the warps in order.
+// single: vector 1 (and 3) are A (and B), and the gate's gradient follows from
+// both.
+constexpr int kBnFoldWarps = 16;
+template <typename T>
 struct BnFold {
     const float *part, *gate_part;
     float *out[4];  // dgamma_pre, dgamma_post, dbeta_pre, dbeta_post (NULL: not wanted)
     float *dgate;
+    const T *gate, *gamma_post, *beta_post;  // single
     int64_t hidden, blocks, parts;
-    int sums;
+    int sums, single;
 };
-static __global__ void __launch_bounds__(256) bn_fold(const BnFold f) {
-    pdl_begin();
-    __shared__ float s[8][32];
-    const int col = threadIdx.x & 31, slice = threadIdx.x >> 5;
-    const int64_t c = (int64_t)blockIdx.x * 32 + col;
-    const int64_t v = blockIdx.y;
-    const float *src;
-    float *dst;
-    int64_t n, step;
-    if (v < f.sums) {
-        dst = f.out[v];
-        src = f.part + v * f.hidden;
-        n = f.blocks;
-        step = f.sums * f.hidden;
-    } else {
-        dst = f.dgate + (v - f.sums) * f.hidden;
-        src = f.gate_part + (v - f.sums) * f.parts * f.hidden;
-        n = f.parts;
-        step = f.hidden;
+template <int C>
+struct BnColumns {
+    float v[C];
+    __device__ __forceinline__ void load(const float *p) {
+        if constexpr (C == 4) {
+            const float4 f = __ldcg(reinterpret_cast<const float4 *>(p));
+            v[0] = f.x;
+            v[1] = f.y;
+            v[2] = f.z;
+            v[3] = f.w;
+        } else {
+            v[0] = __ldcg(p);
+        }
     }
-    if (!dst) return;  // (the whole block)
-    float t = 0.f;
-    if (c < f.hidden) {
-#pragma unroll 8
-        for (int64_t k = slice; k < n; k += 8) t += __ldcg(src + k * step + c);
+};
+// The first warp gets the sums over n parts.
+template <int C>
+__device__ __forceinline__ BnColumns<C> bn_fold_columns(const float *src, int64_t n, int64_t step,
+                                                        bool there, float (*s)[32 * C]) {
+    const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5;
+    BnColumns<C> t = {};
+    if (there) {
+        for (int64_t k0 = slice; k0 < n; k0 += 8 * kBnFoldWarps) {
+            BnColumns<C> f[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                const int64_t k = k0 + (int64_t)u * kBnFoldWarps;
+                f[u] = BnColumns<C>{};
+                if (k < n) f[u].load(src + k * step);
+            }
+#pragma unroll
+            for (int i = 0; i < C; ++i)
+                t.v[i] += ((f[0].v[i] + f[1].v[i]) + (f[2].v[i] + f[3].v[i])) +
+                          ((f[4].v[i] + f[5].v[i]) + (f[6].v[i] + f[7].v[i]));
+        }
     }
-    s[slice][col] = t;
+    __syncthreads();  // the last sums' slices have been read
+#pragma unroll
+    for (int i = 0; i < C; ++i) s[slice][lane * C + i] = t.v[i];
     __syncthreads();
-    if (slice == 0 && c < f.hidden) {
-        for (int k = 1; k < 8; ++k) t += s[k][col];
-        dst[c] = t;
+    if (slice == 0)
+        for (int k = 1; k < kBnFoldWarps; ++k)
+#pragma unroll
+            for (int i = 0; i < C; ++i) t.v[i] += s[k][lane * C + i];
+    return t;
+}
+template <typename T, int C>
+__global__ void __launch_bounds__(32 * kBnFoldWarps) bn_fold(const BnFold<T> f) {
+    pdl_begin();
+    __shared__ float s[kBnFoldWarps][32 * C];
+    const int64_t c = ((int64_t)blockIdx.x * 32 + (threadIdx.x & 31)) * C;
+    const int64_t v = blockIdx.y;
+    const bool there = c < f.hidden, writes = there && threadIdx.x < 32;
+    const int64_t step = f.sums * f.hidden;
+    if (v >= f.sums) {  // a gate's parts
+        const int64_t k = v - f.sums;
+        const BnColumns<C> t = bn_fold_columns<C>(f.gate_part + k * f.parts * f.hidden + c, f.parts,
+                                                  f.hidden, there, s);
+        if (writes)
+            for (int i = 0; i < C; ++i) f.dgate[k * f.hidden + c + i] = t.v[i];
+        return;
     }
+    const bool gate = f.single && f.gate && v == 1;
+    const bool scaled = f.single && f.gate && (v & 1);
+    float *out = f.out[v];
+    if (!out && !gate) return;  // (the whole block)
+    BnColumns<C> t = bn_fold_columns<C>(f.part + v * f.hidden + c, f.blocks, step, there, s);
+    if (writes && out)
+        for (int i = 0; i < C; ++i)
+            out[c + i] = scaled ? t.v[i] * Traits<T>::load1_cached(f.gate + c + i) : t.v[i];
+    if (!gate) return;
+    if (writes && f.gamma_post)
+        for (int i = 0; i < C; ++i) t.v[i] *= Traits<T>::load1_cached(f.gamma_post + c + i);
+    if (f.beta_post) {
+        const BnColumns<C> b =
+            bn_fold_columns<C>(f.part + 3 * f.hidden + c, f.blocks, step, there, s);
+        if (writes)
+            for (int i = 0; i < C; ++i)
+                t.v[i] = fmaf(b.v[i], Traits<T>::load1_cached(f.beta_post + c + i), t.v[i]);
+    }
+    if (writes)
+        for (int i = 0; i < C; ++i) f.dgate[c + i] = t.v[i];
 }
 
 }  // namespace lsr

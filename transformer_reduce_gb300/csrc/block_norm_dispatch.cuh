@@ -15,7 +15,7 @@ namespace lsr {
     X(32, 1) X(32, 2) X(32, 4) X(64, 4) X(128, 4) X(256, 4) X(512, 4) X(1024, 4) X(64, 1) \
     X(128, 1) X(256, 1) X(512, 1) X(1024, 1)
 #define LSR_BN_BW_BUCKETS(X) \
-    X(32, 1) X(32, 2) X(64, 2) X(128, 2) X(256, 2) X(512, 2) X(1024, 2) X(1024, 4)
+    X(32, 1) X(64, 1) X(128, 1) X(256, 1) X(32, 2) X(64, 2) X(128, 2) X(256, 2) X(512, 2) X(1024, 2) X(1024, 4)
 
 // Rows up to which the forward gives every chunk a thread of its own.
 constexpr int64_t kBnFewRows = 608;  // four per SM
@@ -78,47 +78,56 @@ struct BnPlan {
     BnCut cut;
 };
 template <typename T>
-BnPlan bn_plan(int64_t rows, int64_t hidden, int64_t gates) {
+BnPlan bn_plan(int64_t rows, int64_t hidden, int64_t gates, bool layer) {
     BnPlan p = {};
-    pick_bn_bucket(ceil_div(hidden, Traits<T>::kVec), 2, &p.tpr, &p.cpt);
+    const int64_t chunks = ceil_div(hidden, Traits<T>::kVec);
+    pick_bn_bucket(chunks, layer && chunks <= 256 ? 1 : 2, &p.tpr, &p.cpt);
     const int block = p.tpr < 256 ? 256 : p.tpr;
     p.groups = block / p.tpr;
     if (rows <= 0) return p;
-    const int64_t most = kBnSms * (block <= 512 ? 512 / block : 1) * p.groups;
-    const int64_t per = ceil_div(rows, most), count = gates < 1 ? 1 : gates;
+    auto workers = [&](bool multi) {
+        return kBnSms * (block > 512 ? 1 : (p.cpt == 1 && !multi ? 768 : 512) / block) * p.groups;
+    };
+    const int64_t count = gates < 1 ? 1 : gates;
     const int64_t share = rows / count;  // rows of a gate
-    if (gates > 1 && share <= per) {     // whole gates' rows
+    const int64_t per = ceil_div(rows, workers(true));
+    if (gates > 1 && share <= per) {  // whole gates' rows
         p.cut.per = ceil_div(per, share) * share;
         p.cut.parts = 0;
         p.cut.workers = ceil_div(rows, p.cut.per);
     } else {
-        int64_t parts = most / count;
+        int64_t parts = workers(false) / count;
         parts = parts < 1 ? 1 : parts;
         p.cut.per = ceil_div(share, parts);
         p.cut.parts = ceil_div(share, p.cut.per);
         p.cut.workers = count * p.cut.parts;
     }
     p.cut.blocks = ceil_div(p.cut.workers, p.groups);
+    p.cut.single = gates <= 1;
     return p;
 }
 
 template <typename T>
 size_t block_norm_workspace(int64_t rows, int64_t hidden, int64_t gates, bool layer) {
-    const BnPlan p = bn_plan<T>(rows, hidden, gates);
-    const int64_t gate_parts = gates > 0 && p.cut.parts > 1 ? p.cut.workers : 0;
+    const BnPlan p = bn_plan<T>(rows, hidden, gates, layer);
+    const int64_t gate_parts = gates > 1 && p.cut.parts > 1 ? p.cut.workers : 0;
     return (size_t)(p.cut.blocks * (layer ? 4 : 2) + gate_parts) * hidden * sizeof(float);
 }
 
 template <typename T>
 cudaError_t launch_block_norm_bw(const BlockNorm<T> &a, float *part, cudaStream_t st) {
-    const int64_t gates = a.gate ? a.rows / (a.gate_rows < 1 ? 1 : a.gate_rows) : 0;
-    const BnPlan p = bn_plan<T>(a.rows, a.hidden, gates);
+    const int64_t gates = a.gate ? a.gates : 0;
+    const BnPlan p = bn_plan<T>(a.rows, a.hidden, gates, a.layer != 0);
     const int sums = a.layer ? 4 : 2;
+    if (a.rows == 0 && gates > 0) {
+        const cudaError_t z = cudaMemsetAsync(a.dgate, 0, (size_t)(gates * a.hidden) * 4, st);
+        if (z != cudaSuccess) return z;
+    }
     float *gate_part = part + p.cut.blocks * sums * a.hidden;
     cudaError_t e = cudaSuccess;
     if (a.rows > 0) {
         const bool al = bn_aligned<T>(a.hidden, {a.x, a.dy, a.dh, a.h_in, a.gate, a.gamma_post,
-                                                 a.beta_post, a.gamma_pre, a.dx, a.dr});
+                                                 a.beta_post, a.gamma_pre, a.dx, a.dr, a.dgate});
         const bool multi = p.cut.parts == 0;
         const int tpr = p.tpr, cpt = p.cpt;
         auto go = [&](auto kernel, int block, size_t smem) {
@@ -145,7 +154,7 @@ cudaError_t launch_block_norm_bw(const BlockNorm<T> &a, float *part, cudaStream_
 #undef F
         if (e != cudaSuccess) return e;
     }
-    BnFold f = {};
+    BnFold<T> f = {};
     f.part = part;
     f.gate_part = gate_part;
     f.out[0] = a.dgamma_pre;
@@ -157,9 +166,19 @@ cudaError_t launch_block_norm_bw(const BlockNorm<T> &a, float *part, cudaStream_
     f.blocks = p.cut.blocks;
     f.parts = p.cut.parts;
     f.sums = sums;
-    const int64_t vectors = sums + (p.cut.parts > 1 ? gates : 0);
-    return launch_pdl(bn_fold, dim3((unsigned)ceil_div(a.hidden, 32), (unsigned)vectors), dim3(256),
-                      0, st, f);
+    f.single = p.cut.single;
+    f.gate = a.gate;
+    f.gamma_post = a.gamma_post;
+    f.beta_post = a.beta_post;
+    const int64_t vectors = sums + (gates > 1 && p.cut.parts > 1 ? gates : 0);
+    const bool wide = a.hidden % 4 == 0 && reinterpret_cast<uintptr_t>(a.dgate) % 16 == 0 &&
+                      reinterpret_cast<uintptr_t>(a.dgamma_pre) % 16 == 0 &&
+                      reinterpret_cast<uintptr_t>(a.dgamma_post) % 16 == 0 &&
+                      reinterpret_cast<uintptr_t>(a.dbeta_pre) % 16 == 0 &&
+                      reinterpret_cast<uintptr_t>(a.dbeta_post) % 16 == 0;
+    return launch_pdl(wide ? bn_fold<T, 4> : bn_fold<T, 1>,
+                      dim3((unsigned)ceil_div(a.hidden, wide ? 128 : 32), (unsigned)vectors),
+                      dim3(32 * kBnFoldWarps), 0, st, f);
 }
 
 #define LSR_BN_FW_INSTANTIATE(T) \

@@ -172,7 +172,7 @@ cudaError_t launch_diff_bw(DiffRows<T> dx1, DiffRows<T> dx2, float *dlam, const 
 // Norms after and before a block with its gate and residual scale.
 template <typename T>
 struct BlockNorm {
-    int64_t rows, hidden, gate_rows;  // gate_rows: rows that share a gate
+    int64_t rows, hidden, gates, gate_rows;  // gate_rows: rows that share a gate
     float residual_scale, eps;
     int layer;  // LayerNorm, else RMSNorm
     const T *x, *r, *gate, *gamma_post, *beta_post, *gamma_pre, *beta_pre;
