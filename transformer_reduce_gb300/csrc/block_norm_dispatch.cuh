@@ -15,7 +15,7 @@ namespace lsr {
     X(32, 1) X(32, 2) X(32, 4) X(64, 4) X(128, 4) X(256, 4) X(512, 4) X(1024, 4) X(64, 1) \
     X(128, 1) X(256, 1) X(512, 1) X(1024, 1)
 #define LSR_BN_BW_BUCKETS(X) \
-    X(32, 1) X(64, 1) X(128, 1) X(256, 1) X(32, 2) X(64, 2) X(128, 2) X(256, 2) X(512, 2) X(1024, 2) X(1024, 4)
+    X(32, 1) X(32, 2) X(64, 2) X(128, 2) X(256, 2) X(512, 2) X(1024, 2) X(1024, 4)
 
 // Rows up to which the forward gives every chunk a thread of its own.
 constexpr int64_t kBnFewRows = 608;  // four per SM
@@ -78,25 +78,23 @@ struct BnPlan {
     BnCut cut;
 };
 template <typename T>
-BnPlan bn_plan(int64_t rows, int64_t hidden, int64_t gates, bool layer) {
+BnPlan bn_plan(int64_t rows, int64_t hidden, int64_t gates) {
     BnPlan p = {};
     const int64_t chunks = ceil_div(hidden, Traits<T>::kVec);
-    pick_bn_bucket(chunks, layer && chunks <= 256 ? 1 : 2, &p.tpr, &p.cpt);
+    pick_bn_bucket(chunks, 2, &p.tpr, &p.cpt);
     const int block = p.tpr < 256 ? 256 : p.tpr;
     p.groups = block / p.tpr;
     if (rows <= 0) return p;
-    auto workers = [&](bool multi) {
-        return kBnSms * (block > 512 ? 1 : (p.cpt == 1 && !multi ? 768 : 512) / block) * p.groups;
-    };
+    const int64_t most = kBnSms * (block <= 512 ? 512 / block : 1) * p.groups;
     const int64_t count = gates < 1 ? 1 : gates;
     const int64_t share = rows / count;  // rows of a gate
-    const int64_t per = ceil_div(rows, workers(true));
+    const int64_t per = ceil_div(rows, most);
     if (gates > 1 && share <= per) {  // whole gates' rows
         p.cut.per = ceil_div(per, share) * share;
         p.cut.parts = 0;
         p.cut.workers = ceil_div(rows, p.cut.per);
     } else {
-        int64_t parts = workers(false) / count;
+        int64_t parts = most / count;
         parts = parts < 1 ? 1 : parts;
         p.cut.per = ceil_div(share, parts);
         p.cut.parts = ceil_div(share, p.cut.per);
@@ -109,7 +107,7 @@ BnPlan bn_plan(int64_t rows, int64_t hidden, int64_t gates, bool layer) {
 
 template <typename T>
 size_t block_norm_workspace(int64_t rows, int64_t hidden, int64_t gates, bool layer) {
-    const BnPlan p = bn_plan<T>(rows, hidden, gates, layer);
+    const BnPlan p = bn_plan<T>(rows, hidden, gates);
     const int64_t gate_parts = gates > 1 && p.cut.parts > 1 ? p.cut.workers : 0;
     return (size_t)(p.cut.blocks * (layer ? 4 : 2) + gate_parts) * hidden * sizeof(float);
 }
@@ -117,7 +115,7 @@ size_t block_norm_workspace(int64_t rows, int64_t hidden, int64_t gates, bool la
 template <typename T>
 cudaError_t launch_block_norm_bw(const BlockNorm<T> &a, float *part, cudaStream_t st) {
     const int64_t gates = a.gate ? a.gates : 0;
-    const BnPlan p = bn_plan<T>(a.rows, a.hidden, gates, a.layer != 0);
+    const BnPlan p = bn_plan<T>(a.rows, a.hidden, gates);
     const int sums = a.layer ? 4 : 2;
     if (a.rows == 0 && gates > 0) {
         const cudaError_t z = cudaMemsetAsync(a.dgate, 0, (size_t)(gates * a.hidden) * 4, st);
@@ -129,25 +127,35 @@ cudaError_t launch_block_norm_bw(const BlockNorm<T> &a, float *part, cudaStream_
         const bool al = bn_aligned<T>(a.hidden, {a.x, a.dy, a.dh, a.h_in, a.gate, a.gamma_post,
                                                  a.beta_post, a.gamma_pre, a.dx, a.dr, a.dgate});
         const bool multi = p.cut.parts == 0;
+        const int form = !a.gamma_pre || !a.dh           ? kBnAny
+                         : a.gamma_post                  ? (a.gate ? kBnGate : kBnPost)
+                         : a.gate                        ? kBnAny
+                                                         : kBnPlain;
         const int tpr = p.tpr, cpt = p.cpt;
         auto go = [&](auto kernel, int block, size_t smem) {
             return launch_pdl(kernel, dim3((unsigned)p.cut.blocks), dim3(block), smem, st, a, p.cut,
                               part, gate_part);
         };
         e = cudaErrorInvalidValue;  // (the buckets cover every size)
-#define F(TPR_, CPT_, AL_, L_, M_)                                                          \
-    (e = relpos_allow_smem<bn_bw<T, TPR_, CPT_, AL_, L_, M_>>(                              \
+#define F(TPR_, CPT_, AL_, L_, M_, FORM_)                                                   \
+    (e = relpos_allow_smem<bn_bw<T, TPR_, CPT_, AL_, L_, M_, FORM_>>(                       \
          bn_bw_smem<TPR_, CPT_, AL_>(Traits<T>::kVec)),                                     \
-     e == cudaSuccess ? go(bn_bw<T, TPR_, CPT_, AL_, L_, M_>, bn_block<TPR_>(),             \
+     e == cudaSuccess ? go(bn_bw<T, TPR_, CPT_, AL_, L_, M_, FORM_>, bn_block<TPR_>(),      \
                            bn_bw_smem<TPR_, CPT_, AL_>(Traits<T>::kVec))                    \
                       : e)
-#define M(TPR_, CPT_, AL_, L_) \
-    (multi ? F(TPR_, CPT_, AL_, L_, true) : F(TPR_, CPT_, AL_, L_, false))
-#define X(TPR_, CPT_)                                                               \
-    if constexpr (bn_reached<T, TPR_, CPT_>())                                      \
-        if (tpr == TPR_ && cpt == CPT_)                                             \
-        e = a.layer ? (al ? M(TPR_, CPT_, true, true) : M(TPR_, CPT_, false, true)) \
-                    : (al ? M(TPR_, CPT_, true, false) : M(TPR_, CPT_, false, false));
+#define M(TPR_, CPT_, L_)                                                              \
+    (!al ? (multi ? F(TPR_, CPT_, false, L_, true, kBnAny)                             \
+                  : F(TPR_, CPT_, false, L_, false, kBnAny))                           \
+     : multi ? (form == kBnGate ? F(TPR_, CPT_, true, L_, true, kBnGate)               \
+                                : F(TPR_, CPT_, true, L_, true, kBnAny))               \
+     : form == kBnGate  ? F(TPR_, CPT_, true, L_, false, kBnGate)                      \
+     : form == kBnPost  ? F(TPR_, CPT_, true, L_, false, kBnPost)                      \
+     : form == kBnPlain ? F(TPR_, CPT_, true, L_, false, kBnPlain)                     \
+                        : F(TPR_, CPT_, true, L_, false, kBnAny))
+#define X(TPR_, CPT_)                                          \
+    if constexpr (bn_reached<T, TPR_, CPT_>())                 \
+        if (tpr == TPR_ && cpt == CPT_)                        \
+            e = a.layer ? M(TPR_, CPT_, true) : M(TPR_, CPT_, false);
         LSR_BN_BW_BUCKETS(X)
 #undef X
 #undef M
