@@ -1195,6 +1195,7 @@ static lsr::DiffShape diff_shape(int64_t B, int64_t H, int64_t Tq, int64_t Tk, i
                                  int causal, float scale) {
     lsr::DiffShape p = {};
     p.rows = B * H * Tq;
+    p.B = B;
     p.H = H;
     p.Tq = Tq;
     p.Tk = Tk;

@@ -14,8 +14,8 @@ namespace lsr {
     X(4, 1) X(4, 2) X(4, 4) X(8, 3) X(8, 4) X(16, 3) X(16, 4) X(32, 3) X(32, 4) X(64, 3) \
     X(64, 4) X(128, 3) X(128, 4) X(256, 3) X(256, 4) X(512, 3) X(512, 4)                 \
     X(32, 1) X(64, 1) X(128, 1) X(256, 1) X(512, 1)
-// (the backward holds three tensors: 128 registers and 130 to 350 bytes of
-// spills at three and four chunks)
+// (the backward holds three tensors; four chunks spill and took 135 us where two
+// take 120)
 #define LSR_DIFF_BW_BUCKETS(X)                                                            \
     X(4, 1) X(4, 2) X(8, 2) X(16, 2) X(32, 2) X(64, 2) X(128, 2) X(256, 2) X(512, 2)      \
     X(512, 4) X(32, 1) X(64, 1) X(128, 1) X(256, 1) X(512, 1)
@@ -24,25 +24,24 @@ namespace lsr {
 // (a call of so few rows does not fill the GPU with a block per eight rows).
 constexpr int64_t kDiffFewRows = 1216;  // eight per SM
 
-// Bucket of the register-resident kernels, at most `most` chunks per thread;
-// false: the row is too long.
+// Bucket of the register-resident kernels, at most `most` chunks per thread but
+// for the longest rows; false: the row is too long (or a head passes 32 bits).
 inline bool pick_diff_bucket(const DiffShape &p, int V, bool al, int most, int *tpr, int *cpt) {
-    if (p.Tk > (int64_t)512 * 4 * V) return false;
+    if (p.Tk > (int64_t)512 * 4 * V || p.Tq > INT32_MAX / p.Tk) return false;
     const int64_t chunks = al ? p.Tk / V : (p.Tk + 2 * V - 2) / V;
     if (p.rows <= kDiffFewRows && chunks > 16 && chunks <= 512) {
         *tpr = next_pow2(chunks);
         *cpt = 1;
         return true;
     }
-    const bool few = most == 2;
-    if (chunks > 512 * most) most = 4;
-    if (!pick_bucket_dense(chunks, most, 512, tpr, cpt)) return false;
+    const int longest = chunks > 512 * most ? 4 : most;
+    if (!pick_bucket_dense(chunks, longest, 512, tpr, cpt)) return false;
     if (*tpr < 4) {
         const int c = (int)ceil_div(*tpr * *cpt, 4);
         *tpr = 4;
         *cpt = c;
     }
-    if (*cpt == 3 && (*tpr == 4 || few)) *cpt = 4;  // (the instantiated ones)
+    if (*cpt == 3 && (*tpr == 4 || most == 2)) *cpt = 4;  // (the instantiated ones)
     return true;
 }
 
@@ -57,16 +56,17 @@ bool diff_same_phase(const DiffRows<P> &x, int phase, const DiffShape &p) {
 }
 
 template <auto K, int TPR, int CPT, bool AL, typename... Args>
-cudaError_t launch_diff_rows(int tensors, int mask_vec, DiffShape p, cudaStream_t st, Args... args) {
+cudaError_t launch_diff_rows(int tensors, int resident, int mask_vec, DiffShape p, cudaStream_t st, Args... args) {
     const size_t smem = diff_smem<TPR, CPT, AL>(tensors);
     const cudaError_t e = relpos_allow_smem<K>(smem);
     if (e != cudaSuccess) return e;
     const int G = diff_block<TPR>() / TPR;
     const int64_t blocks =
-        (int64_t)device_sm_count() * relpos_resident(diff_min_blocks<TPR, CPT>(), smem);
+        (int64_t)device_sm_count() * relpos_resident(resident, smem);
     p.per = ceil_div(ceil_div(p.rows, blocks), G) * G;
-    return launch_pdl(K, dim3((unsigned)ceil_div(p.rows, p.per)), dim3(diff_block<TPR>()), smem,
-                      st, args..., p, mask_vec);
+    const unsigned grid = (unsigned)ceil_div(p.rows, p.per);
+    if (p.causal && p.Tq > 1) p.per = 0;
+    return launch_pdl(K, dim3(grid), dim3(diff_block<TPR>()), smem, st, args..., p, mask_vec);
 }
 
 template <typename T>
@@ -78,9 +78,9 @@ cudaError_t launch_diff_fw(T *out, float4 *stats, DiffRows<const T> x1, DiffRows
     int tpr = 0, cpt = 0;
     const int mask_vec = relpos_phase<T>(mask) == 0;
     if (pick_diff_bucket(p, V, al, 4, &tpr, &cpt)) {
-#define F(TPR_, CPT_, AL_, M_)                                                              \
-    launch_diff_rows<diff_fw_vec<T, TPR_, CPT_, AL_, M_>, TPR_, CPT_, AL_>(2, mask_vec, p, st, out, stats, \
-                                                                           x1, x2, lam, mask)
+#define F(TPR_, CPT_, AL_, M_)                                                             \
+    launch_diff_rows<diff_fw_vec<T, TPR_, CPT_, AL_, M_>, TPR_, CPT_, AL_>(                 \
+        2, diff_fw_min_blocks<TPR_, CPT_>(), mask_vec, p, st, out, stats, x1, x2, lam, mask)
 #define X(TPR_, CPT_)                                                               \
     if (tpr == TPR_ && cpt == CPT_)                                                 \
         return mask ? (al ? F(TPR_, CPT_, true, true) : F(TPR_, CPT_, false, true)) \
@@ -111,7 +111,8 @@ cudaError_t launch_diff_bw_rows(DiffRows<T> dx1, DiffRows<T> dx2, float *row_dot
         pick_diff_bucket(p, V, al, 2, &tpr, &cpt)) {
 #define F(TPR_, CPT_, AL_, M_)                                                                 \
     launch_diff_rows<diff_bw_vec<T, TPR_, CPT_, AL_, M_>, TPR_, CPT_, AL_>(                     \
-        3, mask_vec, p, st, dx1, dx2, row_dot, dout, x1, x2, lam, stats, mask)
+        3, diff_bw_min_blocks<TPR_, CPT_>(), mask_vec, p, st, dx1, dx2, row_dot, dout, x1, x2, \
+        lam, stats, mask)
 #define X(TPR_, CPT_)                                                               \
     if (tpr == TPR_ && cpt == CPT_)                                                 \
         return mask ? (al ? F(TPR_, CPT_, true, true) : F(TPR_, CPT_, false, true)) \

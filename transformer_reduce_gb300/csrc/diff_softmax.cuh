@@ -37,7 +37,7 @@ constexpr float kDiffNear = 64.f;
 template <int TPR>
 constexpr int diff_block() { return TPR < 256 ? 256 : TPR; }
 
-// Position of a row group, advanced by G rows.
+// Position of a row, for kernels that take rows in any order.
 struct DiffCursor {
     int b, h, i;
     __device__ __forceinline__ DiffCursor(const DiffShape &p, int64_t row) {
@@ -46,15 +46,49 @@ struct DiffCursor {
         b = (int)(bh / p.H);
         h = (int)(bh - (int64_t)b * p.H);
     }
-    // G = gq * Tq + gr
-    __device__ __forceinline__ void advance(const DiffShape &p, int gq, int gr) {
-        i += gr;
-        h += gq;
+};
+
+// The rows of a block: from beg on, G at a time, `step` further each turn.  A run
+// of its own (p.per rows), or, where rows differ in length (causal), turns that
+// lie a whole grid apart, so that no block gets the long rows of a head alone
+// ([8,6,777,777] fp16 backward: 96 us in runs).
+struct DiffBlock {
+    int64_t beg, end;
+    int step;
+    __device__ __forceinline__ DiffBlock(const DiffShape &p, int G) {
+        beg = blockIdx.x * (p.per ? p.per : (int64_t)G);
+        end = p.per ? min(beg + p.per, p.rows) : p.rows;
+        step = p.per ? G : G * (int)gridDim.x;
+    }
+};
+
+// Position of a row group, advanced by a block's step without division.  (The
+// launcher keeps a head's elements below 2^31.)
+struct DiffWalk {
+    int b, h, i;
+    int gb, gh, gi;  // step = (gb * H + gh) * Tq + gi
+    int64_t row;
+    __device__ __forceinline__ DiffWalk(const DiffShape &p, int64_t first, int step) {
+        const DiffCursor c(p, first);
+        b = c.b;
+        h = c.h;
+        i = c.i;
+        row = first;
+        gh = step / (int)p.Tq;
+        gi = step - gh * (int)p.Tq;
+        gb = gh / (int)p.H;
+        gh -= gb * (int)p.H;
+    }
+    __device__ __forceinline__ void advance(const DiffShape &p, int step) {
+        row += step;
+        i += gi;
+        h += gh;
+        b += gb;
         if (i >= (int)p.Tq) {
             i -= (int)p.Tq;
             ++h;
         }
-        while (h >= (int)p.H) {
+        if (h >= (int)p.H) {
             h -= (int)p.H;
             ++b;
         }
@@ -102,12 +136,22 @@ __device__ __forceinline__ void diff_group_sync(int grp) {
 
 // What a row group needs of one row.
 struct DiffRow {
-    int64_t out;  // element offset of the written row
-    int q;        // the query's key position
+    int b, h, i;
     int s;        // elements from a 16-byte address to the written row's start
     int lo, hi;   // window of visible keys; empty for a row that is not there
-    int b;        // batch entry whose mask is added element by element, or -1
-    int h;
+    bool general; // the mask is added element by element
+    // element offset of the row in a tensor
+    template <typename P>
+    __device__ __forceinline__ int64_t at(const DiffRows<P> &x, const DiffShape &p) const {
+        return (int64_t)b * x.batch + (int64_t)h * x.head + i * (int)p.Tk;
+    }
+    __device__ __forceinline__ int64_t dense(const DiffShape &p) const {
+        return ((int64_t)(b * p.H + h) * p.Tq + i) * p.Tk;
+    }
+    // its place among the rows of its head (the fold reads a head's in one piece)
+    __device__ __forceinline__ int64_t by_head(const DiffShape &p) const {
+        return ((int64_t)h * p.B + b) * p.Tq + i;
+    }
 };
 
 // Stages the chunks of one read row that hold a visible key: chunk c is the
@@ -118,10 +162,16 @@ __device__ __forceinline__ int diff_stage(uint4 *slots, const T *base, int64_t e
                                           int s, int lo, int hi, int lane) {
     constexpr int V = Traits<T>::kVec;
     if constexpr (AL) {
+        const T *at = base + off + lane * V;
+        const uint32_t to = smem_addr(slots + lane);
 #pragma unroll
         for (int k = 0; k < CPT; ++k) {
             const int j0 = (k * TPR + lane) * V;
-            if (j0 < hi && j0 + V > lo) cp_async16(&slots[k * TPR + lane], base + off + j0);
+            if (j0 < hi && j0 + V > lo)
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                                 to + k * TPR * 16),
+                             "l"(at + k * TPR * V)
+                             : "memory");
         }
         return 0;
     } else {
@@ -187,28 +237,27 @@ __device__ __forceinline__ bool diff_find_windows(int2 *wtab, const T *mask, con
     return true;
 }
 
-template <int V>
-__device__ __forceinline__ DiffRow diff_row(const DiffShape &p, const DiffCursor &cur, int64_t row,
-                                            bool valid, bool masked, const int2 *wtab, int b0,
-                                            int phase, bool al) {
+template <int V, bool AL, bool MASKED>
+__device__ __forceinline__ DiffRow diff_row(const DiffShape &p, const DiffWalk &cur,
+                                            bool valid, const int2 *wtab, int b0, int phase) {
     DiffRow w;
-    w.out = row * p.Tk;
-    w.q = cur.i + (int)p.qoff;
-    w.s = al ? 0 : (int)((w.out + phase) & (V - 1));
+    w.b = cur.b;
+    w.h = cur.h;
+    w.i = cur.i;
+    w.s = AL ? 0 : (int)((w.dense(p) + phase) & (V - 1));
     w.lo = 0;
     w.hi = valid ? (int)p.Tk : 0;
-    w.b = -1;
-    w.h = cur.h;
-    if (masked && valid) {
+    w.general = false;
+    if (MASKED && valid) {
         const int2 win = wtab ? wtab[cur.b - b0] : make_int2(-1, 0);
         if (win.x < 0) {
-            w.b = cur.b;
+            w.general = true;
         } else {
             w.lo = win.x;
             w.hi = win.y;
         }
     }
-    if (p.causal) w.hi = min(w.hi, w.q + 1);
+    if (p.causal) w.hi = min(w.hi, cur.i + (int)p.qoff + 1);
     if (w.hi <= w.lo) {  // no chunk, not even one that begins before the row, meets it
         w.lo = 0;
         w.hi = -2 * V;
@@ -224,9 +273,16 @@ constexpr size_t diff_smem(int tensors) {
     return (size_t)kDiffStages * tensors * (diff_block<TPR>() / TPR) * diff_slots<TPR, CPT, AL>() *
            16;
 }
+// Resident blocks per SM asked of ptxas (of the backward's two chunks, 128
+// registers: at 80 they spill 24 to 210 bytes, 135 against 120 us on
+// [32,8,512,512] bf16).
 template <int TPR, int CPT>
-constexpr int diff_min_blocks() {
+constexpr int diff_fw_min_blocks() {
     return TPR > 256 ? 1 : (CPT <= 2 ? 3 : 2);
+}
+template <int TPR, int CPT>
+constexpr int diff_bw_min_blocks() {
+    return TPR > 256 ? 1 : (CPT <= 1 ? 3 : 2);
 }
 
 // Values of one chunk of a map: z where a mask is added, else the scores; -inf
@@ -278,7 +334,7 @@ __device__ __forceinline__ DiffExp diff_exponent(float2 (&v)[CPT][H2], float m, 
 }
 
 template <typename T, int TPR, int CPT, bool AL, bool MASKED>
-__global__ void __launch_bounds__(diff_block<TPR>(), (diff_min_blocks<TPR, CPT>()))
+__global__ void __launch_bounds__(diff_block<TPR>(), (diff_fw_min_blocks<TPR, CPT>()))
 diff_fw_vec(T *out, float4 *stats, const DiffRows<const T> x1, const DiffRows<const T> x2,
             const float *lam, const T *mask_or_null, const DiffShape p, int mask_vec) {
     pdl_begin();
@@ -294,41 +350,39 @@ diff_fw_vec(T *out, float4 *stats, const DiffRows<const T> x1, const DiffRows<co
     const int grp = threadIdx.x / TPR;
     const int sub = TPR < 32 ? grp % (32 / (TPR < 32 ? TPR : 32)) : 0;  // group of the warp
     const int Tk = (int)p.Tk;
-    const int gq = G / (int)p.Tq, gr = G - gq * (int)p.Tq;
     const int phase = (int)(reinterpret_cast<uintptr_t>(out) / sizeof(T) % V);
-    const int64_t beg = (int64_t)blockIdx.x * p.per;
-    const int64_t end = min(beg + p.per, p.rows);
+    const DiffBlock blk(p, G);
+    const int64_t beg = blk.beg, end = blk.end;
     const bool windows = diff_find_windows<T, true, BLOCK>(wtab, mask, p, beg, end);
     const int b0 = (int)(beg / (p.H * p.Tq));
     if (windows) __syncthreads();
 
-    int64_t r_issue = beg + grp;
-    DiffCursor ci(p, r_issue);
-    DiffRow next;  // the row issued last, and its maps' shifts
+    DiffWalk walk(p, beg + grp, blk.step);
+    DiffRow next;  // the row issued last, its maps' shifts and its head's weight
     int next_d1 = 0, next_d2 = 0;
+    float next_lam = 0.f;
     auto slots = [&](int s, int map) { return dsmem + ((s * 2 + map) * G + grp) * SLOTS; };
     auto issue = [&](int s) {
         if (!AL && TPR <= 32) __syncwarp();  // (wider groups: the last row's reductions)
-        next = diff_row<V>(p, ci, r_issue, r_issue < end, mask != nullptr,
-                           windows ? wtab : nullptr, b0, phase, AL);
-        if (r_issue < end) {
-            next_d1 = diff_stage<T, TPR, CPT, AL>(slots(s, 0), x1.p, x1.extent,
-                                                  x1.at(ci.b, ci.h, ci.i, p.Tk), next.s, next.lo,
-                                                  next.hi, lane);
-            next_d2 = diff_stage<T, TPR, CPT, AL>(slots(s, 1), x2.p, x2.extent,
-                                                  x2.at(ci.b, ci.h, ci.i, p.Tk), next.s, next.lo,
-                                                  next.hi, lane);
-            r_issue += G;
-            ci.advance(p, gq, gr);
+        next = diff_row<V, AL, MASKED>(p, walk, walk.row < end, windows ? wtab : nullptr, b0,
+                                       phase);
+        if (walk.row < end) {
+            next_d1 = diff_stage<T, TPR, CPT, AL>(slots(s, 0), x1.p, x1.extent, next.at(x1, p),
+                                                  next.s, next.lo, next.hi, lane);
+            next_d2 = diff_stage<T, TPR, CPT, AL>(slots(s, 1), x2.p, x2.extent, next.at(x2, p),
+                                                  next.s, next.lo, next.hi, lane);
+            next_lam = __ldg(lam + next.h * p.lam_step);
         }
+        walk.advance(p, blk.step);
         cp_async_commit();
     };
     issue(0);
     int turn = 0;  // stage of the current row
     // groups that share a warp take the same number of turns (shuffles)
-    for (int64_t rw = beg + grp - sub; rw < end; rw += G, turn ^= 1) {
+    for (int64_t rw = beg + grp - sub; rw < end; rw += blk.step, turn ^= 1) {
         const DiffRow w = next;
         const int d1 = next_d1, d2 = next_d2;
+        const float lam_h = next_lam;
         const bool valid = rw + sub < end;
         issue(turn ^ 1);
         cp_async_wait<1>();  // this thread's copies of the row have landed
@@ -337,8 +391,8 @@ diff_fw_vec(T *out, float4 *stats, const DiffRows<const T> x1, const DiffRows<co
         // keys of the warp's part of chunk k: [k * TPR * V + wj, ... + WK)
         const int wj = (TPR > 32 ? (lane & ~31) * V : 0) - w.s;
         constexpr int WK = (TPR < 32 ? TPR : 32) * V;
-        const T *mrow = w.b >= 0 ? mask + (int64_t)w.b * Tk : nullptr;
-        const float mul = w.b >= 0 ? 1.f : p.scale;
+        const T *mrow = MASKED && w.general ? mask + (int64_t)w.b * Tk : nullptr;
+        const float mul = MASKED && w.general ? 1.f : p.scale;
         const uint4 *s1 = slots(turn, 0) + lane, *s2 = slots(turn, 1) + lane;
         float2 v1[CPT][H2], v2[CPT][H2];
         float m1 = -INFINITY, m2 = -INFINITY;
@@ -382,11 +436,11 @@ diff_fw_vec(T *out, float4 *stats, const DiffRows<const T> x1, const DiffRows<co
         diff_reduce2<TPR, BLOCK, OpSum>(sum1, sum2, red_sum, grp);
         const float i1 = sum1 == 0.f ? 0.f : fast_rcp(sum1);
         const float i2 = sum2 == 0.f ? 0.f : fast_rcp(sum2);
-        const float li2 = -__ldg(lam + w.h * p.lam_step) * i2;
+        const float li2 = -lam_h * i2;
         if (stats && valid && lane == 0)
             stats[rw + sub] = make_float4(m1 == -INFINITY ? 0.f : m1, i1,
                                           m2 == -INFINITY ? 0.f : m2, i2);
-        T *orow = out + w.out;
+        T *orow = out + w.dense(p) + (AL ? lane * V : 0);
 #pragma unroll
         for (int k = 0; k < CPT; ++k) {
             const int j0 = k * TPR * V + j_lane;
@@ -406,7 +460,8 @@ diff_fw_vec(T *out, float4 *stats, const DiffRows<const T> x1, const DiffRows<co
                 }
                 o = pack2<T>(y);
             }
-            if (valid && j0 < Tk) relpos_store<T, AL>(orow, j0, Tk, o);
+            if (valid && j0 < Tk)
+                relpos_store<T, AL>(orow, AL ? k * TPR * V : j0, Tk, o);
         }
     }
     cp_async_wait<0>();  // (only empty groups are left)
@@ -417,7 +472,7 @@ diff_fw_vec(T *out, float4 *stats, const DiffRows<const T> x1, const DiffRows<co
 // is one pass for the two sums and one that writes.
 // ----------------------------------------------------------------------------
 template <typename T, int TPR, int CPT, bool AL, bool MASKED>
-__global__ void __launch_bounds__(diff_block<TPR>(), (diff_min_blocks<TPR, CPT>()))
+__global__ void __launch_bounds__(diff_block<TPR>(), (diff_bw_min_blocks<TPR, CPT>()))
 diff_bw_vec(const DiffRows<T> dx1, const DiffRows<T> dx2, float *row_dot, const T *dout,
             const DiffRows<const T> x1, const DiffRows<const T> x2, const float *lam,
             const float4 *stats, const T *mask_or_null, const DiffShape p, int mask_vec) {
@@ -434,50 +489,41 @@ diff_bw_vec(const DiffRows<T> dx1, const DiffRows<T> dx2, float *row_dot, const 
     const int grp = threadIdx.x / TPR;
     const int sub = TPR < 32 ? grp % (32 / (TPR < 32 ? TPR : 32)) : 0;  // group of the warp
     const int Tk = (int)p.Tk;
-    const int gq = G / (int)p.Tq, gr = G - gq * (int)p.Tq;
     const int phase = (int)(reinterpret_cast<uintptr_t>(dout) / sizeof(T) % V);
-    const int64_t beg = (int64_t)blockIdx.x * p.per;
-    const int64_t end = min(beg + p.per, p.rows);
+    const DiffBlock blk(p, G);
+    const int64_t beg = blk.beg, end = blk.end;
     const bool windows = diff_find_windows<T, true, BLOCK>(wtab, mask, p, beg, end);
     const int b0 = (int)(beg / (p.H * p.Tq));
     if (windows) __syncthreads();
 
-    int64_t r_issue = beg + grp;
-    DiffCursor ci(p, r_issue);
+    DiffWalk walk(p, beg + grp, blk.step);
     DiffRow next;
     int next_d1 = 0, next_d2 = 0;
-    int64_t next_o1 = 0, next_o2 = 0;
     float4 next_st = make_float4(0.f, 0.f, 0.f, 0.f);
     float next_lam = 0.f;
     auto slots = [&](int s, int t) { return dsmem + ((s * 3 + t) * G + grp) * SLOTS; };
     auto issue = [&](int s) {
         if (!AL && TPR <= 32) __syncwarp();  // (wider groups: the last row's reduction)
-        next = diff_row<V>(p, ci, r_issue, r_issue < end, mask != nullptr,
-                           windows ? wtab : nullptr, b0, phase, AL);
-        if (r_issue < end) {
-            next_d1 = diff_stage<T, TPR, CPT, AL>(slots(s, 0), x1.p, x1.extent,
-                                                  x1.at(ci.b, ci.h, ci.i, p.Tk), next.s, next.lo,
-                                                  next.hi, lane);
-            next_d2 = diff_stage<T, TPR, CPT, AL>(slots(s, 1), x2.p, x2.extent,
-                                                  x2.at(ci.b, ci.h, ci.i, p.Tk), next.s, next.lo,
-                                                  next.hi, lane);
-            diff_stage<T, TPR, CPT, AL>(slots(s, 2), dout, p.rows * p.Tk, next.out, next.s,
+        next = diff_row<V, AL, MASKED>(p, walk, walk.row < end, windows ? wtab : nullptr, b0,
+                                       phase);
+        if (walk.row < end) {
+            next_d1 = diff_stage<T, TPR, CPT, AL>(slots(s, 0), x1.p, x1.extent, next.at(x1, p),
+                                                  next.s, next.lo, next.hi, lane);
+            next_d2 = diff_stage<T, TPR, CPT, AL>(slots(s, 1), x2.p, x2.extent, next.at(x2, p),
+                                                  next.s, next.lo, next.hi, lane);
+            diff_stage<T, TPR, CPT, AL>(slots(s, 2), dout, p.rows * p.Tk, next.dense(p), next.s,
                                         next.lo, next.hi, lane);  // shift 0
-            next_o1 = dx1.at(ci.b, ci.h, ci.i, p.Tk);
-            next_o2 = dx2.at(ci.b, ci.h, ci.i, p.Tk);
-            next_st = __ldg(stats + r_issue);
+            next_st = __ldg(stats + walk.row);
             next_lam = __ldg(lam + next.h * p.lam_step);
-            r_issue += G;
-            ci.advance(p, gq, gr);
         }
+        walk.advance(p, blk.step);
         cp_async_commit();
     };
     issue(0);
     int turn = 0;  // stage of the current row
-    for (int64_t rw = beg + grp - sub; rw < end; rw += G, turn ^= 1) {
+    for (int64_t rw = beg + grp - sub; rw < end; rw += blk.step, turn ^= 1) {
         const DiffRow w = next;
         const int d1 = next_d1, d2 = next_d2;
-        const int64_t o1 = next_o1, o2 = next_o2;
         const float4 st = next_st;
         const float lam_h = next_lam;
         const bool valid = rw + sub < end;
@@ -485,11 +531,15 @@ diff_bw_vec(const DiffRows<T> dx1, const DiffRows<T> dx2, float *row_dot, const 
         cp_async_wait<1>();  // this thread's copies of the row have landed
         if (!AL) diff_group_sync<TPR, BLOCK>(grp);
         const int lo = w.lo, hi = w.hi, j_lane = lane * V - w.s;
-        const T *mrow = w.b >= 0 ? mask + (int64_t)w.b * Tk : nullptr;
-        const float mul = w.b >= 0 ? 1.f : p.scale;
+        const T *mrow = MASKED && w.general ? mask + (int64_t)w.b * Tk : nullptr;
+        const float mul = MASKED && w.general ? 1.f : p.scale;
         const uint4 *s1 = slots(turn, 0) + lane, *s2 = slots(turn, 1) + lane;
         const uint4 *sg = slots(turn, 2) + lane;
-        float2 v1[CPT][H2], v2[CPT][H2], g[CPT][H2];
+        float2 v1[CPT][H2], v2[CPT][H2];
+        uint4 g4[CPT];  // dout as it is stored, 0 at invisible keys
+        const bool near = fabsf(st.x) < kDiffNear && fabsf(st.z) < kDiffNear;
+        const float c = mul * kLog2e;
+        float2 t1 = f2(0.f), t2 = f2(0.f);
 #pragma unroll
         for (int k = 0; k < CPT; ++k) {
             const int j0 = k * TPR * V + j_lane;
@@ -498,65 +548,72 @@ diff_bw_vec(const DiffRows<T> dx1, const DiffRows<T> dx2, float *row_dot, const 
                                lo, hi, p.scale);
             diff_values<T, AL>(v2[k], diff_chunk<T, AL>(s2 + k * TPR, d2), mrow, mask_vec != 0, j0,
                                lo, hi, p.scale);
-            uint4 raw = sg[k * TPR];
-            if (mrow || j0 < lo || j0 + V > hi) {  // what dout holds at invisible keys
-                const uint32_t bits = relpos_bits<T>(mrow, j0, lo, hi);
-                keep_elements<T>(raw, bits);
-            }
-            unpack2<T>(raw, g[k]);
-        }
-        const DiffExp x1e = diff_exponent(v1, st.x, mul), x2e = diff_exponent(v2, st.z, mul);
-        float2 t1 = f2(0.f), t2 = f2(0.f);
+            g4[k] = sg[k * TPR];
+            if (mrow || j0 < lo || j0 + V > hi)  // what dout holds at invisible keys
+                keep_elements<T>(g4[k], relpos_bits<T>(mrow, j0, lo, hi));
+            float2 g[H2];
+            unpack2<T>(g4[k], g);
+            float2 c1 = f2(c), c2 = f2(c), n1 = f2(-st.x * kLog2e), n2 = f2(-st.z * kLog2e);
+            if (!near) {  // as the forward: the difference first where the largest z is far from 0
+                const bool far1 = !(fabsf(st.x) < kDiffNear), far2 = !(fabsf(st.z) < kDiffNear);
 #pragma unroll
-        for (int k = 0; k < CPT; ++k) {
-            const int j0 = k * TPR * V + j_lane;
-            if (!(j0 < hi && j0 + V > lo)) continue;
+                for (int h2 = 0; h2 < H2; ++h2) {
+                    if (far1) v1[k][h2] = fma2(v1[k][h2], f2(mul), f2(-st.x));
+                    if (far2) v2[k][h2] = fma2(v2[k][h2], f2(mul), f2(-st.z));
+                }
+                if (far1) c1 = f2(kLog2e), n1 = f2(0.f);
+                if (far2) c2 = f2(kLog2e), n2 = f2(0.f);
+            }
 #pragma unroll
             for (int h2 = 0; h2 < H2; ++h2) {
-                float2 a = fma2(v1[k][h2], f2(x1e.c), f2(x1e.n));
-                float2 b = fma2(v2[k][h2], f2(x2e.c), f2(x2e.n));
+                float2 a = fma2(v1[k][h2], c1, n1);
+                float2 b = fma2(v2[k][h2], c2, n2);
                 a.x = fast_exp2(a.x);
                 a.y = fast_exp2(a.y);
                 b.x = fast_exp2(b.x);
                 b.y = fast_exp2(b.y);
                 v1[k][h2] = a;
                 v2[k][h2] = b;
-                t1 = fma2(a, g[k][h2], t1);
-                t2 = fma2(b, g[k][h2], t2);
+                t1 = fma2(a, g[h2], t1);
+                t2 = fma2(b, g[h2], t2);
             }
         }
         float dot1 = t1.x + t1.y, dot2 = t2.x + t2.y;
         diff_reduce2<TPR, BLOCK, OpSum>(dot1, dot2, red[turn], grp);
         dot1 *= st.y;
         dot2 *= st.w;
-        if (valid && lane == 0) row_dot[rw + sub] = dot2;
-        const float f1 = p.scale * st.y, f2_ = -p.scale * lam_h * st.w;
-        const bool odd = !(fabsf(dot1) + fabsf(dot2) + fabsf(f1) + fabsf(f2_) < INFINITY);
+        if (valid && lane == 0) row_dot[w.by_head(p)] = dot2;
+        const float w1 = p.scale * st.y, w2 = -p.scale * lam_h * st.w;
+        const float2 n1 = f2(-w1 * dot1), n2 = f2(-w2 * dot2);
+        const bool odd = !(fabsf(n1.x) + fabsf(n2.x) + fabsf(w1) + fabsf(w2) < INFINITY);
+        T *r1 = dx1.p + w.at(dx1, p) + (AL ? lane * V : 0);
+        T *r2 = dx2.p + w.at(dx2, p) + (AL ? lane * V : 0);
 #pragma unroll
         for (int k = 0; k < CPT; ++k) {
             const int j0 = k * TPR * V + j_lane;
             uint4 a4 = make_uint4(0u, 0u, 0u, 0u), b4 = a4;
             if (j0 < hi && j0 + V > lo) {
-                float2 a[H2], b[H2];
+                float2 g[H2];
+                unpack2<T>(g4[k], g);
 #pragma unroll
-                for (int h2 = 0; h2 < H2; ++h2) {
-                    a[h2] = mul2(mul2(v1[k][h2], f2(f1)), add2(g[k][h2], f2(-dot1)));
-                    b[h2] = mul2(mul2(v2[k][h2], f2(f2_)), add2(g[k][h2], f2(-dot2)));
+                for (int h2 = 0; h2 < H2; ++h2) {  // p (g - D), scaled
+                    v1[k][h2] = mul2(v1[k][h2], fma2(g[h2], f2(w1), n1));
+                    v2[k][h2] = mul2(v2[k][h2], fma2(g[h2], f2(w2), n2));
                 }
                 if (odd) {  // 0 * NaN: invisible keys stay 0
                     const uint32_t bits = relpos_bits<T>(mrow, j0, lo, hi);
 #pragma unroll
                     for (int h2 = 0; h2 < H2; ++h2) {
-                        if (!((bits >> (2 * h2)) & 1u)) a[h2].x = b[h2].x = 0.f;
-                        if (!((bits >> (2 * h2 + 1)) & 1u)) a[h2].y = b[h2].y = 0.f;
+                        if (!((bits >> (2 * h2)) & 1u)) v1[k][h2].x = v2[k][h2].x = 0.f;
+                        if (!((bits >> (2 * h2 + 1)) & 1u)) v1[k][h2].y = v2[k][h2].y = 0.f;
                     }
                 }
-                a4 = pack2<T>(a);
-                b4 = pack2<T>(b);
+                a4 = pack2<T>(v1[k]);
+                b4 = pack2<T>(v2[k]);
             }
             if (valid && j0 < Tk) {
-                relpos_store<T, AL>(dx1.p + o1, j0, Tk, a4);
-                relpos_store<T, AL>(dx2.p + o2, j0, Tk, b4);
+                relpos_store<T, AL>(r1, AL ? k * TPR * V : j0, Tk, a4);
+                relpos_store<T, AL>(r2, AL ? k * TPR * V : j0, Tk, b4);
             }
         }
     }
@@ -661,7 +718,7 @@ diff_bw_loop(const DiffRows<T> dx1, const DiffRows<T> dx2, float *row_dot, const
         group_sum2<TPR>(a, b, red);
         a *= st.y;
         b *= st.w;
-        if (lane == 0) row_dot[row] = b;
+        if (lane == 0) row_dot[((int64_t)c.h * p.B + c.b) * p.Tq + c.i] = b;
         const float f1 = p.scale * st.y;
         const float f2_ = -p.scale * __ldg(lam + c.h * p.lam_step) * st.w;
         T *o1 = dx1.p + dx1.at(c.b, c.h, c.i, p.Tk), *o2 = dx2.p + dx2.at(c.b, c.h, c.i, p.Tk);
@@ -678,27 +735,33 @@ diff_bw_loop(const DiffRows<T> dx1, const DiffRows<T> dx2, float *row_dot, const
     }
 }
 
-// dlam[h] = -sum over b, i of the row's D_2; one block per head (or one for
-// all): each thread its own rows in order, then the threads in order.
+// dlam[h] = -sum over b, i of the row's D_2, which lie head by head; one block
+// per head (or one for all): each thread its own rows in order, then the threads
+// in order.
 constexpr int kDiffFoldThreads = 1024;
 static __global__ void __launch_bounds__(kDiffFoldThreads)
 diff_fold(float *dlam, const float *row_dot, const DiffShape p) {
     pdl_begin();
     __shared__ double part[32];
-    const bool all = p.lam_step == 0;
-    const int64_t per = all ? p.rows : p.rows / p.H;  // rows of the sum
+    const int64_t n = p.lam_step == 0 ? p.rows : p.rows / p.H;  // rows of the sum
+    const float *src = row_dot + blockIdx.x * n;
+    const bool wide = n % 4 == 0;  // (the workspace is 16-byte aligned)
+    const int64_t steps = wide ? n / 4 : n;
     double v = 0.0;
-    for (int64_t k0 = threadIdx.x; k0 < per; k0 += 8 * kDiffFoldThreads) {
+    for (int64_t k0 = threadIdx.x; k0 < steps; k0 += 8 * kDiffFoldThreads) {
         float f[8];
 #pragma unroll
         for (int u = 0; u < 8; ++u) {
             const int64_t k = k0 + (int64_t)u * kDiffFoldThreads;
-            int64_t row = k;
-            if (!all && k < per) {
-                const int64_t b = k / p.Tq;
-                row = (b * p.H + blockIdx.x) * p.Tq + (k - b * p.Tq);
+            f[u] = 0.f;
+            if (k < steps) {
+                if (wide) {
+                    const float4 q = __ldcg(reinterpret_cast<const float4 *>(src) + k);
+                    f[u] = (q.x + q.y) + (q.z + q.w);
+                } else {
+                    f[u] = __ldcg(src + k);
+                }
             }
-            f[u] = k < per ? __ldcg(row_dot + row) : 0.f;
         }
         v += (double)((f[0] + f[1]) + (f[2] + f[3])) + (double)((f[4] + f[5]) + (f[6] + f[7]));
     }

@@ -144,7 +144,7 @@ cudaError_t launch_grad_clip(float *norm, void *const *out, const void *const *g
 struct DiffShape {
     int64_t rows;  // B * H * Tq, in the order (b, h, i)
     int64_t per;   // rows of a block's run
-    int64_t H, Tq, Tk, qoff;
+    int64_t B, H, Tq, Tk, qoff;
     int lam_step;  // 1: a weight per head, 0: one for all
     int causal;
     float scale;
