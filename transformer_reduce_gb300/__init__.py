@@ -888,15 +888,16 @@ def softmax_fw_diff(scores1, scores2, lam, mask=None, causal: bool = False, scal
     heads; ``lam`` fp32 [H] or [1] (one weight for all heads), ``mask`` additive
     [B,Tk], future keys masked when ``causal``.  Returns (out, stats), stats fp32
     [B,H,Tq,4] saved for the backward.  ``out`` may be a dense ``scores1``."""
-    f32 = _torch().float32
+    torch = _torch()
+    f32 = torch.float32
     shape, dtype, strides = _diff(scores1, scores2, lam, mask)
     B, H, Tq, Tk = shape
     if out is None:
-        out = scores1.new_empty(shape)
+        out = torch.empty(shape, dtype=dtype, device=scores1.device)
     else:
         _want("out", out, shape, dtype)
     if stats is None:
-        stats = scores1.new_empty((B, H, Tq, 4), dtype=f32)
+        stats = torch.empty((B, H, Tq, 4), dtype=f32, device=scores1.device)
     else:
         _want("stats", stats, (B, H, Tq, 4), f32)
     dev = _one_device((scores1, scores2), (lam, mask, out, stats))
@@ -919,7 +920,8 @@ def softmax_bw_diff(dout, scores1, scores2, lam, stats, mask=None, causal: bool 
     summation order.  What ``dout`` and the scores hold at invisible keys never
     matters.  ``dscores1`` may be ``scores1`` and ``dscores2`` ``scores2``, and
     both may be slices of one tensor's heads."""
-    f32 = _torch().float32
+    torch = _torch()
+    f32, device = torch.float32, dout.device
     shape, dtype, strides = _diff(scores1, scores2, lam, mask)
     B, H, Tq, Tk = shape
     if dout.shape != shape or dout.dtype != dtype:
@@ -928,21 +930,21 @@ def softmax_bw_diff(dout, scores1, scores2, lam, stats, mask=None, causal: bool 
         _want("stats", stats, (B, H, Tq, 4), f32)
     if workspace is None:
         n = max(ls_softmax_bw_diff_workspace_size(B, H, Tq), 16) // 4
-        workspace = dout.new_empty(n, dtype=f32)
+        workspace = torch.empty(n, dtype=f32, device=device)
     else:
         _workspace("workspace", workspace)
         n = workspace.numel()
     dense = (H * Tq * Tk, Tq * Tk)
     if dscores1 is None:
-        dscores1, d1 = dout.new_empty(shape), dense
+        dscores1, d1 = torch.empty(shape, dtype=dtype, device=device), dense
     else:
         d1 = _map_strides("dscores1", dscores1, shape, dtype)
     if dscores2 is None:
-        dscores2, d2 = dout.new_empty(shape), dense
+        dscores2, d2 = torch.empty(shape, dtype=dtype, device=device), dense
     else:
         d2 = _map_strides("dscores2", dscores2, shape, dtype)
     if dlam is None:
-        dlam = lam.new_empty(lam.shape)
+        dlam = torch.empty_like(lam)
     else:
         _want("dlam", dlam, lam.shape, f32)
     dev = _one_device((scores1, scores2, dscores1, dscores2),
@@ -997,25 +999,26 @@ def block_norm_fw(x, residual, gamma_pre=None, beta_pre=None, gamma_post=None, b
     hidden]: equal runs of rows share one each.  Returns (h, y, stats), stats
     fp32 [4, rows] saved for the backward.  ``h`` and ``y`` may be x or the
     residual stream (in place)."""
-    f32 = _torch().float32
+    torch = _torch()
+    f32 = torch.float32
     rows, hidden, gates, layer = _block(x, kind, gate, gamma_pre=gamma_pre, beta_pre=beta_pre,
                                         gamma_post=gamma_post, beta_post=beta_post)
     shape, dtype = x.shape, x.dtype
     if residual.shape != shape or residual.dtype != dtype:
         _want("residual", residual, shape, dtype)
     if h is None:
-        h = x.new_empty(shape)
+        h = torch.empty_like(x)
     else:
         _want("h", h, shape, dtype)
     if gamma_pre is None:
         if y is not None:
             raise ValueError("y is not computed without gamma_pre")
     elif y is None:
-        y = x.new_empty(shape)
+        y = torch.empty_like(x)
     else:
         _want("y", y, shape, dtype)
     if stats is None:
-        stats = x.new_empty((4, rows), dtype=f32)
+        stats = torch.empty((4, rows), dtype=f32, device=x.device)
     else:
         _want("stats", stats, (4, rows), f32)
     dev = _same_device(x, residual, gamma_pre, beta_pre, gamma_post, beta_post, gate, h, y, stats)
@@ -1043,7 +1046,8 @@ def block_norm_bw(dy, dh, x, h, stats, gamma_pre=None, gamma_post=None, beta_pos
     of the parameters fp32 in a fixed summation order and None where there is no
     such parameter (the betas' are given for "layer").  ``dx`` may be dy, dh, x
     or h, ``dr`` dy, dh or h (in place)."""
-    f32 = _torch().float32
+    torch = _torch()
+    f32, device = torch.float32, x.device
     rows, hidden, gates, layer = _block(x, kind, gate, gamma_pre=gamma_pre, gamma_post=gamma_post,
                                         beta_post=beta_post)
     shape, dtype = x.shape, x.dtype
@@ -1062,17 +1066,19 @@ def block_norm_bw(dy, dh, x, h, stats, gamma_pre=None, gamma_post=None, beta_pos
     code = ls_dtype(x)
     if workspace is None:
         n = max(ls_block_norm_bw_workspace_size(rows, hidden, gates, layer, code), 16) // 4
-        workspace = x.new_empty(n, dtype=f32)
+        workspace = torch.empty(n, dtype=f32, device=device)
     else:
         _workspace("workspace", workspace)
         n = workspace.numel()
-    dx = x.new_empty(shape) if dx is None else dx
-    dr = x.new_empty(shape) if dr is None else dr
-    dgp = x.new_empty(hidden, dtype=f32) if gamma_post is not None else None
-    dbp = x.new_empty(hidden, dtype=f32) if gamma_post is not None and layer else None
-    dg = x.new_empty(hidden, dtype=f32) if gamma_pre is not None else None
-    db = x.new_empty(hidden, dtype=f32) if gamma_pre is not None and layer else None
-    dgate = x.new_empty((gates, hidden), dtype=f32) if gates else None
+    dx = torch.empty_like(x) if dx is None else dx
+    dr = torch.empty_like(x) if dr is None else dr
+
+    def sums(wanted):
+        return torch.empty(hidden, dtype=f32, device=device) if wanted else None
+
+    post, pre = gamma_post is not None, gamma_pre is not None
+    dgp, dbp, dg, db = sums(post), sums(post and layer), sums(pre), sums(pre and layer)
+    dgate = torch.empty((gates, hidden), dtype=f32, device=device) if gates else None
     dev = _same_device(dy, dh, x, h, stats, gamma_pre, gamma_post, beta_post, gate, workspace, dx,
                        dr)
     _launch("ls_block_norm_bw", dev, dx.data_ptr(), dr.data_ptr(), _ptr(dgate), _ptr(dgp),
@@ -1110,21 +1116,22 @@ def linear_cross_entropy_fw(hidden, weight, target, workspace=None, loss=None, l
     """Per-row softmax cross entropy of the logits hidden @ weight.T (hidden
     [rows, D], weight [vocab, D]), which are not stored, against int32 target
     [rows] (negative = ignored row); returns (loss, lse), fp32."""
-    f32 = _torch().float32
+    torch = _torch()
+    f32, device = torch.float32, hidden.device
     rows, D, V = _linear(hidden, weight, target)
     code = ls_dtype(hidden)
     if workspace is None:
         n = max(ls_linear_cross_entropy_fw_workspace_size(rows, D, V, code), 16) // 4
-        workspace = hidden.new_empty(n, dtype=f32)
+        workspace = torch.empty(n, dtype=f32, device=device)
     else:
         _workspace("workspace", workspace)
         n = workspace.numel()
     if loss is None:
-        loss = hidden.new_empty(rows, dtype=f32)
+        loss = torch.empty(rows, dtype=f32, device=device)
     else:
         _want("loss", loss, (rows,), f32)
     if lse is None:
-        lse = hidden.new_empty(rows, dtype=f32)
+        lse = torch.empty(rows, dtype=f32, device=device)
     else:
         _want("lse", lse, (rows,), f32)
     dev = _same_device(hidden, weight, target, workspace, loss, lse)
@@ -1139,13 +1146,13 @@ def linear_cross_entropy_bw(hidden, weight, target, lse, dloss, weight_grad: boo
     upstream gradient of each row's loss: (dhidden, dweight) in the inputs'
     dtype, dweight None without ``weight_grad`` (a frozen vocabulary)."""
     torch = _torch()
-    f32 = torch.float32
+    f32, device = torch.float32, hidden.device
     rows, D, V = _linear(hidden, weight, target)
     _stats(rows, hidden, lse=lse, dloss=dloss)
     code = ls_dtype(hidden)
     if workspace is None:
         n = max(ls_linear_cross_entropy_bw_workspace_size(rows, D, V, code), 16) // 4
-        workspace = hidden.new_empty(n, dtype=f32)
+        workspace = torch.empty(n, dtype=f32, device=device)
     else:
         _workspace("workspace", workspace)
         n = workspace.numel()

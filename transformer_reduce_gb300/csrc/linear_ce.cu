@@ -76,7 +76,7 @@ static LceLayout lce_layout(bool backward, int64_t rows, int64_t D, int64_t V, s
         l.row_lse2 = take(l.row_cap * 4);
         l.row_up = take(l.row_cap * 4);
         l.q = take(l.planes * l.row_cap * l.q_pitch * 2);
-        if (l.pieces > 1 || l.splits > 1) l.dx_sum = take(l.splits * l.row_cap * D * 4);
+        if (l.pieces > 1 || l.splits > 1) l.dx_sum = take(l.splits * l.row_cap * round_up(D, 8) * 4);
     } else {
         l.row_hit = take(l.row_cap * 4);
         l.part = take(2 * ceil_div(V, kLceN) * l.row_cap * 8);
@@ -242,6 +242,9 @@ cudaError_t launch_linear_ce_bw(T *dx, T *dw, const T *x, const T *w, const int3
     g.with_dw = dw != nullptr;
     g.splits = l.splits;
     g.split_k = l.split_k;
+    g.sum_pitch = round_up(D, 8);
+    g.aligned = D * sizeof(T) % 16 == 0 && reinterpret_cast<uintptr_t>(dx) % 16 == 0 &&
+                reinterpret_cast<uintptr_t>(dw) % 16 == 0;
     CUtensorMap x_k, x_n, w_k, w_n, q_k, q_n;  // along K, and not
     const int64_t x_plane = l.row_cap * l.pitch, q_plane = l.row_cap * l.q_pitch;
     for (const bool k : {true, false}) {
@@ -269,8 +272,8 @@ cudaError_t launch_linear_ce_bw(T *dx, T *dw, const T *x, const T *w, const int3
         if (e == cudaSuccess) e = lce_launch<kLceGrads, T>(q_k, w_n, q_n, x_n, g, st);
     }
     if (e != cudaSuccess || l.splits == 1 || rows == 0) return e;
-    const int64_t blocks = ceil_div(rows * D, 256), most = (int64_t)device_sm_count() * 8;
-    return launch_pdl(lce_join_dx<T>, dim3((unsigned)(blocks < most ? blocks : most)), dim3(256), 0,
+    const int64_t most = (int64_t)device_sm_count() * 8;
+    return launch_pdl(lce_join_dx<T>, dim3((unsigned)(rows < most ? rows : most)), dim3(256), 0,
                       st, g);
 }
 

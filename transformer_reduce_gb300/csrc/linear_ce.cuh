@@ -29,8 +29,8 @@
 //  * fp32 operands are three bf16 planes each (8 + 8 + 8 bits of the 24); six
 //    products of planes, smallest first, leave out terms below 2^-24.  The
 //    tensor cores cut the accumulator off where a step of 16 is added, so that
-//    a long sum drifts; after every 256 elements of fp32 operands the sum so far
-//    is therefore added up, rounding to nearest, in a second accumulator.
+//    a long sum drifts; of fp32 operands the sums of 256 elements are therefore
+//    added up in registers, rounding to nearest.
 //
 // Every sum has one order, given by the sizes: the results are reproducible.
 #pragma once
@@ -48,7 +48,11 @@ constexpr int kLceStages = 6;
 constexpr int kLceBox = 64 * kLceK * 2;  // bytes of one 64 x 64 TMA box
 constexpr int kLceStage = 2 * kLceHalf / 64 * kLceBox;
 constexpr int kLceThreads = 320;  // loader, issuer, eight warps on the accumulators
-constexpr size_t kLceSmem = (size_t)kLceStages * kLceStage + 1024;
+// Columns that a warp turns at a time where the rows of an output do not start on
+// 16-byte addresses, and the floats it takes.
+constexpr int kLceTurn = 16;
+constexpr int kLceTurnFloats = 32 * (kLceTurn + 1);
+constexpr size_t kLceSmem = (size_t)kLceStages * kLceStage + 8 * kLceTurnFloats * 4 + 1024;
 constexpr int kLceSms = 152;  // what the cuts are made for
 // fp32: steps of kLceK whose products are summed before they join the tile's sum
 // ([1001,333] by [10007,333], largest error of dx over the largest dx: 1.9e-5
@@ -82,7 +86,9 @@ struct LceArgs {
     float *row_hit;         // [row_cap] the target's logit
     float2 *part;           // [half tiles of V][row_cap] (largest logit * log2 e, sum)
     void *q;                // [planes][row_cap][q_pitch]
-    float *dx_sum;          // [splits][row_cap][D] over the pieces so far
+    float *dx_sum;          // [splits][row_cap][sum_pitch] over the pieces so far
+    int64_t sum_pitch;
+    int aligned;            // the rows of dx and dw start on 16-byte addresses
     void *dx, *dw;          // outputs
 };
 
@@ -479,6 +485,31 @@ __device__ __forceinline__ void lce_store32(T *p, const float (&f)[32], int n) {
     }
 }
 
+// A warp's 32 rows of N values to rows that start anywhere: turned in shared
+// memory so that 16 lanes write neighbouring columns (a lane that writes its own
+// row touches a sector per element: the gradients' product of [1001,333] fp32 by
+// 10007 took 98 us, 74 turned).  out: the lane's row, or NULL.
+template <typename T, int N>
+__device__ __forceinline__ void lce_store_turned(float *turn, T *out, const float (&f)[N], float un,
+                                                 int width) {
+    const int lane = threadIdx.x & 31, col = lane & (kLceTurn - 1);
+#pragma unroll
+    for (int c = 0; c < N; c += kLceTurn) {
+        if (c >= width) break;
+        __syncwarp();
+#pragma unroll
+        for (int e = 0; e < kLceTurn; ++e) turn[lane * (kLceTurn + 1) + e] = f[c + e] * un;
+        __syncwarp();
+#pragma unroll 4
+        for (int r = lane / kLceTurn; r < 32; r += 32 / kLceTurn) {
+            T *row = reinterpret_cast<T *>(
+                __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(out), r));
+            if (row && c + col < width)
+                row[c + col] = lce_round<T>(turn[r * (kLceTurn + 1) + col]);
+        }
+    }
+}
+
 // T: storage type of the call.  Maps: a0, b0 of the only product or of dx; a1,
 // b1 of dW; in boxes of 64 by 128 rows where the operand lies along K, else of
 // 64 by 64.
@@ -528,7 +559,7 @@ lce_product(const __grid_constant__ CUtensorMap a0, const __grid_constant__ CUte
     walk.begin();
     const int64_t tiles = walk.tiles();
     constexpr bool kCut = sizeof(T) == 4;  // planes, and sums cut in parts
-    constexpr int kBufs = kCut ? 1 : 2;    // accumulators in turn; kCut: the second holds the sum
+    constexpr int kBufs = 2;               // accumulators in turn
     constexpr int kSegs = kCut ? 6 : 1;
     auto part_of = [](int64_t left) { return kCut && left > kLceCut ? (int64_t)kLceCut : left; };
 
@@ -647,6 +678,9 @@ lce_product(const __grid_constant__ CUtensorMap a0, const __grid_constant__ CUte
         // ---- accumulators ----
         // a warp reads the 32 rows that its number allows, and half of the columns
         const int quarter = warp & 3;
+        float *turn = reinterpret_cast<float *>(lce_smem + (base - smem_addr(lce_smem)) +
+                                                kLceStages * kLceStage) +
+                      (warp - 2) * kLceTurnFloats;
         const int half = (warp - 2) >> 2;
         const int row_in = rank * kLceHalf + 32 * quarter + lane;
         int buf = 0;
@@ -672,56 +706,43 @@ lce_product(const __grid_constant__ CUtensorMap a0, const __grid_constant__ CUte
                     acc_phase ^= 1u;
                 }
             };
-            // fp32: all parts of the sum but the last
-            bool more = false;
-            if constexpr (kCut) {
-                for (int64_t left = t.nk - kLceCut; left > 0; left -= kLceCut) {
-                    arrived();
-                    if (ok) {
-#pragma unroll 1
-                        for (int c = 0; c < kLceN / 2 / 32; ++c) {
-                            float f[32], sum[32];
-                            tmem_load32(f, 0, mine + 32 * c);
-                            if (more) tmem_load32(sum, 0, mine + kLceN + 32 * c);
-                            tmem_wait(f);
-                            if (more) {
-                                tmem_wait(sum);
-#pragma unroll
-                                for (int e = 0; e < 32; ++e) f[e] += sum[e];
-                            }
-                            tmem_store32(mine + kLceN + 32 * c, f);
-                        }
-                    }
-                    more = true;
-                    release();
-                }
-            }
-            arrived();
-            const uint32_t src = mine + buf * kLceN;
             const int64_t row = t.m * kLceM + row_in;
-            // the row's half of the tile; NaN if the product did not come.  The
+            // The row's half of the tile; NaN if the product did not come.  An
             // accumulator is free once it is read.
             constexpr int kCols = kLceN / 2;
             float f[kCols];
+            arrived();
             if (some && ok) {
+                const uint32_t src = mine + buf * kLceN;
 #pragma unroll
                 for (int c = 0; c < kCols; c += 32) tmem_load32(f, c, src + c);
                 tmem_wait(f);
-                if (kCut && more) {
-#pragma unroll
-                    for (int c = 0; c < kCols; c += 32) {
-                        float sum[32];
-                        tmem_load32(sum, 0, mine + kLceN + c);
-                        tmem_wait(sum);
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) f[c + e] += sum[e];
-                    }
-                }
             } else {
 #pragma unroll
                 for (int e = 0; e < kCols; ++e) f[e] = ok ? 0.f : __int_as_float(0x7fc00000);
             }
             release();
+            if constexpr (kCut) {  // the further parts of the sum
+                for (int64_t left = t.nk - kLceCut; left > 0; left -= kLceCut) {
+                    arrived();
+                    if (ok) {
+                        const uint32_t src = mine + buf * kLceN;
+#pragma unroll
+                        for (int c = 0; c < kCols; c += 32) {
+                            float part[32];
+                            tmem_load32(part, 0, src + c);
+                            tmem_wait(part);
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) f[c + e] += part[e];
+                        }
+                    } else {
+                        f[0] = __int_as_float(0x7fc00000);
+#pragma unroll
+                        for (int e = 1; e < kCols; ++e) f[e] = f[0];
+                    }
+                    release();
+                }
+            }
             if constexpr (EPI == kLceStats) {
                 const int64_t n0 = t.n * kLceN + half * kCols;
                 const int width = (int)min((int64_t)kCols, g.V - n0);
@@ -822,27 +843,37 @@ lce_product(const __grid_constant__ CUtensorMap a0, const __grid_constant__ CUte
                 if (live)
                     out = t.job ? static_cast<T *>(g.dw) + (g.v0 + row) * g.D + n0
                                 : static_cast<T *>(g.dx) + (int64_t)g.row_of[row] * g.D + n0;
-                float *sums = g.dx_sum + (t.split * g.row_cap + row) * g.D + n0;
+                if (!g.aligned && (t.job || (g.first && g.last && g.splits == 1))) {
+                    lce_store_turned<T>(turn, out, f, un, width);
+                    continue;
+                }
+                const bool add = !t.job && !g.first, keep = !t.job && !(g.last && g.splits == 1);
+                float *sums = g.dx_sum + (t.split * g.row_cap + row) * g.sum_pitch + n0;
+                if (live) {
 #pragma unroll
-                for (int c = 0; c < kCols; c += 32) {
-                    const int n = width - c;
-                    if (n <= 0 || !live) continue;
-                    float v[32];
+                    for (int c = 0; c < kCols; c += 32) {
+                        const int n = width - c;
+                        if (n <= 0) continue;
+                        float v[32];
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) v[e] = f[c + e] * un;
-                    if (t.job) {
-                        lce_store32<T>(out + c, v, n);
-                        continue;
+                        for (int e = 0; e < 32; ++e) v[e] = f[c + e] * un;
+                        if (add) {  // (the rows of the sums reach to a multiple of 8)
+#pragma unroll
+                            for (int e = 0; e < 32; e += 4) {
+                                if (e >= n) continue;
+                                const float4 q =
+                                    *reinterpret_cast<const float4 *>(sums + c + e);
+                                v[e] += q.x;
+                                v[e + 1] += q.y;
+                                v[e + 2] += q.z;
+                                v[e + 3] += q.w;
+                            }
+                        }
+                        if (keep)
+                            lce_store32<float>(sums + c, v, (n + 7) & ~7);
+                        else
+                            lce_store32<T>(out + c, v, n);
                     }
-                    if (!g.first) {
-#pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            if (e < n) v[e] += sums[c + e];
-                    }
-                    if (g.last && g.splits == 1)
-                        lce_store32<T>(out + c, v, n);
-                    else
-                        lce_store32<float>(sums + c, v, n);
                 }
             }
         }
@@ -861,13 +892,16 @@ lce_product(const __grid_constant__ CUtensorMap a0, const __grid_constant__ CUte
 template <typename T>
 __global__ void __launch_bounds__(256) lce_join_dx(const LceArgs g) {
     pdl_begin();
-    const int64_t n = (int64_t)*g.count * g.D, step = g.row_cap * g.D;
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
-        float v = __ldcg(g.dx_sum + i);
-#pragma unroll 4
-        for (int64_t s = 1; s < g.splits; ++s) v += __ldcg(g.dx_sum + s * step + i);
-        const int64_t r = i / g.D;
-        static_cast<T *>(g.dx)[g.row_of[r] * g.D + (i - r * g.D)] = lce_round<T>(v);
+    const int64_t step = g.row_cap * g.sum_pitch;
+    for (int64_t r = blockIdx.x; r < *g.count; r += gridDim.x) {
+        const float *src = g.dx_sum + r * g.sum_pitch;
+        T *dst = static_cast<T *>(g.dx) + (int64_t)g.row_of[r] * g.D;
+        for (int64_t d = threadIdx.x; d < g.D; d += 256) {
+            float v = __ldcg(src + d);
+#pragma unroll 8
+            for (int64_t s = 1; s < g.splits; ++s) v += __ldcg(src + s * step + d);
+            dst[d] = lce_round<T>(v);
+        }
     }
 }
 
