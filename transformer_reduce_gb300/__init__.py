@@ -858,8 +858,8 @@ def _map_strides(name, t, shape, dtype):
     if t.shape != shape or t.dtype != dtype:
         _want(name, t, shape, dtype)
     sb, sh, sq, sk = t.stride()
-    B, H, Tq, Tk = shape
-    if (Tk > 1 and sk != 1) or (Tq > 1 and sq != Tk):
+    _, _, Tq, Tk = shape
+    if ((Tk > 1 and sk != 1) or (Tq > 1 and sq != Tk)) and t.numel():
         raise ValueError(f"{name} must have dense rows and columns in every head")
     return sb, sh
 
