@@ -255,6 +255,35 @@ def test_diff_in_place(lib, Tk):
         assert e1 is x1 and torch.equal(e1, d1) and torch.equal(e2, d2) and torch.equal(el, dl)
 
 
+def test_diff_without_statistics(lib):
+    """Through the C entry point: NULL statistics are not written."""
+    L = lib
+    for Tk in (64, 77, 20000):
+        x1, x2 = (_randn((1, 2, 3, Tk), torch.bfloat16, s) for s in (1, 2))
+        lam = torch.tensor([0.3, 0.8], device=DEV)
+        want, _ = L.softmax_fw_diff(x1, x2, lam, causal=True)
+        got = torch.empty_like(want)
+        s = L.ls_softmax_fw_diff(got.data_ptr(), None, x1.data_ptr(), x2.data_ptr(), lam.data_ptr(),
+                                 None, 1, 2, 3, Tk, 6 * Tk, 3 * Tk, 6 * Tk, 3 * Tk, 2, 1, 1.0, 2,
+                                 torch.cuda.current_stream().cuda_stream)
+        torch.cuda.synchronize()
+        assert s == 0 and torch.equal(got, want)
+
+
+def test_diff_one_map_for_both(lib):
+    """The same scores twice, and strides of 0: one head's scores for every head."""
+    L = lib
+    x = _randn((2, 1, 5, 48), torch.float32, 1)
+    lam = torch.tensor([1.0, 0.25, 0.0], device=DEV)
+    e = x.expand(2, 3, 5, 48)
+    got, _ = L.softmax_fw_diff(e, e, lam)
+    p = torch.softmax(x.double(), -1)
+    # round(e i) - e i, of which the second product is not rounded (fused): half a step of p,
+    # which is itself off by a few steps
+    assert (got[:, 0].abs().double() <= R.U * 1.001 * p[:, 0]).all()
+    assert torch.allclose(got.double(), (1 - lam.double())[None, :, None, None] * p, atol=1e-6)
+
+
 def test_diff_empty(lib):
     L = lib
     lam = torch.ones(2, device=DEV)

@@ -29,9 +29,10 @@
 
 namespace lsr {
 
-// |m| up to which e^(z - m) is one fused multiply-add before ex2: the rounding
-// of m * log2 e then puts at most 64 * 1.45 * 2^-24 = 6e-6 on the saved sum
-// (the weights lose it in the quotient).
+// |m| up to which the forward's e^(z - m) is one fused multiply-add before ex2.
+// The roundings of scale * log2 e and m * log2 e then put up to 2 * 64 * 1.45 *
+// 2^-24 = 1e-5 on a row's sum; the weights lose that in the quotient, and the
+// saved inverse is corrected for it (DiffExp::inverse).
 constexpr float kDiffNear = 64.f;
 
 template <int TPR>
@@ -317,10 +318,17 @@ __device__ __forceinline__ void diff_values(float2 (&v)[Traits<T>::kVec / 2], co
     }
 }
 
-// e^(mul * v - m) as a multiplier and an addend of v before ex2, given m; values
-// far from 0 are shifted first.
+// e^(mul * v - m) as a multiplier and an addend of v before ex2, given the
+// largest v and m = mul * top; values far from 0 are shifted first.
 struct DiffExp {
     float c, n;
+    // 1 / sum without what the roundings of c and n put on the exponent at v = top,
+    // where the row's weight lies (2^off is 1 + off ln 2)
+    __device__ __forceinline__ float inverse(float inv, float top, float m, float mul) const {
+        if (!(fabsf(m) < kDiffNear)) return inv;
+        const float off = fmaf(top, fmaf(-mul, kLog2e, c), fmaf(m, kLog2e, n));
+        return fmaf(inv, off * 0.6931471805599453f, inv);
+    }
 };
 template <int CPT, int H2>
 __device__ __forceinline__ DiffExp diff_exponent(float2 (&v)[CPT][H2], float m, float mul) {
@@ -411,6 +419,7 @@ diff_fw_vec(T *out, float4 *stats, const DiffRows<const T> x1, const DiffRows<co
             }
         }
         diff_reduce2<TPR, BLOCK, OpMax>(m1, m2, red_max, grp);
+        const float top1 = m1, top2 = m2;
         m1 *= mul;
         m2 *= mul;
         const DiffExp x1e = diff_exponent(v1, m1, mul), x2e = diff_exponent(v2, m2, mul);
@@ -438,8 +447,8 @@ diff_fw_vec(T *out, float4 *stats, const DiffRows<const T> x1, const DiffRows<co
         const float i2 = sum2 == 0.f ? 0.f : fast_rcp(sum2);
         const float li2 = -lam_h * i2;
         if (stats && valid && lane == 0)
-            stats[rw + sub] = make_float4(m1 == -INFINITY ? 0.f : m1, i1,
-                                          m2 == -INFINITY ? 0.f : m2, i2);
+            stats[rw + sub] = make_float4(m1 == -INFINITY ? 0.f : m1, x1e.inverse(i1, top1, m1, mul),
+                                          m2 == -INFINITY ? 0.f : m2, x2e.inverse(i2, top2, m2, mul));
         T *orow = out + w.dense(p) + (AL ? lane * V : 0);
 #pragma unroll
         for (int k = 0; k < CPT; ++k) {
@@ -537,8 +546,6 @@ diff_bw_vec(const DiffRows<T> dx1, const DiffRows<T> dx2, float *row_dot, const 
         const uint4 *sg = slots(turn, 2) + lane;
         float2 v1[CPT][H2], v2[CPT][H2];
         uint4 g4[CPT];  // dout as it is stored, 0 at invisible keys
-        const bool near = fabsf(st.x) < kDiffNear && fabsf(st.z) < kDiffNear;
-        const float c = mul * kLog2e;
         float2 t1 = f2(0.f), t2 = f2(0.f);
 #pragma unroll
         for (int k = 0; k < CPT; ++k) {
@@ -553,21 +560,12 @@ diff_bw_vec(const DiffRows<T> dx1, const DiffRows<T> dx2, float *row_dot, const 
                 keep_elements<T>(g4[k], relpos_bits<T>(mrow, j0, lo, hi));
             float2 g[H2];
             unpack2<T>(g4[k], g);
-            float2 c1 = f2(c), c2 = f2(c), n1 = f2(-st.x * kLog2e), n2 = f2(-st.z * kLog2e);
-            if (!near) {  // as the forward: the difference first where the largest z is far from 0
-                const bool far1 = !(fabsf(st.x) < kDiffNear), far2 = !(fabsf(st.z) < kDiffNear);
-#pragma unroll
-                for (int h2 = 0; h2 < H2; ++h2) {
-                    if (far1) v1[k][h2] = fma2(v1[k][h2], f2(mul), f2(-st.x));
-                    if (far2) v2[k][h2] = fma2(v2[k][h2], f2(mul), f2(-st.z));
-                }
-                if (far1) c1 = f2(kLog2e), n1 = f2(0.f);
-                if (far2) c2 = f2(kLog2e), n2 = f2(0.f);
-            }
 #pragma unroll
             for (int h2 = 0; h2 < H2; ++h2) {
-                float2 a = fma2(v1[k][h2], c1, n1);
-                float2 b = fma2(v2[k][h2], c2, n2);
+                // z - m first, at one rounding: what is left of one in the exponent goes by
+                // the difference and not by m, and dlam sums all rows' weights
+                float2 a = mul2(fma2(v1[k][h2], f2(mul), f2(-st.x)), f2(kLog2e));
+                float2 b = mul2(fma2(v2[k][h2], f2(mul), f2(-st.z)), f2(kLog2e));
                 a.x = fast_exp2(a.x);
                 a.y = fast_exp2(a.y);
                 b.x = fast_exp2(b.x);
