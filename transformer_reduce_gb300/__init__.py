@@ -963,27 +963,29 @@ def softmax_bw_diff(dout, scores1, scores2, lam, stats, mask=None, causal: bool 
 _NORM_KINDS = {"rms": 0, "layer": 1}
 
 
-def _block(x, kind, gate, **vectors):
+def _block(x, kind, gate, gamma_pre, beta_pre, gamma_post, beta_post):
     """(rows, hidden, gates, layer) of the norms around a block."""
     rows, hidden = _rows_hidden(x)
     layer = _NORM_KINDS.get(kind)
     if layer is None:
         raise ValueError(f"kind must be 'rms' or 'layer', got {kind!r}")
-    want = (hidden,)
-    for name, t in vectors.items():
-        if t is None:
-            continue
-        if t.shape != want or t.dtype != x.dtype:
-            _want(name, t, want, x.dtype)
-        if name[:4] == "beta" and (not layer or vectors.get("gamma" + name[4:]) is None):
-            raise ValueError(f"{name} wants kind='layer' and gamma{name[4:]}")
+    want, dtype = (hidden,), x.dtype
+    for t in (gamma_pre, beta_pre, gamma_post, beta_post):
+        if t is not None and (t.shape != want or t.dtype != dtype):
+            for name, v in (("gamma_pre", gamma_pre), ("beta_pre", beta_pre),
+                            ("gamma_post", gamma_post), ("beta_post", beta_post)):
+                _want(name, v, want, dtype)
+    if beta_pre is not None and (not layer or gamma_pre is None):
+        raise ValueError("beta_pre wants kind='layer' and gamma_pre")
+    if beta_post is not None and (not layer or gamma_post is None):
+        raise ValueError("beta_post wants kind='layer' and gamma_post")
     gates = 0
     if gate is not None:
         if gate.dim() != 2 or gate.shape[0] < 1 or rows % gate.shape[0]:
             raise ValueError(f"gate must be [gates, {hidden}] with gates a divisor of {rows} rows")
         gates = gate.shape[0]
-        if gate.shape[1] != hidden or gate.dtype != x.dtype:
-            _want("gate", gate, (gates, hidden), x.dtype)
+        if gate.shape[1] != hidden or gate.dtype != dtype:
+            _want("gate", gate, (gates, hidden), dtype)
     return rows, hidden, gates, layer
 
 
@@ -1001,8 +1003,8 @@ def block_norm_fw(x, residual, gamma_pre=None, beta_pre=None, gamma_post=None, b
     residual stream (in place)."""
     torch = _torch()
     f32 = torch.float32
-    rows, hidden, gates, layer = _block(x, kind, gate, gamma_pre=gamma_pre, beta_pre=beta_pre,
-                                        gamma_post=gamma_post, beta_post=beta_post)
+    rows, hidden, gates, layer = _block(x, kind, gate, gamma_pre, beta_pre, gamma_post,
+                                        beta_post)
     shape, dtype = x.shape, x.dtype
     if residual.shape != shape or residual.dtype != dtype:
         _want("residual", residual, shape, dtype)
@@ -1048,8 +1050,7 @@ def block_norm_bw(dy, dh, x, h, stats, gamma_pre=None, gamma_post=None, beta_pos
     or h, ``dr`` dy, dh or h (in place)."""
     torch = _torch()
     f32, device = torch.float32, x.device
-    rows, hidden, gates, layer = _block(x, kind, gate, gamma_pre=gamma_pre, gamma_post=gamma_post,
-                                        beta_post=beta_post)
+    rows, hidden, gates, layer = _block(x, kind, gate, gamma_pre, None, gamma_post, beta_post)
     shape, dtype = x.shape, x.dtype
     if gamma_pre is None:
         if dy is not None:

@@ -186,8 +186,7 @@ static __global__ void __launch_bounds__(256) lce_count(const LcePack p) {
     }
 }
 
-// Copies kLcePackRows rows of x to their places; the last block also clears
-// the rows up to the next tile.  T: type of x.  dx: of a backward, where the
+// Copies kLcePackRows rows of x to their places.  T: type of x.  dx: of a backward, where the
 // rows that do not count become 0.
 template <typename T>
 __global__ void __launch_bounds__(256)
@@ -297,12 +296,16 @@ lce_pack_rows(typename LceSplit<T>::O *out, const T *x, T *dx, const LcePack p) 
                 LceSplit<T>::put(o + d, plane, T(0.f));
         }
     }
-    if (blockIdx.x == gridDim.x - 1) {
-        const int64_t end = ((int64_t)all + kLceM - 1) / kLceM * kLceM;
-        for (int64_t r = all + warp; r < end; r += 8) {
-            for (int64_t d = lane; d < p.pitch; d += 32)
-                LceSplit<T>::put(out + r * p.pitch + d, plane, T(0.f));
-        }
+    // The product q^T x goes over whole steps of K: the rows up to the next are 0.
+    // (Others past the last only meet outputs that are not written.)
+    if (p.backward && blockIdx.x == gridDim.x - 1) {
+        const int64_t end = ((int64_t)all + kLceK - 1) / kLceK * kLceK;
+        const int64_t vectors = (end - all) * p.pitch / 8;
+#pragma unroll
+        for (int k = 0; k < LceSplit<T>::kPlanes; ++k)
+            for (int64_t c = tid; c < vectors; c += 256)
+                reinterpret_cast<uint4 *>(out + k * plane + all * p.pitch)[c] =
+                    make_uint4(0u, 0u, 0u, 0u);
     }
 }
 
@@ -518,7 +521,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLceThreads, 1)
 lce_product(const __grid_constant__ CUtensorMap a0, const __grid_constant__ CUtensorMap b0,
             const __grid_constant__ CUtensorMap a1, const __grid_constant__ CUtensorMap b1,
             const LceArgs g) {
-    pdl_begin();
+    // what needs nothing of the kernels before runs while they end
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     extern __shared__ __align__(1024) uint8_t lce_smem[];
     __shared__ __align__(8) uint64_t bars[2 * kLceStages + 5];
     __shared__ uint32_t tmem_at;
@@ -552,6 +556,7 @@ lce_product(const __grid_constant__ CUtensorMap a0, const __grid_constant__ CUte
     __syncthreads();
     cluster_sync();
     tc_fence_after();
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const uint32_t tmem = tmem_at;
     volatile int *abort = &abort_s;
     const int64_t count = *g.count;
