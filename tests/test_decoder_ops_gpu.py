@@ -284,6 +284,43 @@ def test_diff_one_map_for_both(lib):
     assert torch.allclose(got.double(), (1 - lam.double())[None, :, None, None] * p, atol=1e-6)
 
 
+@pytest.mark.parametrize("dt", list(DT))
+@pytest.mark.parametrize("Tk", [1, 2, 3, 8, 64, 100, 257, 1001, 1024, 2049, 5000, 20000])
+def test_diff_rows_with_one_visible_key(lib, dt, Tk):
+    """All weight is on one key whatever its score: p (g - sum p g) is 0 but for the
+    roundings of p = e i.  scale * x less the row's saved maximum is not 0 where their
+    product is rounded, so that neither is p exactly 1; in steps of 2^-24: e in either
+    direction 4 (2^-22 of ex2), the reciprocal 2, its correction, e g and (e g) i 1 each."""
+    B, H, Tq = 2, 2, 3
+    x1, x2 = _maps((B, H, Tq, Tk), DT[dt], "halves", Tk, 3.0)
+    lam = torch.rand(H, generator=_gen(Tk + 2), device=DEV)
+    dout = _randn((B, H, Tq, Tk), DT[dt], Tk + 3)
+    m = torch.full((B, Tk), -INF, dtype=DT[dt], device=DEV)
+    for b in range(B):
+        m[b, (b * 7 + 3) % Tk] = 0
+    _, stats = lib.softmax_fw_diff(x1, x2, lam, m, scale=0.3)
+    d1, d2, _ = lib.softmax_bw_diff(dout, x1, x2, lam, stats, m, scale=0.3)
+
+    def check(got, g, factor):  # 13 steps; the output's own rounding, of fp16 down to 2^-24
+        lim = 14 * 2.0 ** -24 * factor * g.double().abs()
+        assert (got.double().abs() <= lim + (2.0 ** -25 if dt == "f16" else 0)).all()
+
+    lam_h = lam.double().abs()[None, :, None, None]
+    hidden = (m == -INF)[:, None, None, :].expand_as(d1)
+    assert not d1[hidden].any() and not d2[hidden].any()
+    check(d1, dout, 0.3)
+    check(d2, dout, 0.3 * lam_h)
+    shape = (B, H, Tk if Tk < 300 else 1, Tk)  # causal: the first query sees one key
+    y1, y2 = _maps(shape, DT[dt], "halves", Tk + 5, 3.0)
+    g = _randn(shape, DT[dt], Tk + 8)
+    if shape[2] == Tk:
+        _, stats = lib.softmax_fw_diff(y1, y2, lam, causal=True)
+        d1, d2, _ = lib.softmax_bw_diff(g, y1, y2, lam, stats, causal=True)
+        assert not d1[:, :, 0, 1:].any() and not d2[:, :, 0, 1:].any()
+        check(d1[:, :, :1], g[:, :, :1], 1.0)
+        check(d2[:, :, :1], g[:, :, :1], lam_h)
+
+
 def test_diff_empty(lib):
     L = lib
     lam = torch.ones(2, device=DEV)

@@ -52,7 +52,7 @@ struct DiffCursor {
 // The rows of a block: from beg on, G at a time, `step` further each turn.  A run
 // of its own (p.per rows), or, where rows differ in length (causal), turns that
 // lie a whole grid apart, so that no block gets the long rows of a head alone
-// ([8,6,777,777] fp16 backward: 96 us in runs).
+// ([8,6,777,777] fp16 backward: 96 us in runs, 82 dealt out).
 struct DiffBlock {
     int64_t beg, end;
     int step;
@@ -582,8 +582,7 @@ diff_bw_vec(const DiffRows<T> dx1, const DiffRows<T> dx2, float *row_dot, const 
         dot2 *= st.w;
         if (valid && lane == 0) row_dot[w.by_head(p)] = dot2;
         const float w1 = p.scale * st.y, w2 = -p.scale * lam_h * st.w;
-        const float2 n1 = f2(-w1 * dot1), n2 = f2(-w2 * dot2);
-        const bool odd = !(fabsf(n1.x) + fabsf(n2.x) + fabsf(w1) + fabsf(w2) < INFINITY);
+        const bool odd = !(fabsf(dot1) + fabsf(dot2) + fabsf(w1) + fabsf(w2) < INFINITY);
         T *r1 = dx1.p + w.at(dx1, p) + (AL ? lane * V : 0);
         T *r2 = dx2.p + w.at(dx2, p) + (AL ? lane * V : 0);
 #pragma unroll
@@ -594,9 +593,9 @@ diff_bw_vec(const DiffRows<T> dx1, const DiffRows<T> dx2, float *row_dot, const 
                 float2 g[H2];
                 unpack2<T>(g4[k], g);
 #pragma unroll
-                for (int h2 = 0; h2 < H2; ++h2) {  // p (g - D), scaled
-                    v1[k][h2] = mul2(v1[k][h2], fma2(g[h2], f2(w1), n1));
-                    v2[k][h2] = mul2(v2[k][h2], fma2(g[h2], f2(w2), n2));
+                for (int h2 = 0; h2 < H2; ++h2) {  // g - D first: it cancels where one key has all weight
+                    v1[k][h2] = mul2(mul2(v1[k][h2], f2(w1)), add2(g[h2], f2(-dot1)));
+                    v2[k][h2] = mul2(mul2(v2[k][h2], f2(w2)), add2(g[h2], f2(-dot2)));
                 }
                 if (odd) {  // 0 * NaN: invisible keys stay 0
                     const uint32_t bits = relpos_bits<T>(mrow, j0, lo, hi);

@@ -185,7 +185,6 @@ cudaError_t lce_prepare(LceArgs *g, const void **w_at, const LceLayout &l, bool 
     g->row_cap = l.row_cap;
     g->vc = V;
     g->q_pitch = l.q_pitch;
-    g->planes = l.planes;
     g->bf16 = !std::is_same<T, __half>::value;
     g->first = g->last = 1;
     g->count = p.count;

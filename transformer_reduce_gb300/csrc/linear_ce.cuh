@@ -71,7 +71,6 @@ struct LceArgs {
     int64_t row_cap;        // rows of the dense copy, a multiple of kLceM
     int64_t v0, vc;         // the piece: vocabulary entries [v0, v0 + vc)
     int64_t q_pitch;        // elements of a row of q
-    int planes;             // 1, or 3 for fp32
     int bf16;               // operand type of the products
     int first, last;        // of the pieces
     int with_dw;
@@ -85,7 +84,7 @@ struct LceArgs {
     const float *unscale;   // what q is to be multiplied with
     float *row_hit;         // [row_cap] the target's logit
     float2 *part;           // [half tiles of V][row_cap] (largest logit * log2 e, sum)
-    void *q;                // [planes][row_cap][q_pitch]
+    void *q;                // [1, fp32: 3][row_cap][q_pitch]
     float *dx_sum;          // [splits][row_cap][sum_pitch] over the pieces so far
     int64_t sum_pitch;
     int aligned;            // the rows of dx and dw start on 16-byte addresses
