@@ -29,10 +29,15 @@
 
 namespace lsr {
 
-// |m| up to which the forward's e^(z - m) is one fused multiply-add before ex2.
-// The roundings of scale * log2 e and m * log2 e then put up to 2 * 64 * 1.45 *
+// |m| up to which the largest z's rounding is left out of account: the forward's
+// e^(z - m) is then one fused multiply-add before ex2, the backward's z - m one.
+// The roundings of scale * log2 e and m * log2 e put up to 2 * 64 * 1.45 *
 // 2^-24 = 1e-5 on a row's sum; the weights lose that in the quotient, and the
-// saved inverse is corrected for it (DiffExp::inverse).
+// saved inverse is corrected for it (DiffExp::inverse).  Beyond it z is rounded
+// before m, the largest of the rounded ones, is taken off: a product that stays
+// unrounded differs from m by up to 2^-24 |m|, which from |m| = 2^30 on leaves
+// the exponent's range, and whichever kernel made the statistics, and whether it
+// added the mask or knew its window, the backward meets the same differences.
 constexpr float kDiffNear = 64.f;
 
 template <int TPR>
@@ -318,8 +323,8 @@ __device__ __forceinline__ void diff_values(float2 (&v)[Traits<T>::kVec / 2], co
     }
 }
 
-// e^(mul * v - m) as a multiplier and an addend of v before ex2, given the
-// largest v and m = mul * top; values far from 0 are shifted first.
+// e^(mul * v - m) as a multiplier and an addend of v before ex2, given m = mul *
+// the largest v; values far from 0 are rounded and shifted first.
 struct DiffExp {
     float c, n;
     // 1 / sum without what the roundings of c and n put on the exponent at v = top,
@@ -330,6 +335,11 @@ struct DiffExp {
         return fmaf(inv, off * 0.6931471805599453f, inv);
     }
 };
+// scale * x rounded.  (Scalar products: the compiler does fuse a pair's product
+// with the sum that follows it.)
+__device__ __forceinline__ float2 diff_rounded(float2 v, float mul) {
+    return make_float2(__fmul_rn(v.x, mul), __fmul_rn(v.y, mul));
+}
 template <int CPT, int H2>
 __device__ __forceinline__ DiffExp diff_exponent(float2 (&v)[CPT][H2], float m, float mul) {
     if (fabsf(m) < kDiffNear) return DiffExp{mul * kLog2e, -m * kLog2e};
@@ -337,7 +347,7 @@ __device__ __forceinline__ DiffExp diff_exponent(float2 (&v)[CPT][H2], float m, 
 #pragma unroll
     for (int k = 0; k < CPT; ++k)
 #pragma unroll
-        for (int h2 = 0; h2 < H2; ++h2) v[k][h2] = fma2(v[k][h2], f2(mul), nm);
+        for (int h2 = 0; h2 < H2; ++h2) v[k][h2] = add2(diff_rounded(v[k][h2], mul), nm);
     return DiffExp{kLog2e, 0.f};
 }
 
@@ -542,6 +552,9 @@ diff_bw_vec(const DiffRows<T> dx1, const DiffRows<T> dx2, float *row_dot, const 
         const int lo = w.lo, hi = w.hi, j_lane = lane * V - w.s;
         const T *mrow = MASKED && w.general ? mask + (int64_t)w.b * Tk : nullptr;
         const float mul = MASKED && w.general ? 1.f : p.scale;
+        // z is rounded before m is taken off (of both maps: the weights of one that
+        // is near move by less than its bound)
+        const bool far = !(fmaxf(fabsf(st.x), fabsf(st.z)) < kDiffNear);
         const uint4 *s1 = slots(turn, 0) + lane, *s2 = slots(turn, 1) + lane;
         const uint4 *sg = slots(turn, 2) + lane;
         float2 v1[CPT][H2], v2[CPT][H2];
@@ -560,12 +573,25 @@ diff_bw_vec(const DiffRows<T> dx1, const DiffRows<T> dx2, float *row_dot, const 
                 keep_elements<T>(g4[k], relpos_bits<T>(mrow, j0, lo, hi));
             float2 g[H2];
             unpack2<T>(g4[k], g);
+            // z - m first, at one rounding: what is left of one in the exponent goes by the
+            // difference and not by m, and dlam sums all rows' weights
+            if (!far) {
+#pragma unroll
+                for (int h2 = 0; h2 < H2; ++h2) {
+                    v1[k][h2] = fma2(v1[k][h2], f2(mul), f2(-st.x));
+                    v2[k][h2] = fma2(v2[k][h2], f2(mul), f2(-st.z));
+                }
+            } else {
+#pragma unroll
+                for (int h2 = 0; h2 < H2; ++h2) {
+                    v1[k][h2] = add2(diff_rounded(v1[k][h2], mul), f2(-st.x));
+                    v2[k][h2] = add2(diff_rounded(v2[k][h2], mul), f2(-st.z));
+                }
+            }
 #pragma unroll
             for (int h2 = 0; h2 < H2; ++h2) {
-                // z - m first, at one rounding: what is left of one in the exponent goes by
-                // the difference and not by m, and dlam sums all rows' weights
-                float2 a = mul2(fma2(v1[k][h2], f2(mul), f2(-st.x)), f2(kLog2e));
-                float2 b = mul2(fma2(v2[k][h2], f2(mul), f2(-st.z)), f2(kLog2e));
+                float2 a = mul2(v1[k][h2], f2(kLog2e));
+                float2 b = mul2(v2[k][h2], f2(kLog2e));
                 a.x = fast_exp2(a.x);
                 a.y = fast_exp2(a.y);
                 b.x = fast_exp2(b.x);
