@@ -156,10 +156,11 @@ __device__ __forceinline__ float fmax3(float a, float b, float c) {
 }
 
 // Pair arithmetic on Blackwell's packed FP32x2 instructions: two independent
-// FP32 operations per instruction, each rounded to nearest exactly as its
-// scalar form (add2, mul2 are never contracted into a fused multiply-add;
-// fma2 fuses once), so results are bitwise those of scalar code while the
-// issue slots spent on FP32 arithmetic halve.
+// FP32 operations per instruction, rounded to nearest, so that the issue slots
+// spent on FP32 arithmetic halve.  The compiler does fuse a mul2 with an add2
+// that follows it (seen where z = scale * x was to be rounded before its row's
+// maximum was taken off): where the product's own rounding matters it is made
+// by __fmul_rn, or the sum comes first.
 __device__ __forceinline__ float2 add2(float2 a, float2 b) { return __fadd2_rn(a, b); }
 __device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }

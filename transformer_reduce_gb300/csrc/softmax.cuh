@@ -242,13 +242,17 @@ softmax_fw_vec(T *out, const T *inp, const T *mask, int64_t rows,
         m = group_reduce<TPR, OpMax>(m, red);
         // e = 2^(v * mul - m * log2e); window rows of the scaled softmax hold
         // x, whose maximum times scale (> 0) is the maximum of scale * x
+        const float top = m;
         if (SCALED && !gen) m *= scale;
         float mL = m == -INFINITY ? 0.f : m * kLog2e;  // a row with no visible key sums to 0
         float2 mul = f2(SCALED && !gen ? scale * kLog2e : kLog2e);
         // The rounding of m * log2 e multiplies the whole row by one number,
         // which the quotient loses while it is small: 2^(1/16) at most for
         // |m| < 2^20.  Rows of larger maxima (only keys hidden by a finite
-        // mask are left) take the difference first.
+        // mask are left, or scores filled with lowest values) take the
+        // difference first, before the scale: a product that is fused with the
+        // subtraction, as the compiler does, differs from the rounded maximum
+        // by up to 2^-24 |m|.
         if (!(fabsf(m) < 0x1p20f) && m != -INFINITY) {
             const float2 by = f2(SCALED && !gen ? scale : 1.f);
 #pragma unroll
@@ -256,7 +260,7 @@ softmax_fw_vec(T *out, const T *inp, const T *mask, int64_t rows,
                 const int j0 = (kk * TPR + lane) * V;
                 if (j0 < hi && j0 + V > lo)
 #pragma unroll
-                    for (int h = 0; h < H2; ++h) v[kk][h] = add2(mul2(v[kk][h], by), f2(-m));
+                    for (int h = 0; h < H2; ++h) v[kk][h] = mul2(add2(v[kk][h], f2(-top)), by);
             }
             mL = 0.f;
             mul = f2(kLog2e);
