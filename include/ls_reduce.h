@@ -824,7 +824,9 @@ size_t ls_linear_cross_entropy_bw_workspace_size(int64_t rows, int64_t hidden, i
  * For each row r with target class t = target[r]:
  *     lse_r  = log sum_v exp(z_rv),   loss_r = lse_r - z_rt
  * The logits are FP32 sums of exact products of the stored values (fp32: of
- * products good to about 2^-23) and are not rounded.  Ignored rows (negative
+ * products good to about 2^-23) and are not rounded to the storage type; the
+ * tensor cores cut a sum off every 16 products, and parts of it are added
+ * rounding to nearest (up to about 2^-17 of a sum of terms of one sign).  Ignored rows (negative
  * target): loss = lse = 0; target >= vocab: NaN; neither row of x is read.
  *
  *   loss, lse  [rows] float32, device, written.

@@ -27,10 +27,10 @@
 //    rounded to the operands' 16-bit type, in the workspace; q W is added to dx
 //    in FP32 over the pieces, q^T x is the piece's rows of dW.
 //  * fp32 operands are three bf16 planes each (8 + 8 + 8 bits of the 24); six
-//    products of planes, smallest first, leave out terms below 2^-24.  The
-//    tensor cores cut the accumulator off where a step of 16 is added, so that
-//    a long sum drifts; of fp32 operands the sums of 256 elements are therefore
-//    added up in registers, rounding to nearest.
+//    products of planes, smallest first, leave out terms below 2^-24.
+//  * The tensor cores cut the accumulator off where a step of 16 is added, so that
+//    a long sum drifts: sums of so many elements (lce_cut) are therefore added up
+//    in registers, rounding to nearest.
 //
 // Every sum has one order, given by the sizes: the results are reproducible.
 #pragma once
@@ -54,16 +54,26 @@ constexpr int kLceTurn = 16;
 constexpr int kLceTurnFloats = 32 * (kLceTurn + 1);
 constexpr size_t kLceSmem = (size_t)kLceStages * kLceStage + 8 * kLceTurnFloats * 4 + 1024;
 constexpr int kLceSms = 152;  // what the cuts are made for
-// fp32: steps of kLceK whose products are summed before they join the tile's sum
-// ([1001,333] by [10007,333], largest error of dx over the largest dx: 1.9e-5
-// without the cut).
-constexpr int kLceCut = 4;
 constexpr int kLceChunk = 1024;  // rows counted together
 constexpr int kLcePackRows = 8;  // one per warp
 // Rows up to which every block of the packing counts all targets itself,
 // without a launch before it (at 8192 rows that took 35 us in the backward
 // instead of 5 and 10).
 constexpr int64_t kLceCountRows = 2048;
+
+enum { kLceStats = 0, kLceQ = 1, kLceGrads = 2 };
+
+// Steps of kLceK whose products the tensor cores sum before registers add them to
+// the tile's sum.  The accumulator is cut off, not rounded, where a step of 16 is
+// added, so that a sum of terms of one sign loses up to 2^-23 of itself with each
+// (measured: two thirds of that): uncut, dW of [2097152,8] was 1.2 % off and the
+// lse of 65536 hidden elements 8e-3.  With these cuts 64 * 16 elements lose at most
+// 8e-6 and 64 * 64 3e-5.  (Cuts of 4 and 16 steps took 8 % of the forward and of
+// the backward of [8192,1024] bf16 by 50257.)
+template <int EPI, typename T>
+constexpr int lce_cut() {
+    return sizeof(T) == 4 ? 4 : EPI == kLceGrads ? 64 : 16;
+}
 
 // What the kernels of one call share.
 struct LceArgs {
@@ -328,8 +338,6 @@ lce_pack_weight(typename LceSplit<T>::O *out, const T *w, int64_t V, int64_t D, 
 // ----------------------------------------------------------------------------
 // The products.
 // ----------------------------------------------------------------------------
-enum { kLceStats = 0, kLceQ = 1, kLceGrads = 2 };
-
 // A tile of a launch.
 struct LceTile {
     int job;        // kLceGrads: 0 dx, 1 dW
@@ -515,7 +523,8 @@ __device__ __forceinline__ void lce_store_turned(float *turn, T *out, const floa
 // T: storage type of the call.  Maps: a0, b0 of the only product or of dx; a1,
 // b1 of dW; in boxes of 64 by 128 rows where the operand lies along K, else of
 // 64 by 64.
-template <int EPI, typename T>
+// PARTS: sums along K of more than lce_cut steps are taken in parts.
+template <int EPI, typename T, bool PARTS>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLceThreads, 1)
 lce_product(const __grid_constant__ CUtensorMap a0, const __grid_constant__ CUtensorMap b0,
             const __grid_constant__ CUtensorMap a1, const __grid_constant__ CUtensorMap b1,
@@ -562,10 +571,10 @@ lce_product(const __grid_constant__ CUtensorMap a0, const __grid_constant__ CUte
     LceWalk<EPI> walk(g, count);
     walk.begin();
     const int64_t tiles = walk.tiles();
-    constexpr bool kCut = sizeof(T) == 4;  // planes, and sums cut in parts
-    constexpr int kBufs = 2;               // accumulators in turn
-    constexpr int kSegs = kCut ? 6 : 1;
-    auto part_of = [](int64_t left) { return kCut && left > kLceCut ? (int64_t)kLceCut : left; };
+    constexpr int kBufs = 2;  // accumulators in turn
+    constexpr int kSegs = sizeof(T) == 4 ? 6 : 1;  // products of planes
+    constexpr int kCut = lce_cut<EPI, T>();
+    auto part_of = [](int64_t left) { return PARTS && left > kCut ? (int64_t)kCut : left; };
 
     if (warp == 0) {
         // ---- loader ----
@@ -583,10 +592,10 @@ lce_product(const __grid_constant__ CUtensorMap a0, const __grid_constant__ CUte
                 const bool a_mn = t.job == 1, b_mn = EPI == kLceGrads;
                 const int m0 = (int)(t.m * kLceM) + rank * kLceHalf;
                 const int n0 = (int)(t.n * kLceN) + rank * kLceHalf;
-                for (int64_t kp = 0; kp < t.nk && ok; kp += kLceCut) {
+                for (int64_t kp = 0; kp < t.nk && ok; kp += kCut) {
                     const int len = (int)part_of(t.nk - kp);
                     for (int j = 0, seg = 0, k0 = (int)(t.k0 + kp) * kLceK; seg < kSegs;) {
-                        const int2 pl = kCut ? lce_planes(seg) : make_int2(0, 0);
+                        const int2 pl = kSegs > 1 ? lce_planes(seg) : make_int2(0, 0);
                         ok = mbar_wait(empty(s), phase ^ 1u, abort);
                         if (!ok) break;
                         if (rank == 0) mbar_expect(full(s), 2 * kLceStage);
@@ -617,7 +626,7 @@ lce_product(const __grid_constant__ CUtensorMap a0, const __grid_constant__ CUte
                             phase ^= 1u;
                         }
                     }
-                    if (!kCut) break;
+                    if (!PARTS) break;
                 }
             }
             // no copy may be in flight when the block ends: the last ones have been
@@ -641,7 +650,7 @@ lce_product(const __grid_constant__ CUtensorMap a0, const __grid_constant__ CUte
                 if (t.nk == 0) continue;
                 const bool a_mn = t.job == 1, b_mn = EPI == kLceGrads;
                 const uint32_t idesc = tc_idesc(g.bf16 != 0, a_mn, b_mn, kLceM, kLceN);
-                for (int64_t kp = 0; kp < t.nk && ok; kp += kLceCut) {
+                for (int64_t kp = 0; kp < t.nk && ok; kp += kCut) {
                     const int len = (int)part_of(t.nk - kp) * kSegs;
                     ok = mbar_wait(acc_empty(buf), acc_phase ^ 1u, abort);
                     if (!ok) break;
@@ -672,7 +681,7 @@ lce_product(const __grid_constant__ CUtensorMap a0, const __grid_constant__ CUte
                         buf = 0;
                         acc_phase ^= 1u;
                     }
-                    if (!kCut) break;
+                    if (!PARTS) break;
                 }
             }
             tc_commit_own(drained);
@@ -692,16 +701,13 @@ lce_product(const __grid_constant__ CUtensorMap a0, const __grid_constant__ CUte
         bool ok = true;
         for (int64_t i = 0; i < tiles; ++i) {
             const LceTile t = walk.next(g);
-            const bool some = t.nk > 0;
             const uint32_t mine =
                 tmem + ((uint32_t)(32 * quarter) << 16) + half * (kLceN / 2);
             auto arrived = [&]() {  // the whole warp agrees on whether the product came
-                if (some && ok)
-                    ok = __all_sync(0xffffffffu, mbar_wait(acc_full(buf), acc_phase, abort));
+                if (ok) ok = __all_sync(0xffffffffu, mbar_wait(acc_full(buf), acc_phase, abort));
                 tc_fence_after();
             };
             auto release = [&]() {
-                if (!some) return;
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive_cluster(cluster_addr(acc_empty(buf), 0));
@@ -711,42 +717,41 @@ lce_product(const __grid_constant__ CUtensorMap a0, const __grid_constant__ CUte
                 }
             };
             const int64_t row = t.m * kLceM + row_in;
-            // The row's half of the tile; NaN if the product did not come.  An
-            // accumulator is free once it is read.
+            // The row's half of the tile, summed over its parts along K (rounding to
+            // nearest).  An accumulator is free once it is read.
             constexpr int kCols = kLceN / 2;
             float f[kCols];
-            arrived();
-            if (some && ok) {
+            if (t.nk > 0) {
+                arrived();
                 const uint32_t src = mine + buf * kLceN;
 #pragma unroll
                 for (int c = 0; c < kCols; c += 32) tmem_load32(f, c, src + c);
                 tmem_wait(f);
+                release();
             } else {
 #pragma unroll
-                for (int e = 0; e < kCols; ++e) f[e] = ok ? 0.f : __int_as_float(0x7fc00000);
+                for (int e = 0; e < kCols; ++e) f[e] = 0.f;
             }
-            release();
-            if constexpr (kCut) {  // the further parts of the sum
-                for (int64_t left = t.nk - kLceCut; left > 0; left -= kLceCut) {
-                    arrived();
-                    if (ok) {
-                        const uint32_t src = mine + buf * kLceN;
+            for (int64_t left = PARTS ? t.nk - kCut : 0; left > 0; left -= kCut) {
+                arrived();
+                const uint32_t src = mine + buf * kLceN;
 #pragma unroll
-                        for (int c = 0; c < kCols; c += 32) {
-                            float part[32];
-                            tmem_load32(part, 0, src + c);
-                            tmem_wait(part);
+                for (int c = 0; c < kCols; c += 16) {
+                    float part[16];
+                    tmem_load16(part, src + c);
+                    tmem_wait16(part);
+                    if (c + 16 == kCols) release();
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) f[c + e] += part[e];
-                        }
-                    } else {
-                        f[0] = __int_as_float(0x7fc00000);
-#pragma unroll
-                        for (int e = 1; e < kCols; ++e) f[e] = f[0];
+                    for (int e = 0; e < 16; e += 2) {
+                        const float2 v = add2(make_float2(f[c + e], f[c + e + 1]),
+                                              make_float2(part[e], part[e + 1]));
+                        f[c + e] = v.x;
+                        f[c + e + 1] = v.y;
                     }
-                    release();
                 }
             }
+            // what a tile whose product did not come is multiplied with
+            const float gone = ok ? 1.f : __int_as_float(0x7fc00000);
             if constexpr (EPI == kLceStats) {
                 const int64_t n0 = t.n * kLceN + half * kCols;
                 const int width = (int)min((int64_t)kCols, g.V - n0);
@@ -761,7 +766,7 @@ lce_product(const __grid_constant__ CUtensorMap a0, const __grid_constant__ CUte
 #pragma unroll
                     for (int e = 0; e < kCols; ++e)
                         if (hit == e) v = f[e];
-                    g.row_hit[row] = v;
+                    g.row_hit[row] = v * gone;
                 }
                 // four chains each
                 float top[4];
@@ -786,7 +791,7 @@ lce_product(const __grid_constant__ CUtensorMap a0, const __grid_constant__ CUte
                     s2[e / 2 % 4] = add2(s2[e / 2 % 4], z);
                 }
                 const float2 t2 = add2(add2(s2[0], s2[1]), add2(s2[2], s2[3]));
-                const float sum = t2.x + t2.y;
+                const float sum = (t2.x + t2.y) * gone;
                 if (row < count) g.part[(2 * t.n + half) * g.row_cap + row] = make_float2(m, sum);
             } else if constexpr (EPI == kLceQ) {
                 using O = typename LceSplit<T>::O;
@@ -794,7 +799,7 @@ lce_product(const __grid_constant__ CUtensorMap a0, const __grid_constant__ CUte
                 const int width = (int)min((int64_t)kCols, g.V - g.v0 - n0);
                 const bool live = row < count;
                 const float l2 = live ? g.row_lse2[row] : 0.f;
-                const float up = live ? g.row_up[row] : 0.f;
+                const float up = live ? g.row_up[row] * gone : 0.f;
                 const int hit = live ? g.target[row] - (int)(g.v0 + n0) : -1;
                 O *q = static_cast<O *>(g.q) + row * g.q_pitch + n0;
                 const int64_t plane = g.row_cap * g.q_pitch;
@@ -839,7 +844,7 @@ lce_product(const __grid_constant__ CUtensorMap a0, const __grid_constant__ CUte
                     }
                 }
             } else {
-                const float un = *g.unscale;
+                const float un = *g.unscale * gone;
                 const int64_t n0 = t.n * kLceN + half * kCols;
                 const int width = (int)min((int64_t)kCols, g.D - n0);
                 const bool live = t.job ? row < g.vc : row < count;

@@ -178,6 +178,25 @@ __device__ __forceinline__ void tmem_load32(float (&f)[N], int at, uint32_t addr
         : "r"(addr)
         : "memory");
 }
+// 16 columns, and the wait for them.
+__device__ __forceinline__ void tmem_load16(float (&f)[16], uint32_t addr) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=f"(f[0]), "=f"(f[1]), "=f"(f[2]), "=f"(f[3]), "=f"(f[4]), "=f"(f[5]), "=f"(f[6]),
+          "=f"(f[7]), "=f"(f[8]), "=f"(f[9]), "=f"(f[10]), "=f"(f[11]), "=f"(f[12]), "=f"(f[13]),
+          "=f"(f[14]), "=f"(f[15])
+        : "r"(addr)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_wait16(float (&f)[16]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+f"(f[0]), "+f"(f[1]), "+f"(f[2]), "+f"(f[3]), "+f"(f[4]), "+f"(f[5]),
+                   "+f"(f[6]), "+f"(f[7]), "+f"(f[8]), "+f"(f[9]), "+f"(f[10]), "+f"(f[11]),
+                   "+f"(f[12]), "+f"(f[13]), "+f"(f[14]), "+f"(f[15])
+                 :
+                 : "memory");
+}
 // Waits for the loads into f; what reads it comes after.
 template <int N>
 __device__ __forceinline__ void tmem_wait(float (&f)[N]) {
