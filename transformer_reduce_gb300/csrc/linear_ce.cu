@@ -22,7 +22,7 @@ struct LceLayout {
     int64_t row_cap, chunks, pitch, w_pitch, vc, pieces, q_pitch, splits, split_k;
     int planes;
     bool pack_w;
-    size_t chunk_count, chunk_up, single, row_of, row_target, row_lse2, row_up, row_hit, x, w, part,
+    size_t chunk_count, chunk_up, single, row_of, row_target, row_lse, row_up, row_hit, x, w, part,
         q, dx_sum, total;
 };
 
@@ -73,7 +73,7 @@ static LceLayout lce_layout(bool backward, int64_t rows, int64_t D, int64_t V, s
     l.x = take(l.planes * l.row_cap * l.pitch * 2);
     if (l.pack_w) l.w = take(l.planes * V * l.w_pitch * 2);
     if (backward) {
-        l.row_lse2 = take(l.row_cap * 4);
+        l.row_lse = take(l.row_cap * 4);
         l.row_up = take(l.row_cap * 4);
         l.q = take(l.planes * l.row_cap * l.q_pitch * 2);
         if (l.pieces > 1 || l.splits > 1) l.dx_sum = take(l.splits * l.row_cap * round_up(D, 8) * 4);
@@ -169,7 +169,7 @@ cudaError_t lce_prepare(LceArgs *g, const void **w_at, const LceLayout &l, bool 
     p.unscale = reinterpret_cast<float *>(ws + l.single + 4);
     p.row_of = reinterpret_cast<int *>(ws + l.row_of);
     p.row_target = reinterpret_cast<int *>(ws + l.row_target);
-    p.row_lse2 = reinterpret_cast<float *>(ws + l.row_lse2);
+    p.row_lse = reinterpret_cast<float *>(ws + l.row_lse);
     p.row_up = reinterpret_cast<float *>(ws + l.row_up);
     p.loss = loss;
     p.lse_out = lse_out;
@@ -201,7 +201,7 @@ cudaError_t lce_prepare(LceArgs *g, const void **w_at, const LceLayout &l, bool 
     g->count = p.count;
     g->row_of = p.row_of;
     g->target = p.row_target;
-    g->row_lse2 = p.row_lse2;
+    g->row_lse = p.row_lse;
     g->row_up = p.row_up;
     g->unscale = p.unscale;
     return e;
