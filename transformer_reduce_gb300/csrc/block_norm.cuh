@@ -71,22 +71,31 @@ struct BnReduce {
 };
 
 // Chunk of V elements at column c of a row; columns from `hidden` on are 0.
-// AL: rows of whole chunks on 16-byte addresses.
+// AL: rows of whole chunks on 16-byte addresses.  An output may be the same tensor:
+// no loads that want memory to be read-only for the whole kernel.
 template <typename T, bool AL>
-__device__ __forceinline__ uint4 bn_load(const T *row, int c, int hidden, bool stream) {
+__device__ __forceinline__ uint4 bn_row(const T *row, int c, int hidden) {
     constexpr int V = Traits<T>::kVec;
-    if (AL) return stream ? ld_stream16(row + c) : ld_cached16(row + c);
+    if (AL) return ld_stream16(row + c);
     float f[V];
 #pragma unroll
-    for (int e = 0; e < V; ++e)
-        f[e] = c + e < hidden ? Traits<T>::load1_cached(row + c + e) : 0.f;
+    for (int e = 0; e < V; ++e) f[e] = c + e < hidden ? Traits<T>::load1(row + c + e) : 0.f;
     return Traits<T>::pack(f);
 }
-// The same as pairs, of a vector that every row reads.
+// The same as pairs, of a gate, gamma or beta, which every row reads and no output is.
 template <typename T, bool AL>
 __device__ __forceinline__ void bn_pairs(const T *row, int c, int hidden,
                                          float2 (&f)[Traits<T>::kVec / 2]) {
-    unpack2<T>(bn_load<T, AL>(row, c, hidden, false), f);
+    constexpr int V = Traits<T>::kVec;
+    if (AL) {
+        unpack2<T>(ld_cached16(row + c), f);
+    } else {
+        float v[V];
+#pragma unroll
+        for (int e = 0; e < V; ++e)
+            v[e] = c + e < hidden ? Traits<T>::load1_cached(row + c + e) : 0.f;
+        unpack2<T>(Traits<T>::pack(v), f);
+    }
 }
 template <typename T, bool AL>
 __device__ __forceinline__ void bn_store(T *row, int c, int hidden,
@@ -164,8 +173,8 @@ bn_fw(const BlockNorm<T> a, int64_t per) {
             const int c = (k * TPR + lane) * V;
             xr[k] = rr[k] = make_uint4(0u, 0u, 0u, 0u);
             if (c < hidden && row < end) {
-                xr[k] = bn_load<T, AL>(a.x + row * a.hidden, c, hidden, true);
-                rr[k] = bn_load<T, AL>(a.r + row * a.hidden, c, hidden, true);
+                xr[k] = bn_row<T, AL>(a.x + row * a.hidden, c, hidden);
+                rr[k] = bn_row<T, AL>(a.r + row * a.hidden, c, hidden);
             }
         }
     };
@@ -348,7 +357,7 @@ bn_bw(const BlockNorm<T> a, const BnCut cut, float *part, float *gate_part) {
         if (kStaged)
             unpack2<T>(stage[((s * 4 + which) * CPT + k) * BLOCK], f);
         else
-            bn_pairs<T, AL>(row, c, hidden, f);
+            unpack2<T>(bn_row<T, AL>(row, c, hidden), f);
     };
     float2 g2[CPT][H2], b2[CPT][H2], sa[CPT][H2], sb[CPT][H2], gp[CPT][H2], bp[CPT][H2];
 #pragma unroll
