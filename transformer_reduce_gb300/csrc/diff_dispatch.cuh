@@ -55,7 +55,21 @@ bool diff_same_phase(const DiffRows<P> &x, int phase, const DiffShape &p) {
            (x.batch - p.H * dense) % V == 0;
 }
 
-template <auto K, int TPR, int CPT, bool AL, typename... Args>
+// Whether the rows of a causal call are dealt over the grid, in turns of G rows,
+// instead of cut into runs of `per`.  A block that meets every batch entry looks
+// through all their masks first, and past kRelposWinMax of them adds the mask
+// element by element; a run of half a head or more is balanced by itself.  Dealt
+// and in runs, us, forward and backward, bf16 with padding:
+//     [64,1,16,1000] 24.3, 27.7 and  9.3,  13.2     [70,6,333,333]   118, 249 and  98, 200
+//     [32,8,512,512] 70.1, 118  and 63.9, 116       [8,8,1024,1024] 64.1, 107 and 73.6, 123
+//     [64,8,256,256] 42.6, 74.2 and 35.1, 62.7      [4,8,2048,2048]  125, 194 and  150, 229
+template <bool MASKED>
+bool diff_dealt(const DiffShape &p, int G) {
+    if (!p.causal || p.Tq == 1) return false;
+    return !MASKED || (p.per * 2 < p.Tq && p.B <= p.per / G && p.B <= kRelposWinMax);
+}
+
+template <auto K, int TPR, int CPT, bool AL, bool MASKED, typename... Args>
 cudaError_t launch_diff_rows(int tensors, int resident, int mask_vec, DiffShape p, cudaStream_t st, Args... args) {
     const size_t smem = diff_smem<TPR, CPT, AL>(tensors);
     const cudaError_t e = relpos_allow_smem<K>(smem);
@@ -65,7 +79,7 @@ cudaError_t launch_diff_rows(int tensors, int resident, int mask_vec, DiffShape 
         (int64_t)device_sm_count() * relpos_resident(resident, smem);
     p.per = ceil_div(ceil_div(p.rows, blocks), G) * G;
     const unsigned grid = (unsigned)ceil_div(p.rows, p.per);
-    if (p.causal && p.Tq > 1) p.per = 0;
+    if (diff_dealt<MASKED>(p, G)) p.per = 0;
     return launch_pdl(K, dim3(grid), dim3(diff_block<TPR>()), smem, st, args..., p, mask_vec);
 }
 
@@ -79,7 +93,7 @@ cudaError_t launch_diff_fw(T *out, float4 *stats, DiffRows<const T> x1, DiffRows
     const int mask_vec = relpos_phase<T>(mask) == 0;
     if (pick_diff_bucket(p, V, al, 4, &tpr, &cpt)) {
 #define F(TPR_, CPT_, AL_, M_)                                                             \
-    launch_diff_rows<diff_fw_vec<T, TPR_, CPT_, AL_, M_>, TPR_, CPT_, AL_>(                 \
+    launch_diff_rows<diff_fw_vec<T, TPR_, CPT_, AL_, M_>, TPR_, CPT_, AL_, M_>(             \
         2, diff_fw_min_blocks<TPR_, CPT_>(), mask_vec, p, st, out, stats, x1, x2, lam, mask)
 #define X(TPR_, CPT_)                                                               \
     if (tpr == TPR_ && cpt == CPT_)                                                 \
@@ -110,7 +124,7 @@ cudaError_t launch_diff_bw_rows(DiffRows<T> dx1, DiffRows<T> dx2, float *row_dot
     if (diff_same_phase<T>(dx1, phase, p) && diff_same_phase<T>(dx2, phase, p) &&
         pick_diff_bucket(p, V, al, 2, &tpr, &cpt)) {
 #define F(TPR_, CPT_, AL_, M_)                                                                 \
-    launch_diff_rows<diff_bw_vec<T, TPR_, CPT_, AL_, M_>, TPR_, CPT_, AL_>(                     \
+    launch_diff_rows<diff_bw_vec<T, TPR_, CPT_, AL_, M_>, TPR_, CPT_, AL_, M_>(                 \
         3, diff_bw_min_blocks<TPR_, CPT_>(), mask_vec, p, st, dx1, dx2, row_dot, dout, x1, x2, \
         lam, stats, mask)
 #define X(TPR_, CPT_)                                                               \
