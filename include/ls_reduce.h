@@ -806,12 +806,20 @@ ls_status ls_block_norm_bw(void *dx, void *dr, float *dgate, float *dgamma_post,
 #define LS_MAX_LINEAR_VOCAB ((int64_t)1 << 28)
 
 /*
- * Bytes of device workspace the cross entropy from hidden states needs.  The
- * forward's holds a copy of the rows that count and 8 bytes per row and 256
- * vocabulary entries; the backward's also a piece of the vocabulary's logit
- * gradients (about 512 MiB, or 4096 entries per row if that is more).  Both
- * hold a copy of w for fp32 and where hidden is no multiple of 8.  0 for sizes
- * that are refused and, forward, without rows.  Host-only; launches nothing.
+ * Bytes of device workspace the cross entropy from hidden states needs, with R
+ * the rows up to a multiple of 256, D hidden up to a multiple of 8, and 2 bytes an
+ * element of a copy (fp32: 6, three planes):
+ *   both      a copy of the rows that count, R D elements; for fp32 and where
+ *             hidden is no multiple of 8 a copy of w, vocab D elements; up to
+ *             16 bytes per row beside them
+ *   forward   16 bytes per row of R and 256 vocabulary entries
+ *   backward  the logits' gradients of a piece of the vocabulary, R times as many
+ *             elements as it has entries (all of it where that takes up to
+ *             512 MiB, else as much as does, 4096 entries at least); where dx is
+ *             summed over pieces or cuts of them 4 R D bytes for each cut, at
+ *             most 32 (cut are the sums of few rows over a large vocabulary)
+ * 0 for sizes that are refused and, forward, without rows.  Host-only; launches
+ * nothing.
  */
 size_t ls_linear_cross_entropy_fw_workspace_size(int64_t rows, int64_t hidden, int64_t vocab,
                                                  ls_dtype dt);
@@ -826,8 +834,9 @@ size_t ls_linear_cross_entropy_bw_workspace_size(int64_t rows, int64_t hidden, i
  * The logits are FP32 sums of exact products of the stored values (fp32: of
  * products good to about 2^-23) and are not rounded to the storage type; the
  * tensor cores cut a sum off every 16 products, and parts of it are added
- * rounding to nearest (up to about 2^-17 of a sum of terms of one sign).  Ignored rows (negative
- * target): loss = lse = 0; target >= vocab: NaN; neither row of x is read.
+ * rounding to nearest (up to about 2^-17 of a sum of terms of one sign).
+ * Ignored rows (negative target): loss = lse = 0; target >= vocab: NaN; neither
+ * row of x is read.
  *
  *   loss, lse  [rows] float32, device, written.
  *   x          [rows, hidden] dt, device, read.
