@@ -837,6 +837,9 @@ size_t ls_linear_cross_entropy_bw_workspace_size(int64_t rows, int64_t hidden, i
  * rounding to nearest (up to about 2^-17 of a sum of terms of one sign).
  * Ignored rows (negative target): loss = lse = 0; target >= vocab: NaN; neither
  * row of x is read.
+ * No wait inside the kernels lasts longer than two seconds of wall-clock time:
+ * what hung on one that ran out (the GPU was taken away for so long) comes out as
+ * NaN, in both directions, without a status.
  *
  *   loss, lse  [rows] float32, device, written.
  *   x          [rows, hidden] dt, device, read.
