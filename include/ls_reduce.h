@@ -784,7 +784,9 @@ size_t ls_block_norm_bw_workspace_size(int64_t rows, int64_t hidden, int64_t gat
  *          NULL (with gamma_pre): none.
  *   x      as given to the forward; read with gamma_post or gate.
  *   h, stats  as written by the forward (h read with gamma_pre).
- *   gate, gamma_post, beta_post, gamma_pre  as given to the forward.
+ *   gate, gamma_post, beta_post, gamma_pre  as given to the forward.  (beta_post
+ *          only enters dgate, which is that of a forward without it where it is
+ *          left out: no status tells.)
  *   workspace  device scratch of at least ls_block_norm_bw_workspace_size(...)
  *          bytes, 16-byte aligned, contents ignored; may be NULL when that is 0.
  *          Calls that overlap on the GPU must not share it.

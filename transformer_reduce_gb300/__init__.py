@@ -1046,8 +1046,10 @@ def block_norm_bw(dy, dh, x, h, stats, gamma_pre=None, gamma_post=None, beta_pos
     uses (``dh``, None: there are none), the forward's x and its h and stats:
     (dx, dresidual, dgamma_pre, dbeta_pre, dgamma_post, dbeta_post, dgate), those
     of the parameters fp32 in a fixed summation order and None where there is no
-    such parameter (the betas' are given for "layer").  ``dx`` may be dy, dh, x
-    or h, ``dr`` dy, dh or h (in place)."""
+    such parameter (the betas' are given for "layer").  ``beta_post`` has to be
+    given wherever the forward had one: dgate is made of it, and nothing here can
+    tell that it is missing.  ``dx`` may be dy, dh, x or h, ``dr`` dy, dh or h (in
+    place)."""
     torch = _torch()
     f32, device = torch.float32, x.device
     rows, hidden, gates, layer = _block(x, kind, gate, gamma_pre, None, gamma_post, beta_post)
