@@ -57,7 +57,7 @@ struct DiffCursor {
 // The rows of a block: from beg on, G at a time, `step` further each turn.  A run
 // of its own (p.per rows), or, where rows differ in length (causal; the launcher's
 // rule), turns that lie a whole grid apart, so that no block gets the long rows of
-// a head alone ([8,6,777,777] fp16 backward: 96 us in runs, 82 dealt out; with
+// a head alone ([8,6,777,777] fp16 backward: 96 us in runs, 83 dealt out; with
 // turns of one run taken from a head's start and end alternately 89).
 struct DiffBlock {
     int64_t beg, end;
