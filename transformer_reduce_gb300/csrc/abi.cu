@@ -1300,6 +1300,8 @@ ls_status ls_softmax_bw_diff(void *dx1, void *dx2, float *dlam, const void *dout
                             {span_of(dout, p.rows * Tk, es), span_of(stats, 4 * p.rows, 4),
                              span_of(mask, B * Tk, es), span_of(lam, lam_count, 4)}))
             return LS_ERR_INVALID_ARG;
+        for (const HeadSpan &f : {flat[1], flat[4]})  // the workspace and dlam
+            if (heads_meet(i1, f, B, H) || heads_meet(i2, f, B, H)) return LS_ERR_INVALID_ARG;
         for (const HeadSpan *o : {&o1, &o2}) {
             const HeadSpan &own = o == &o1 ? i1 : i2, &other = o == &o1 ? i2 : i1;
             if ((heads_meet(*o, own, B, H) && !heads_same(*o, own, B, H)) ||
