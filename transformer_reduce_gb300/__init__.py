@@ -963,12 +963,17 @@ def softmax_bw_diff(dout, scores1, scores2, lam, stats, mask=None, causal: bool 
 _NORM_KINDS = {"rms": 0, "layer": 1}
 
 
-def _block(x, kind, gate, gamma_pre, beta_pre, gamma_post, beta_post):
-    """(rows, hidden, gates, layer) of the norms around a block."""
-    rows, hidden = _rows_hidden(x)
+def _norm_kind(kind) -> int:
     layer = _NORM_KINDS.get(kind)
     if layer is None:
         raise ValueError(f"kind must be 'rms' or 'layer', got {kind!r}")
+    return layer
+
+
+def _block(x, kind, gate, gamma_pre, beta_pre, gamma_post, beta_post):
+    """(rows, hidden, gates, layer) of the norms around a block."""
+    rows, hidden = _rows_hidden(x)
+    layer = _norm_kind(kind)
     want, dtype = (hidden,), x.dtype
     for t in (gamma_pre, beta_pre, gamma_post, beta_post):
         if t is not None and (t.shape != want or t.dtype != dtype):
@@ -1035,7 +1040,7 @@ def block_norm_workspace(rows: int, hidden: int, gates: int, kind: str, dtype, d
     """A workspace tensor of the size ls_block_norm_bw needs (``gates`` 0 without
     a gate)."""
     torch = _torch()
-    n = ls_block_norm_bw_workspace_size(rows, hidden, gates, _NORM_KINDS[kind],
+    n = ls_block_norm_bw_workspace_size(rows, hidden, gates, _norm_kind(kind),
                                         ls_dtype(torch.empty(0, dtype=dtype)))
     return torch.empty(max(n, 16) // 4, device=device, dtype=torch.float32)
 
