@@ -69,11 +69,12 @@ enum { kLceStats = 0, kLceQ = 1, kLceGrads = 2 };
 // (measured: two thirds of that): uncut, dW of [2097152,8] was 1.2 % off and the
 // lse of 65536 hidden elements 8e-3.  With these cuts 64 * 16 elements lose at most
 // 8e-6 and 64 * 64 3e-5.  (Cuts of 4 and 16 steps took 8 % of the forward and of
-// the backward of [8192,1024] bf16 by 50257.)  fp32 logits are cut at every step:
-// exp(z - lse) - 1 of a row whose weight is on its target magnifies their errors.
-// Of [14,1024] by 65 with such targets dx and dW were four times as far from 64
-// bits as a plain FP32 form's at cuts of 4 steps, twice at 2, and are as near as
-// those at 1 (the backward of [1001,333] by 10007: 129, 133 and 137 us).
+// the backward of [8192,1024] bf16 by 50257.)  fp32 sums are cut every 256 elements
+// (dx of [1001,333] by 10007 was 1.9e-5 of its largest off uncut), the logits at
+// every step: exp(z - lse) - 1 of a row whose weight is on its target magnifies
+// their errors.  Of [14,1024] by 65 with such targets dx and dW were four times as
+// far from 64 bits as a plain FP32 form's at cuts of 4 steps, twice at 2, and are as
+// near as those at 1 (the backward of [1001,333] by 10007: 129, 133 and 137 us).
 template <int EPI, typename T>
 constexpr int lce_cut() {
     return sizeof(T) == 4 ? (EPI == kLceGrads ? 4 : 1) : EPI == kLceGrads ? 64 : 16;
